@@ -378,6 +378,155 @@ int ice_debug_set_flags(ice_index* ix, int32_t flags);
 int ice_key_codes_noalloc(const ice_params* params, const void* keys, int64_t n_tokens,
                           uint64_t* morton_out, int32_t* e_out, void* stream);
 
+/* ======================================================================== */
+/* The plain paged cache of a batch whose requests share a prefix            */
+/* ======================================================================== */
+
+/*
+ * The calls below serve the layers (or models) whose attention is not sparse,
+ * for a batch of requests that continue one shared prefix: a system prompt, a
+ * document with many questions, parallel samples of one prompt. K and V live in
+ * pages of page_size tokens that the caller owns; a request has a row of page
+ * ids (its block table) for its own tokens, and the prefix has one list of page
+ * ids for the whole batch. Everything that a step needs is on the GPU: one call
+ * moves the block tables on from the requests' lengths and finds the slots of
+ * the new tokens, one writes their K and V rows, one attends.
+ *
+ * One ice_paged handle holds the geometry, the scratch memory of the attention
+ * and a device status word. Conventions are those of the top of this file, and:
+ *  - a layer's pages are two arrays k_pages, v_pages, device,
+ *    [n_pages][n_kv_heads][page_size][d], dtype, 16-byte aligned. The same block
+ *    tables and slots serve every layer; prefix and own tokens may use pages of
+ *    the same arrays.
+ *  - the buffers are device memory of the GPU that was current when the handle
+ *    was made, which must be current in every call (ICE_ERR_INVALID_ARG
+ *    otherwise). They are checked as those of the calls above; page-locked host
+ *    memory is not taken.
+ *  - lengths, page ids and slots are read on the GPU, so the calls can be captured
+ *    in a CUDA graph and replayed as these change. Values out of range are
+ *    reported through ice_paged_get_error; no memory outside the given buffers is
+ *    read or written for them.
+ *  - calls on one handle share its scratch: on different streams (or as captured
+ *    graphs) they must be ordered by the caller.
+ */
+typedef struct ice_paged ice_paged; /* opaque */
+
+typedef struct ice_paged_params {
+    int32_t d;            /* head dimension; the kernels support 128                  */
+    int32_t n_kv_heads;   /* KV heads (>= 1)                                          */
+    int32_t n_q_heads;    /* query heads; n_q_heads / n_kv_heads = 1, 2, 4 or 8       */
+    int32_t page_size;    /* P: tokens per page, 1..64                                */
+    int32_t dtype;        /* ICE_BF16 or ICE_F32                                      */
+    int32_t max_requests; /* requests per call, 1..8192                               */
+    int32_t max_blocks;   /* columns of the block table: pages per request;           */
+                          /* max_blocks * page_size <= 2^30                           */
+    int32_t max_tokens;   /* new tokens per ice_paged_attn call, 1..2^20              */
+    int64_t n_pages;      /* pages of the pool; n_pages * n_kv_heads * page_size      */
+                          /* < 2^31                                                   */
+} ice_paged_params;
+
+/* ice_paged_create - a handle for the current device. Allocates the scratch of
+ * the attention: 528 bytes for each of max(2 R, min(64 R, 262144)) partial rows
+ * with R = max_tokens * n_q_heads (ICE_ERR_CAPACITY if that fails). */
+int ice_paged_create(const ice_paged_params* params, ice_paged** out);
+
+/* ice_paged_destroy - waits for the device, then frees the handle. */
+void ice_paged_destroy(ice_paged* pg);
+
+/* ice_paged_get_error - waits for `stream`, then returns and clears the handle's
+ * device status word (ICE_OK if no kernel reported an error). */
+int ice_paged_get_error(ice_paged* pg, void* stream);
+
+/*
+ * ice_paged_tables - block tables and slot maps of one step, from the requests'
+ * lengths.
+ *
+ * seq_len: device int32 [n_req], tokens that each request holds.
+ * n_new: device int32 [n_req], by how many tokens each changes: new tokens (>= 0),
+ *   or tokens given up (< 0; -seq_len ends the request, a few tokens are drafts
+ *   that were rejected).
+ * block_table: device int32 [n_req][max_blocks], in and out. Entry [r][j] is the
+ *   page of tokens j*P .. j*P + P - 1 of request r.
+ * free_pages: device int32 [n_pages], in and out: a ring of free page ids.
+ * free_state: device int64 [2]: head and tail of the ring, which only grow; the
+ *   free pages are free_pages[i % n_pages], head <= i < tail. A fresh pool has
+ *   free_pages = 0 .. n_pages - 1, head 0, tail n_pages.
+ * seq_len_out, free_state_out: device, as seq_len and free_state; receive the
+ *   lengths and the ring after the step. Each may be its input (in place).
+ * q_start: device int32 [n_req + 1]; receives where each request's new tokens
+ *   begin among all new tokens, and their number at the end.
+ * slot_map: device int64 [n_slots]; receives the slot (page * P + offset) of
+ *   each new token, request by request, and -1 behind the last.
+ * positions: device int32 [n_slots] or NULL; receives the index of each new token
+ *   among its request's own tokens, and 0 behind the last.
+ *
+ * A request that grows takes pages from the head of the ring, and one that
+ * shrinks gives the pages that it no longer touches back at the tail, each in the
+ * order of the requests and then of the pages; pages given back by this call are
+ * not taken by it. Entries of pages given back stay in the block table. The
+ * result does not depend on how the work is spread over the GPU.
+ *
+ * All or nothing: if the free pages, the columns or the slots do not suffice
+ * (ICE_ERR_CAPACITY), or a length or the ring is impossible (ICE_ERR_BOUNDS: a
+ * length below 0 or above the block table, head > tail, more than n_pages free), the
+ * status word says so, block_table and free_pages stay as they were,
+ * seq_len_out and free_state_out are the inputs, q_start is all 0 and slot_map
+ * all -1, so that calls which follow add nothing.
+ */
+int ice_paged_tables(ice_paged* pg, int32_t n_req, const int32_t* seq_len, const int32_t* n_new,
+                     int32_t* block_table, int32_t* free_pages, const int64_t* free_state,
+                     int32_t* seq_len_out, int64_t* free_state_out, int32_t* q_start,
+                     int64_t* slot_map, int32_t* positions, int32_t n_slots, void* stream);
+
+/*
+ * ice_paged_append - writes the new tokens' K and V rows into their slots.
+ *
+ * k, v: device, n_tokens x [n_kv_heads][d], dtype; token i starts k_stride (v_stride)
+ *   elements after token i - 1 (a slice of a fused projection's output is fine).
+ *   Base addresses and strides are multiples of 16 bytes.
+ * slot_map: device int64 [n_tokens], as written by ice_paged_tables. A token
+ *   whose slot is -1 is skipped; any other slot outside the pool is skipped and
+ *   reported (ICE_ERR_BOUNDS). The slots of one call are distinct.
+ */
+int ice_paged_append(ice_paged* pg, int32_t n_tokens, const void* k, int64_t k_stride, const void* v,
+                     int64_t v_stride, const int64_t* slot_map, void* k_pages, void* v_pages,
+                     void* stream);
+
+/*
+ * ice_paged_attn - attention of the batch's new tokens over the shared prefix,
+ * whose keys and values are read once for the whole batch, and over each request's
+ * own tokens.
+ *
+ * q: device, n_tokens x [n_q_heads][d], dtype; q_stride as k_stride above.
+ * q_start: device int32 [n_req + 1]; request r's new tokens are q_start[r] ..
+ *   q_start[r + 1] - 1 of q, in order (one for a decode step, more for draft
+ *   tokens or a chunk of a prompt, none for a request that waits). q_start[0] = 0,
+ *   q_start[n_req] <= n_tokens.
+ * seq_len: device int32 [n_req], each request's own tokens, the new ones among them.
+ * block_table: device int32 [n_req][max_blocks].
+ * prefix_table: device int32 [ceil(prefix_len / P)], the prefix's pages; NULL when
+ *   prefix_len is 0. prefix_len may end inside a page.
+ * out: device, [n_tokens][n_q_heads][d], dtype, not overlapping q.
+ *
+ * Query head g of KV head h is h * G + g. The i-th new token of request r sees every
+ * prefix token and the own tokens t <= seq_len[r] - (q_start[r + 1] - q_start[r]) + i:
+ * out = sum_t softmax_t(q . k_t / sqrt(d)) v_t over both together. A token that
+ * sees nothing gets zeros. Rows of out behind q_start[n_req] are left as they
+ * were. Slots of the pages behind a length are not used, whatever they hold;
+ * values of tokens that exist are finite (a token hidden from some rows of its tile
+ * has weight zero there, and zero times an infinity would be NaN).
+ * Sums, softmax statistics and the parts' joining are in fp32; with bf16 the
+ * weights are rounded to bf16 before they meet the values, as the values are.
+ *
+ * A page id outside the pool reads as a page of zeros and is reported
+ * (ICE_ERR_BOUNDS); q_start or seq_len out of range are reported and out is left
+ * as it was.
+ */
+int ice_paged_attn(ice_paged* pg, int32_t n_req, int32_t n_tokens, const void* q, int64_t q_stride,
+                   const int32_t* q_start, const int32_t* seq_len, const int32_t* block_table,
+                   const int32_t* prefix_table, int32_t prefix_len, const void* k_pages,
+                   const void* v_pages, void* out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -38,7 +38,9 @@ ICE_BF16 = 1
 EXPORTS = ["ice_build", "ice_insert", "ice_select", "ice_select_attn", "ice_sparse_attn", "ice_get_error",
            "ice_destroy", "ice_status_string", "ice_get_info", "ice_debug_dump", "ice_debug_page",
            "ice_key_codes_noalloc", "ice_select_attn_reuse", "ice_reuse_reset",
-           "ice_debug_set_flags", "ice_select_heads", "ice_decode_step", "ice_set_cluster_size"]
+           "ice_debug_set_flags", "ice_select_heads", "ice_decode_step", "ice_set_cluster_size",
+           "ice_paged_create", "ice_paged_destroy", "ice_paged_get_error", "ice_paged_tables",
+           "ice_paged_append", "ice_paged_attn"]
 
 
 class ice_params(ctypes.Structure):
@@ -63,6 +65,14 @@ class ice_info(ctypes.Structure):
                 ("n_composite", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("host_bytes", ctypes.c_int64),
                 ("kv_location", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class ice_paged_params(ctypes.Structure):
+    _fields_ = [("d", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("n_q_heads", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("max_requests", ctypes.c_int32),
+                ("max_blocks", ctypes.c_int32), ("max_tokens", ctypes.c_int32),
+                ("n_pages", ctypes.c_int64)]
 
 
 class IceError(RuntimeError):
@@ -114,6 +124,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ice_debug_set_flags.restype = ctypes.c_int
     lib.ice_set_cluster_size.argtypes = [vp, i32]
     lib.ice_set_cluster_size.restype = ctypes.c_int
+    lib.ice_paged_create.argtypes = [P(ice_paged_params), P(vp)]
+    lib.ice_paged_create.restype = ctypes.c_int
+    lib.ice_paged_destroy.argtypes = [vp]
+    lib.ice_paged_destroy.restype = None
+    lib.ice_paged_get_error.argtypes = [vp, vp]
+    lib.ice_paged_get_error.restype = ctypes.c_int
+    lib.ice_paged_tables.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp]
+    lib.ice_paged_tables.restype = ctypes.c_int
+    lib.ice_paged_append.argtypes = [vp, i32, vp, i64, vp, i64, vp, vp, vp, vp]
+    lib.ice_paged_append.restype = ctypes.c_int
+    lib.ice_paged_attn.argtypes = [vp, i32, i32, vp, i64, vp, vp, vp, vp, i32, vp, vp, vp, vp]
+    lib.ice_paged_attn.restype = ctypes.c_int
     return lib
 
 
@@ -387,6 +409,165 @@ class IceIndex:
         _check(_lib.ice_debug_page(self._h, unit, page_id, hk.data_ptr(), hv.data_ptr(),
                                    _stream(stream)), "ice_debug_page")
         return hk, hv
+
+
+class PagedCache:
+    """The plain paged cache of a batch whose requests share a prefix (an ice_paged
+    handle: geometry, scratch and status word; the pages and tables are the caller's
+    tensors). One step, for each layer the last two calls:
+
+        seq_len, state, q_start, slots, pos = pc.tables(seq_len, n_new, table, ring, state, n)
+        pc.append(k, v, slots, k_pages, v_pages)
+        out = pc.attn(q, q_start, seq_len, table, k_pages, v_pages, prefix_table, prefix_len)
+    """
+
+    def __init__(self, *, n_kv_heads: int, n_q_heads: int, page_size: int, n_pages: int,
+                 max_requests: int, max_blocks: int, max_tokens: int,
+                 dtype: torch.dtype = torch.bfloat16, d: int = 128):
+        self.params = ice_paged_params(d=d, n_kv_heads=n_kv_heads, n_q_heads=n_q_heads,
+                                       page_size=page_size, dtype=_code(dtype),
+                                       max_requests=max_requests, max_blocks=max_blocks,
+                                       max_tokens=max_tokens, n_pages=n_pages)
+        self.dtype = dtype
+        self._h = ctypes.c_void_p()
+        self.device = torch.device("cuda", torch.cuda.current_device())
+        _check(_lib.ice_paged_create(ctypes.byref(self.params), ctypes.byref(self._h)),
+               "ice_paged_create")
+        self._page_shape = (n_pages, n_kv_heads, page_size, d)
+
+    # -- tensors of the shapes that the calls take -----------------------------------
+    def new_pages(self):
+        """(k_pages, v_pages) of one layer, uninitialised."""
+        return (torch.empty(self._page_shape, dtype=self.dtype, device=self.device),
+                torch.empty(self._page_shape, dtype=self.dtype, device=self.device))
+
+    def new_tables(self, n_req: int):
+        """(seq_len, block_table, free_pages, free_state) of n_req empty requests and a pool
+        whose pages are all free."""
+        n_pages = self.params.n_pages
+        return (torch.zeros((n_req,), dtype=torch.int32, device=self.device),
+                torch.full((n_req, self.params.max_blocks), -1, dtype=torch.int32, device=self.device),
+                torch.arange(n_pages, dtype=torch.int32, device=self.device),
+                torch.tensor([0, n_pages], dtype=torch.int64, device=self.device))
+
+    # -- checks ------------------------------------------------------------------------
+    def _ints(self, t, dtype, shape, name):
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+        return _dev_ptr(t, dtype, name, host_ok=False)
+
+    def _rows(self, t, heads, name):
+        """Pointer and token stride of [tokens, heads, d] whose rows of heads are contiguous."""
+        d = self.params.d
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype != self.dtype:
+            raise ValueError(f"{name} must be {self.dtype}, got {t.dtype}")
+        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+            raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {tuple(t.shape)}")
+        stride, head, one = t.stride()
+        if one != 1 or (head != d and heads > 1):
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+        return t.data_ptr(), stride if t.shape[0] > 1 else heads * d
+
+    def _pages(self, k_pages, v_pages):
+        for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+            if t.shape != self._page_shape:
+                raise ValueError(f"{name} must be {self._page_shape}, got {tuple(t.shape)}")
+        return (_dev_ptr(k_pages, self.dtype, "k_pages", host_ok=False),
+                _dev_ptr(v_pages, self.dtype, "v_pages", host_ok=False))
+
+    # -- the three calls -----------------------------------------------------------------
+    def tables(self, seq_len: torch.Tensor, n_new: torch.Tensor, block_table: torch.Tensor,
+               free_pages: torch.Tensor, free_state: torch.Tensor, n_slots: int,
+               seq_len_out: torch.Tensor | None = None, free_state_out: torch.Tensor | None = None,
+               q_start: torch.Tensor | None = None, slot_map: torch.Tensor | None = None,
+               positions: torch.Tensor | None = None, stream=None):
+        """ice_paged_tables; returns (seq_len_out, free_state_out, q_start, slot_map, positions).
+
+        block_table and free_pages are updated in place; seq_len_out and free_state_out may
+        be seq_len and free_state. n_slots: room for new tokens (entries behind the last
+        are -1 in slot_map)."""
+        n, dev = seq_len.shape[0], seq_len.device
+        if seq_len_out is None:
+            seq_len_out = torch.empty_like(seq_len)
+        if free_state_out is None:
+            free_state_out = torch.empty_like(free_state)
+        if q_start is None:
+            q_start = torch.empty((n + 1,), dtype=torch.int32, device=dev)
+        if slot_map is None:
+            slot_map = torch.empty((n_slots,), dtype=torch.int64, device=dev)
+        if positions is None:
+            positions = torch.empty((n_slots,), dtype=torch.int32, device=dev)
+        i32, i64 = torch.int32, torch.int64
+        _check(_lib.ice_paged_tables(
+            self._h, n, self._ints(seq_len, i32, (n,), "seq_len"), self._ints(n_new, i32, (n,), "n_new"),
+            self._ints(block_table, i32, (n, self.params.max_blocks), "block_table"),
+            self._ints(free_pages, i32, (self.params.n_pages,), "free_pages"),
+            self._ints(free_state, i64, (2,), "free_state"),
+            self._ints(seq_len_out, i32, (n,), "seq_len_out"),
+            self._ints(free_state_out, i64, (2,), "free_state_out"),
+            self._ints(q_start, i32, (n + 1,), "q_start"),
+            self._ints(slot_map, i64, (n_slots,), "slot_map"),
+            self._ints(positions, i32, (n_slots,), "positions"), n_slots, _stream(stream)),
+            "ice_paged_tables")
+        return seq_len_out, free_state_out, q_start, slot_map, positions
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor,
+               k_pages: torch.Tensor, v_pages: torch.Tensor, stream=None):
+        """ice_paged_append of k, v [tokens, kv_heads, d] (a token stride is allowed)."""
+        n = slot_map.shape[0]
+        kp, ks = self._rows(k, self.params.n_kv_heads, "k")
+        vp, vs = self._rows(v, self.params.n_kv_heads, "v")
+        if k.shape[0] != n or v.shape[0] != n:
+            raise ValueError("k, v and slot_map must have as many tokens")
+        kg, vg = self._pages(k_pages, v_pages)
+        _check(_lib.ice_paged_append(self._h, n, kp, ks, vp, vs,
+                                     self._ints(slot_map, torch.int64, (n,), "slot_map"), kg, vg,
+                                     _stream(stream)), "ice_paged_append")
+
+    def attn(self, q: torch.Tensor, q_start: torch.Tensor, seq_len: torch.Tensor,
+             block_table: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+             prefix_table: torch.Tensor | None = None, prefix_len: int = 0,
+             out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """ice_paged_attn of q [tokens, q_heads, d] (a token stride is allowed); returns out,
+        contiguous."""
+        p, n = self.params, seq_len.shape[0]
+        qp, qs = self._rows(q, p.n_q_heads, "q")
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif out.shape != q.shape:
+            raise ValueError("out must be shaped like q")
+        kg, vg = self._pages(k_pages, v_pages)
+        pt = None
+        if prefix_len:
+            if prefix_table is None or prefix_table.numel() * p.page_size < prefix_len:
+                raise ValueError("prefix_table must hold the pages of prefix_len tokens")
+            pt = _dev_ptr(prefix_table, torch.int32, "prefix_table", host_ok=False)
+        _check(_lib.ice_paged_attn(
+            self._h, n, q.shape[0], qp, qs, self._ints(q_start, torch.int32, (n + 1,), "q_start"),
+            self._ints(seq_len, torch.int32, (n,), "seq_len"),
+            self._ints(block_table, torch.int32, (n, p.max_blocks), "block_table"), pt, int(prefix_len),
+            kg, vg, _dev_ptr(out, self.dtype, "out", host_ok=False), _stream(stream)), "ice_paged_attn")
+        return out
+
+    # -- status, teardown ------------------------------------------------------------------
+    def get_error(self, stream=None) -> int:
+        return int(_lib.ice_paged_get_error(self._h, _stream(stream)))
+
+    def check(self, stream=None):
+        _check(self.get_error(stream), "device status")
+
+    def destroy(self):
+        if self._h and self._h.value:
+            _lib.ice_paged_destroy(self._h)
+            self._h = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
 
 
 def key_codes_noalloc(keys: torch.Tensor, *, n_composite: int = 2, n_proj: int = 8, seed: int = 0,

@@ -1,0 +1,80 @@
+"""Argument checks of the paged cache's C entries that need no GPU, its ctypes mirror, and
+the plain statement of the tables that the GPU tests compare with."""
+import ctypes
+import os
+import shutil
+import subprocess
+
+import pytest
+
+from tests import paged_helpers as H
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from semantic_paged_kv_head_gb300 import build
+    build.build_lib()
+    from semantic_paged_kv_head_gb300 import ice
+    return ice
+
+
+def _params(lib, **over):
+    p = dict(d=128, n_kv_heads=8, n_q_heads=32, page_size=16, dtype=lib.ICE_BF16, max_requests=4, max_blocks=8,
+             max_tokens=16, n_pages=64)
+    p.update(over)
+    return lib.ice_paged_params(**p)
+
+
+@pytest.mark.parametrize("field,value,code", [
+    ("d", 64, "UNSUPPORTED"), ("n_kv_heads", 0, "INVALID_ARG"), ("n_q_heads", 30, "INVALID_ARG"),
+    ("n_q_heads", 4, "INVALID_ARG"), ("n_q_heads", 24, "UNSUPPORTED"), ("n_q_heads", 128, "UNSUPPORTED"),
+    ("page_size", 0, "INVALID_ARG"), ("page_size", 65, "INVALID_ARG"), ("dtype", 7, "INVALID_ARG"),
+    ("max_requests", 0, "INVALID_ARG"), ("max_requests", 8193, "INVALID_ARG"), ("max_blocks", 0, "INVALID_ARG"),
+    ("max_blocks", (1 << 26) + 1, "INVALID_ARG"), ("max_tokens", 0, "INVALID_ARG"),
+    ("max_tokens", (1 << 20) + 1, "INVALID_ARG"), ("n_pages", 0, "INVALID_ARG"), ("n_pages", 1 << 24, "UNSUPPORTED")])
+def test_refused_parameters(lib, field, value, code):
+    out = ctypes.c_void_p(1)
+    p = _params(lib, **{field: value})
+    assert lib.raw_library().ice_paged_create(ctypes.byref(p), ctypes.byref(out)) == getattr(lib, "ICE_ERR_" + code)
+    assert out.value is None
+
+
+def test_null_arguments(lib):
+    raw, E = lib.raw_library(), lib.ICE_ERR_INVALID_ARG
+    out = ctypes.c_void_p()
+    assert raw.ice_paged_create(None, ctypes.byref(out)) == E
+    assert raw.ice_paged_create(ctypes.byref(_params(lib)), None) == E
+    assert raw.ice_paged_get_error(None, None) == E
+    assert raw.ice_paged_tables(None, 1, 16, 16, 16, 16, 16, 16, 16, 16, 16, 16, 1, None) == E
+    assert raw.ice_paged_append(None, 1, 16, 1024, 16, 1024, 16, 16, 16, None) == E
+    assert raw.ice_paged_attn(None, 1, 1, 16, 4096, 16, 16, 16, None, 0, 16, 16, 16, None) == E
+    raw.ice_paged_destroy(None)  # a no-op
+
+
+def test_struct_layout_matches_the_header(lib, tmp_path):
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no host C compiler")
+    cls = lib.ice_paged_params
+    lines = ['#include <stdio.h>', '#include "ice.h"', "int main(void) {",
+             'printf("size %zu\\n", sizeof(ice_paged_params));']
+    lines += [f'printf("{f} %zu\\n", offsetof(ice_paged_params, {f}));' for f, _ in cls._fields_]
+    src, exe = tmp_path / "layout.c", tmp_path / "layout"
+    src.write_text("\n".join(lines + ["return 0; }"]) + "\n")
+    subprocess.run([cc, "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    got = dict(x.split() for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.splitlines())
+    assert int(got["size"]) == ctypes.sizeof(cls)
+    for f, _ in cls._fields_:
+        assert int(got[f]) == getattr(cls, f).offset, f
+
+
+def test_plain_tables_by_hand():
+    # P = 4, 6 pages, ring holding 5, 3, 1 from head 4; request 0 has page 2, request 1 pages 0 and 4
+    table = [[2, -1, -1], [0, 4, -1]]
+    code, lens, state, q0, slots, pos, table, ring = H.plain_tables(
+        [3, 6], [3, -4], table, [1, -1, -1, -1, 5, 3], [4, 7], 5, 4)
+    assert code == 0 and lens == [6, 2] and state == [5, 8] and q0 == [0, 3, 3]
+    assert slots == [11, 20, 21, -1, -1] and pos == [3, 4, 5, 0, 0]
+    assert table == [[2, 5, -1], [0, 4, -1]] and ring == [1, 4, -1, -1, 5, 3]
