@@ -1,5 +1,5 @@
-// Attention of a batch that shares a prefix: the kernel on the CUDA cores, the joining of
-// the parts, and the choice of the parts.
+// Attention of a batch that shares a prefix: the fp32 kernel on the CUDA cores, the joining
+// of the parts, and the choice of the parts.
 #include <algorithm>
 
 #include "ice_paged.cuh"
@@ -23,7 +23,6 @@ constexpr int kSimtStrideP = kSimtKeys + 4;
 constexpr int kSimtSmem = 4 * (kSimtRows * kSimtStrideK + kSimtKeys * kSimtStrideK + kSimtKeys * kD +
                                kSimtRows * kSimtStrideP);
 
-template <typename T>
 __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(PagedAttn a) {
     extern __shared__ __align__(16) float simt_smem[];
     __shared__ PlanShared sh;
@@ -48,7 +47,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(PagedAttn a) {
             const int r = x / (kD / 4), c = (x % (kD / 4)) * 4;
             float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             if (r < nrow)
-                load4((const T*)a.q + (it.tok0 + r / a.G) * a.q_stride + (it.h * a.G + r % a.G) * kD + c, v);
+                load4((const float*)a.q + (it.tok0 + r / a.G) * a.q_stride + (it.h * a.G + r % a.G) * kD + c, v);
             *reinterpret_cast<float4*>(sQ + r * kSimtStrideK + c) = make_float4(v[0], v[1], v[2], v[3]);
         }
         float m[4], l[4], o[4][8];
@@ -72,8 +71,8 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(PagedAttn a) {
                     const int page = it.table[key / a.P];
                     if (page >= 0 && page < a.n_pages) {
                         const long long row = ((long long)page * a.H + it.h) * a.P + key % a.P;
-                        load4((const T*)a.k_pages + row * kD + c, vk);
-                        load4((const T*)a.v_pages + row * kD + c, vv);
+                        load4((const float*)a.k_pages + row * kD + c, vk);
+                        load4((const float*)a.v_pages + row * kD + c, vv);
                     } else {
                         set_status(a.status, ICE_ERR_BOUNDS);
                     }
@@ -158,11 +157,11 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(PagedAttn a) {
             const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
             if (it.direct) {
                 if (tok >= valid_tok) continue;
-                T* dst = (T*)a.out + row * kD;
+                float* dst = (float*)a.out + row * kD;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    dst[kg * 4 + k] = from_f<T>(o[j][k] * inv);
-                    dst[64 + kg * 4 + k] = from_f<T>(o[j][4 + k] * inv);
+                    dst[kg * 4 + k] = o[j][k] * inv;
+                    dst[64 + kg * 4 + k] = o[j][4 + k] * inv;
                 }
             } else {
                 float* dst = a.part_o + (it.slot * rows_all + row) * kD;
@@ -230,14 +229,17 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttn a, i
 static int simt_bytes(int n_req) { return kSimtSmem + (n_req + 1) * 4; }
 
 cudaError_t paged_tables_prepare();
+cudaError_t paged_tc_prepare();
+int paged_tc_keys(int P);
+int paged_tc_tokens(int G);
+cudaError_t launch_paged_tc(const PagedAttn& a, int n_sm, cudaStream_t s);
 
 cudaError_t paged_prepare() {
     cudaError_t e = paged_tables_prepare();
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(paged_simt_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             simt_bytes(kPagedMaxRequests));
+    e = paged_tc_prepare();
     if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(paged_simt_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(paged_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 simt_bytes(kPagedMaxRequests));
 }
 
@@ -262,19 +264,18 @@ static int prefix_parts(long long n_base, int tiles, int limit, int n_sm) {
 cudaError_t launch_paged_attn(PagedAttn a, int dtype, long long rows_cap, int n_sm, cudaStream_t s) {
     const long long rows = (long long)a.n_tokens * a.H * a.G;
     const int slots = (int)std::min<long long>(rows_cap / rows, 1 << 20);  // >= 2
-    const int KT = kSimtKeys, TB = kSimtRows / a.G;
+    const bool tc = dtype == ICE_BF16;
+    const int KT = tc ? paged_tc_keys(a.P) : kSimtKeys, TB = tc ? paged_tc_tokens(a.G) : kSimtRows / a.G;
     const long long n_base = (long long)((a.n_tokens + TB - 1) / TB) * a.H;
     a.prefix_splits =
         a.prefix_len > 0 ? prefix_parts(n_base, (a.prefix_len + KT - 1) / KT, slots - 1, n_sm) : 0;
     a.max_splits = slots - a.prefix_splits;
     a.target_items = 2 * n_sm;
     cudaError_t e;
-    if (dtype == ICE_BF16)
-        e = launch_pdl(paged_simt_kernel<__nv_bfloat16>, dim3(n_sm), dim3(kSimtThreads),
-                       (size_t)simt_bytes(a.n_req), s, a);
+    if (tc)
+        e = launch_paged_tc(a, n_sm, s);
     else
-        e = launch_pdl(paged_simt_kernel<float>, dim3(n_sm), dim3(kSimtThreads), (size_t)simt_bytes(a.n_req),
-                       s, a);
+        e = launch_pdl(paged_simt_kernel, dim3(n_sm), dim3(kSimtThreads), (size_t)simt_bytes(a.n_req), s, a);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
     if (dtype == ICE_BF16)

@@ -1,0 +1,529 @@
+// Attention of a batch that shares a prefix, bf16, on the fifth-generation tensor cores.
+#include <algorithm>
+#include <climits>
+#include <mutex>
+
+#include <cuda.h>
+
+#include "ice_paged.cuh"
+#include "ice_select_common.cuh"
+
+namespace ice {
+
+// ---------------------------------------------------------------------------
+// One block per SM takes items in turn: one or two tiles of 128 rows (new tokens
+// x G heads) against a range of tiles of KT keys (KT = the whole pages in 128
+// keys). For each row tile and key tile
+//   S = Q K^T      tcgen05.mma 128 x 128 x 128, accumulator S in tensor memory
+//   P = 2^(S c - m) one thread a row: S read back, maximum, weights rounded to
+//                  bf16 and written over S
+//   O += P V       tcgen05.mma with A = P from tensor memory, V [key][d] as the
+//                  N-major operand, accumulator O in tensor memory
+// Warps 0-3 and 4-7 do the softmax of row tile 0 and 1, warp 8 issues the copies,
+// one thread of warp 9 the matrix products (10 and 11 fill their warpgroup). With two row tiles the tensor cores work
+// on one while the other's weights are made, and both use the key tile that was
+// read once. Tensor memory is full: S0 S1 O0 O1, 128 columns each.
+//
+// The maximum m that the weights refer to moves only when a row's true maximum
+// has grown by more than 8 (weights stay below 2^8, exact enough in bf16, whose
+// rounding is relative); only then O is read back and rescaled. The sum l is of
+// the rounded weights, the ones that meet V.
+//
+// Pages are read by the tensor memory accelerator, a box of P rows x 64 dimensions
+// (128-byte swizzle, the layout that the operand descriptors name), into a ring of
+// 32 KB stages. Key tiles end where pages do; rows of a stage behind the last key
+// are zeroed before they meet weights of zero, whatever the page's free slots hold.
+// ---------------------------------------------------------------------------
+constexpr int kFaThreads = 384;
+// registers a thread: 168 at launch, moved from the copy and product warps to the softmax warps.
+// 128 x 80 + 256 x 208 = 63488 of the launch's 384 x 168 = 64512.
+constexpr int kFaRegsIssue = 80, kFaRegsSoftmax = 208;
+static_assert(128 * kFaRegsIssue + 256 * kFaRegsSoftmax <= kFaThreads * 168, "the shares fit the launch's registers");
+constexpr int kFaRows = 128;              // rows of a tile (the MMA's M)
+constexpr int kFaKeys = 128;              // key rows of a stage (N of S, K of O)
+constexpr int kFaTileB = kFaRows * kD * 2;  // 32 KB: Q tile, K or V stage
+constexpr int kFaHalfB = kFaTileB / 2;    // 64 dimensions
+constexpr int kFaStages = 4;
+constexpr float kFaSlack = 8.0f;          // growth of the maximum (log2) that is let pass
+
+struct FaShared {
+    unsigned long long q_full, q_empty, kv_full[kFaStages], kv_empty[kFaStages];
+    unsigned long long s_full[2], p_ready[2], o_done[2], drain;
+    unsigned tmem;
+    int abort;
+    PlanShared plan;
+};
+
+__host__ __device__ constexpr int fa_smem(int n_req) {
+    return 1024 + (2 + kFaStages) * kFaTileB + (n_req + 1) * 4;  // with slack for the 1 KB alignment
+}
+
+// K-major operand (Q, K), 128-byte swizzle: rows of 128 B, 1024 B between groups of 8.
+__device__ __forceinline__ unsigned long long fa_desc_k(unsigned saddr) {
+    return (unsigned long long)((saddr & 0x3FFFFu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+// N-major operand (V): 64 dimensions are a row of 128 B, kFaHalfB between the two
+// halves (leading offset), 1024 B between groups of 8 keys (stride offset).
+__device__ __forceinline__ unsigned long long fa_desc_v(unsigned saddr) {
+    return (unsigned long long)((saddr & 0x3FFFFu) >> 4) | ((unsigned long long)(kFaHalfB >> 4) << 16) | (64ull << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+// fp32 accumulator, bf16 A and B, M = N = 128; bit 16: B is N-major.
+constexpr unsigned kFaIdescS = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+constexpr unsigned kFaIdescO = kFaIdescS | (1u << 16);
+
+__device__ __forceinline__ void fa_bar_init(unsigned long long* bar, int count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void fa_arrive(unsigned long long* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fa_expect(unsigned long long* bar, unsigned bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool fa_try(unsigned bar, unsigned parity) {
+    unsigned done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+// Waits for phase `parity`, at most kWaitNs; false if it ran out here or elsewhere in the block
+// (then every role leaves its loop).
+__device__ __forceinline__ bool fa_wait(unsigned long long* b, unsigned parity, volatile int* abort) {
+    const unsigned bar = smem_u32(b);
+    if (fa_try(bar, parity)) return true;
+    const unsigned long long t0 = global_ns();
+    for (;;) {
+        if (fa_try(bar, parity)) return true;
+        if (*abort) return false;
+        if (global_ns() - t0 > kWaitNs) {
+            *abort = 1;
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ void fa_commit(unsigned long long* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fa_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fa_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+
+// S = Q K^T of one row tile: 8 steps of 16 dimensions, 32 B along the swizzled rows.
+__device__ __forceinline__ void fa_mma_s(unsigned tmem, unsigned sq, unsigned sk) {
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+        const unsigned off = (unsigned)((ks >> 2) * kFaHalfB + (ks & 3) * 32);
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem),
+            "l"(fa_desc_k(sq + off)), "l"(fa_desc_k(sk + off)), "r"(kFaIdescS), "r"(ks > 0 ? 1u : 0u)
+            : "memory");
+    }
+}
+// O (+)= P V: 8 steps of 16 keys, 8 columns of packed weights, 2048 B of V rows.
+__device__ __forceinline__ void fa_mma_o(unsigned tmem_o, unsigned tmem_p, unsigned sv, bool add) {
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks)
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_o),
+            "r"(tmem_p + 8 * ks), "l"(fa_desc_v(sv + 2048 * ks)), "r"(kFaIdescO), "r"(add || ks > 0 ? 1u : 0u)
+            : "memory");
+}
+
+// N columns of the warp's 32 lanes of tensor memory, as register bits.
+__device__ __forceinline__ void fa_ld(unsigned addr, unsigned (&u)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+                 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15"
+                 "}, [%16];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+                   "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void fa_st(unsigned addr, const unsigned (&u)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {"
+                 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15"
+                 "};" ::"r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
+                 "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]),
+                 "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void fa_ld(unsigned addr, unsigned (&u)[32]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+                 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
+                 "}, [%32];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+                   "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+                   "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+                   "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void fa_st(unsigned addr, const unsigned (&u)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {"
+                 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
+                 "};" ::"r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
+                 "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]),
+                 "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]),
+                 "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31]),
+                 "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void fa_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fa_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ unsigned fa_pack(float lo, float hi) {
+    unsigned u;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(hi), "f"(lo));
+    return u;
+}
+
+__global__ void __launch_bounds__(kFaThreads, 1)
+    paged_tc_kernel(PagedAttn a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                    const __grid_constant__ CUtensorMap mv, int KT) {
+    extern __shared__ unsigned char fa_raw[];
+    __shared__ __align__(8) FaShared sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const unsigned raw0 = smem_u32(fa_raw);
+    const unsigned base = (raw0 + 1023u) & ~1023u;  // the swizzle's pattern repeats every 1024 B
+    unsigned char* mem = fa_raw + (base - raw0);
+    const unsigned s_q = base, s_kv = base + 2 * kFaTileB;
+    int* cum = reinterpret_cast<int*>(mem + (2 + kFaStages) * kFaTileB);
+    const int tpt = kFaRows / a.G, TB = 2 * tpt;  // tokens of a row tile, of an item
+    if (tid == 0) {
+        sh.abort = 0;
+        fa_bar_init(&sh.q_full, 1);
+        fa_bar_init(&sh.q_empty, 1);
+        for (int k = 0; k < kFaStages; ++k) {
+            fa_bar_init(&sh.kv_full[k], 1);
+            fa_bar_init(&sh.kv_empty[k], 1);
+        }
+        for (int k = 0; k < 2; ++k) {
+            fa_bar_init(&sh.s_full[k], 1);
+            fa_bar_init(&sh.p_ready[k], 4);
+            fa_bar_init(&sh.o_done[k], 1);
+        }
+        fa_bar_init(&sh.drain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // rows of a stage that no page reaches (P does not divide 128) stay zero
+    for (int x = tid; x < (kFaKeys - KT) * 8 * 2 * kFaStages; x += kFaThreads) {
+        const int c = x & 7, half = (x >> 3) % (2 * kFaStages), row = KT + (x >> 3) / (2 * kFaStages);
+        *reinterpret_cast<uint4*>(mem + 2 * kFaTileB + half * kFaHalfB + row * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    fa_before();
+    pdl_wait_then_release();
+    make_plan<kFaThreads>(a, KT, TB, cum, sh.plan);  // its barriers also publish the setup
+    fa_after();
+    const unsigned tmem = sh.tmem;
+    volatile int* abort = &sh.abort;
+    const long long rows_all = (long long)a.n_tokens * a.H * a.G;
+    PagedItem it;
+    // lengths out of range: reported by the plan, every role has nothing to do
+    const long long first = sh.plan.ok ? blockIdx.x : LLONG_MAX / 2;
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFaRegsIssue));
+        if (warp == 8) {
+            // ---- copies ----
+            unsigned pos = 0, items = 0;  // stages and query tiles issued
+            bool ok = true;
+            const int ppt = KT / a.P;
+            const int oob = (int)(a.n_pages * a.H * a.P);  // a row past the pool: reads as zeros
+            for (long long i = first; ok && get_item(a, KT, TB, cum, sh.plan, i, it); i += gridDim.x) {
+                const int n = it.kt1 - it.kt0;
+                if (n == 0) continue;
+                ok = fa_wait(&sh.q_empty, (items & 1) ^ 1, abort);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                if (lane == 0) {
+                    const int ns = it.ntok > tpt ? 2 : 1;
+                    fa_expect(&sh.q_full, ns * kFaTileB);
+                    for (int h = 0; h < 2 * ns; ++h)
+                        asm volatile(
+                            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                                s_q + h * kFaHalfB),
+                            "l"(reinterpret_cast<unsigned long long>(&mq)), "r"((h & 1) * 64), "r"(it.h * a.G),
+                            "r"(it.tok0 + (h >> 1) * tpt), "r"(smem_u32(&sh.q_full))
+                            : "memory");
+                }
+                ++items;
+                // K0, K1, V0, K2, V1, ...: the next scores' keys before these weights' values
+                for (int x = 0; x < 2 * n; ++x) {
+                    const bool is_k = x == 0 || ((x & 1) && x < 2 * n - 1);
+                    const int j = is_k ? (x + 1) >> 1 : x == 2 * n - 1 ? n - 1 : (x - 2) >> 1;
+                    const unsigned st = pos % kFaStages;
+                    ok = fa_wait(&sh.kv_empty[st], ((pos / kFaStages) & 1) ^ 1, abort);
+                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                    const int page0 = (it.kt0 + j) * ppt;
+                    const int np = min(ppt, ceil_div(it.kv_len, a.P) - page0);
+                    const unsigned bar = smem_u32(&sh.kv_full[st]), dst = s_kv + st * kFaTileB;
+                    if (lane == 0) fa_expect(&sh.kv_full[st], (unsigned)(np * a.P * kD * 2));
+                    __syncwarp();
+                    const unsigned long long map = reinterpret_cast<unsigned long long>(is_k ? &mk : &mv);
+                    for (int p = lane; p < np; p += 32) {
+                        const int id = it.table[page0 + p];
+                        int row = oob;
+                        if (id >= 0 && id < a.n_pages) row = (id * a.H + it.h) * a.P;
+                        else set_status(a.status, ICE_ERR_BOUNDS);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            asm volatile(
+                                "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                                    dst + h * kFaHalfB + p * a.P * 128),
+                                "l"(map), "r"(h * 64), "r"(row), "r"(bar)
+                                : "memory");
+                    }
+                    ++pos;
+                }
+            }
+            // copies in flight land (bounded) before the block ends, whatever ended the loop
+            if (lane == 0) {
+                if (!ok) set_status(a.status, ICE_ERR_TIMEOUT);
+                if (items) mbar_wait_bounded(smem_u32(&sh.q_full), (items - 1) & 1);
+                for (unsigned k = pos > kFaStages ? pos - kFaStages : 0; k < pos; ++k)
+                    mbar_wait_bounded(smem_u32(&sh.kv_full[k % kFaStages]), (k / kFaStages) & 1);
+            }
+        } else if (warp == 9 && lane == 0) {
+            // ---- matrix products (one thread) ----
+            unsigned pos = 0, items = 0, pn[2] = {0, 0};
+            bool ok = true;
+            for (long long i = first; ok && get_item(a, KT, TB, cum, sh.plan, i, it); i += gridDim.x) {
+                const int n = it.kt1 - it.kt0, ns = it.ntok > tpt ? 2 : 1;
+                if (n == 0) continue;
+                ok = fa_wait(&sh.q_full, items & 1, abort) && fa_wait(&sh.kv_full[pos % kFaStages], (pos / kFaStages) & 1, abort);
+                if (!ok) break;
+                ++items;
+                fa_after();
+                for (int s = 0; s < ns; ++s) {
+                    fa_mma_s(tmem + 128 * s, s_q + s * kFaTileB, s_kv + (pos % kFaStages) * kFaTileB);
+                    fa_commit(&sh.s_full[s]);
+                }
+                fa_commit(&sh.kv_empty[pos % kFaStages]);
+                if (n == 1) fa_commit(&sh.q_empty);
+                for (int j = 0; ok && j < n; ++j) {
+                    const bool more = j + 1 < n;
+                    const unsigned pk = pos + 2 * j + 1, pv = more ? pos + 2 * j + 2 : pos + 2 * n - 1;
+                    for (int s = 0; s < ns; ++s) {
+                        if (s == 0) ok = fa_wait(&sh.kv_full[pv % kFaStages], (pv / kFaStages) & 1, abort);
+                        ok = ok && fa_wait(&sh.p_ready[s], pn[s] & 1, abort);
+                        if (!ok) break;
+                        ++pn[s];
+                        fa_after();
+                        fa_mma_o(tmem + 256 + 128 * s, tmem + 128 * s, s_kv + (pv % kFaStages) * kFaTileB, j > 0);
+                        if (!more) fa_commit(&sh.o_done[s]);
+                        if (more) {
+                            if (s == 0) ok = fa_wait(&sh.kv_full[pk % kFaStages], (pk / kFaStages) & 1, abort);
+                            if (!ok) break;
+                            fa_mma_s(tmem + 128 * s, s_q + s * kFaTileB, s_kv + (pk % kFaStages) * kFaTileB);
+                            fa_commit(&sh.s_full[s]);
+                        }
+                    }
+                    if (!ok) break;
+                    if (more) fa_commit(&sh.kv_empty[pk % kFaStages]);
+                    fa_commit(&sh.kv_empty[pv % kFaStages]);
+                    if (j + 2 == n) fa_commit(&sh.q_empty);  // the last scores are issued
+                }
+                pos += 2 * n;
+            }
+            // products in flight end (bounded) before the tensor memory is given back
+            if (!ok) set_status(a.status, ICE_ERR_TIMEOUT);
+            if (items) {
+                fa_commit(&sh.drain);
+                mbar_wait_bounded(smem_u32(&sh.drain), 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---- softmax and output: thread = row of tile `s` ----
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFaRegsSoftmax));
+        const int s = warp >> 2, wq = warp & 3, row = 32 * wq + lane;
+        const unsigned t_s = tmem + 128 * s + ((unsigned)(32 * wq) << 16), t_o = t_s + 256;
+        const int valid_tok = a.q_start[a.n_req];
+        unsigned sn = 0, on = 0, pos = 0;
+        bool ok = true;
+        for (long long i = first; ok && get_item(a, KT, TB, cum, sh.plan, i, it); i += gridDim.x) {
+            const int n = it.kt1 - it.kt0;
+            const int nrow = (it.ntok - s * tpt) * a.G;  // rows of this tile, <= 0: tile not there
+            pos += 2 * n;
+            if (nrow <= 0) continue;
+            const bool busy = 32 * wq < nrow;  // a warp without rows only keeps the barriers going
+            const int tok = it.tok0 + s * tpt + row / a.G;
+            const int lim = min(it.kv_len, tok + it.lim_off);
+            float m = -INFINITY, l = 0.0f;
+            for (int j = 0; j < n; ++j) {
+                ok = __all_sync(0xffffffffu, fa_wait(&sh.s_full[s], sn & 1, abort));
+                if (!ok) break;
+                ++sn;
+                const int key0 = (it.kt0 + j) * KT;
+                if (busy) {
+                    fa_after();
+                    unsigned v[4][32];  // scores, as bits
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) fa_ld(t_s + 32 * k, v[k]);
+                    fa_wait_ld();
+                    const int c_lim = min(lim - key0, KT);
+                    if (__any_sync(0xffffffffu, c_lim < kFaKeys)) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (32 * k + c >= c_lim) v[k][c] = 0xFF800000u;  // -inf
+                    }
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) mx = fmaxf(mx, __uint_as_float(v[k][c]));
+                    mx *= a.scale_log2;
+                    const bool grow = mx > m + kFaSlack;  // also the first finite one
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float f = grow ? exp2_approx(m - mx) : 1.0f;
+                        if (grow) m = mx;
+                        l *= f;
+                        if (j > 0) {  // O of the tiles before is complete: its products precede S in the pipe
+#pragma unroll 1
+                            for (int k = 0; k < kD; k += 16) {
+                                unsigned u[16];
+                                fa_ld(t_o + k, u);
+                                fa_wait_ld();
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * f);
+                                fa_st(t_o + k, u);
+                            }
+                        }
+                    }
+                    const float nm = m == -INFINITY ? 0.0f : -m;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        unsigned u[16];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            const float p0 = exp2_approx(fmaf(__uint_as_float(v[k][2 * c]), a.scale_log2, nm));
+                            const float p1 = exp2_approx(fmaf(__uint_as_float(v[k][2 * c + 1]), a.scale_log2, nm));
+                            u[c] = fa_pack(p0, p1);
+                            l += __uint_as_float(u[c] << 16) + __uint_as_float(u[c] & 0xFFFF0000u);
+                        }
+                        fa_st(t_s + 16 * k, u);
+                    }
+                    fa_wait_st();
+                    fa_before();
+                }
+                if (key0 + KT > it.kv_len) {  // the last tile of the list: rows behind the last key
+                    const unsigned pv = pos - 1, st = pv % kFaStages;
+                    ok = __all_sync(0xffffffffu, fa_wait(&sh.kv_full[st], (pv / kFaStages) & 1, abort));
+                    if (!ok) break;
+                    const int r0 = it.kv_len - key0;
+                    unsigned char* v_st = mem + 2 * kFaTileB + st * kFaTileB;
+                    for (int x = row; x < (KT - r0) * 16; x += kFaRows)
+                        *reinterpret_cast<uint4*>(v_st + ((x >> 3) & 1) * kFaHalfB + (r0 + (x >> 4)) * 128 + (x & 7) * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                __syncwarp();
+                if (lane == 0) fa_arrive(&sh.p_ready[s]);
+            }
+            if (!ok) break;
+            if (n > 0) {
+                ok = __all_sync(0xffffffffu, fa_wait(&sh.o_done[s], on & 1, abort));
+                if (!ok) break;
+                ++on;
+            }
+            if (!busy) continue;
+            fa_after();
+            const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+            const long long r = (long long)tok * a.H * a.G + it.h * a.G + row % a.G;
+            const bool mine = row < nrow;
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                unsigned u[32];
+                float o[32];
+                if (n > 0) {
+                    fa_ld(t_o + 32 * k, u);
+                    fa_wait_ld();
+                }
+#pragma unroll
+                for (int c = 0; c < 32; ++c)  // O was not written where n = 0
+                    o[c] = n > 0 && l != 0.0f ? __uint_as_float(u[c]) * inv : 0.0f;
+                if (mine && it.direct) {
+                    if (tok < valid_tok) {
+                        uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + r * kD + 32 * k);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            dst[c] = make_uint4(fa_pack(o[8 * c], o[8 * c + 1]), fa_pack(o[8 * c + 2], o[8 * c + 3]),
+                                                fa_pack(o[8 * c + 4], o[8 * c + 5]), fa_pack(o[8 * c + 6], o[8 * c + 7]));
+                    }
+                } else if (mine) {
+                    float4* dst = reinterpret_cast<float4*>(a.part_o + (it.slot * rows_all + r) * kD + 32 * k);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) dst[c] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                }
+            }
+            if (mine && !it.direct) a.part_ml[it.slot * rows_all + r] = make_float2(m, l);
+            fa_before();
+        }
+    }
+    fa_before();
+    __syncthreads();
+    fa_after();
+    if (warp == 9)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+typedef CUresult (*FaEncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static FaEncodeFn fa_encoder() {
+    static FaEncodeFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<FaEncodeFn>(p);
+        cudaGetLastError();
+    });
+    return fn;
+}
+
+static bool fa_map(CUtensorMap* m, const void* p, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                   const cuuint32_t* box) {
+    const cuuint32_t estr[3] = {1, 1, 1};
+    FaEncodeFn enc = fa_encoder();
+    return enc != nullptr &&
+           enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(p), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int paged_tc_keys(int P) { return kFaKeys / P * P; }
+int paged_tc_tokens(int G) { return 2 * kFaRows / G; }
+
+cudaError_t launch_paged_tc(const PagedAttn& a, int n_sm, cudaStream_t s) {
+    CUtensorMap mq, mk, mv;
+    const cuuint64_t qd[3] = {kD, (cuuint64_t)(a.H * a.G), (cuuint64_t)a.n_tokens};
+    const cuuint64_t qs[2] = {kD * 2, (cuuint64_t)a.q_stride * 2};
+    const cuuint32_t qb[3] = {64, (cuuint32_t)a.G, (cuuint32_t)(kFaRows / a.G)};
+    const cuuint64_t kd[2] = {kD, (cuuint64_t)(a.n_pages * a.H * a.P)};
+    const cuuint64_t ks[1] = {kD * 2};
+    const cuuint32_t kb[2] = {64, (cuuint32_t)a.P};
+    if (!fa_map(&mq, a.q, 3, qd, qs, qb) || !fa_map(&mk, a.k_pages, 2, kd, ks, kb) || !fa_map(&mv, a.v_pages, 2, kd, ks, kb))
+        return cudaErrorNotSupported;
+    return launch_pdl(paged_tc_kernel, dim3(n_sm), dim3(kFaThreads), (size_t)fa_smem(a.n_req), s, a, mq, mk, mv,
+                      paged_tc_keys(a.P));
+}
+
+cudaError_t paged_tc_prepare() {
+    return cudaFuncSetAttribute(paged_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, fa_smem(kPagedMaxRequests));
+}
+
+}  // namespace ice
