@@ -19,8 +19,8 @@ namespace ice {
 //                  bf16 and written over S
 //   O += P V       tcgen05.mma with A = P from tensor memory, V [key][d] as the
 //                  N-major operand, accumulator O in tensor memory
-// Warps 0-3 and 4-7 do the softmax of row tile 0 and 1, warp 8 issues the copies,
-// one thread of warp 9 the matrix products (10 and 11 fill their warpgroup). With two row tiles the tensor cores work
+// Warps 0-3 and 4-7 do the softmax of row tile 0 and 1, warps 8 and 10 issue the
+// copies, one thread of warp 9 the matrix products (11 fills the warpgroup). With two row tiles the tensor cores work
 // on one while the other's weights are made, and both use the key tile that was
 // read once. Tensor memory is full: S0 S1 O0 O1, 128 columns each.
 //
@@ -43,12 +43,13 @@ constexpr int kFaRows = 128;              // rows of a tile (the MMA's M)
 constexpr int kFaKeys = 128;              // key rows of a stage (N of S, K of O)
 constexpr int kFaTileB = kFaRows * kD * 2;  // 32 KB: Q tile, K or V stage
 constexpr int kFaHalfB = kFaTileB / 2;    // 64 dimensions
-constexpr int kFaStages = 4;
+constexpr int kFaStagesK = 2, kFaStagesV = 2;
+constexpr int kFaStages = kFaStagesK + kFaStagesV;
 constexpr float kFaSlack = 8.0f;          // growth of the maximum (log2) that is let pass
 
 struct FaShared {
-    unsigned long long q_full, q_empty, kv_full[kFaStages], kv_empty[kFaStages];
-    unsigned long long s_full[2], p_ready[2], o_done[2], drain;
+    unsigned long long q_full, q_empty, k_full[kFaStagesK], k_empty[kFaStagesK], v_full[kFaStagesV], v_empty[kFaStagesV];
+    unsigned long long s_full[2], p_ready[2][2], o_done[2], drain;  // p_ready: halves of a tile's weights
     unsigned tmem;
     int abort;
     PlanShared plan;
@@ -91,15 +92,18 @@ __device__ __forceinline__ bool fa_try(unsigned bar, unsigned parity) {
     return done != 0;
 }
 // Waits for phase `parity`, at most kWaitNs; false if it ran out here or elsewhere in the block
-// (then every role leaves its loop).
+// (then every role leaves its loop). The wall clock is slow to read (a handover between
+// warps would wait for it), so it is read every 64th try only.
 __device__ __forceinline__ bool fa_wait(unsigned long long* b, unsigned parity, volatile int* abort) {
     const unsigned bar = smem_u32(b);
-    if (fa_try(bar, parity)) return true;
-    const unsigned long long t0 = global_ns();
-    for (;;) {
+    unsigned long long t0 = 0;
+    for (unsigned k = 1;; ++k) {
         if (fa_try(bar, parity)) return true;
+        if (k % 64) continue;
         if (*abort) return false;
-        if (global_ns() - t0 > kWaitNs) {
+        const unsigned long long t = global_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > kWaitNs) {
             *abort = 1;
             return false;
         }
@@ -110,6 +114,16 @@ __device__ __forceinline__ void fa_commit(unsigned long long* bar) {
 }
 __device__ __forceinline__ void fa_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fa_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+
+// True in one thread of the (converged) warp. The compiler knows that at most one thread
+// passes it, so the product instructions, whose operands are warp-wide registers, need no
+// loop over the active threads (with lane == 0 instead, a product took 105 cycles to issue).
+__device__ __forceinline__ bool fa_elect() {
+    unsigned one;
+    asm volatile(
+        "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+    return one != 0;
+}
 
 // S = Q K^T of one row tile: 8 steps of 16 dimensions, 32 B along the swizzled rows.
 __device__ __forceinline__ void fa_mma_s(unsigned tmem, unsigned sq, unsigned sk) {
@@ -123,15 +137,18 @@ __device__ __forceinline__ void fa_mma_s(unsigned tmem, unsigned sq, unsigned sk
             : "memory");
     }
 }
-// O (+)= P V: 8 steps of 16 keys, 8 columns of packed weights, 2048 B of V rows.
-__device__ __forceinline__ void fa_mma_o(unsigned tmem_o, unsigned tmem_p, unsigned sv, bool add) {
+// O (+)= P V over one half of a key tile: 4 steps of 16 keys, each 8 columns of packed weights
+// and 2048 B of V rows.
+__device__ __forceinline__ void fa_mma_o(unsigned tmem_o, unsigned tmem_p, unsigned sv, int half, bool add) {
 #pragma unroll
-    for (int ks = 0; ks < 8; ++ks)
+    for (int k = 0; k < 4; ++k) {
+        const int ks = 4 * half + k;
         asm volatile(
             "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
             " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_o),
-            "r"(tmem_p + 8 * ks), "l"(fa_desc_v(sv + 2048 * ks)), "r"(kFaIdescO), "r"(add || ks > 0 ? 1u : 0u)
+            "r"(tmem_p + 8 * ks), "l"(fa_desc_v(sv + 2048 * ks)), "r"(kFaIdescO), "r"(add || k > 0 ? 1u : 0u)
             : "memory");
+    }
 }
 
 // N columns of the warp's 32 lanes of tensor memory, as register bits.
@@ -182,6 +199,47 @@ __device__ __forceinline__ unsigned fa_pack(float lo, float hi) {
     return u;
 }
 
+__device__ __forceinline__ float fa_max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fa_fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+        " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 fa_add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+        " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// The pages of a key tile as rows of the pool's tensor map, page p in lane p % 32.
+struct FaPages {
+    int n, row[4];
+    __device__ __forceinline__ void fetch(const PagedAttn& a, const PagedItem& it, int page0, int ppt, int lane) {
+        n = min(ppt, ceil_div(it.kv_len, a.P) - page0);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int p = lane + 32 * u;
+            row[u] = (int)(a.n_pages * a.H * a.P);  // past the pool: reads as zeros
+            if (p < n) {
+                const int id = it.table[page0 + p];
+                if (id >= 0 && id < a.n_pages) row[u] = (id * a.H + it.h) * a.P;
+                else set_status(a.status, ICE_ERR_BOUNDS);
+            }
+        }
+    }
+};
+
 __global__ void __launch_bounds__(kFaThreads, 1)
     paged_tc_kernel(PagedAttn a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                     const __grid_constant__ CUtensorMap mv, int KT) {
@@ -191,20 +249,24 @@ __global__ void __launch_bounds__(kFaThreads, 1)
     const unsigned raw0 = smem_u32(fa_raw);
     const unsigned base = (raw0 + 1023u) & ~1023u;  // the swizzle's pattern repeats every 1024 B
     unsigned char* mem = fa_raw + (base - raw0);
-    const unsigned s_q = base, s_kv = base + 2 * kFaTileB;
+    const unsigned s_q = base, s_k = base + 2 * kFaTileB, s_v = s_k + kFaStagesK * kFaTileB;
     int* cum = reinterpret_cast<int*>(mem + (2 + kFaStages) * kFaTileB);
     const int tpt = kFaRows / a.G, TB = 2 * tpt;  // tokens of a row tile, of an item
     if (tid == 0) {
         sh.abort = 0;
         fa_bar_init(&sh.q_full, 1);
         fa_bar_init(&sh.q_empty, 1);
-        for (int k = 0; k < kFaStages; ++k) {
-            fa_bar_init(&sh.kv_full[k], 1);
-            fa_bar_init(&sh.kv_empty[k], 1);
+        for (int k = 0; k < kFaStagesK; ++k) {
+            fa_bar_init(&sh.k_full[k], 1);
+            fa_bar_init(&sh.k_empty[k], 1);
+        }
+        for (int k = 0; k < kFaStagesV; ++k) {
+            fa_bar_init(&sh.v_full[k], 1);
+            fa_bar_init(&sh.v_empty[k], 1);
         }
         for (int k = 0; k < 2; ++k) {
             fa_bar_init(&sh.s_full[k], 1);
-            fa_bar_init(&sh.p_ready[k], 4);
+            for (int h = 0; h < 2; ++h) fa_bar_init(&sh.p_ready[k][h], 4);
             fa_bar_init(&sh.o_done[k], 1);
         }
         fa_bar_init(&sh.drain, 1);
@@ -232,106 +294,120 @@ __global__ void __launch_bounds__(kFaThreads, 1)
     const long long first = sh.plan.ok ? blockIdx.x : LLONG_MAX / 2;
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFaRegsIssue));
-        if (warp == 8) {
-            // ---- copies ----
-            unsigned pos = 0, items = 0;  // stages and query tiles issued
+        if (warp == 8 || warp == 10) {
+            // ---- copies: warp 8 queries and keys, warp 10 values ----
+            const bool is_k = warp == 8;
+            const int stages = is_k ? kFaStagesK : kFaStagesV;
+            unsigned long long* full = is_k ? sh.k_full : sh.v_full;
+            unsigned long long* empty = is_k ? sh.k_empty : sh.v_empty;
+            const unsigned dst0 = is_k ? s_k : s_v;
+            const unsigned long long map = reinterpret_cast<unsigned long long>(is_k ? &mk : &mv);
+            unsigned cnt = 0, items = 0;  // tiles and query tiles issued
             bool ok = true;
             const int ppt = KT / a.P;
-            const int oob = (int)(a.n_pages * a.H * a.P);  // a row past the pool: reads as zeros
             for (long long i = first; ok && get_item(a, KT, TB, cum, sh.plan, i, it); i += gridDim.x) {
                 const int n = it.kt1 - it.kt0;
                 if (n == 0) continue;
-                ok = fa_wait(&sh.q_empty, (items & 1) ^ 1, abort);
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                if (lane == 0) {
-                    const int ns = it.ntok > tpt ? 2 : 1;
-                    fa_expect(&sh.q_full, ns * kFaTileB);
-                    for (int h = 0; h < 2 * ns; ++h)
-                        asm volatile(
-                            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-                                s_q + h * kFaHalfB),
-                            "l"(reinterpret_cast<unsigned long long>(&mq)), "r"((h & 1) * 64), "r"(it.h * a.G),
-                            "r"(it.tok0 + (h >> 1) * tpt), "r"(smem_u32(&sh.q_full))
-                            : "memory");
-                }
-                ++items;
-                // K0, K1, V0, K2, V1, ...: the next scores' keys before these weights' values
-                for (int x = 0; x < 2 * n; ++x) {
-                    const bool is_k = x == 0 || ((x & 1) && x < 2 * n - 1);
-                    const int j = is_k ? (x + 1) >> 1 : x == 2 * n - 1 ? n - 1 : (x - 2) >> 1;
-                    const unsigned st = pos % kFaStages;
-                    ok = fa_wait(&sh.kv_empty[st], ((pos / kFaStages) & 1) ^ 1, abort);
-                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                    const int page0 = (it.kt0 + j) * ppt;
-                    const int np = min(ppt, ceil_div(it.kv_len, a.P) - page0);
-                    const unsigned bar = smem_u32(&sh.kv_full[st]), dst = s_kv + st * kFaTileB;
-                    if (lane == 0) fa_expect(&sh.kv_full[st], (unsigned)(np * a.P * kD * 2));
+                FaPages next;  // of the next tile, fetched a tile ahead
+                next.fetch(a, it, it.kt0 * ppt, ppt, lane);
+                if (is_k) {
+                    ok = __all_sync(0xffffffffu, fa_wait(&sh.q_empty, (items & 1) ^ 1, abort));
+                    if (!ok) break;
+                    if (fa_elect()) {
+                        const int ns = it.ntok > tpt ? 2 : 1;
+                        fa_expect(&sh.q_full, ns * kFaTileB);
+                        for (int h = 0; h < 2 * ns; ++h)
+                            asm volatile(
+                                "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                                    s_q + h * kFaHalfB),
+                                "l"(reinterpret_cast<unsigned long long>(&mq)), "r"((h & 1) * 64), "r"(it.h * a.G),
+                                "r"(it.tok0 + (h >> 1) * tpt), "r"(smem_u32(&sh.q_full))
+                                : "memory");
+                    }
                     __syncwarp();
-                    const unsigned long long map = reinterpret_cast<unsigned long long>(is_k ? &mk : &mv);
-                    for (int p = lane; p < np; p += 32) {
-                        const int id = it.table[page0 + p];
-                        int row = oob;
-                        if (id >= 0 && id < a.n_pages) row = (id * a.H + it.h) * a.P;
-                        else set_status(a.status, ICE_ERR_BOUNDS);
+                    ++items;
+                }
+                for (int j = 0; j < n; ++j) {
+                    const FaPages cur = next;
+                    if (j + 1 < n) next.fetch(a, it, (it.kt0 + j + 1) * ppt, ppt, lane);
+                    const unsigned st = cnt % stages;
+                    ok = __all_sync(0xffffffffu, fa_wait(&empty[st], ((cnt / stages) & 1) ^ 1, abort));
+                    if (!ok) break;
+                    const unsigned bar = smem_u32(&full[st]), dst = dst0 + st * kFaTileB;
+                    if (lane == 0) fa_expect(&full[st], (unsigned)(cur.n * a.P * kD * 2));
+                    __syncwarp();
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int p = lane + 32 * u;
+                        if (p >= cur.n) break;
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
                             asm volatile(
                                 "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
                                     dst + h * kFaHalfB + p * a.P * 128),
-                                "l"(map), "r"(h * 64), "r"(row), "r"(bar)
+                                "l"(map), "r"(h * 64), "r"(cur.row[u]), "r"(bar)
                                 : "memory");
                     }
-                    ++pos;
+                    __syncwarp();
+                    ++cnt;
                 }
             }
             // copies in flight land (bounded) before the block ends, whatever ended the loop
             if (lane == 0) {
                 if (!ok) set_status(a.status, ICE_ERR_TIMEOUT);
                 if (items) mbar_wait_bounded(smem_u32(&sh.q_full), (items - 1) & 1);
-                for (unsigned k = pos > kFaStages ? pos - kFaStages : 0; k < pos; ++k)
-                    mbar_wait_bounded(smem_u32(&sh.kv_full[k % kFaStages]), (k / kFaStages) & 1);
+                for (unsigned k = cnt > (unsigned)stages ? cnt - stages : 0; k < cnt; ++k)
+                    mbar_wait_bounded(smem_u32(&full[k % stages]), (k / stages) & 1);
             }
-        } else if (warp == 9 && lane == 0) {
+        } else if (warp == 9 && fa_elect()) {
             // ---- matrix products (one thread) ----
-            unsigned pos = 0, items = 0, pn[2] = {0, 0};
+            unsigned kn = 0, vn = 0, items = 0, pn[2] = {0, 0};
             bool ok = true;
             for (long long i = first; ok && get_item(a, KT, TB, cum, sh.plan, i, it); i += gridDim.x) {
                 const int n = it.kt1 - it.kt0, ns = it.ntok > tpt ? 2 : 1;
                 if (n == 0) continue;
-                ok = fa_wait(&sh.q_full, items & 1, abort) && fa_wait(&sh.kv_full[pos % kFaStages], (pos / kFaStages) & 1, abort);
+                ok = fa_wait(&sh.q_full, items & 1, abort) && fa_wait(&sh.k_full[kn % kFaStagesK], (kn / kFaStagesK) & 1, abort);
                 if (!ok) break;
                 ++items;
                 fa_after();
                 for (int s = 0; s < ns; ++s) {
-                    fa_mma_s(tmem + 128 * s, s_q + s * kFaTileB, s_kv + (pos % kFaStages) * kFaTileB);
+                    fa_mma_s(tmem + 128 * s, s_q + s * kFaTileB, s_k + (kn % kFaStagesK) * kFaTileB);
                     fa_commit(&sh.s_full[s]);
                 }
-                fa_commit(&sh.kv_empty[pos % kFaStages]);
+                fa_commit(&sh.k_empty[kn % kFaStagesK]);
+                ++kn;
                 if (n == 1) fa_commit(&sh.q_empty);
-                for (int j = 0; ok && j < n; ++j) {
+                for (int j = 0; ok && j < n; ++j, ++vn) {
                     const bool more = j + 1 < n;
-                    const unsigned pk = pos + 2 * j + 1, pv = more ? pos + 2 * j + 2 : pos + 2 * n - 1;
+                    const unsigned ks = kn % kFaStagesK, vs = vn % kFaStagesV;
                     for (int s = 0; s < ns; ++s) {
-                        if (s == 0) ok = fa_wait(&sh.kv_full[pv % kFaStages], (pv / kFaStages) & 1, abort);
-                        ok = ok && fa_wait(&sh.p_ready[s], pn[s] & 1, abort);
+                        if (s == 0) ok = fa_wait(&sh.v_full[vs], (vn / kFaStagesV) & 1, abort);
+                        // the weights come in two halves: the first one's products run while
+                        // the second is made
+                        for (int half = 0; ok && half < 2; ++half) {
+                            ok = fa_wait(&sh.p_ready[s][half], pn[s] & 1, abort);
+                            if (!ok) break;
+                            fa_after();
+                            fa_mma_o(tmem + 256 + 128 * s, tmem + 128 * s, s_v + vs * kFaTileB, half, j > 0 || half > 0);
+                        }
                         if (!ok) break;
                         ++pn[s];
-                        fa_after();
-                        fa_mma_o(tmem + 256 + 128 * s, tmem + 128 * s, s_kv + (pv % kFaStages) * kFaTileB, j > 0);
                         if (!more) fa_commit(&sh.o_done[s]);
                         if (more) {
-                            if (s == 0) ok = fa_wait(&sh.kv_full[pk % kFaStages], (pk / kFaStages) & 1, abort);
+                            if (s == 0) ok = fa_wait(&sh.k_full[ks], (kn / kFaStagesK) & 1, abort);
                             if (!ok) break;
-                            fa_mma_s(tmem + 128 * s, s_q + s * kFaTileB, s_kv + (pk % kFaStages) * kFaTileB);
+                            fa_mma_s(tmem + 128 * s, s_q + s * kFaTileB, s_k + ks * kFaTileB);
                             fa_commit(&sh.s_full[s]);
                         }
                     }
                     if (!ok) break;
-                    if (more) fa_commit(&sh.kv_empty[pk % kFaStages]);
-                    fa_commit(&sh.kv_empty[pv % kFaStages]);
+                    fa_commit(&sh.v_empty[vs]);
+                    if (more) {
+                        fa_commit(&sh.k_empty[ks]);
+                        ++kn;
+                    }
                     if (j + 2 == n) fa_commit(&sh.q_empty);  // the last scores are issued
                 }
-                pos += 2 * n;
             }
             // products in flight end (bounded) before the tensor memory is given back
             if (!ok) set_status(a.status, ICE_ERR_TIMEOUT);
@@ -347,12 +423,12 @@ __global__ void __launch_bounds__(kFaThreads, 1)
         const int s = warp >> 2, wq = warp & 3, row = 32 * wq + lane;
         const unsigned t_s = tmem + 128 * s + ((unsigned)(32 * wq) << 16), t_o = t_s + 256;
         const int valid_tok = a.q_start[a.n_req];
-        unsigned sn = 0, on = 0, pos = 0;
+        unsigned sn = 0, on = 0, vn = 0;
         bool ok = true;
         for (long long i = first; ok && get_item(a, KT, TB, cum, sh.plan, i, it); i += gridDim.x) {
             const int n = it.kt1 - it.kt0;
             const int nrow = (it.ntok - s * tpt) * a.G;  // rows of this tile, <= 0: tile not there
-            pos += 2 * n;
+            vn += n;
             if (nrow <= 0) continue;
             const bool busy = 32 * wq < nrow;  // a warp without rows only keeps the barriers going
             const int tok = it.tok0 + s * tpt + row / a.G;
@@ -363,72 +439,82 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 if (!ok) break;
                 ++sn;
                 const int key0 = (it.kt0 + j) * KT;
-                if (busy) {
-                    fa_after();
-                    unsigned v[4][32];  // scores, as bits
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) fa_ld(t_s + 32 * k, v[k]);
-                    fa_wait_ld();
-                    const int c_lim = min(lim - key0, KT);
-                    if (__any_sync(0xffffffffu, c_lim < kFaKeys)) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-#pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                if (32 * k + c >= c_lim) v[k][c] = 0xFF800000u;  // -inf
-                    }
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) mx = fmaxf(mx, __uint_as_float(v[k][c]));
-                    mx *= a.scale_log2;
-                    const bool grow = mx > m + kFaSlack;  // also the first finite one
-                    if (__any_sync(0xffffffffu, grow)) {
-                        const float f = grow ? exp2_approx(m - mx) : 1.0f;
-                        if (grow) m = mx;
-                        l *= f;
-                        if (j > 0) {  // O of the tiles before is complete: its products precede S in the pipe
-#pragma unroll 1
-                            for (int k = 0; k < kD; k += 16) {
-                                unsigned u[16];
-                                fa_ld(t_o + k, u);
-                                fa_wait_ld();
-#pragma unroll
-                                for (int c = 0; c < 16; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * f);
-                                fa_st(t_o + k, u);
-                            }
-                        }
-                    }
-                    const float nm = m == -INFINITY ? 0.0f : -m;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        unsigned u[16];
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            const float p0 = exp2_approx(fmaf(__uint_as_float(v[k][2 * c]), a.scale_log2, nm));
-                            const float p1 = exp2_approx(fmaf(__uint_as_float(v[k][2 * c + 1]), a.scale_log2, nm));
-                            u[c] = fa_pack(p0, p1);
-                            l += __uint_as_float(u[c] << 16) + __uint_as_float(u[c] & 0xFFFF0000u);
-                        }
-                        fa_st(t_s + 16 * k, u);
-                    }
-                    fa_wait_st();
-                    fa_before();
-                }
                 if (key0 + KT > it.kv_len) {  // the last tile of the list: rows behind the last key
-                    const unsigned pv = pos - 1, st = pv % kFaStages;
-                    ok = __all_sync(0xffffffffu, fa_wait(&sh.kv_full[st], (pv / kFaStages) & 1, abort));
+                    const unsigned st = (vn - 1) % kFaStagesV;
+                    ok = __all_sync(0xffffffffu, fa_wait(&sh.v_full[st], ((vn - 1) / kFaStagesV) & 1, abort));
                     if (!ok) break;
                     const int r0 = it.kv_len - key0;
-                    unsigned char* v_st = mem + 2 * kFaTileB + st * kFaTileB;
+                    unsigned char* v_st = mem + (2 + kFaStagesK + st) * kFaTileB;
                     for (int x = row; x < (KT - r0) * 16; x += kFaRows)
                         *reinterpret_cast<uint4*>(v_st + ((x >> 3) & 1) * kFaHalfB + (r0 + (x >> 4)) * 128 + (x & 7) * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                __syncwarp();
-                if (lane == 0) fa_arrive(&sh.p_ready[s]);
+                if (!busy) {
+                    __syncwarp();
+                    if (lane == 0) fa_arrive(&sh.p_ready[s][0]), fa_arrive(&sh.p_ready[s][1]);
+                    continue;
+                }
+                fa_after();
+                unsigned v[4][32];  // scores, as bits
+#pragma unroll
+                for (int k = 0; k < 4; ++k) fa_ld(t_s + 32 * k, v[k]);
+                fa_wait_ld();
+                const int c_lim = min(lim - key0, KT);
+                if (__any_sync(0xffffffffu, c_lim < kFaKeys)) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (32 * k + c >= c_lim) v[k][c] = 0xFF800000u;  // -inf
+                }
+                float mx[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    mx[k] = fmaxf(__uint_as_float(v[k][0]), __uint_as_float(v[k][1]));
+#pragma unroll
+                    for (int c = 2; c < 32; c += 2)
+                        mx[k] = fa_max3(mx[k], __uint_as_float(v[k][c]), __uint_as_float(v[k][c + 1]));
+                }
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+                const bool grow = top > m + kFaSlack;  // also the first finite one
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float f = grow ? exp2_approx(m - top) : 1.0f;
+                    if (grow) m = top;
+                    l *= f;
+                    if (j > 0) {  // O of the tiles before is complete: its products precede S in the pipe
+#pragma unroll 1
+                        for (int k = 0; k < kD; k += 16) {
+                            unsigned u[16];
+                            fa_ld(t_o + k, u);
+                            fa_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * f);
+                            fa_st(t_o + k, u);
+                        }
+                    }
+                }
+                const float nm = m == -INFINITY ? 0.0f : -m;
+                const float2 c2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(nm, nm);
+                float2 l2[2] = {make_float2(l, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    unsigned u[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const float2 x = fa_fma2(make_float2(__uint_as_float(v[k][2 * c]), __uint_as_float(v[k][2 * c + 1])), c2, nm2);
+                        u[c] = fa_pack(exp2_approx(x.x), exp2_approx(x.y));
+                        l2[c & 1] = fa_add2(l2[c & 1], make_float2(__uint_as_float(u[c] << 16), __uint_as_float(u[c] & 0xFFFF0000u)));
+                    }
+                    fa_st(t_s + 16 * k, u);
+                    if (k & 1) {  // a half of the weights is written
+                        fa_wait_st();
+                        fa_before();
+                        __syncwarp();
+                        if (lane == 0) fa_arrive(&sh.p_ready[s][k >> 1]);
+                    }
+                }
+                l = (l2[0].x + l2[1].x) + (l2[0].y + l2[1].y);
             }
             if (!ok) break;
             if (n > 0) {

@@ -151,9 +151,16 @@ def _check(code: int, what: str):
         raise IceError(code, what)
 
 
+# the current stream's handle without a Stream object around it (0.1 against 2.9 us a call)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+
+
 def _stream(stream=None) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _dev_ptr(t: torch.Tensor, dtype=None, name="tensor", host_ok=True) -> int:
@@ -452,6 +459,8 @@ class PagedCache:
 
     # -- checks ------------------------------------------------------------------------
     def _ints(self, t, dtype, shape, name):
+        if t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
         if t.shape != shape:
             raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
         return _dev_ptr(t, dtype, name, host_ok=False)
@@ -471,11 +480,8 @@ class PagedCache:
         return t.data_ptr(), stride if t.shape[0] > 1 else heads * d
 
     def _pages(self, k_pages, v_pages):
-        for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-            if t.shape != self._page_shape:
-                raise ValueError(f"{name} must be {self._page_shape}, got {tuple(t.shape)}")
-        return (_dev_ptr(k_pages, self.dtype, "k_pages", host_ok=False),
-                _dev_ptr(v_pages, self.dtype, "v_pages", host_ok=False))
+        return (self._ints(k_pages, self.dtype, self._page_shape, "k_pages"),
+                self._ints(v_pages, self.dtype, self._page_shape, "v_pages"))
 
     # -- the three calls -----------------------------------------------------------------
     def tables(self, seq_len: torch.Tensor, n_new: torch.Tensor, block_table: torch.Tensor,
@@ -488,18 +494,17 @@ class PagedCache:
         block_table and free_pages are updated in place; seq_len_out and free_state_out may
         be seq_len and free_state. n_slots: room for new tokens (entries behind the last
         are -1 in slot_map)."""
-        n, dev = seq_len.shape[0], seq_len.device
+        n, i32, i64 = seq_len.shape[0], torch.int32, torch.int64
         if seq_len_out is None:
             seq_len_out = torch.empty_like(seq_len)
         if free_state_out is None:
             free_state_out = torch.empty_like(free_state)
         if q_start is None:
-            q_start = torch.empty((n + 1,), dtype=torch.int32, device=dev)
+            q_start = torch.empty((n + 1,), dtype=i32, device=self.device)
         if slot_map is None:
-            slot_map = torch.empty((n_slots,), dtype=torch.int64, device=dev)
+            slot_map = torch.empty((n_slots,), dtype=i64, device=self.device)
         if positions is None:
-            positions = torch.empty((n_slots,), dtype=torch.int32, device=dev)
-        i32, i64 = torch.int32, torch.int64
+            positions = torch.empty((n_slots,), dtype=i32, device=self.device)
         _check(_lib.ice_paged_tables(
             self._h, n, self._ints(seq_len, i32, (n,), "seq_len"), self._ints(n_new, i32, (n,), "n_new"),
             self._ints(block_table, i32, (n, self.params.max_blocks), "block_table"),
