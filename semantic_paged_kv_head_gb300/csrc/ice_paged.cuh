@@ -26,17 +26,23 @@ struct PagedAttn {
     const void* k_pages;
     const void* v_pages;
     void* out;
-    float* part_o;   // [slot][n_tokens * Hq][D]: a part's output, normalised
-    float2* part_ml; // [slot][n_tokens * Hq]: its maximum (log2 units) and sum
+    // Parts, by slot and KV head; row R = token * G + head in the group, RP = n_tokens * G
+    // rounded up to 32. Rows are innermost: a warp of the attention holds 32 rows, one a
+    // lane, and writes full lines (as [row][d] the stores of an item took 7 us).
+    float* part_o;   // [slot][H][D][RP]: a part's output, normalised
+    float2* part_ml; // [slot][H][RP]: its maximum (log2 units) and sum
     int* plan;       // kPlanWords, written by the attention kernel for the joining kernel
+    unsigned* next;  // [2]: items handed out beyond the first of each block, blocks done; zero between calls
     int* status;
     float scale_log2;  // log2(e) / sqrt(d)
     int n_req, n_tokens, H, G, P, max_blocks, prefix_len;
     long long n_pages;
+    int RP;
     int prefix_splits;  // parts of the prefix: slots 0 .. prefix_splits - 1
-    int max_splits;     // most parts of a request's own tokens (slots after the prefix's)
-    int target_items;   // items of own tokens aimed at
+    int max_splits;     // most parts of a request's own tokens (slots after the prefix's), >= 2
+    int target_items;   // items of own tokens aimed at where they are few
 };
+constexpr int kPagedMaxSlots = 128;
 
 enum { kPlanOk = 0, kPlanChunk = 1, kPlanOwn = 2, kPlanWords = 4 };
 
@@ -55,13 +61,28 @@ cudaError_t paged_prepare();
 
 // ---- the plan of an attention call, made by every block from the lengths ---------
 // Keys per tile KT, new tokens per row block TB. Request r with nq new tokens
-// and s own tokens is ceil(nq / TB) row blocks, each against up to ceil(s / KT)
-// tiles, cut into ceil(ceil(s / KT) / chunk) parts; chunk is the least that keeps
-// the items near target_items and the parts within max_splits.
+// and s own tokens is ceil(nq / TB) row blocks, each against up to t = ceil(s / KT)
+// tiles, cut into ceil(t / chunk) ranges. Where the rows of a request fill
+// one row tile or less (nq <= TD), a range is cut once more, into two parts that one
+// block attends side by side. chunk gives about target_items items in all, but no range is
+// longer than kPagedMaxRange tiles (the last items to end are then short), and keeps the
+// parts within max_splits.
+constexpr int kPagedMaxRange = 48;
+
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-__device__ __forceinline__ int plan_splits(int nq, int s, int KT, int chunk) {
-    return nq > 0 && s > 0 ? ceil_div(ceil_div(s, KT), chunk) : 0;
+struct PagedTiles {
+    int KT, TB, TD;  // TD = 0: no second cut
+};
+
+__device__ __forceinline__ int plan_parts(int nq, int s, const PagedTiles& z, int chunk) {
+    if (nq <= 0 || s <= 0) return 0;
+    const int t = ceil_div(s, z.KT), ranges = ceil_div(t, chunk);
+    return nq <= z.TD ? min(t, 2 * ranges) : ranges;
+}
+// Items of a row block of the request.
+__device__ __forceinline__ int plan_items(int nq, int parts, const PagedTiles& z) {
+    return nq <= z.TD ? (parts + 1) >> 1 : parts;
 }
 
 struct PlanShared {
@@ -75,7 +96,7 @@ struct PlanShared {
 // Fills cum[0 .. n_req] (items before each request, one KV head) and sh; all threads of the
 // block call it. Block-uniform results after the last barrier.
 template <int NT>
-__device__ __forceinline__ void make_plan(const PagedAttn& a, int KT, int TB, int* cum, PlanShared& sh) {
+__device__ __forceinline__ void make_plan(const PagedAttn& a, const PagedTiles& z, int* cum, PlanShared& sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int NW = NT / 32;
     const int n = a.n_req, per = (n + NT - 1) / NT;
@@ -88,8 +109,8 @@ __device__ __forceinline__ void make_plan(const PagedAttn& a, int KT, int TB, in
         if (b < 0 || e < b || e > a.n_tokens || s < 0 || s > cap || (r == 0 && b != 0)) {
             bad = 1;
         } else if (e > b && s > 0) {
-            const int t = ceil_div(s, KT);
-            w += (long long)t * ceil_div(e - b, TB);
+            const int t = ceil_div(s, z.KT);
+            w += (long long)t * ceil_div(e - b, z.TB);
             mx = max(mx, t);
         }
     }
@@ -112,14 +133,14 @@ __device__ __forceinline__ void make_plan(const PagedAttn& a, int KT, int TB, in
         mx = max(mx, sh.mx[k]);
         bad |= sh.bad[k];
     }
-    long long chunk = max((w * a.H + a.target_items - 1) / a.target_items, 1LL);
-    chunk = max(chunk, (long long)ceil_div(mx, a.max_splits));
-    const int ch = (int)min(chunk, (long long)(1 << 30));
+    long long chunk = min(max((w * a.H + a.target_items - 1) / a.target_items, 1LL), (long long)kPagedMaxRange);
+    chunk = max(chunk, (long long)ceil_div(mx, z.TD > 0 ? a.max_splits / 2 : a.max_splits));
+    const int ch = (int)chunk;
     int mine = 0;
     if (!bad)
         for (int r = r0; r < r1; ++r) {
             const int nq = a.q_start[r + 1] - a.q_start[r];
-            mine += ceil_div(max(nq, 0), TB) * plan_splits(nq, a.seq_len[r], KT, ch);
+            mine += ceil_div(nq, z.TB) * plan_items(nq, plan_parts(nq, a.seq_len[r], z, ch), z);
         }
     int inc = mine;
 #pragma unroll
@@ -139,7 +160,7 @@ __device__ __forceinline__ void make_plan(const PagedAttn& a, int KT, int TB, in
         for (int r = r0; r < r1; ++r) {
             cum[r] = before;
             const int nq = a.q_start[r + 1] - a.q_start[r];
-            before += ceil_div(max(nq, 0), TB) * plan_splits(nq, a.seq_len[r], KT, ch);
+            before += ceil_div(nq, z.TB) * plan_items(nq, plan_parts(nq, a.seq_len[r], z, ch), z);
         }
     if (tid == 0) {
         cum[n] = total;
@@ -157,38 +178,54 @@ __device__ __forceinline__ void make_plan(const PagedAttn& a, int KT, int TB, in
 }
 
 // One item of work: rows of new tokens tok0 .. tok0 + ntok - 1 of KV head h against
-// key tiles kt0 .. kt1 - 1 of a page list. Token t sees keys below
-// min(kv_len, t + lim_off).
+// key tiles of a page list. Token t sees keys below min(kv_len, t + lim_off).
 struct PagedItem {
     const int* table;
-    int h, tok0, ntok, kt0, kt1, kv_len, lim_off, slot;
-    bool direct;  // the rows have no other part: write the output itself
+    int h, tok0, ntok, kv_len, lim_off;
+    int kt0, n[2];  // tiles kt0 .. kt0 + n[0] - 1; a second part, if any: the n[1] tiles that follow
+    int parts;      // 1, or 2 (slots slot and slot + 1)
+    int slot;
+    int direct;     // the rows have no other part: write the output itself
 };
 
-// Most items there can be is known on the host only as a bound; item index i runs
-// over prefix items and then own items. False when i is past the last.
-__device__ __forceinline__ bool get_item(const PagedAttn& a, int KT, int TB, const int* cum,
+__device__ __forceinline__ long long item_count(const PagedAttn& a, const PagedTiles& z, const PlanShared& sh) {
+    return ((long long)ceil_div(a.n_tokens, z.TB) * a.prefix_splits + sh.items) * a.H;
+}
+
+// Item i < item_count. Prefix items and own items alternate as long as there are both: the
+// former are bound by arithmetic, the latter by memory, and they overlap on
+// different SMs.
+__device__ __forceinline__ void get_item(const PagedAttn& a, const PagedTiles& z, const int* cum,
                                          const PlanShared& sh, long long i, PagedItem& it) {
-    const int nb = ceil_div(a.n_tokens, TB);
-    const long long n_pre = (long long)nb * a.H * a.prefix_splits;
-    if (i < n_pre) {
+    const int nb = ceil_div(a.n_tokens, z.TB);
+    const long long n_pre = (long long)nb * a.H * a.prefix_splits, n_own = (long long)sh.items * a.H;
+    const long long both = 2 * min(n_pre, n_own);
+    bool pre;
+    if (i < both) {
+        pre = !(i & 1);
+        i >>= 1;
+    } else {
+        pre = n_pre > n_own;
+        i -= both >> 1;
+    }
+    it.n[1] = 0;
+    it.parts = 1;
+    if (pre) {
         // row blocks fastest: the blocks that run together read the same keys (from L2)
-        it.tok0 = (int)(i % nb) * TB;
+        it.tok0 = (int)(i % nb) * z.TB;
         i /= nb;
         it.h = (int)(i % a.H);
         it.slot = (int)(i / a.H);
-        it.ntok = min(TB, a.n_tokens - it.tok0);
-        const int nt = ceil_div(a.prefix_len, KT);
+        it.ntok = min(z.TB, a.n_tokens - it.tok0);
+        const int nt = ceil_div(a.prefix_len, z.KT);
         it.kt0 = (int)((long long)nt * it.slot / a.prefix_splits);
-        it.kt1 = (int)((long long)nt * (it.slot + 1) / a.prefix_splits);
+        it.n[0] = (int)((long long)nt * (it.slot + 1) / a.prefix_splits) - it.kt0;
         it.kv_len = a.prefix_len;
         it.lim_off = 1 << 30;
         it.table = a.prefix_table;
         it.direct = a.prefix_splits == 1 && sh.items == 0;
-        return true;
+        return;
     }
-    i -= n_pre;
-    if (i >= (long long)sh.items * a.H) return false;
     it.h = (int)(i % a.H);  // heads fastest: neighbours in a page
     const int k = (int)(i / a.H);
     int lo = 0, hi = a.n_req;  // the last r with cum[r] <= k
@@ -198,20 +235,25 @@ __device__ __forceinline__ bool get_item(const PagedAttn& a, int KT, int TB, con
         else hi = mid;
     }
     const int b = a.q_start[lo], e = a.q_start[lo + 1], s = a.seq_len[lo];
-    const int splits = plan_splits(e - b, s, KT, sh.chunk);
-    const int rb = (k - cum[lo]) / splits, part = (k - cum[lo]) - rb * splits;
-    it.tok0 = b + rb * TB;
-    it.ntok = min(TB, e - it.tok0);
+    const int parts = plan_parts(e - b, s, z, sh.chunk), items = plan_items(e - b, parts, z);
+    const int rb = (k - cum[lo]) / items, x = (k - cum[lo]) - rb * items;
+    it.tok0 = b + rb * z.TB;
+    it.ntok = min(z.TB, e - it.tok0);
     it.lim_off = s - e + 1;  // the last new token, e - 1, sees all s
     it.kv_len = s;
     const int seen = min(s, it.tok0 + it.ntok - 1 + it.lim_off);
-    const int nt = seen > 0 ? ceil_div(seen, KT) : 0;
-    it.kt0 = (int)((long long)nt * part / splits);
-    it.kt1 = (int)((long long)nt * (part + 1) / splits);
-    it.slot = a.prefix_splits + part;
+    const int nt = seen > 0 ? ceil_div(seen, z.KT) : 0;
+    const int p0 = e - b <= z.TD ? 2 * x : x;
+    auto edge = [&](int p) { return (int)((long long)nt * p / parts); };
+    it.kt0 = edge(p0);
+    it.n[0] = edge(p0 + 1) - it.kt0;
+    if (e - b <= z.TD && p0 + 1 < parts) {
+        it.parts = 2;
+        it.n[1] = edge(p0 + 2) - edge(p0 + 1);
+    }
+    it.slot = a.prefix_splits + p0;
     it.table = a.block_table + (long long)lo * a.max_blocks;
-    it.direct = a.prefix_splits == 0 && splits == 1;
-    return true;
+    it.direct = a.prefix_splits == 0 && parts == 1;
 }
 
 }  // namespace ice

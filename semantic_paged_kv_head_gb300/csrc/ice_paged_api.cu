@@ -13,9 +13,9 @@ struct ice_paged {
     ice_paged_params p;
     int G = 0, device = 0, n_sm = 0;
     long long rows_cap = 0;    // rows of partial results
-    float* part_o = nullptr;   // [rows_cap][D]
-    float2* part_ml = nullptr; // [rows_cap]
-    int* words = nullptr;      // status word, ticket, plan
+    float* part_o = nullptr;   // rows_cap x D
+    float2* part_ml = nullptr; // rows_cap
+    int* words = nullptr;      // status word, ticket, item counters, plan
 };
 
 namespace {
@@ -25,7 +25,7 @@ struct ApiRange {
     ~ApiRange() { nvtxRangePop(); }
 };
 
-enum { kWordStatus = 0, kWordTicket = 1, kWordPlan = 4, kWords = 8 };
+enum { kWordStatus = 0, kWordTicket = 1, kWordNext = 2, kWordPlan = 4, kWords = 8 };
 
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
@@ -107,8 +107,8 @@ int ice_paged_create(const ice_paged_params* params, ice_paged** out) {
     if (!pg) return ICE_ERR_CAPACITY;
     pg->p = *params;
     pg->G = params->n_q_heads / params->n_kv_heads;
-    const long long R = (long long)params->max_tokens * params->n_q_heads;
-    pg->rows_cap = std::max(2 * R, std::min(64 * R, 262144LL));
+    const long long R = ((long long)params->max_tokens * pg->G + 31) / 32 * 32 * params->n_kv_heads;
+    pg->rows_cap = std::max(3 * R, std::min(64 * R, 262144LL));
     if (cudaGetDevice(&pg->device) != cudaSuccess ||
         cudaDeviceGetAttribute(&pg->n_sm, cudaDevAttrMultiProcessorCount, pg->device) != cudaSuccess ||
         paged_prepare() != cudaSuccess) {
@@ -227,6 +227,7 @@ int ice_paged_attn(ice_paged* pg, int32_t n_req, int32_t n_tokens, const void* q
     a.part_o = pg->part_o;
     a.part_ml = pg->part_ml;
     a.plan = pg->words + kWordPlan;
+    a.next = (unsigned*)pg->words + kWordNext;
     a.status = pg->words + kWordStatus;
     a.scale_log2 = 1.44269504088896341f * 0.08838834764831845f;  // log2(e) / sqrt(128)
     a.n_req = n_req;

@@ -23,6 +23,8 @@ constexpr int kSimtStrideP = kSimtKeys + 4;
 constexpr int kSimtSmem = 4 * (kSimtRows * kSimtStrideK + kSimtKeys * kSimtStrideK + kSimtKeys * kD +
                                kSimtRows * kSimtStrideP);
 
+__host__ __device__ inline PagedTiles simt_tiles(int G) { return {kSimtKeys, kSimtRows / G, 0}; }
+
 __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(PagedAttn a) {
     extern __shared__ __align__(16) float simt_smem[];
     __shared__ PlanShared sh;
@@ -32,14 +34,15 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(PagedAttn a) {
     float* sP = sV + kSimtKeys * kD;
     int* cum = reinterpret_cast<int*>(sP + kSimtRows * kSimtStrideP);
     const int tid = threadIdx.x, rg = tid >> 4, kg = tid & 15;
-    const int TB = kSimtRows / a.G;
+    const PagedTiles z = simt_tiles(a.G);
     pdl_wait_then_release();
-    make_plan<kSimtThreads>(a, kSimtKeys, TB, cum, sh);
+    make_plan<kSimtThreads>(a, z, cum, sh);
     if (!sh.ok) return;
-    const long long rows_all = (long long)a.n_tokens * a.H * a.G;
     const int valid_tok = a.q_start[a.n_req];
+    const long long n_items = item_count(a, z, sh);
     PagedItem it;
-    for (long long i = blockIdx.x; get_item(a, kSimtKeys, TB, cum, sh, i, it); i += gridDim.x) {
+    for (long long i = blockIdx.x; i < n_items; i += gridDim.x) {
+        get_item(a, z, cum, sh, i, it);
         const int nrow = it.ntok * a.G;
         __syncthreads();
         // row r: token tok0 + r / G, head h G + r % G; rows past the item's are zero
@@ -61,7 +64,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(PagedAttn a) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) o[j][k] = 0.0f;
         }
-        for (int kt = it.kt0; kt < it.kt1; ++kt) {
+        for (int kt = it.kt0; kt < it.kt0 + it.n[0]; ++kt) {
             const int key0 = kt * kSimtKeys;
             __syncthreads();
             for (int x = tid; x < kSimtKeys * (kD / 4); x += kSimtThreads) {
@@ -145,93 +148,149 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(PagedAttn a) {
             }
             __syncwarp();
         }
+        __syncthreads();  // the key tile's memory takes the output, [d][row]
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float sum = l[j];
 #pragma unroll
             for (int d = 8; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
             const int r = rg * 4 + j;
-            if (r >= nrow) continue;
-            const int tok = it.tok0 + r / a.G;
-            const long long row = (long long)tok * a.H * a.G + it.h * a.G + r % a.G;
             const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-            if (it.direct) {
-                if (tok >= valid_tok) continue;
-                float* dst = (float*)a.out + row * kD;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    dst[kg * 4 + k] = o[j][k] * inv;
-                    dst[64 + kg * 4 + k] = o[j][4 + k] * inv;
-                }
-            } else {
-                float* dst = a.part_o + (it.slot * rows_all + row) * kD;
-                *reinterpret_cast<float4*>(dst + kg * 4) =
-                    make_float4(o[j][0] * inv, o[j][1] * inv, o[j][2] * inv, o[j][3] * inv);
-                *reinterpret_cast<float4*>(dst + 64 + kg * 4) =
-                    make_float4(o[j][4] * inv, o[j][5] * inv, o[j][6] * inv, o[j][7] * inv);
-                if (kg == 0) a.part_ml[it.slot * rows_all + row] = make_float2(m[j], sum);
+            for (int k = 0; k < 8; ++k)
+                sK[((k >> 2) * 64 + kg * 4 + (k & 3)) * (kSimtRows + 1) + r] = o[j][k] * inv;
+            if (kg == 0 && r < nrow && !it.direct)
+                a.part_ml[((long long)it.slot * a.H + it.h) * a.RP + it.tok0 * a.G + r] = make_float2(m[j], sum);
+        }
+        __syncthreads();
+        if (it.direct) {
+            for (int x = tid; x < nrow * kD; x += kSimtThreads) {
+                const int r = x / kD, c = x % kD, tok = it.tok0 + r / a.G;
+                if (tok < valid_tok)
+                    ((float*)a.out)[((long long)tok * a.H * a.G + it.h * a.G + r % a.G) * kD + c] =
+                        sK[c * (kSimtRows + 1) + r];
             }
+        } else {
+            float* dst = a.part_o + ((long long)it.slot * a.H + it.h) * kD * a.RP + it.tok0 * a.G;
+            const int r = tid % kSimtRows;
+            if (r < nrow)
+                for (int c = tid / kSimtRows; c < kD; c += kSimtThreads / kSimtRows)
+                    dst[(long long)c * a.RP + r] = sK[c * (kSimtRows + 1) + r];
         }
     }
 }
 
 // ---------------------------------------------------------------------------
-// Joining: a warp per row. With parts (m_i, l_i, o_i), M = max m_i and
-// w_i = l_i 2^(m_i - M): out = sum w_i o_i / sum w_i, zeros where nothing was
-// seen. Rows with one part were written by the attention kernel.
+// Joining: a block for 32 rows of a KV head, a lane a row. With parts (m_i, l_i, o_i),
+// M = max m_i and w_i = l_i 2^(m_i - M): out = sum w_i o_i / sum w_i, zeros where
+// nothing was seen. Rows with one part were written by the attention kernel. Bound by the
+// parts' bytes, read once, where there are many rows, and by the latency of a
+// chain of loads where there are few. PW of the 8 warps therefore share the parts of 16
+// dimensions (and the block has 8 / PW groups of 16): one where the rows fill the GPU,
+// eight where a row has many parts and little else runs.
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinDims = 16;
 
-template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttn a, int KT) {
+template <typename T, int PW>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttn a, PagedTiles z) {
+    constexpr int kDims = kJoinDims * (kJoinWarps / PW);  // dimensions of the block
+    __shared__ float wt[kPagedMaxSlots][32];  // weights of the parts, by row
+    __shared__ float tile[PW][32][kDims + 1];
+    __shared__ float red[kJoinWarps][32];
+    __shared__ int own_of[32];                // own parts of each token, -1: nothing to write
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int h = blockIdx.y, R0 = blockIdx.x * 32, d0 = blockIdx.z * kDims, G = a.G;
     pdl_wait_then_release();
     if (!a.plan[kPlanOk]) return;
-    const int lane = threadIdx.x & 31, Hq = a.H * a.G;
-    const long long row = (long long)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
-    const long long rows_all = (long long)a.n_tokens * Hq;
-    if (row >= rows_all) return;
-    const int tok = (int)(row / Hq);
-    // the request of the token: 32 probes a step
-    if (tok >= a.q_start[a.n_req]) return;
-    int lo = 0, hi = a.n_req;  // q_start[lo] <= tok < q_start[hi]
-    while (hi - lo > 1) {
-        const int w = (hi - lo + 31) / 32;
-        const int probe = lo + lane * w;
-        const unsigned le = __ballot_sync(0xffffffffu, probe < hi && a.q_start[min(probe, a.n_req)] <= tok);
-        const int k = 31 - __clz(le);  // lane 0 always holds
-        hi = min(hi, lo + (k + 1) * w);
-        lo = lo + k * w;
+    const int valid_tok = a.q_start[a.n_req], chunk = a.plan[kPlanChunk], own_items = a.plan[kPlanOwn];
+    for (int t = warp; t < 32 / G; t += kJoinWarps) {
+        const int tok = R0 / G + t;
+        int own = -1;
+        if (tok < valid_tok) {
+            int lo = 0, hi = a.n_req;  // q_start[lo] <= tok < q_start[hi]; 32 probes a step
+            while (hi - lo > 1) {
+                const int w = (hi - lo + 31) / 32, probe = lo + lane * w;
+                const unsigned le =
+                    __ballot_sync(0xffffffffu, probe < hi && a.q_start[min(probe, a.n_req)] <= tok);
+                const int k = 31 - __clz(le);  // lane 0 always holds
+                hi = min(hi, lo + (k + 1) * w);
+                lo = lo + k * w;
+            }
+            own = plan_parts(a.q_start[lo + 1] - a.q_start[lo], a.seq_len[lo], z, chunk);
+            // the attention kernel's own conditions for writing the output itself
+            if ((a.prefix_splits == 0 && own == 1) || (a.prefix_splits == 1 && own_items == 0)) own = -1;
+        }
+        if (lane == 0) own_of[t] = own;
     }
-    const int own = plan_splits(a.q_start[lo + 1] - a.q_start[lo], a.seq_len[lo], KT, a.plan[kPlanChunk]);
-    const int n = a.prefix_splits + own;
-    if (n == 1 && (a.prefix_splits == 0 || a.plan[kPlanOwn] == 0)) return;
+    __syncthreads();
+    const int n = own_of[lane / G] < 0 ? 0 : a.prefix_splits + own_of[lane / G];  // parts of row R0 + lane
+    const float2* ml = a.part_ml + (long long)h * a.RP + R0 + lane;
+    const long long ml_step = (long long)a.H * a.RP;
     float M = -INFINITY;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, a.part_ml[i * rows_all + row].x);
+#pragma unroll 4
+    for (int p = warp; p < n; p += kJoinWarps) M = fmaxf(M, ml[p * ml_step].x);
+    red[warp][lane] = M;
+    __syncthreads();
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int k = 0; k < kJoinWarps; ++k) M = fmaxf(M, red[k][lane]);
     if (M == -INFINITY) M = 0.0f;
-    float W = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int i = 0; i < n; ++i) {
-        const float2 ml = a.part_ml[i * rows_all + row];
-        const float w = ml.y * exp2_approx(ml.x - M);
-        float v[4];
-        load4(a.part_o + (i * rows_all + row) * kD + lane * 4, v);
+    for (int p = warp; p < n; p += kJoinWarps) {
+        const float2 x = ml[p * ml_step];
+        wt[p][lane] = x.y * exp2_approx(x.x - M);
+    }
+    __syncthreads();
+    const int pw = warp % PW, dw = warp / PW;
+    const float* src = a.part_o + ((long long)h * kD + d0 + dw * kJoinDims) * a.RP + R0 + lane;
+    const long long step = (long long)a.H * kD * a.RP;
+    float W = 0.0f, acc[kJoinDims];
+#pragma unroll
+    for (int k = 0; k < kJoinDims; ++k) acc[k] = 0.0f;
+#pragma unroll 2
+    for (int p = pw; p < n; p += PW) {
+        const float w = wt[p][lane];
         W += w;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[k] = fmaf(w, v[k], acc[k]);
+        for (int k = 0; k < kJoinDims; ++k) acc[k] = fmaf(w, src[p * step + (long long)k * a.RP], acc[k]);
+    }
+    if (PW > 1) {  // the whole sum of weights
+        red[warp][lane] = W;
+        __syncthreads();
+        W = 0.0f;
+#pragma unroll
+        for (int k = 0; k < PW; ++k) W += red[dw * PW + k][lane];
     }
     const float inv = W > 0.0f ? 1.0f / W : (W == 0.0f ? 0.0f : W);
-    T* dst = (T*)a.out + row * kD + lane * 4;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) dst[k] = from_f<T>(acc[k] * inv);
+    for (int k = 0; k < kJoinDims; ++k) tile[pw][lane][dw * kJoinDims + k] = acc[k] * inv;
+    __syncthreads();
+    for (int x = tid; x < 32 * kDims; x += kJoinThreads) {
+        const int r = x / kDims, c = x % kDims;
+        if (own_of[r / G] < 0) continue;
+        float v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < PW; ++k) v += tile[k][r][c];
+        ((T*)a.out)[((long long)((R0 + r) / G) * a.H * G + h * G + (R0 + r) % G) * kD + d0 + c] = from_f<T>(v);
+    }
+}
+
+template <typename T>
+static cudaError_t launch_join(const PagedAttn& a, const PagedTiles& z, int n_sm, cudaStream_t s) {
+    // warps that share a row's parts: as many as leave the blocks near two a SM
+    const long long groups = (long long)(a.RP / 32) * a.H;
+    const dim3 block(kJoinThreads);
+    auto grid = [&](int pw) { return dim3((unsigned)(a.RP / 32), (unsigned)a.H, (unsigned)pw); };
+    if (groups >= 2 * n_sm) return launch_pdl(paged_join_kernel<T, 1>, grid(1), block, 0, s, a, z);
+    if (groups >= n_sm / 2) return launch_pdl(paged_join_kernel<T, 4>, grid(4), block, 0, s, a, z);
+    return launch_pdl(paged_join_kernel<T, 8>, grid(8), block, 0, s, a, z);
 }
 
 static int simt_bytes(int n_req) { return kSimtSmem + (n_req + 1) * 4; }
 
 cudaError_t paged_tables_prepare();
 cudaError_t paged_tc_prepare();
-int paged_tc_keys(int P);
-int paged_tc_tokens(int G);
+PagedTiles paged_tc_tiles(int P, int G);
 cudaError_t launch_paged_tc(const PagedAttn& a, int n_sm, cudaStream_t s);
 
 cudaError_t paged_prepare() {
@@ -262,25 +321,22 @@ static int prefix_parts(long long n_base, int tiles, int limit, int n_sm) {
 }
 
 cudaError_t launch_paged_attn(PagedAttn a, int dtype, long long rows_cap, int n_sm, cudaStream_t s) {
-    const long long rows = (long long)a.n_tokens * a.H * a.G;
-    const int slots = (int)std::min<long long>(rows_cap / rows, 1 << 20);  // >= 2
     const bool tc = dtype == ICE_BF16;
-    const int KT = tc ? paged_tc_keys(a.P) : kSimtKeys, TB = tc ? paged_tc_tokens(a.G) : kSimtRows / a.G;
-    const long long n_base = (long long)((a.n_tokens + TB - 1) / TB) * a.H;
+    const PagedTiles z = tc ? paged_tc_tiles(a.P, a.G) : simt_tiles(a.G);
+    a.RP = (a.n_tokens * a.G + 31) / 32 * 32;
+    const int slots = (int)std::min<long long>(rows_cap / ((long long)a.H * a.RP), kPagedMaxSlots);  // >= 3
+    const long long n_base = (long long)((a.n_tokens + z.TB - 1) / z.TB) * a.H;
     a.prefix_splits =
-        a.prefix_len > 0 ? prefix_parts(n_base, (a.prefix_len + KT - 1) / KT, slots - 1, n_sm) : 0;
+        a.prefix_len > 0 ? prefix_parts(n_base, (a.prefix_len + z.KT - 1) / z.KT, slots / 2, n_sm) : 0;
     a.max_splits = slots - a.prefix_splits;
-    a.target_items = 2 * n_sm;
+    a.target_items = n_sm;
     cudaError_t e;
     if (tc)
         e = launch_paged_tc(a, n_sm, s);
     else
         e = launch_pdl(paged_simt_kernel, dim3(n_sm), dim3(kSimtThreads), (size_t)simt_bytes(a.n_req), s, a);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
-    if (dtype == ICE_BF16)
-        return launch_pdl(paged_join_kernel<__nv_bfloat16>, grid, dim3(kJoinThreads), 0, s, a, KT);
-    return launch_pdl(paged_join_kernel<float>, grid, dim3(kJoinThreads), 0, s, a, KT);
+    return tc ? launch_join<__nv_bfloat16>(a, z, n_sm, s) : launch_join<float>(a, z, n_sm, s);
 }
 
 }  // namespace ice

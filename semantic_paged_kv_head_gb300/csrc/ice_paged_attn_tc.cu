@@ -49,9 +49,11 @@ constexpr float kFaSlack = 8.0f;          // growth of the maximum (log2) that i
 
 struct FaShared {
     unsigned long long q_full, q_empty, k_full[kFaStagesK], k_empty[kFaStagesK], v_full[kFaStagesV], v_empty[kFaStagesV];
-    unsigned long long s_full[2], p_ready[2][2], o_done[2], drain;  // p_ready: halves of a tile's weights
+    unsigned long long s_full[2], p_ready[2][2], o_done[2], drain;  // p_ready: portions of a tile's weights
+    unsigned long long item_full[2], item_empty[2], item_want;
     unsigned tmem;
-    int abort;
+    int abort, left[2];  // left: whether the item exists
+    PagedItem item[2];
     PlanShared plan;
 };
 
@@ -137,16 +139,16 @@ __device__ __forceinline__ void fa_mma_s(unsigned tmem, unsigned sq, unsigned sk
             : "memory");
     }
 }
-// O (+)= P V over one half of a key tile: 4 steps of 16 keys, each 8 columns of packed weights
-// and 2048 B of V rows.
-__device__ __forceinline__ void fa_mma_o(unsigned tmem_o, unsigned tmem_p, unsigned sv, int half, bool add) {
+// O (+)= P V over a portion of a key tile, keys 0 .. 95 or 96 .. 127: steps of 16 keys, each 8
+// columns of packed weights and 2048 B of V rows.
+template <int PORTION>
+__device__ __forceinline__ void fa_mma_o(unsigned tmem_o, unsigned tmem_p, unsigned sv, bool add) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int ks = 4 * half + k;
+    for (int ks = PORTION ? 6 : 0; ks < (PORTION ? 8 : 6); ++ks) {
         asm volatile(
             "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
             " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_o),
-            "r"(tmem_p + 8 * ks), "l"(fa_desc_v(sv + 2048 * ks)), "r"(kFaIdescO), "r"(add || k > 0 ? 1u : 0u)
+            "r"(tmem_p + 8 * ks), "l"(fa_desc_v(sv + 2048 * ks)), "r"(kFaIdescO), "r"(add || ks > 0 ? 1u : 0u)
             : "memory");
     }
 }
@@ -240,9 +242,33 @@ struct FaPages {
     }
 };
 
+// The items of a block, read by its warps from a ring of two that warp 11 fills. An item is
+// taken when the copies of the one before are nearly issued, not earlier: a block in a
+// long item would keep a second one waiting that another block could have begun.
+constexpr int kFaReaders = 11;  // warps 0 .. 10
+struct FaItems {
+    unsigned cnt = 0;
+    // One warp, or its one active thread (whole = false). False at the end or when a wait ran out (ok = false).
+    __device__ __forceinline__ bool next(FaShared& sh, PagedItem& it, bool& ok, bool whole) {
+        const unsigned k = cnt & 1;
+        bool got = fa_wait(&sh.item_full[k], (cnt >> 1) & 1, &sh.abort);
+        if (whole) got = __all_sync(0xffffffffu, got);
+        if (!got) {
+            ok = false;
+            return false;
+        }
+        ++cnt;
+        const bool left = sh.left[k] != 0;
+        it = sh.item[k];
+        if (whole) __syncwarp();
+        if (!whole || (threadIdx.x & 31) == 0) fa_arrive(&sh.item_empty[k]);
+        return left;
+    }
+};
+
 __global__ void __launch_bounds__(kFaThreads, 1)
     paged_tc_kernel(PagedAttn a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                    const __grid_constant__ CUtensorMap mv, int KT) {
+                    const __grid_constant__ CUtensorMap mv, PagedTiles z) {
     extern __shared__ unsigned char fa_raw[];
     __shared__ __align__(8) FaShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -251,7 +277,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
     unsigned char* mem = fa_raw + (base - raw0);
     const unsigned s_q = base, s_k = base + 2 * kFaTileB, s_v = s_k + kFaStagesK * kFaTileB;
     int* cum = reinterpret_cast<int*>(mem + (2 + kFaStages) * kFaTileB);
-    const int tpt = kFaRows / a.G, TB = 2 * tpt;  // tokens of a row tile, of an item
+    const int KT = z.KT, tpt = z.TD;  // keys of a tile, tokens of a row tile
     if (tid == 0) {
         sh.abort = 0;
         fa_bar_init(&sh.q_full, 1);
@@ -268,7 +294,10 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             fa_bar_init(&sh.s_full[k], 1);
             for (int h = 0; h < 2; ++h) fa_bar_init(&sh.p_ready[k][h], 4);
             fa_bar_init(&sh.o_done[k], 1);
+            fa_bar_init(&sh.item_full[k], 1);
+            fa_bar_init(&sh.item_empty[k], kFaReaders);
         }
+        fa_bar_init(&sh.item_want, 1);
         fa_bar_init(&sh.drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -284,14 +313,13 @@ __global__ void __launch_bounds__(kFaThreads, 1)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     fa_before();
     pdl_wait_then_release();
-    make_plan<kFaThreads>(a, KT, TB, cum, sh.plan);  // its barriers also publish the setup
+    make_plan<kFaThreads>(a, z, cum, sh.plan);  // its barriers also publish the setup
     fa_after();
     const unsigned tmem = sh.tmem;
     volatile int* abort = &sh.abort;
-    const long long rows_all = (long long)a.n_tokens * a.H * a.G;
     PagedItem it;
-    // lengths out of range: reported by the plan, every role has nothing to do
-    const long long first = sh.plan.ok ? blockIdx.x : LLONG_MAX / 2;
+    FaItems items;
+    bool ok = true;
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFaRegsIssue));
         if (warp == 8 || warp == 10) {
@@ -302,21 +330,32 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             unsigned long long* empty = is_k ? sh.k_empty : sh.v_empty;
             const unsigned dst0 = is_k ? s_k : s_v;
             const unsigned long long map = reinterpret_cast<unsigned long long>(is_k ? &mk : &mv);
-            unsigned cnt = 0, items = 0;  // tiles and query tiles issued
-            bool ok = true;
+            unsigned cnt = 0, qcnt = 0;  // key or value tiles and query tiles issued
             const int ppt = KT / a.P;
-            for (long long i = first; ok && get_item(a, KT, TB, cum, sh.plan, i, it); i += gridDim.x) {
-                const int n = it.kt1 - it.kt0;
+            while (ok && items.next(sh, it, ok, true)) {
+                const int n = it.n[0] + it.n[1];
+                if (is_k && n < 2 && lane == 0) fa_arrive(&sh.item_want);
                 if (n == 0) continue;
+                // the x-th tile in the order of use: two parts take turns
+                const int turns = 2 * min(it.n[0], it.n[1]);
+                auto page_of = [&](int x) {
+                    int t = x;
+                    if (it.n[1] > 0) {
+                        const int j = x < turns ? x >> 1 : x - (turns >> 1);
+                        const bool second = x < turns ? (x & 1) : it.n[1] > it.n[0];
+                        t = second ? it.n[0] + j : j;
+                    }
+                    return (it.kt0 + t) * ppt;
+                };
                 FaPages next;  // of the next tile, fetched a tile ahead
-                next.fetch(a, it, it.kt0 * ppt, ppt, lane);
+                next.fetch(a, it, page_of(0), ppt, lane);
                 if (is_k) {
-                    ok = __all_sync(0xffffffffu, fa_wait(&sh.q_empty, (items & 1) ^ 1, abort));
+                    ok = __all_sync(0xffffffffu, fa_wait(&sh.q_empty, (qcnt & 1) ^ 1, abort));
                     if (!ok) break;
                     if (fa_elect()) {
-                        const int ns = it.ntok > tpt ? 2 : 1;
-                        fa_expect(&sh.q_full, ns * kFaTileB);
-                        for (int h = 0; h < 2 * ns; ++h)
+                        const int nt = it.ntok > tpt ? 2 : 1;
+                        fa_expect(&sh.q_full, nt * kFaTileB);
+                        for (int h = 0; h < 2 * nt; ++h)
                             asm volatile(
                                 "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
                                     s_q + h * kFaHalfB),
@@ -325,11 +364,12 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                                 : "memory");
                     }
                     __syncwarp();
-                    ++items;
+                    ++qcnt;
                 }
-                for (int j = 0; j < n; ++j) {
+                for (int x = 0; x < n; ++x) {
                     const FaPages cur = next;
-                    if (j + 1 < n) next.fetch(a, it, (it.kt0 + j + 1) * ppt, ppt, lane);
+                    if (x + 1 < n) next.fetch(a, it, page_of(x + 1), ppt, lane);
+                    if (is_k && n >= 2 && x == n - 2 && lane == 0) fa_arrive(&sh.item_want);
                     const unsigned st = cnt % stages;
                     ok = __all_sync(0xffffffffu, fa_wait(&empty[st], ((cnt / stages) & 1) ^ 1, abort));
                     if (!ok) break;
@@ -355,93 +395,127 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             // copies in flight land (bounded) before the block ends, whatever ended the loop
             if (lane == 0) {
                 if (!ok) set_status(a.status, ICE_ERR_TIMEOUT);
-                if (items) mbar_wait_bounded(smem_u32(&sh.q_full), (items - 1) & 1);
+                if (qcnt) mbar_wait_bounded(smem_u32(&sh.q_full), (qcnt - 1) & 1);
                 for (unsigned k = cnt > (unsigned)stages ? cnt - stages : 0; k < cnt; ++k)
                     mbar_wait_bounded(smem_u32(&full[k % stages]), (k / stages) & 1);
             }
-        } else if (warp == 9 && fa_elect()) {
-            // ---- matrix products (one thread) ----
-            unsigned kn = 0, vn = 0, items = 0, pn[2] = {0, 0};
-            bool ok = true;
-            for (long long i = first; ok && get_item(a, KT, TB, cum, sh.plan, i, it); i += gridDim.x) {
-                const int n = it.kt1 - it.kt0, ns = it.ntok > tpt ? 2 : 1;
-                if (n == 0) continue;
-                ok = fa_wait(&sh.q_full, items & 1, abort) && fa_wait(&sh.k_full[kn % kFaStagesK], (kn / kFaStagesK) & 1, abort);
-                if (!ok) break;
-                ++items;
-                fa_after();
-                for (int s = 0; s < ns; ++s) {
-                    fa_mma_s(tmem + 128 * s, s_q + s * kFaTileB, s_k + (kn % kFaStagesK) * kFaTileB);
-                    fa_commit(&sh.s_full[s]);
-                }
-                fa_commit(&sh.k_empty[kn % kFaStagesK]);
-                ++kn;
-                if (n == 1) fa_commit(&sh.q_empty);
-                for (int j = 0; ok && j < n; ++j, ++vn) {
-                    const bool more = j + 1 < n;
-                    const unsigned ks = kn % kFaStagesK, vs = vn % kFaStagesV;
-                    for (int s = 0; s < ns; ++s) {
-                        if (s == 0) ok = fa_wait(&sh.v_full[vs], (vn / kFaStagesV) & 1, abort);
-                        // the weights come in two halves: the first one's products run while
-                        // the second is made
-                        for (int half = 0; ok && half < 2; ++half) {
-                            ok = fa_wait(&sh.p_ready[s][half], pn[s] & 1, abort);
-                            if (!ok) break;
-                            fa_after();
-                            fa_mma_o(tmem + 256 + 128 * s, tmem + 128 * s, s_v + vs * kFaTileB, half, j > 0 || half > 0);
-                        }
-                        if (!ok) break;
-                        ++pn[s];
-                        if (!more) fa_commit(&sh.o_done[s]);
-                        if (more) {
-                            if (s == 0) ok = fa_wait(&sh.k_full[ks], (kn / kFaStagesK) & 1, abort);
-                            if (!ok) break;
-                            fa_mma_s(tmem + 128 * s, s_q + s * kFaTileB, s_k + ks * kFaTileB);
-                            fa_commit(&sh.s_full[s]);
-                        }
+        } else if (warp == 11) {
+            // ---- items: the block's first is its own number, the others are handed out ----
+            if (fa_elect()) {
+                const long long n_items = sh.plan.ok ? item_count(a, z, sh.plan) : 0;
+                long long i = blockIdx.x;
+                for (unsigned c = 0;; ++c) {
+                    const unsigned k = c & 1;
+                    if ((c > 0 && !fa_wait(&sh.item_want, (c - 1) & 1, abort)) ||
+                        !fa_wait(&sh.item_empty[k], ((c >> 1) & 1) ^ 1, abort)) {
+                        set_status(a.status, ICE_ERR_TIMEOUT);
+                        break;
                     }
-                    if (!ok) break;
-                    fa_commit(&sh.v_empty[vs]);
-                    if (more) {
-                        fa_commit(&sh.k_empty[ks]);
+                    if (c > 0) i = gridDim.x + (long long)atomicAdd(&a.next[0], 1u);
+                    const bool left = i < n_items;
+                    if (left) get_item(a, z, cum, sh.plan, i, sh.item[k]);
+                    sh.left[k] = left;
+                    fa_arrive(&sh.item_full[k]);
+                    if (!left) break;
+                }
+            }
+            __syncwarp();
+        } else if (fa_elect()) {
+            // ---- matrix products (one thread of warp 9) ----
+            unsigned kn = 0, vn = 0, qn = 0, pn[2] = {0, 0};
+            while (ok && items.next(sh, it, ok, false)) {
+                const bool dual = it.parts == 2;  // two key ranges for one row tile; else one for all
+                const int ns = dual || it.ntok > tpt ? 2 : 1;
+                const int n_s[2] = {it.n[0], ns == 1 ? 0 : dual ? it.n[1] : it.n[0]};
+                const int n = max(n_s[0], n_s[1]);
+                if (n == 0) continue;
+                ok = fa_wait(&sh.q_full, qn & 1, abort);
+                ++qn;
+                // scores of stream s against the next key tile; one tile serves both streams
+                // unless they have a range each
+                auto scores = [&](int s) {
+                    const unsigned st = kn % kFaStagesK;
+                    if (dual || s == 0) {
+                        ok = ok && fa_wait(&sh.k_full[st], (kn / kFaStagesK) & 1, abort);
+                        if (!ok) return;
+                        fa_after();
+                    }
+                    fa_mma_s(tmem + 128 * s, s_q + (dual ? 0 : s * kFaTileB), s_k + st * kFaTileB);
+                    fa_commit(&sh.s_full[s]);
+                    if (dual || s == ns - 1) {
+                        fa_commit(&sh.k_empty[st]);
                         ++kn;
+                    }
+                };
+                for (int s = 0; ok && s < ns; ++s)
+                    if (n_s[s] > 0) scores(s);
+                if (n == 1) fa_commit(&sh.q_empty);
+                for (int j = 0; ok && j < n; ++j) {
+                    for (int s = 0; ok && s < ns; ++s) {
+                        if (j >= n_s[s]) continue;
+                        const unsigned st = vn % kFaStagesV;
+                        if (dual || s == 0) ok = fa_wait(&sh.v_full[st], (vn / kFaStagesV) & 1, abort);
+                        // the weights come in two portions: the first one's products run
+                        // while the second is made
+                        const unsigned t_p = tmem + 128 * s, t_o = t_p + 256, sv = s_v + st * kFaTileB;
+                        ok = ok && fa_wait(&sh.p_ready[s][0], pn[s] & 1, abort);
+                        if (!ok) break;
+                        fa_after();
+                        fa_mma_o<0>(t_o, t_p, sv, j > 0);
+                        ok = fa_wait(&sh.p_ready[s][1], pn[s] & 1, abort);
+                        if (!ok) break;
+                        fa_after();
+                        fa_mma_o<1>(t_o, t_p, sv, true);
+                        ++pn[s];
+                        if (j + 1 == n_s[s]) fa_commit(&sh.o_done[s]);
+                        if (dual || s == ns - 1) {
+                            fa_commit(&sh.v_empty[st]);
+                            ++vn;
+                        }
+                        if (j + 1 < n_s[s]) scores(s);
                     }
                     if (j + 2 == n) fa_commit(&sh.q_empty);  // the last scores are issued
                 }
             }
             // products in flight end (bounded) before the tensor memory is given back
             if (!ok) set_status(a.status, ICE_ERR_TIMEOUT);
-            if (items) {
+            if (qn) {
                 fa_commit(&sh.drain);
                 mbar_wait_bounded(smem_u32(&sh.drain), 0);
             }
         }
         __syncwarp();
     } else {
-        // ---- softmax and output: thread = row of tile `s` ----
+        // ---- softmax and output: thread = row of stream s ----
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFaRegsSoftmax));
         const int s = warp >> 2, wq = warp & 3, row = 32 * wq + lane;
         const unsigned t_s = tmem + 128 * s + ((unsigned)(32 * wq) << 16), t_o = t_s + 256;
         const int valid_tok = a.q_start[a.n_req];
         unsigned sn = 0, on = 0, vn = 0;
-        bool ok = true;
-        for (long long i = first; ok && get_item(a, KT, TB, cum, sh.plan, i, it); i += gridDim.x) {
-            const int n = it.kt1 - it.kt0;
-            const int nrow = (it.ntok - s * tpt) * a.G;  // rows of this tile, <= 0: tile not there
-            vn += n;
+        while (ok && items.next(sh, it, ok, true)) {
+            const bool dual = it.parts == 2;
+            const int n0 = it.n[0], n1 = it.n[1];
+            const int n = dual && s ? n1 : n0, kt0 = it.kt0 + (dual && s ? n0 : 0);
+            const int tok0 = it.tok0 + (dual ? 0 : s * tpt);
+            // rows of this stream; none where the item has one row tile and one part
+            const int nrow = s && !dual && it.ntok <= tpt ? 0 : min(tpt, it.ntok - (tok0 - it.tok0)) * a.G;
+            const unsigned vn0 = vn;
+            vn += dual ? n0 + n1 : n0;
             if (nrow <= 0) continue;
             const bool busy = 32 * wq < nrow;  // a warp without rows only keeps the barriers going
-            const int tok = it.tok0 + s * tpt + row / a.G;
+            const int tok = tok0 + row / a.G;
             const int lim = min(it.kv_len, tok + it.lim_off);
+            // keys that every row of the warp sees (the first row sees the fewest)
+            const int lim_all = min(it.kv_len, tok0 + 32 * wq / a.G + it.lim_off);
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; j < n; ++j) {
                 ok = __all_sync(0xffffffffu, fa_wait(&sh.s_full[s], sn & 1, abort));
                 if (!ok) break;
                 ++sn;
-                const int key0 = (it.kt0 + j) * KT;
+                const int key0 = (kt0 + j) * KT;
                 if (key0 + KT > it.kv_len) {  // the last tile of the list: rows behind the last key
-                    const unsigned st = (vn - 1) % kFaStagesV;
-                    ok = __all_sync(0xffffffffu, fa_wait(&sh.v_full[st], ((vn - 1) / kFaStagesV) & 1, abort));
+                    const unsigned v = vn0 + (!dual ? j : s ? j + min(n0, j + 1) : j + min(n1, j)), st = v % kFaStagesV;
+                    ok = __all_sync(0xffffffffu, fa_wait(&sh.v_full[st], (v / kFaStagesV) & 1, abort));
                     if (!ok) break;
                     const int r0 = it.kv_len - key0;
                     unsigned char* v_st = mem + (2 + kFaStagesK + st) * kFaTileB;
@@ -457,25 +531,30 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 }
                 fa_after();
                 unsigned v[4][32];  // scores, as bits
-#pragma unroll
-                for (int k = 0; k < 4; ++k) fa_ld(t_s + 32 * k, v[k]);
+                fa_ld(t_s, v[0]);
+                fa_ld(t_s + 32, v[1]);
                 fa_wait_ld();
+                fa_ld(t_s + 64, v[2]);
+                fa_ld(t_s + 96, v[3]);
+                const bool cut = key0 + kFaKeys > lim_all || KT < kFaKeys;  // some key is hidden from some row
                 const int c_lim = min(lim - key0, KT);
-                if (__any_sync(0xffffffffu, c_lim < kFaKeys)) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                float mx[4];
+                auto max_of = [&](int k) {
+                    if (cut) {
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
                             if (32 * k + c >= c_lim) v[k][c] = 0xFF800000u;  // -inf
-                }
-                float mx[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                    }
                     mx[k] = fmaxf(__uint_as_float(v[k][0]), __uint_as_float(v[k][1]));
 #pragma unroll
                     for (int c = 2; c < 32; c += 2)
                         mx[k] = fa_max3(mx[k], __uint_as_float(v[k][c]), __uint_as_float(v[k][c + 1]));
-                }
+                };
+                max_of(0);
+                max_of(1);
+                fa_wait_ld();
+                max_of(2);
+                max_of(3);
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
                 const bool grow = top > m + kFaSlack;  // also the first finite one
                 if (__any_sync(0xffffffffu, grow)) {
@@ -497,6 +576,12 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 const float nm = m == -INFINITY ? 0.0f : -m;
                 const float2 c2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(nm, nm);
                 float2 l2[2] = {make_float2(l, 0.0f), make_float2(0.0f, 0.0f)};
+                auto ready = [&](int h) {  // portion h of the weights is written
+                    fa_wait_st();
+                    fa_before();
+                    __syncwarp();
+                    if (lane == 0) fa_arrive(&sh.p_ready[s][h]);
+                };
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     unsigned u[16];
@@ -506,14 +591,10 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                         u[c] = fa_pack(exp2_approx(x.x), exp2_approx(x.y));
                         l2[c & 1] = fa_add2(l2[c & 1], make_float2(__uint_as_float(u[c] << 16), __uint_as_float(u[c] & 0xFFFF0000u)));
                     }
+                    if (k == 3) ready(0);  // keys 0 .. 95, stored while these were made
                     fa_st(t_s + 16 * k, u);
-                    if (k & 1) {  // a half of the weights is written
-                        fa_wait_st();
-                        fa_before();
-                        __syncwarp();
-                        if (lane == 0) fa_arrive(&sh.p_ready[s][k >> 1]);
-                    }
                 }
+                ready(1);
                 l = (l2[0].x + l2[1].x) + (l2[0].y + l2[1].y);
             }
             if (!ok) break;
@@ -525,8 +606,9 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             if (!busy) continue;
             fa_after();
             const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-            const long long r = (long long)tok * a.H * a.G + it.h * a.G + row % a.G;
             const bool mine = row < nrow;
+            const long long part = (long long)(it.slot + (dual ? s : 0)) * a.H + it.h;
+            const int R = tok0 * a.G + row;
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) {
                 unsigned u[32];
@@ -540,19 +622,20 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                     o[c] = n > 0 && l != 0.0f ? __uint_as_float(u[c]) * inv : 0.0f;
                 if (mine && it.direct) {
                     if (tok < valid_tok) {
-                        uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + r * kD + 32 * k);
+                        uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)a.out +
+                                                              ((long long)tok * a.H * a.G + it.h * a.G + row % a.G) * kD + 32 * k);
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
                             dst[c] = make_uint4(fa_pack(o[8 * c], o[8 * c + 1]), fa_pack(o[8 * c + 2], o[8 * c + 3]),
                                                 fa_pack(o[8 * c + 4], o[8 * c + 5]), fa_pack(o[8 * c + 6], o[8 * c + 7]));
                     }
                 } else if (mine) {
-                    float4* dst = reinterpret_cast<float4*>(a.part_o + (it.slot * rows_all + r) * kD + 32 * k);
+                    float* dst = a.part_o + (part * kD + 32 * k) * a.RP + R;
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) dst[c] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                    for (int c = 0; c < 32; ++c) dst[(long long)c * a.RP] = o[c];
                 }
             }
-            if (mine && !it.direct) a.part_ml[it.slot * rows_all + r] = make_float2(m, l);
+            if (mine && !it.direct) a.part_ml[part * a.RP + R] = make_float2(m, l);
             fa_before();
         }
     }
@@ -561,6 +644,13 @@ __global__ void __launch_bounds__(kFaThreads, 1)
     fa_after();
     if (warp == 9)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    if (tid == 0) {  // the last block to end leaves the counters at zero
+        __threadfence();
+        if (atomicAdd(&a.next[1], 1u) == gridDim.x - 1) {
+            a.next[0] = 0;
+            a.next[1] = 0;
+        }
+    }
 }
 
 typedef CUresult (*FaEncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -591,8 +681,7 @@ static bool fa_map(CUtensorMap* m, const void* p, int rank, const cuuint64_t* di
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int paged_tc_keys(int P) { return kFaKeys / P * P; }
-int paged_tc_tokens(int G) { return 2 * kFaRows / G; }
+PagedTiles paged_tc_tiles(int P, int G) { return {kFaKeys / P * P, 2 * kFaRows / G, kFaRows / G}; }
 
 cudaError_t launch_paged_tc(const PagedAttn& a, int n_sm, cudaStream_t s) {
     CUtensorMap mq, mk, mv;
@@ -605,7 +694,7 @@ cudaError_t launch_paged_tc(const PagedAttn& a, int n_sm, cudaStream_t s) {
     if (!fa_map(&mq, a.q, 3, qd, qs, qb) || !fa_map(&mk, a.k_pages, 2, kd, ks, kb) || !fa_map(&mv, a.v_pages, 2, kd, ks, kb))
         return cudaErrorNotSupported;
     return launch_pdl(paged_tc_kernel, dim3(n_sm), dim3(kFaThreads), (size_t)fa_smem(a.n_req), s, a, mq, mk, mv,
-                      paged_tc_keys(a.P));
+                      paged_tc_tiles(a.P, a.G));
 }
 
 cudaError_t paged_tc_prepare() {
