@@ -38,7 +38,8 @@ struct PagedAttn {
     int n_req, n_tokens, H, G, P, max_blocks, prefix_len;
     long long n_pages;
     int RP;
-    int prefix_splits;  // parts of the prefix: slots 0 .. prefix_splits - 1
+    int prefix_splits;  // parts of the prefix: slots 0 .. prefix_splits - 1 (even in number or one a
+                        // tile where two are attended side by side)
     int max_splits;     // most parts of a request's own tokens (slots after the prefix's), >= 2
     int target_items;   // items of own tokens aimed at where they are few
 };
@@ -188,18 +189,25 @@ struct PagedItem {
     int direct;     // the rows have no other part: write the output itself
 };
 
-__device__ __forceinline__ long long item_count(const PagedAttn& a, const PagedTiles& z, const PlanShared& sh) {
-    return ((long long)ceil_div(a.n_tokens, z.TB) * a.prefix_splits + sh.items) * a.H;
+// Items of the prefix: row blocks x heads x ranges; ranges are cut into two parts where
+// all the rows fill one row tile or less.
+__device__ __forceinline__ int prefix_items(const PagedAttn& a, const PagedTiles& z) {
+    return ceil_div(a.n_tokens, z.TB) * a.H * plan_items(a.n_tokens, a.prefix_splits, z);
+}
+
+// Fits an int: the scratch for the rows alone would pass the GPU's memory before.
+__device__ __forceinline__ int item_count(const PagedAttn& a, const PagedTiles& z, const PlanShared& sh) {
+    return prefix_items(a, z) + sh.items * a.H;
 }
 
 // Item i < item_count. Prefix items and own items alternate as long as there are both: the
 // former are bound by arithmetic, the latter by memory, and they overlap on
 // different SMs.
 __device__ __forceinline__ void get_item(const PagedAttn& a, const PagedTiles& z, const int* cum,
-                                         const PlanShared& sh, long long i, PagedItem& it) {
-    const int nb = ceil_div(a.n_tokens, z.TB);
-    const long long n_pre = (long long)nb * a.H * a.prefix_splits, n_own = (long long)sh.items * a.H;
-    const long long both = 2 * min(n_pre, n_own);
+                                         const PlanShared& sh, int i, PagedItem& out) {
+    PagedItem it;
+    const int n_pre = prefix_items(a, z), n_own = sh.items * a.H;
+    const int both = 2 * min(n_pre, n_own);
     bool pre;
     if (i < both) {
         pre = !(i & 1);
@@ -210,50 +218,57 @@ __device__ __forceinline__ void get_item(const PagedAttn& a, const PagedTiles& z
     }
     it.n[1] = 0;
     it.parts = 1;
+    int nt, parts, p0, twin;
     if (pre) {
         // row blocks fastest: the blocks that run together read the same keys (from L2)
-        it.tok0 = (int)(i % nb) * z.TB;
-        i /= nb;
-        it.h = (int)(i % a.H);
-        it.slot = (int)(i / a.H);
+        const int nb = ceil_div(a.n_tokens, z.TB);
+        const int rb = i % nb, k = i / nb;
+        it.tok0 = rb * z.TB;
+        it.h = k % a.H;
         it.ntok = min(z.TB, a.n_tokens - it.tok0);
-        const int nt = ceil_div(a.prefix_len, z.KT);
-        it.kt0 = (int)((long long)nt * it.slot / a.prefix_splits);
-        it.n[0] = (int)((long long)nt * (it.slot + 1) / a.prefix_splits) - it.kt0;
         it.kv_len = a.prefix_len;
         it.lim_off = 1 << 30;
         it.table = a.prefix_table;
         it.direct = a.prefix_splits == 1 && sh.items == 0;
-        return;
+        nt = ceil_div(a.prefix_len, z.KT);
+        parts = a.prefix_splits;
+        twin = a.n_tokens <= z.TD;
+        p0 = (k / a.H) << twin;
+        it.slot = p0;
+    } else {
+        const int k = i / a.H;
+        it.h = i - k * a.H;  // heads fastest: neighbours in a page
+        int lo = 0, hi = a.n_req;  // the last r with cum[r] <= k
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (cum[mid] <= k) lo = mid;
+            else hi = mid;
+        }
+        const int b = a.q_start[lo], e = a.q_start[lo + 1], s = a.seq_len[lo];
+        parts = plan_parts(e - b, s, z, sh.chunk);
+        const int x0 = k - cum[lo], items = plan_items(e - b, parts, z);
+        const int rb = x0 / items;
+        it.tok0 = b + rb * z.TB;
+        it.ntok = min(z.TB, e - it.tok0);
+        it.lim_off = s - e + 1;  // the last new token, e - 1, sees all s
+        it.kv_len = s;
+        it.table = a.block_table + (long long)lo * a.max_blocks;
+        it.direct = a.prefix_splits == 0 && parts == 1;
+        const int seen = min(s, it.tok0 + it.ntok - 1 + it.lim_off);
+        nt = seen > 0 ? ceil_div(seen, z.KT) : 0;
+        twin = e - b <= z.TD;
+        p0 = (x0 - rb * items) << twin;
+        it.slot = a.prefix_splits + p0;
     }
-    it.h = (int)(i % a.H);  // heads fastest: neighbours in a page
-    const int k = (int)(i / a.H);
-    int lo = 0, hi = a.n_req;  // the last r with cum[r] <= k
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cum[mid] <= k) lo = mid;
-        else hi = mid;
-    }
-    const int b = a.q_start[lo], e = a.q_start[lo + 1], s = a.seq_len[lo];
-    const int parts = plan_parts(e - b, s, z, sh.chunk), items = plan_items(e - b, parts, z);
-    const int rb = (k - cum[lo]) / items, x = (k - cum[lo]) - rb * items;
-    it.tok0 = b + rb * z.TB;
-    it.ntok = min(z.TB, e - it.tok0);
-    it.lim_off = s - e + 1;  // the last new token, e - 1, sees all s
-    it.kv_len = s;
-    const int seen = min(s, it.tok0 + it.ntok - 1 + it.lim_off);
-    const int nt = seen > 0 ? ceil_div(seen, z.KT) : 0;
-    const int p0 = e - b <= z.TD ? 2 * x : x;
     auto edge = [&](int p) { return (int)((long long)nt * p / parts); };
     it.kt0 = edge(p0);
-    it.n[0] = edge(p0 + 1) - it.kt0;
-    if (e - b <= z.TD && p0 + 1 < parts) {
+    const int kt1 = edge(p0 + 1);
+    it.n[0] = kt1 - it.kt0;
+    if (twin && p0 + 1 < parts) {
         it.parts = 2;
-        it.n[1] = edge(p0 + 2) - edge(p0 + 1);
+        it.n[1] = edge(p0 + 2) - kt1;
     }
-    it.slot = a.prefix_splits + p0;
-    it.table = a.block_table + (long long)lo * a.max_blocks;
-    it.direct = a.prefix_splits == 0 && parts == 1;
+    out = it;
 }
 
 }  // namespace ice

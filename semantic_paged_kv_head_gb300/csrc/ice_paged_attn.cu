@@ -39,9 +39,9 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(PagedAttn a) {
     make_plan<kSimtThreads>(a, z, cum, sh);
     if (!sh.ok) return;
     const int valid_tok = a.q_start[a.n_req];
-    const long long n_items = item_count(a, z, sh);
+    const int n_items = item_count(a, z, sh);
     PagedItem it;
-    for (long long i = blockIdx.x; i < n_items; i += gridDim.x) {
+    for (int i = blockIdx.x; i < n_items; i += gridDim.x) {
         get_item(a, z, cum, sh, i, it);
         const int nrow = it.ntok * a.G;
         __syncthreads();
@@ -199,15 +199,15 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttn a, P
     __shared__ float wt[kPagedMaxSlots][32];  // weights of the parts, by row
     __shared__ float tile[PW][32][kDims + 1];
     __shared__ float red[kJoinWarps][32];
-    __shared__ int own_of[32];                // own parts of each token, -1: nothing to write
+    __shared__ int own_of[32], len_of[32];    // own parts of each token, -1: nothing to write
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = blockIdx.y, R0 = blockIdx.x * 32, d0 = blockIdx.z * kDims, G = a.G;
-    pdl_wait_then_release();
-    if (!a.plan[kPlanOk]) return;
-    const int valid_tok = a.q_start[a.n_req], chunk = a.plan[kPlanChunk], own_items = a.plan[kPlanOwn];
+    // Before the wait: q_start and seq_len were complete when the attention kernel's blocks let
+    // this one be scheduled (they wait for the kernels before them first).
+    const int valid_tok = a.q_start[a.n_req];
     for (int t = warp; t < 32 / G; t += kJoinWarps) {
         const int tok = R0 / G + t;
-        int own = -1;
+        int nq = -1, own_len = 0;
         if (tok < valid_tok) {
             int lo = 0, hi = a.n_req;  // q_start[lo] <= tok < q_start[hi]; 32 probes a step
             while (hi - lo > 1) {
@@ -218,11 +218,22 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttn a, P
                 hi = min(hi, lo + (k + 1) * w);
                 lo = lo + k * w;
             }
-            own = plan_parts(a.q_start[lo + 1] - a.q_start[lo], a.seq_len[lo], z, chunk);
-            // the attention kernel's own conditions for writing the output itself
-            if ((a.prefix_splits == 0 && own == 1) || (a.prefix_splits == 1 && own_items == 0)) own = -1;
+            nq = a.q_start[lo + 1] - a.q_start[lo];
+            own_len = a.seq_len[lo];
         }
-        if (lane == 0) own_of[t] = own;
+        if (lane == 0) {
+            own_of[t] = nq;
+            len_of[t] = own_len;
+        }
+    }
+    pdl_wait_then_release();
+    if (!a.plan[kPlanOk]) return;
+    const int chunk = a.plan[kPlanChunk], own_items = a.plan[kPlanOwn];
+    __syncthreads();
+    if (tid < 32 / G && own_of[tid] >= 0) {
+        const int own = plan_parts(own_of[tid], len_of[tid], z, chunk);
+        // the attention kernel's own conditions for writing the output itself
+        own_of[tid] = (a.prefix_splits == 0 && own == 1) || (a.prefix_splits == 1 && own_items == 0) ? -1 : own;
     }
     __syncthreads();
     const int n = own_of[lane / G] < 0 ? 0 : a.prefix_splits + own_of[lane / G];  // parts of row R0 + lane
@@ -302,14 +313,14 @@ cudaError_t paged_prepare() {
                                 simt_bytes(kPagedMaxRequests));
 }
 
-// Parts of the prefix: n_base row blocks x heads, each part a wave's share of
-// tiles. The time of s parts is taken as waves x (tiles of a part + the fixed cost of
-// an item, in tiles); the least wins, the fewest parts among equals.
-static int prefix_parts(long long n_base, int tiles, int limit, int n_sm) {
+// Ranges of the prefix: n_base row blocks x heads, each range a wave's share of
+// tiles. The time of s ranges is taken as waves x (tiles of a range + the fixed cost of
+// an item, in tiles); the least wins, the fewest ranges among equals.
+static int prefix_ranges(long long n_base, int tiles, int limit, int n_sm) {
     constexpr int kItemCost = 3;
     int best = 1;
     long long best_t = -1;
-    for (int s = 1; s <= std::min(std::min(limit, tiles), kPagedMaxPrefixSplits); ++s) {
+    for (int s = 1; s <= std::min(limit, tiles); ++s) {
         const long long waves = (n_base * s + n_sm - 1) / n_sm;
         const long long t = waves * ((tiles + s - 1) / s + kItemCost);
         if (best_t < 0 || t < best_t) {
@@ -326,8 +337,13 @@ cudaError_t launch_paged_attn(PagedAttn a, int dtype, long long rows_cap, int n_
     a.RP = (a.n_tokens * a.G + 31) / 32 * 32;
     const int slots = (int)std::min<long long>(rows_cap / ((long long)a.H * a.RP), kPagedMaxSlots);  // >= 3
     const long long n_base = (long long)((a.n_tokens + z.TB - 1) / z.TB) * a.H;
-    a.prefix_splits =
-        a.prefix_len > 0 ? prefix_parts(n_base, (a.prefix_len + z.KT - 1) / z.KT, slots / 2, n_sm) : 0;
+    a.prefix_splits = 0;
+    if (a.prefix_len > 0) {
+        const int tiles = (a.prefix_len + z.KT - 1) / z.KT, limit = std::min(slots / 2, kPagedMaxPrefixSplits);
+        const bool twin = a.n_tokens <= z.TD;  // two parts a range
+        a.prefix_splits = prefix_ranges(n_base, tiles, twin ? std::max(1, limit / 2) : limit, n_sm);
+        if (twin) a.prefix_splits = std::min(std::min(2 * a.prefix_splits, limit), tiles);
+    }
     a.max_splits = slots - a.prefix_splits;
     a.target_items = n_sm;
     cudaError_t e;

@@ -48,7 +48,7 @@ constexpr int kFaStages = kFaStagesK + kFaStagesV;
 constexpr float kFaSlack = 8.0f;          // growth of the maximum (log2) that is let pass
 
 struct FaShared {
-    unsigned long long q_full, q_empty, k_full[kFaStagesK], k_empty[kFaStagesK], v_full[kFaStagesV], v_empty[kFaStagesV];
+    unsigned long long q_full[2], q_empty[2], k_full[kFaStagesK], k_empty[kFaStagesK], v_full[kFaStagesV], v_empty[kFaStagesV];
     unsigned long long s_full[2], p_ready[2][2], o_done[2], drain;  // p_ready: portions of a tile's weights
     unsigned long long item_full[2], item_empty[2], item_want;
     unsigned tmem;
@@ -243,8 +243,9 @@ struct FaPages {
 };
 
 // The items of a block, read by its warps from a ring of two that warp 11 fills. An item is
-// taken when the copies of the one before are nearly issued, not earlier: a block in a
+// taken when kFaAhead tiles of the one before are left to copy, not earlier: a block in a
 // long item would keep a second one waiting that another block could have begun.
+constexpr int kFaAhead = 8;
 constexpr int kFaReaders = 11;  // warps 0 .. 10
 struct FaItems {
     unsigned cnt = 0;
@@ -280,8 +281,6 @@ __global__ void __launch_bounds__(kFaThreads, 1)
     const int KT = z.KT, tpt = z.TD;  // keys of a tile, tokens of a row tile
     if (tid == 0) {
         sh.abort = 0;
-        fa_bar_init(&sh.q_full, 1);
-        fa_bar_init(&sh.q_empty, 1);
         for (int k = 0; k < kFaStagesK; ++k) {
             fa_bar_init(&sh.k_full[k], 1);
             fa_bar_init(&sh.k_empty[k], 1);
@@ -291,6 +290,8 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             fa_bar_init(&sh.v_empty[k], 1);
         }
         for (int k = 0; k < 2; ++k) {
+            fa_bar_init(&sh.q_full[k], 1);
+            fa_bar_init(&sh.q_empty[k], 1);
             fa_bar_init(&sh.s_full[k], 1);
             for (int h = 0; h < 2; ++h) fa_bar_init(&sh.p_ready[k][h], 4);
             fa_bar_init(&sh.o_done[k], 1);
@@ -334,7 +335,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             const int ppt = KT / a.P;
             while (ok && items.next(sh, it, ok, true)) {
                 const int n = it.n[0] + it.n[1];
-                if (is_k && n < 2 && lane == 0) fa_arrive(&sh.item_want);
+                if (is_k && n <= kFaAhead && lane == 0) fa_arrive(&sh.item_want);
                 if (n == 0) continue;
                 // the x-th tile in the order of use: two parts take turns
                 const int turns = 2 * min(it.n[0], it.n[1]);
@@ -350,26 +351,28 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 FaPages next;  // of the next tile, fetched a tile ahead
                 next.fetch(a, it, page_of(0), ppt, lane);
                 if (is_k) {
-                    ok = __all_sync(0xffffffffu, fa_wait(&sh.q_empty, (qcnt & 1) ^ 1, abort));
-                    if (!ok) break;
-                    if (fa_elect()) {
-                        const int nt = it.ntok > tpt ? 2 : 1;
-                        fa_expect(&sh.q_full, nt * kFaTileB);
-                        for (int h = 0; h < 2 * nt; ++h)
-                            asm volatile(
-                                "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-                                    s_q + h * kFaHalfB),
-                                "l"(reinterpret_cast<unsigned long long>(&mq)), "r"((h & 1) * 64), "r"(it.h * a.G),
-                                "r"(it.tok0 + (h >> 1) * tpt), "r"(smem_u32(&sh.q_full))
-                                : "memory");
+                    const int nt = it.ntok > tpt ? 2 : 1;
+                    for (int t = 0; ok && t < nt; ++t, ++qcnt) {
+                        const unsigned st = qcnt & 1;
+                        ok = __all_sync(0xffffffffu, fa_wait(&sh.q_empty[st], ((qcnt >> 1) & 1) ^ 1, abort));
+                        if (ok && fa_elect()) {
+                            fa_expect(&sh.q_full[st], kFaTileB);
+                            for (int h = 0; h < 2; ++h)
+                                asm volatile(
+                                    "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                                        s_q + st * kFaTileB + h * kFaHalfB),
+                                    "l"(reinterpret_cast<unsigned long long>(&mq)), "r"(h * 64), "r"(it.h * a.G),
+                                    "r"(it.tok0 + t * tpt), "r"(smem_u32(&sh.q_full[st]))
+                                    : "memory");
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                    ++qcnt;
+                    if (!ok) break;
                 }
                 for (int x = 0; x < n; ++x) {
                     const FaPages cur = next;
                     if (x + 1 < n) next.fetch(a, it, page_of(x + 1), ppt, lane);
-                    if (is_k && n >= 2 && x == n - 2 && lane == 0) fa_arrive(&sh.item_want);
+                    if (is_k && n > kFaAhead && x == n - kFaAhead && lane == 0) fa_arrive(&sh.item_want);
                     const unsigned st = cnt % stages;
                     ok = __all_sync(0xffffffffu, fa_wait(&empty[st], ((cnt / stages) & 1) ^ 1, abort));
                     if (!ok) break;
@@ -395,15 +398,16 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             // copies in flight land (bounded) before the block ends, whatever ended the loop
             if (lane == 0) {
                 if (!ok) set_status(a.status, ICE_ERR_TIMEOUT);
-                if (qcnt) mbar_wait_bounded(smem_u32(&sh.q_full), (qcnt - 1) & 1);
+                for (unsigned k = qcnt > 2 ? qcnt - 2 : 0; k < qcnt; ++k)
+                    mbar_wait_bounded(smem_u32(&sh.q_full[k & 1]), (k >> 1) & 1);
                 for (unsigned k = cnt > (unsigned)stages ? cnt - stages : 0; k < cnt; ++k)
                     mbar_wait_bounded(smem_u32(&full[k % stages]), (k / stages) & 1);
             }
         } else if (warp == 11) {
             // ---- items: the block's first is its own number, the others are handed out ----
             if (fa_elect()) {
-                const long long n_items = sh.plan.ok ? item_count(a, z, sh.plan) : 0;
-                long long i = blockIdx.x;
+                const int n_items = sh.plan.ok ? item_count(a, z, sh.plan) : 0;
+                int i = blockIdx.x;
                 for (unsigned c = 0;; ++c) {
                     const unsigned k = c & 1;
                     if ((c > 0 && !fa_wait(&sh.item_want, (c - 1) & 1, abort)) ||
@@ -411,7 +415,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                         set_status(a.status, ICE_ERR_TIMEOUT);
                         break;
                     }
-                    if (c > 0) i = gridDim.x + (long long)atomicAdd(&a.next[0], 1u);
+                    if (c > 0) i = gridDim.x + atomicAdd(&a.next[0], 1u);
                     const bool left = i < n_items;
                     if (left) get_item(a, z, cum, sh.plan, i, sh.item[k]);
                     sh.left[k] = left;
@@ -429,8 +433,11 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 const int n_s[2] = {it.n[0], ns == 1 ? 0 : dual ? it.n[1] : it.n[0]};
                 const int n = max(n_s[0], n_s[1]);
                 if (n == 0) continue;
-                ok = fa_wait(&sh.q_full, qn & 1, abort);
-                ++qn;
+                const int nq = it.ntok > tpt ? 2 : 1;  // query tiles; two parts share one
+                for (int t = 0; ok && t < nq; ++t) ok = fa_wait(&sh.q_full[(qn + t) & 1], ((qn + t) >> 1) & 1, abort);
+                auto q_done = [&]() {
+                    for (int t = 0; t < nq; ++t) fa_commit(&sh.q_empty[(qn + t) & 1]);
+                };
                 // scores of stream s against the next key tile; one tile serves both streams
                 // unless they have a range each
                 auto scores = [&](int s) {
@@ -440,7 +447,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                         if (!ok) return;
                         fa_after();
                     }
-                    fa_mma_s(tmem + 128 * s, s_q + (dual ? 0 : s * kFaTileB), s_k + st * kFaTileB);
+                    fa_mma_s(tmem + 128 * s, s_q + ((qn + (dual ? 0 : s)) & 1) * kFaTileB, s_k + st * kFaTileB);
                     fa_commit(&sh.s_full[s]);
                     if (dual || s == ns - 1) {
                         fa_commit(&sh.k_empty[st]);
@@ -449,7 +456,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 };
                 for (int s = 0; ok && s < ns; ++s)
                     if (n_s[s] > 0) scores(s);
-                if (n == 1) fa_commit(&sh.q_empty);
+                if (n == 1) q_done();
                 for (int j = 0; ok && j < n; ++j) {
                     for (int s = 0; ok && s < ns; ++s) {
                         if (j >= n_s[s]) continue;
@@ -474,8 +481,9 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                         }
                         if (j + 1 < n_s[s]) scores(s);
                     }
-                    if (j + 2 == n) fa_commit(&sh.q_empty);  // the last scores are issued
+                    if (j + 2 == n) q_done();  // the last scores are issued
                 }
+                qn += nq;
             }
             // products in flight end (bounded) before the tensor memory is given back
             if (!ok) set_status(a.status, ICE_ERR_TIMEOUT);
