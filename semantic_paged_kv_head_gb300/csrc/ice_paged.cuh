@@ -5,6 +5,8 @@
 // rows of one KV head are P * D contiguous elements.
 #pragma once
 
+#include <limits.h>
+
 #include "ice_internal.cuh"
 
 namespace ice {
@@ -14,8 +16,8 @@ constexpr int kPagedMaxPrefixSplits = 64;  // parts of the prefix that are atten
 
 // Attention of one call, passed by value. The work is a list of items, each a
 // block of rows (new tokens x the G query heads of a KV head) against a range of
-// key tiles: first the prefix items, whose rows are the whole batch's, then the
-// items of the requests' own tokens. Items of one row are joined afterwards.
+// key tiles: prefix items, whose rows are the whole batch's, and items of single
+// requests. The parts of one row are joined afterwards.
 struct PagedAttn {
     const void* q;
     long long q_stride;  // elements
@@ -32,6 +34,7 @@ struct PagedAttn {
     float* part_o;   // [slot][H][D][RP]: a part's output, normalised
     float2* part_ml; // [slot][H][RP]: its maximum (log2 units) and sum
     int* plan;       // kPlanWords, written by the attention kernel for the joining kernel
+    int* first_long; // [n_req]: number of each request's first row block x head, if it is long
     unsigned* next;  // [2]: items handed out beyond the first of each block, blocks done; zero between calls
     int* status;
     float scale_log2;  // log2(e) / sqrt(d)
@@ -45,7 +48,9 @@ struct PagedAttn {
 };
 constexpr int kPagedMaxSlots = 128;
 
-enum { kPlanOk = 0, kPlanChunk = 1, kPlanOwn = 2, kPlanWords = 4 };
+// plan words: lengths in range, tiles of a range of own tokens, the two of PagedLong, whether the
+// prefix items write the output themselves
+enum { kPlanOk = 0, kPlanChunk = 1, kPlanWhole = 2, kPlanSplit = 3, kPlanDirect = 4, kPlanWords = 5 };
 
 cudaError_t launch_paged_tables(int n_req, int max_blocks, int P, long long n_pages, const int* seq_len,
                                 const int* n_new, int* block_table, int* free_pages,
@@ -61,41 +66,79 @@ cudaError_t launch_paged_attn(PagedAttn a, int dtype, long long rows_cap, int n_
 cudaError_t paged_prepare();
 
 // ---- the plan of an attention call, made by every block from the lengths ---------
-// Keys per tile KT, new tokens per row block TB. Request r with nq new tokens
-// and s own tokens is ceil(nq / TB) row blocks, each against up to t = ceil(s / KT)
-// tiles, cut into ceil(t / chunk) ranges. Where the rows of a request fill
-// one row tile or less (nq <= TD), a range is cut once more, into two parts that one
-// block attends side by side. chunk gives about target_items items in all, but no range is
-// longer than kPagedMaxRange tiles (the last items to end are then short), and keeps the
-// parts within max_splits.
+// Keys per tile KT, new tokens per row block TB. Tiles are numbered through the
+// prefix's NP and on through a request's own.
+//
+// A request of more than TS new tokens fills row blocks of its own: nothing is gained by
+// sharing, so its items run through the prefix and its own tokens in one pass
+// and have nothing to join, except those of the last, incomplete wave over the GPU, which are cut
+// into `split` parts each. The other requests' rows share the prefix items, and their own tokens
+// are cut into ranges of `chunk` tiles; with TD > 0 one block attends two streams side
+// by side: two parts of a range, or two KV heads where there is one part.
+// chunk gives about target_items items in all, but no range is longer than
+// kPagedMaxRange tiles (the last items to end are then short), and keeps the parts
+// within max_splits.
 constexpr int kPagedMaxRange = 48;
 
-__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+__host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 struct PagedTiles {
-    int KT, TB, TD;  // TD = 0: no second cut
+    int KT, TB, TS, TD;  // TD = TS, or 0: one stream at a time
+    int NP, pages;       // tiles of the prefix, pages of a tile (TD > 0)
 };
 
-__device__ __forceinline__ int plan_parts(int nq, int s, const PagedTiles& z, int chunk) {
-    if (nq <= 0 || s <= 0) return 0;
+// Parts of the own tokens of a request that shares the prefix items.
+__device__ __forceinline__ int plan_parts(int s, const PagedTiles& z, int chunk) {
+    if (s <= 0) return 0;
     const int t = ceil_div(s, z.KT), ranges = ceil_div(t, chunk);
-    return nq <= z.TD ? min(t, 2 * ranges) : ranges;
+    return z.TD > 0 ? min(t, 2 * ranges) : ranges;
 }
-// Items of a row block of the request.
-__device__ __forceinline__ int plan_items(int nq, int parts, const PagedTiles& z) {
-    return nq <= z.TD ? (parts + 1) >> 1 : parts;
+// Row blocks x heads of long requests are numbered: request by request, head by head. Those
+// below `whole` are one item each, the others `split`.
+struct PagedLong {
+    int whole, split;
+};
+// Of a long request whose first number is g0, those that are one item each.
+__device__ __forceinline__ int long_whole(int g0, int n, const PagedLong& f) { return min(max(f.whole - g0, 0), n); }
+
+__device__ __forceinline__ int long_blocks(int nq, int s, const PagedTiles& z) {
+    return nq > z.TS && (z.NP > 0 || s > 0) ? ceil_div(nq, z.TB) : 0;
+}
+// Items of a request.
+__device__ __forceinline__ int plan_items(int nq, int s, int H, int g0, const PagedTiles& z, int chunk, const PagedLong& f) {
+    if (nq <= 0) return 0;
+    if (nq > z.TS) {
+        const int n = long_blocks(nq, s, z) * H, w = long_whole(g0, n, f);
+        return w + (n - w) * f.split;
+    }
+    const int parts = plan_parts(s, z, chunk);
+    if (z.TD == 0) return parts * H;
+    return parts == 1 ? (H + 1) >> 1 : ((parts + 1) >> 1) * H;
 }
 
 struct PlanShared {
-    long long w[32];  // per warp: tiles of all row blocks
-    int mx[32];       // per warp: most tiles of a request
-    int bad[32];
+    long long w[32];   // per warp: tiles of the own tokens of requests that share the prefix
+    long long wl[32];  // per warp: tiles of the row blocks of long requests
+    int mx[32];        // per warp: most own tiles of a request that shares the prefix
+    int nl[32];        // per warp: row blocks of long requests
+    int fl[32];        // per warp: 1 bad length, 2 a request that shares the prefix, 4 one with own tokens
     int sum[32];
-    int ok, chunk, items;  // items: of own tokens and one KV head
+    int sum2[32];
+    int ok, chunk, own, pre, direct;  // items of requests, of the prefix
+    int some_long;
+    PagedLong f;
+    const int *q_start, *seq_len;            // in shared memory where they fit
+    const int* first_long;
 };
 
-// Fills cum[0 .. n_req] (items before each request, one KV head) and sh; all threads of the
-// block call it. Block-uniform results after the last barrier.
+// Bytes of shared memory for the plan's lists: items before each request, and (where the
+// room for kPagedMaxRequests allows) the lengths.
+__host__ __device__ constexpr int plan_ints(int n_req) {
+    return 4 * (n_req + 1) <= kPagedMaxRequests + 1 ? 4 * (n_req + 1) : n_req + 1;
+}
+
+// Fills cum[0 .. n_req] (items before each request) and sh; all threads of the block call
+// it. Block-uniform results after the last barrier.
 template <int NT>
 __device__ __forceinline__ void make_plan(const PagedAttn& a, const PagedTiles& z, int* cum, PlanShared& sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -103,45 +146,99 @@ __device__ __forceinline__ void make_plan(const PagedAttn& a, const PagedTiles& 
     const int n = a.n_req, per = (n + NT - 1) / NT;
     const int r0 = min(tid * per, n), r1 = min(r0 + per, n);
     const long long cap = (long long)a.max_blocks * a.P;
-    long long w = 0;
-    int mx = 0, bad = 0;
+    const int NP = z.NP;
+    const bool keep = plan_ints(n) > n + 1;
+    int *qs = cum + n + 1, *sl = qs + n + 1, *gl = sl + n + 1;
+    long long w = 0, wl = 0;
+    int mx = 0, nl = 0, fl = 0;
     for (int r = r0; r < r1; ++r) {
         const int b = a.q_start[r], e = a.q_start[r + 1], s = a.seq_len[r];
+        if (keep) {
+            qs[r] = b;
+            sl[r] = s;
+            if (r == n - 1) qs[n] = e;
+        }
         if (b < 0 || e < b || e > a.n_tokens || s < 0 || s > cap || (r == 0 && b != 0)) {
-            bad = 1;
-        } else if (e > b && s > 0) {
+            fl |= 1;
+        } else if (e - b > z.TS) {
+            const int blocks = long_blocks(e - b, s, z);
+            nl += blocks;
+            wl += (long long)blocks * (NP + ceil_div(s, z.KT));
+        } else if (e > b) {
+            fl |= s > 0 ? 6 : 2;
             const int t = ceil_div(s, z.KT);
-            w += (long long)t * ceil_div(e - b, z.TB);
+            w += t;
             mx = max(mx, t);
         }
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) {
         w += __shfl_xor_sync(0xffffffffu, w, o);
+        wl += __shfl_xor_sync(0xffffffffu, wl, o);
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+        nl += __shfl_xor_sync(0xffffffffu, nl, o);
+        fl |= __shfl_xor_sync(0xffffffffu, fl, o);
     }
     if (lane == 0) {
         sh.w[warp] = w;
+        sh.wl[warp] = wl;
         sh.mx[warp] = mx;
-        sh.bad[warp] = bad;
+        sh.nl[warp] = nl;
+        sh.fl[warp] = fl;
     }
     __syncthreads();
-    w = 0, mx = 0, bad = 0;
+    w = 0, wl = 0, mx = 0, nl = 0, fl = 0;
 #pragma unroll
     for (int k = 0; k < NW; ++k) {
         w += sh.w[k];
+        wl += sh.wl[k];
         mx = max(mx, sh.mx[k]);
-        bad |= sh.bad[k];
+        nl += sh.nl[k];
+        fl |= sh.fl[k];
     }
+    const bool bad = fl & 1;
     long long chunk = min(max((w * a.H + a.target_items - 1) / a.target_items, 1LL), (long long)kPagedMaxRange);
     chunk = max(chunk, (long long)ceil_div(mx, z.TD > 0 ? a.max_splits / 2 : a.max_splits));
     const int ch = (int)chunk;
-    int mine = 0;
+    // parts of the last wave's: waves x (tiles of a part + the fixed cost of an item, and of
+    // joining it, in tiles), the least of 1 to 16
+    // (where the lengths do not fit in shared memory, with thousands of requests, all are whole)
+    PagedLong f = {INT_MAX, 1};
+    if (nl > 0 && keep) {
+        const int all = nl * a.H, rest = all % a.target_items, mean = (int)(wl / nl);
+        f.whole = all - rest;  // the last `rest` are an incomplete wave
+        int best = INT_MAX;
+        for (int k = 1; rest > 0 && k <= min(16, min(a.max_splits, max(mean, 1))); ++k) {
+            const int t = ceil_div(rest * k, a.target_items) * (ceil_div(mean, k) + (k > 1 ? 6 : 3));
+            if (t < best) {
+                best = t;
+                f.split = k;
+            }
+        }
+    }
+    // long row blocks before each request, then items
+    int lmine = 0, linc;
+    if (!bad && nl > 0)
+        for (int r = r0; r < r1; ++r) lmine += long_blocks(a.q_start[r + 1] - a.q_start[r], a.seq_len[r], z);
+    linc = lmine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, linc, o);
+        if (lane >= o) linc += x;
+    }
+    if (lane == 31) sh.sum2[warp] = linc;
+    __syncthreads();
+    int g0 = linc - lmine;
+#pragma unroll
+    for (int k = 0; k < NW; ++k)
+        if (k < warp) g0 += sh.sum2[k];
+    g0 *= a.H;
+    int mine = 0, g = g0;
     if (!bad)
         for (int r = r0; r < r1; ++r) {
-            const int nq = a.q_start[r + 1] - a.q_start[r];
-            mine += ceil_div(nq, z.TB) * plan_items(nq, plan_parts(nq, a.seq_len[r], z, ch), z);
+            const int nq = a.q_start[r + 1] - a.q_start[r], s = a.seq_len[r];
+            mine += plan_items(nq, s, a.H, g, z, ch, f);
+            g += long_blocks(nq, s, z) * a.H;
         }
     int inc = mine;
 #pragma unroll
@@ -157,118 +254,192 @@ __device__ __forceinline__ void make_plan(const PagedAttn& a, const PagedTiles& 
         if (k < warp) before += sh.sum[k];
         total += sh.sum[k];
     }
-    if (!bad)
+    if (!bad) {
+        g = g0;
         for (int r = r0; r < r1; ++r) {
+            const int nq = a.q_start[r + 1] - a.q_start[r], s = a.seq_len[r];
             cum[r] = before;
-            const int nq = a.q_start[r + 1] - a.q_start[r];
-            before += ceil_div(nq, z.TB) * plan_items(nq, plan_parts(nq, a.seq_len[r], z, ch), z);
+            before += plan_items(nq, s, a.H, g, z, ch, f);
+            if (nl > 0 && keep) {
+                gl[r] = g;
+                if (blockIdx.x == 0) a.first_long[r] = g;  // for the joining kernel
+            }
+            g += long_blocks(nq, s, z) * a.H;
         }
+    }
     if (tid == 0) {
         cum[n] = total;
         sh.ok = !bad;
         sh.chunk = ch;
-        sh.items = total;
+        sh.f = f;
+        sh.own = total;
+        sh.some_long = nl > 0;
+        // the prefix's: row blocks x heads x ranges, cut in two where all rows fit one stream
+        const int ranges = z.TD > 0 && a.n_tokens <= z.TD ? (a.prefix_splits + 1) >> 1 : a.prefix_splits;
+        sh.pre = fl & 2 ? ceil_div(a.n_tokens, z.TB) * a.H * ranges : 0;
+        sh.direct = a.prefix_splits == 1 && !(fl & 4) && nl == 0;
+        sh.q_start = keep ? qs : a.q_start;
+        sh.seq_len = keep ? sl : a.seq_len;
+        sh.first_long = gl;
         if (blockIdx.x == 0) {
             a.plan[kPlanOk] = !bad;
             a.plan[kPlanChunk] = ch;
-            a.plan[kPlanOwn] = total;
+            a.plan[kPlanWhole] = f.whole;
+            a.plan[kPlanSplit] = f.split;
+            a.plan[kPlanDirect] = sh.direct;
             if (bad) set_status(a.status, ICE_ERR_BOUNDS);
         }
     }
     __syncthreads();
 }
 
-// One item of work: rows of new tokens tok0 .. tok0 + ntok - 1 of KV head h against
-// key tiles of a page list. Token t sees keys below min(kv_len, t + lim_off).
-struct PagedItem {
-    const int* table;
-    int h, tok0, ntok, kv_len, lim_off;
-    int kt0, n[2];  // tiles kt0 .. kt0 + n[0] - 1; a second part, if any: the n[1] tiles that follow
-    int parts;      // 1, or 2 (slots slot and slot + 1)
-    int slot;
-    int direct;     // the rows have no other part: write the output itself
+// Rows of new tokens tok0 .. tok0 + ntok - 1 of KV head h against tiles kt0 .. kt0 + n - 1.
+// Token t sees the prefix and the own tokens below min(own_len, t + lim_off).
+struct PagedStream {
+    const int* own_table;
+    int h, tok0, ntok, own_len, lim_off, kt0, n, slot;
+    int direct;  // the rows have no other part: write the output itself
 };
 
-// Items of the prefix: row blocks x heads x ranges; ranges are cut into two parts where
-// all the rows fill one row tile or less.
-__device__ __forceinline__ int prefix_items(const PagedAttn& a, const PagedTiles& z) {
-    return ceil_div(a.n_tokens, z.TB) * a.H * plan_items(a.n_tokens, a.prefix_splits, z);
+struct PagedItem {
+    PagedStream st[2];
+    int ns;      // streams: 1 or 2 (0: nothing to do)
+    int shared;  // both streams, row tiles of one block, read the same key tiles
+    int same_q;  // both streams, parts of one range, have the same rows
+};
+
+// A tile of a stream: its page list, the first key in it, the list's keys.
+struct PagedTile {
+    const int* table;
+    int key0, len;
+    bool own;
+};
+__device__ __forceinline__ PagedTile tile_of(const PagedAttn& a, const PagedTiles& z, const PagedStream& s, int x) {
+    PagedTile t;
+    t.own = x >= z.NP;
+    t.table = t.own ? s.own_table : a.prefix_table;
+    t.key0 = (t.own ? x - z.NP : x) * z.KT;
+    t.len = t.own ? s.own_len : a.prefix_len;
+    return t;
 }
 
-// Fits an int: the scratch for the rows alone would pass the GPU's memory before.
-__device__ __forceinline__ int item_count(const PagedAttn& a, const PagedTiles& z, const PlanShared& sh) {
-    return prefix_items(a, z) + sh.items * a.H;
+// The last r in [0, n) with v[r] <= i (v[0] <= i).
+__device__ __forceinline__ int find_last(const int* v, int n, int i) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (v[mid] <= i) lo = mid;
+        else hi = mid;
+    }
+    return lo;
 }
 
-// Item i < item_count. Prefix items and own items alternate as long as there are both: the
-// former are bound by arithmetic, the latter by memory, and they overlap on
-// different SMs.
+// Item i < sh.pre + sh.own. Prefix items and the others alternate as long as there are both:
+// the former are bound by arithmetic, own tokens of few rows by memory, and they
+// overlap on different SMs.
 __device__ __forceinline__ void get_item(const PagedAttn& a, const PagedTiles& z, const int* cum,
                                          const PlanShared& sh, int i, PagedItem& out) {
-    PagedItem it;
-    const int n_pre = prefix_items(a, z), n_own = sh.items * a.H;
-    const int both = 2 * min(n_pre, n_own);
+    const int both = 2 * min(sh.pre, sh.own);
     bool pre;
     if (i < both) {
         pre = !(i & 1);
         i >>= 1;
     } else {
-        pre = n_pre > n_own;
+        pre = sh.pre > sh.own;
         i -= both >> 1;
     }
-    it.n[1] = 0;
-    it.parts = 1;
-    int nt, parts, p0, twin;
+    const int NP = z.NP;
+    const int tpt = z.TD > 0 ? z.TD : z.TB;  // tokens of a row tile
+    PagedStream st;
+    int ns = 1, shared = 0, base, nt, parts, p0;
+    bool twin = false, two_heads = false;
     if (pre) {
         // row blocks fastest: the blocks that run together read the same keys (from L2)
         const int nb = ceil_div(a.n_tokens, z.TB);
-        const int rb = i % nb, k = i / nb;
-        it.tok0 = rb * z.TB;
-        it.h = k % a.H;
-        it.ntok = min(z.TB, a.n_tokens - it.tok0);
-        it.kv_len = a.prefix_len;
-        it.lim_off = 1 << 30;
-        it.table = a.prefix_table;
-        it.direct = a.prefix_splits == 1 && sh.items == 0;
-        nt = ceil_div(a.prefix_len, z.KT);
+        const int k = i / nb, rb = i - k * nb;
+        st.tok0 = rb * z.TB;
+        st.h = k % a.H;
+        st.ntok = min(z.TB, a.n_tokens - st.tok0);
+        st.own_table = nullptr;
+        st.own_len = 0;
+        st.lim_off = 0;
+        st.direct = sh.direct;
+        base = 0;
+        nt = NP;
         parts = a.prefix_splits;
-        twin = a.n_tokens <= z.TD;
-        p0 = (k / a.H) << twin;
-        it.slot = p0;
-    } else {
-        const int k = i / a.H;
-        it.h = i - k * a.H;  // heads fastest: neighbours in a page
-        int lo = 0, hi = a.n_req;  // the last r with cum[r] <= k
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (cum[mid] <= k) lo = mid;
-            else hi = mid;
+        twin = z.TD > 0 && a.n_tokens <= z.TD;
+        p0 = (k / a.H) << (int)twin;
+        st.slot = p0;
+        if (sh.some_long) {  // nothing to do where the block's tokens are all of long requests
+            bool any = false;
+            for (int r = find_last(sh.q_start, a.n_req, st.tok0); r < a.n_req && !any; ++r) {
+                const int b = sh.q_start[r], e = sh.q_start[r + 1];
+                if (b >= st.tok0 + st.ntok) break;
+                any = e > max(b, st.tok0) && e - b <= z.TS;
+            }
+            if (!any) ns = 0;
         }
-        const int b = a.q_start[lo], e = a.q_start[lo + 1], s = a.seq_len[lo];
-        parts = plan_parts(e - b, s, z, sh.chunk);
-        const int x0 = k - cum[lo], items = plan_items(e - b, parts, z);
-        const int rb = x0 / items;
-        it.tok0 = b + rb * z.TB;
-        it.ntok = min(z.TB, e - it.tok0);
-        it.lim_off = s - e + 1;  // the last new token, e - 1, sees all s
-        it.kv_len = s;
-        it.table = a.block_table + (long long)lo * a.max_blocks;
-        it.direct = a.prefix_splits == 0 && parts == 1;
-        const int seen = min(s, it.tok0 + it.ntok - 1 + it.lim_off);
-        nt = seen > 0 ? ceil_div(seen, z.KT) : 0;
-        twin = e - b <= z.TD;
-        p0 = (x0 - rb * items) << twin;
-        it.slot = a.prefix_splits + p0;
+    } else {
+        const int lo = find_last(cum, a.n_req, i);
+        const int b = sh.q_start[lo], e = sh.q_start[lo + 1], s = sh.seq_len[lo], x = i - cum[lo];
+        st.own_table = a.block_table + (long long)lo * a.max_blocks;
+        st.own_len = s;
+        st.lim_off = s - e + 1;  // the last new token, e - 1, sees all s
+        int rb = 0;
+        if (e - b > z.TS) {
+            const int blocks = ceil_div(e - b, z.TB), n = blocks * a.H;
+            const int whole = long_whole(sh.f.whole == INT_MAX ? 0 : sh.first_long[lo], n, sh.f);
+            int y = x;  // head, row block: the blocks of a head run together
+            p0 = 0;
+            parts = 1;
+            if (x >= whole) {
+                p0 = (x - whole) / (n - whole);
+                y = x - p0 * (n - whole);
+                parts = sh.f.split;
+            }
+            st.h = y / blocks;
+            rb = y - st.h * blocks;
+            base = 0;
+            st.direct = parts == 1;
+        } else {
+            parts = plan_parts(s, z, sh.chunk);
+            base = NP;
+            twin = z.TD > 0 && parts > 1;
+            two_heads = z.TD > 0 && parts == 1;
+            st.h = two_heads ? 2 * x : x % a.H;
+            p0 = two_heads ? 0 : (x / a.H) << (int)twin;
+            st.direct = a.prefix_splits == 0 && parts == 1;
+        }
+        st.tok0 = b + rb * z.TB;
+        st.ntok = min(z.TB, e - st.tok0);
+        st.slot = a.prefix_splits + p0;
+        const int seen = min(s, st.tok0 + st.ntok - 1 + st.lim_off);
+        nt = NP - base + (seen > 0 ? ceil_div(seen, z.KT) : 0);
     }
-    auto edge = [&](int p) { return (int)((long long)nt * p / parts); };
-    it.kt0 = edge(p0);
+    auto edge = [&](int p) { return base + (int)((long long)nt * p / parts); };
+    st.kt0 = edge(p0);
     const int kt1 = edge(p0 + 1);
-    it.n[0] = kt1 - it.kt0;
-    if (twin && p0 + 1 < parts) {
-        it.parts = 2;
-        it.n[1] = edge(p0 + 2) - kt1;
+    st.n = kt1 - st.kt0;
+    out.st[1] = st;
+    out.same_q = twin && p0 + 1 < parts;
+    if (out.same_q) {
+        ns *= 2;
+        out.st[1].kt0 = kt1;
+        out.st[1].n = edge(p0 + 2) - kt1;
+        out.st[1].slot = st.slot + 1;
+    } else if (two_heads && st.h + 1 < a.H) {
+        ns *= 2;
+        out.st[1].h = st.h + 1;
+    } else if (st.ntok > tpt) {
+        ns *= 2;
+        shared = 1;
+        out.st[1].tok0 = st.tok0 + tpt;
+        out.st[1].ntok = st.ntok - tpt;
+        st.ntok = tpt;
     }
-    out = it;
+    out.st[0] = st;
+    out.ns = ns;
+    out.shared = shared;
 }
 
 }  // namespace ice

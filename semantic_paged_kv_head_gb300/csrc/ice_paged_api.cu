@@ -15,7 +15,7 @@ struct ice_paged {
     long long rows_cap = 0;    // rows of partial results
     float* part_o = nullptr;   // rows_cap x D
     float2* part_ml = nullptr; // rows_cap
-    int* words = nullptr;      // status word, ticket, item counters, plan
+    int* words = nullptr;      // status word, ticket, item counters, plan, then [max_requests] of the plan
 };
 
 namespace {
@@ -25,7 +25,7 @@ struct ApiRange {
     ~ApiRange() { nvtxRangePop(); }
 };
 
-enum { kWordStatus = 0, kWordTicket = 1, kWordNext = 2, kWordPlan = 4, kWords = 8 };
+enum { kWordStatus = 0, kWordTicket = 1, kWordNext = 2, kWordPlan = 4, kWords = 16 };
 
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
@@ -118,7 +118,7 @@ int ice_paged_create(const ice_paged_params* params, ice_paged** out) {
     }
     if (cudaMalloc(&pg->part_o, (size_t)pg->rows_cap * kD * 4) != cudaSuccess ||
         cudaMalloc(&pg->part_ml, (size_t)pg->rows_cap * 8) != cudaSuccess ||
-        cudaMalloc(&pg->words, kWords * 4) != cudaSuccess) {
+        cudaMalloc(&pg->words, (kWords + params->max_requests) * 4) != cudaSuccess) {
         cudaGetLastError();
         free_all(pg);
         delete pg;
@@ -227,6 +227,7 @@ int ice_paged_attn(ice_paged* pg, int32_t n_req, int32_t n_tokens, const void* q
     a.part_o = pg->part_o;
     a.part_ml = pg->part_ml;
     a.plan = pg->words + kWordPlan;
+    a.first_long = pg->words + kWords;
     a.next = (unsigned*)pg->words + kWordNext;
     a.status = pg->words + kWordStatus;
     a.scale_log2 = 1.44269504088896341f * 0.08838834764831845f;  // log2(e) / sqrt(128)

@@ -23,9 +23,7 @@ constexpr int kSimtStrideP = kSimtKeys + 4;
 constexpr int kSimtSmem = 4 * (kSimtRows * kSimtStrideK + kSimtKeys * kSimtStrideK + kSimtKeys * kD +
                                kSimtRows * kSimtStrideP);
 
-__host__ __device__ inline PagedTiles simt_tiles(int G) { return {kSimtKeys, kSimtRows / G, 0}; }
-
-__global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(PagedAttn a) {
+__global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(PagedAttn a, PagedTiles z) {
     extern __shared__ __align__(16) float simt_smem[];
     __shared__ PlanShared sh;
     float* sQ = simt_smem;
@@ -34,15 +32,16 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(PagedAttn a) {
     float* sP = sV + kSimtKeys * kD;
     int* cum = reinterpret_cast<int*>(sP + kSimtRows * kSimtStrideP);
     const int tid = threadIdx.x, rg = tid >> 4, kg = tid & 15;
-    const PagedTiles z = simt_tiles(a.G);
     pdl_wait_then_release();
     make_plan<kSimtThreads>(a, z, cum, sh);
     if (!sh.ok) return;
     const int valid_tok = a.q_start[a.n_req];
-    const int n_items = item_count(a, z, sh);
-    PagedItem it;
+    const int n_items = sh.pre + sh.own;
+    PagedItem item;
     for (int i = blockIdx.x; i < n_items; i += gridDim.x) {
-        get_item(a, z, cum, sh, i, it);
+        get_item(a, z, cum, sh, i, item);
+        if (item.ns == 0) continue;
+        const PagedStream& it = item.st[0];
         const int nrow = it.ntok * a.G;
         __syncthreads();
         // row r: token tok0 + r / G, head h G + r % G; rows past the item's are zero
@@ -60,18 +59,19 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(PagedAttn a) {
             m[j] = -INFINITY;
             l[j] = 0.0f;
             const int r = rg * 4 + j;
-            lim[j] = r < nrow ? min(it.kv_len, it.tok0 + r / a.G + it.lim_off) : 0;
+            lim[j] = r < nrow ? min(it.own_len, it.tok0 + r / a.G + it.lim_off) : 0;  // of own tokens
 #pragma unroll
             for (int k = 0; k < 8; ++k) o[j][k] = 0.0f;
         }
-        for (int kt = it.kt0; kt < it.kt0 + it.n[0]; ++kt) {
-            const int key0 = kt * kSimtKeys;
+        for (int kt = it.kt0; kt < it.kt0 + it.n; ++kt) {
+            const PagedTile t = tile_of(a, z, it, kt);
+            const int key0 = t.key0;
             __syncthreads();
             for (int x = tid; x < kSimtKeys * (kD / 4); x += kSimtThreads) {
                 const int r = x / (kD / 4), c = (x % (kD / 4)) * 4, key = key0 + r;
                 float vk[4] = {0.0f, 0.0f, 0.0f, 0.0f}, vv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (key < it.kv_len) {
-                    const int page = it.table[key / a.P];
+                if (key < t.len) {
+                    const int page = t.table[key / a.P];
                     if (page >= 0 && page < a.n_pages) {
                         const long long row = ((long long)page * a.H + it.h) * a.P + key % a.P;
                         load4((const float*)a.k_pages + row * kD + c, vk);
@@ -107,9 +107,10 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(PagedAttn a) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float mx = m[j];
+                const int end = t.own ? lim[j] : t.len;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    s[j][k] = key0 + kg + 16 * k < lim[j] ? s[j][k] * a.scale_log2 : -INFINITY;
+                    s[j][k] = key0 + kg + 16 * k < end ? s[j][k] * a.scale_log2 : -INFINITY;
                     mx = fmaxf(mx, s[j][k]);
                 }
 #pragma unroll
@@ -129,15 +130,15 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(PagedAttn a) {
             }
             __syncwarp();  // a row's weights are written and read by one warp
 #pragma unroll 2
-            for (int t = 0; t < kSimtKeys; t += 4) {
+            for (int k0 = 0; k0 < kSimtKeys; k0 += 4) {
                 float4 pv[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    pv[j] = *reinterpret_cast<const float4*>(sP + (rg * 4 + j) * kSimtStrideP + t);
+                    pv[j] = *reinterpret_cast<const float4*>(sP + (rg * 4 + j) * kSimtStrideP + k0);
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const float4 v0 = *reinterpret_cast<const float4*>(sV + (t + u) * kD + kg * 4);
-                    const float4 v1 = *reinterpret_cast<const float4*>(sV + (t + u) * kD + 64 + kg * 4);
+                    const float4 v0 = *reinterpret_cast<const float4*>(sV + (k0 + u) * kD + kg * 4);
+                    const float4 v1 = *reinterpret_cast<const float4*>(sV + (k0 + u) * kD + 64 + kg * 4);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float p = u == 0 ? pv[j].x : u == 1 ? pv[j].y : u == 2 ? pv[j].z : pv[j].w;
@@ -199,7 +200,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttn a, P
     __shared__ float wt[kPagedMaxSlots][32];  // weights of the parts, by row
     __shared__ float tile[PW][32][kDims + 1];
     __shared__ float red[kJoinWarps][32];
-    __shared__ int own_of[32], len_of[32];    // own parts of each token, -1: nothing to write
+    __shared__ int req_of[32], blk_of[32];    // request of each token, its row block
+    __shared__ int own_of[32], len_of[32];    // new and own tokens of each token's request, then its parts
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = blockIdx.y, R0 = blockIdx.x * 32, d0 = blockIdx.z * kDims, G = a.G;
     // Before the wait: q_start and seq_len were complete when the attention kernel's blocks let
@@ -220,6 +222,10 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttn a, P
             }
             nq = a.q_start[lo + 1] - a.q_start[lo];
             own_len = a.seq_len[lo];
+            if (lane == 0) {
+                req_of[t] = lo;
+                blk_of[t] = (tok - a.q_start[lo]) / z.TB;
+            }
         }
         if (lane == 0) {
             own_of[t] = nq;
@@ -228,16 +234,29 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttn a, P
     }
     pdl_wait_then_release();
     if (!a.plan[kPlanOk]) return;
-    const int chunk = a.plan[kPlanChunk], own_items = a.plan[kPlanOwn];
+    const int chunk = a.plan[kPlanChunk], pre_direct = a.plan[kPlanDirect];
+    const PagedLong f = {a.plan[kPlanWhole], a.plan[kPlanSplit]};
     __syncthreads();
-    if (tid < 32 / G && own_of[tid] >= 0) {
-        const int own = plan_parts(own_of[tid], len_of[tid], z, chunk);
-        // the attention kernel's own conditions for writing the output itself
-        own_of[tid] = (a.prefix_splits == 0 && own == 1) || (a.prefix_splits == 1 && own_items == 0) ? -1 : own;
+    if (tid < 32 / G) {
+        // the parts' first slot and number; none where the attention kernel wrote the output itself
+        const int nq = own_of[tid], s = len_of[tid];
+        int first = 0, parts = -1;
+        if (nq > z.TS) {
+            const int blocks = long_blocks(nq, s, z);
+            first = a.prefix_splits;
+            const bool whole = f.whole == INT_MAX || a.first_long[req_of[tid]] + h * blocks + blk_of[tid] < f.whole;
+            parts = blocks == 0 ? 0 : whole || f.split == 1 ? -1 : f.split;
+        } else if (nq > 0) {
+            const int own = plan_parts(s, z, chunk);
+            parts = (a.prefix_splits == 0 && own == 1) || pre_direct ? -1 : a.prefix_splits + own;
+        }
+        own_of[tid] = parts;
+        len_of[tid] = first;
     }
     __syncthreads();
-    const int n = own_of[lane / G] < 0 ? 0 : a.prefix_splits + own_of[lane / G];  // parts of row R0 + lane
-    const float2* ml = a.part_ml + (long long)h * a.RP + R0 + lane;
+    const int n = max(own_of[lane / G], 0);  // parts of row R0 + lane
+    const int first = len_of[lane / G];
+    const float2* ml = a.part_ml + ((long long)first * a.H + h) * a.RP + R0 + lane;
     const long long ml_step = (long long)a.H * a.RP;
     float M = -INFINITY;
 #pragma unroll 4
@@ -253,7 +272,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttn a, P
     }
     __syncthreads();
     const int pw = warp % PW, dw = warp / PW;
-    const float* src = a.part_o + ((long long)h * kD + d0 + dw * kJoinDims) * a.RP + R0 + lane;
+    const float* src = a.part_o + (((long long)first * a.H + h) * kD + d0 + dw * kJoinDims) * a.RP + R0 + lane;
     const long long step = (long long)a.H * kD * a.RP;
     float W = 0.0f, acc[kJoinDims];
 #pragma unroll
@@ -297,12 +316,12 @@ static cudaError_t launch_join(const PagedAttn& a, const PagedTiles& z, int n_sm
     return launch_pdl(paged_join_kernel<T, 8>, grid(8), block, 0, s, a, z);
 }
 
-static int simt_bytes(int n_req) { return kSimtSmem + (n_req + 1) * 4; }
+static int simt_bytes(int n_req) { return kSimtSmem + plan_ints(n_req) * 4; }
 
 cudaError_t paged_tables_prepare();
 cudaError_t paged_tc_prepare();
 PagedTiles paged_tc_tiles(int P, int G);
-cudaError_t launch_paged_tc(const PagedAttn& a, int n_sm, cudaStream_t s);
+cudaError_t launch_paged_tc(const PagedAttn& a, const PagedTiles& z, int n_sm, cudaStream_t s);
 
 cudaError_t paged_prepare() {
     cudaError_t e = paged_tables_prepare();
@@ -310,7 +329,7 @@ cudaError_t paged_prepare() {
     e = paged_tc_prepare();
     if (e != cudaSuccess) return e;
     return cudaFuncSetAttribute(paged_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                simt_bytes(kPagedMaxRequests));
+                                kSimtSmem + (kPagedMaxRequests + 1) * 4);
 }
 
 // Ranges of the prefix: n_base row blocks x heads, each range a wave's share of
@@ -333,13 +352,14 @@ static int prefix_ranges(long long n_base, int tiles, int limit, int n_sm) {
 
 cudaError_t launch_paged_attn(PagedAttn a, int dtype, long long rows_cap, int n_sm, cudaStream_t s) {
     const bool tc = dtype == ICE_BF16;
-    const PagedTiles z = tc ? paged_tc_tiles(a.P, a.G) : simt_tiles(a.G);
+    PagedTiles z = tc ? paged_tc_tiles(a.P, a.G) : PagedTiles{kSimtKeys, kSimtRows / a.G, kSimtRows / a.G, 0, 0, 0};
+    z.NP = (a.prefix_len + z.KT - 1) / z.KT;
     a.RP = (a.n_tokens * a.G + 31) / 32 * 32;
     const int slots = (int)std::min<long long>(rows_cap / ((long long)a.H * a.RP), kPagedMaxSlots);  // >= 3
     const long long n_base = (long long)((a.n_tokens + z.TB - 1) / z.TB) * a.H;
     a.prefix_splits = 0;
     if (a.prefix_len > 0) {
-        const int tiles = (a.prefix_len + z.KT - 1) / z.KT, limit = std::min(slots / 2, kPagedMaxPrefixSplits);
+        const int tiles = z.NP, limit = std::min(slots / 2, kPagedMaxPrefixSplits);
         const bool twin = a.n_tokens <= z.TD;  // two parts a range
         a.prefix_splits = prefix_ranges(n_base, tiles, twin ? std::max(1, limit / 2) : limit, n_sm);
         if (twin) a.prefix_splits = std::min(std::min(2 * a.prefix_splits, limit), tiles);
@@ -348,9 +368,9 @@ cudaError_t launch_paged_attn(PagedAttn a, int dtype, long long rows_cap, int n_
     a.target_items = n_sm;
     cudaError_t e;
     if (tc)
-        e = launch_paged_tc(a, n_sm, s);
+        e = launch_paged_tc(a, z, n_sm, s);
     else
-        e = launch_pdl(paged_simt_kernel, dim3(n_sm), dim3(kSimtThreads), (size_t)simt_bytes(a.n_req), s, a);
+        e = launch_pdl(paged_simt_kernel, dim3(n_sm), dim3(kSimtThreads), (size_t)simt_bytes(a.n_req), s, a, z);
     if (e != cudaSuccess) return e;
     return tc ? launch_join<__nv_bfloat16>(a, z, n_sm, s) : launch_join<float>(a, z, n_sm, s);
 }

@@ -48,7 +48,7 @@ constexpr int kFaStages = kFaStagesK + kFaStagesV;
 constexpr float kFaSlack = 8.0f;          // growth of the maximum (log2) that is let pass
 
 struct FaShared {
-    unsigned long long q_full[2], q_empty[2], k_full[kFaStagesK], k_empty[kFaStagesK], v_full[kFaStagesV], v_empty[kFaStagesV];
+    unsigned long long q_full[4], q_empty[4], k_full[kFaStagesK], k_empty[kFaStagesK], v_full[kFaStagesV], v_empty[kFaStagesV];
     unsigned long long s_full[2], p_ready[2][2], o_done[2], drain;  // p_ready: portions of a tile's weights
     unsigned long long item_full[2], item_empty[2], item_want;
     unsigned tmem;
@@ -58,7 +58,7 @@ struct FaShared {
 };
 
 __host__ __device__ constexpr int fa_smem(int n_req) {
-    return 1024 + (2 + kFaStages) * kFaTileB + (n_req + 1) * 4;  // with slack for the 1 KB alignment
+    return 1024 + (2 + kFaStages) * kFaTileB + plan_ints(n_req) * 4;  // with slack for the 1 KB alignment
 }
 
 // K-major operand (Q, K), 128-byte swizzle: rows of 128 B, 1024 B between groups of 8.
@@ -227,20 +227,31 @@ __device__ __forceinline__ float2 fa_add2(float2 a, float2 b) {
 // The pages of a key tile as rows of the pool's tensor map, page p in lane p % 32.
 struct FaPages {
     int n, row[4];
-    __device__ __forceinline__ void fetch(const PagedAttn& a, const PagedItem& it, int page0, int ppt, int lane) {
-        n = min(ppt, ceil_div(it.kv_len, a.P) - page0);
+    __device__ __forceinline__ void fetch(const PagedAttn& a, const PagedTiles& z, const PagedStream& st, int x, int lane) {
+        const PagedTile t = tile_of(a, z, st, x);
+        const int page0 = (t.own ? x - z.NP : x) * z.pages;
+        n = min(z.pages, ceil_div(t.len, a.P) - page0);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int p = lane + 32 * u;
             row[u] = (int)(a.n_pages * a.H * a.P);  // past the pool: reads as zeros
             if (p < n) {
-                const int id = it.table[page0 + p];
-                if (id >= 0 && id < a.n_pages) row[u] = (id * a.H + it.h) * a.P;
+                const int id = t.table[page0 + p];
+                if (id >= 0 && id < a.n_pages) row[u] = (id * a.H + st.h) * a.P;
                 else set_status(a.status, ICE_ERR_BOUNDS);
             }
         }
     }
 };
+
+// Query tiles, one a stream: the p-th has slot p % 2. A tile of kFaFew rows or less is read as a
+// box of kFaFew rows; the product reads 128 rows from it on, of which the others do
+// not matter. Two of them in a slot lie 1 KB apart, so that the next item's queries arrive
+// while this one's are in use.
+constexpr int kFaFew = 8;
+__device__ __forceinline__ unsigned fa_q_off(unsigned p, bool few) {
+    return (p & 1) * kFaTileB + (few ? ((p >> 1) & 1) * 1024 : 0);
+}
 
 // The items of a block, read by its warps from a ring of two that warp 11 fills. An item is
 // taken when kFaAhead tiles of the one before are left to copy, not earlier: a block in a
@@ -268,8 +279,8 @@ struct FaItems {
 };
 
 __global__ void __launch_bounds__(kFaThreads, 1)
-    paged_tc_kernel(PagedAttn a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                    const __grid_constant__ CUtensorMap mv, PagedTiles z) {
+    paged_tc_kernel(PagedAttn a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mf,
+                    const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, PagedTiles z) {
     extern __shared__ unsigned char fa_raw[];
     __shared__ __align__(8) FaShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -278,9 +289,13 @@ __global__ void __launch_bounds__(kFaThreads, 1)
     unsigned char* mem = fa_raw + (base - raw0);
     const unsigned s_q = base, s_k = base + 2 * kFaTileB, s_v = s_k + kFaStagesK * kFaTileB;
     int* cum = reinterpret_cast<int*>(mem + (2 + kFaStages) * kFaTileB);
-    const int KT = z.KT, tpt = z.TD;  // keys of a tile, tokens of a row tile
+    const int KT = z.KT;
     if (tid == 0) {
         sh.abort = 0;
+        for (int k = 0; k < 4; ++k) {
+            fa_bar_init(&sh.q_full[k], 1);
+            fa_bar_init(&sh.q_empty[k], 1);
+        }
         for (int k = 0; k < kFaStagesK; ++k) {
             fa_bar_init(&sh.k_full[k], 1);
             fa_bar_init(&sh.k_empty[k], 1);
@@ -290,8 +305,6 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             fa_bar_init(&sh.v_empty[k], 1);
         }
         for (int k = 0; k < 2; ++k) {
-            fa_bar_init(&sh.q_full[k], 1);
-            fa_bar_init(&sh.q_empty[k], 1);
             fa_bar_init(&sh.s_full[k], 1);
             for (int h = 0; h < 2; ++h) fa_bar_init(&sh.p_ready[k][h], 4);
             fa_bar_init(&sh.o_done[k], 1);
@@ -332,46 +345,58 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             const unsigned dst0 = is_k ? s_k : s_v;
             const unsigned long long map = reinterpret_cast<unsigned long long>(is_k ? &mk : &mv);
             unsigned cnt = 0, qcnt = 0;  // key or value tiles and query tiles issued
-            const int ppt = KT / a.P;
+            unsigned last_few = 0;       // bit k: the query tile k + 1 before was of few rows
             while (ok && items.next(sh, it, ok, true)) {
-                const int n = it.n[0] + it.n[1];
+                const int n1 = it.ns == 2 && !it.shared ? it.st[1].n : 0;
+                const int n = it.ns > 0 ? it.st[0].n + n1 : 0;  // tiles to copy
                 if (is_k && n <= kFaAhead && lane == 0) fa_arrive(&sh.item_want);
                 if (n == 0) continue;
-                // the x-th tile in the order of use: two parts take turns
-                const int turns = 2 * min(it.n[0], it.n[1]);
-                auto page_of = [&](int x) {
-                    int t = x;
-                    if (it.n[1] > 0) {
-                        const int j = x < turns ? x >> 1 : x - (turns >> 1);
-                        const bool second = x < turns ? (x & 1) : it.n[1] > it.n[0];
-                        t = second ? it.n[0] + j : j;
-                    }
-                    return (it.kt0 + t) * ppt;
-                };
+                // the x-th tile in the order of use: two lists take turns
+                const int turns = 2 * min(it.st[0].n, n1);
                 FaPages next;  // of the next tile, fetched a tile ahead
-                next.fetch(a, it, page_of(0), ppt, lane);
+                auto fetch = [&](int x) {
+                    int j = x;
+                    bool second = false;
+                    if (n1 > 0) {
+                        j = x < turns ? x >> 1 : x - (turns >> 1);
+                        second = x < turns ? (x & 1) : n1 > it.st[0].n;
+                    }
+                    if (second) next.fetch(a, z, it.st[1], it.st[1].kt0 + j, lane);
+                    else next.fetch(a, z, it.st[0], it.st[0].kt0 + j, lane);
+                };
+                fetch(0);
                 if (is_k) {
-                    const int nt = it.ntok > tpt ? 2 : 1;
-                    for (int t = 0; ok && t < nt; ++t, ++qcnt) {
-                        const unsigned st = qcnt & 1;
-                        ok = __all_sync(0xffffffffu, fa_wait(&sh.q_empty[st], ((qcnt >> 1) & 1) ^ 1, abort));
+                    for (int t = 0; ok && t < (it.same_q ? 1 : it.ns); ++t) {
+                        const PagedStream st = t ? it.st[1] : it.st[0];
+                        if (st.n == 0) continue;
+                        // free once the tile before in the slot is used up, or the one before that
+                        // where those in between and this one are of few rows
+                        const bool few = st.ntok * a.G <= kFaFew;
+                        const unsigned back = few && (last_few & 2) ? 4 : 2;
+                        if (qcnt >= back) {
+                            const unsigned w = qcnt - back;
+                            ok = __all_sync(0xffffffffu, fa_wait(&sh.q_empty[w & 3], (w >> 2) & 1, abort));
+                        }
                         if (ok && fa_elect()) {
-                            fa_expect(&sh.q_full[st], kFaTileB);
+                            unsigned long long* bar = &sh.q_full[qcnt & 3];
+                            fa_expect(bar, few ? kFaFew * kD * 2 : kFaTileB);
                             for (int h = 0; h < 2; ++h)
                                 asm volatile(
                                     "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-                                        s_q + st * kFaTileB + h * kFaHalfB),
-                                    "l"(reinterpret_cast<unsigned long long>(&mq)), "r"(h * 64), "r"(it.h * a.G),
-                                    "r"(it.tok0 + t * tpt), "r"(smem_u32(&sh.q_full[st]))
+                                        s_q + fa_q_off(qcnt, few) + h * kFaHalfB),
+                                    "l"(few ? reinterpret_cast<unsigned long long>(&mf) : reinterpret_cast<unsigned long long>(&mq)),
+                                    "r"(h * 64), "r"(st.h * a.G), "r"(st.tok0), "r"(smem_u32(bar))
                                     : "memory");
                         }
                         __syncwarp();
+                        ++qcnt;
+                        last_few = (last_few << 1) | (few ? 1 : 0);
                     }
                     if (!ok) break;
                 }
                 for (int x = 0; x < n; ++x) {
                     const FaPages cur = next;
-                    if (x + 1 < n) next.fetch(a, it, page_of(x + 1), ppt, lane);
+                    if (x + 1 < n) fetch(x + 1);
                     if (is_k && n > kFaAhead && x == n - kFaAhead && lane == 0) fa_arrive(&sh.item_want);
                     const unsigned st = cnt % stages;
                     ok = __all_sync(0xffffffffu, fa_wait(&empty[st], ((cnt / stages) & 1) ^ 1, abort));
@@ -398,15 +423,15 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             // copies in flight land (bounded) before the block ends, whatever ended the loop
             if (lane == 0) {
                 if (!ok) set_status(a.status, ICE_ERR_TIMEOUT);
-                for (unsigned k = qcnt > 2 ? qcnt - 2 : 0; k < qcnt; ++k)
-                    mbar_wait_bounded(smem_u32(&sh.q_full[k & 1]), (k >> 1) & 1);
+                for (unsigned k = qcnt > 4 ? qcnt - 4 : 0; k < qcnt; ++k)
+                    mbar_wait_bounded(smem_u32(&sh.q_full[k & 3]), (k >> 2) & 1);
                 for (unsigned k = cnt > (unsigned)stages ? cnt - stages : 0; k < cnt; ++k)
                     mbar_wait_bounded(smem_u32(&full[k % stages]), (k / stages) & 1);
             }
         } else if (warp == 11) {
             // ---- items: the block's first is its own number, the others are handed out ----
             if (fa_elect()) {
-                const int n_items = sh.plan.ok ? item_count(a, z, sh.plan) : 0;
+                const int n_items = sh.plan.ok ? sh.plan.pre + sh.plan.own : 0;
                 int i = blockIdx.x;
                 for (unsigned c = 0;; ++c) {
                     const unsigned k = c & 1;
@@ -426,64 +451,63 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             __syncwarp();
         } else if (fa_elect()) {
             // ---- matrix products (one thread of warp 9) ----
-            unsigned kn = 0, vn = 0, qn = 0, pn[2] = {0, 0};
+            unsigned kn = 0, vn = 0, qn = 0, pn0 = 0, pn1 = 0;  // tiles used, weights used by stream
             while (ok && items.next(sh, it, ok, false)) {
-                const bool dual = it.parts == 2;  // two key ranges for one row tile; else one for all
-                const int ns = dual || it.ntok > tpt ? 2 : 1;
-                const int n_s[2] = {it.n[0], ns == 1 ? 0 : dual ? it.n[1] : it.n[0]};
-                const int n = max(n_s[0], n_s[1]);
+                const int ns = it.ns, n0 = ns > 0 ? it.st[0].n : 0, n1 = ns > 1 ? it.st[1].n : 0;
+                const int n = max(n0, n1);
                 if (n == 0) continue;
-                const int nq = it.ntok > tpt ? 2 : 1;  // query tiles; two parts share one
-                for (int t = 0; ok && t < nq; ++t) ok = fa_wait(&sh.q_full[(qn + t) & 1], ((qn + t) >> 1) & 1, abort);
-                auto q_done = [&]() {
-                    for (int t = 0; t < nq; ++t) fa_commit(&sh.q_empty[(qn + t) & 1]);
-                };
-                // scores of stream s against the next key tile; one tile serves both streams
-                // unless they have a range each
-                auto scores = [&](int s) {
-                    const unsigned st = kn % kFaStagesK;
-                    if (dual || s == 0) {
-                        ok = ok && fa_wait(&sh.k_full[st], (kn / kFaStagesK) & 1, abort);
-                        if (!ok) return;
-                        fa_after();
-                    }
-                    fa_mma_s(tmem + 128 * s, s_q + ((qn + (dual ? 0 : s)) & 1) * kFaTileB, s_k + st * kFaTileB);
+                const bool apart = !it.shared;  // each stream has key tiles of its own
+                // query tiles: number, address
+                const unsigned q0 = qn, q1 = it.same_q || n0 == 0 ? qn : qn + 1;
+                const unsigned sq0 = s_q + fa_q_off(q0, it.st[0].ntok * a.G <= kFaFew);
+                const unsigned sq1 = s_q + fa_q_off(q1, it.st[1].ntok * a.G <= kFaFew);
+                qn = n1 > 0 ? q1 + 1 : q0 + 1;
+                // scores of stream s against its next key tile, the j-th
+                auto scores = [&](int s, int j) {
+                    const unsigned st = kn % kFaStagesK, q = s ? q1 : q0;
+                    if (j == 0) ok = ok && fa_wait(&sh.q_full[q & 3], (q >> 2) & 1, abort);
+                    if (apart || s == 0) ok = ok && fa_wait(&sh.k_full[st], (kn / kFaStagesK) & 1, abort);
+                    if (!ok) return;
+                    fa_after();
+                    fa_mma_s(tmem + 128 * s, s ? sq1 : sq0, s_k + st * kFaTileB);
                     fa_commit(&sh.s_full[s]);
-                    if (dual || s == ns - 1) {
+                    if (apart || s == ns - 1) {
                         fa_commit(&sh.k_empty[st]);
                         ++kn;
                     }
+                    // a query tile of both is done with the last scores of the two
+                    if (it.same_q ? j + 1 == n && (s ? n1 >= n0 : n0 > n1) : j + 1 == (s ? n1 : n0))
+                        fa_commit(&sh.q_empty[q & 3]);
                 };
-                for (int s = 0; ok && s < ns; ++s)
-                    if (n_s[s] > 0) scores(s);
-                if (n == 1) q_done();
-                for (int j = 0; ok && j < n; ++j) {
+                if (n0 > 0) scores(0, 0);
+                if (ok && n1 > 0) scores(1, 0);
+                for (int j = 0; ok && j < n; ++j)
                     for (int s = 0; ok && s < ns; ++s) {
-                        if (j >= n_s[s]) continue;
+                        const int ne = s ? n1 : n0;
+                        if (j >= ne) continue;
                         const unsigned st = vn % kFaStagesV;
-                        if (dual || s == 0) ok = fa_wait(&sh.v_full[st], (vn / kFaStagesV) & 1, abort);
+                        if (apart || s == 0) ok = fa_wait(&sh.v_full[st], (vn / kFaStagesV) & 1, abort);
                         // the weights come in two portions: the first one's products run
                         // while the second is made
                         const unsigned t_p = tmem + 128 * s, t_o = t_p + 256, sv = s_v + st * kFaTileB;
-                        ok = ok && fa_wait(&sh.p_ready[s][0], pn[s] & 1, abort);
+                        const unsigned np = s ? pn1 : pn0;
+                        ok = ok && fa_wait(&sh.p_ready[s][0], np & 1, abort);
                         if (!ok) break;
                         fa_after();
                         fa_mma_o<0>(t_o, t_p, sv, j > 0);
-                        ok = fa_wait(&sh.p_ready[s][1], pn[s] & 1, abort);
+                        ok = fa_wait(&sh.p_ready[s][1], np & 1, abort);
                         if (!ok) break;
                         fa_after();
                         fa_mma_o<1>(t_o, t_p, sv, true);
-                        ++pn[s];
-                        if (j + 1 == n_s[s]) fa_commit(&sh.o_done[s]);
-                        if (dual || s == ns - 1) {
+                        if (s) ++pn1;
+                        else ++pn0;
+                        if (j + 1 == ne) fa_commit(&sh.o_done[s]);
+                        if (apart || s == ns - 1) {
                             fa_commit(&sh.v_empty[st]);
                             ++vn;
                         }
-                        if (j + 1 < n_s[s]) scores(s);
+                        if (j + 1 < ne) scores(s, j + 1);
                     }
-                    if (j + 2 == n) q_done();  // the last scores are issued
-                }
-                qn += nq;
             }
             // products in flight end (bounded) before the tensor memory is given back
             if (!ok) set_status(a.status, ICE_ERR_TIMEOUT);
@@ -501,32 +525,31 @@ __global__ void __launch_bounds__(kFaThreads, 1)
         const int valid_tok = a.q_start[a.n_req];
         unsigned sn = 0, on = 0, vn = 0;
         while (ok && items.next(sh, it, ok, true)) {
-            const bool dual = it.parts == 2;
-            const int n0 = it.n[0], n1 = it.n[1];
-            const int n = dual && s ? n1 : n0, kt0 = it.kt0 + (dual && s ? n0 : 0);
-            const int tok0 = it.tok0 + (dual ? 0 : s * tpt);
-            // rows of this stream; none where the item has one row tile and one part
-            const int nrow = s && !dual && it.ntok <= tpt ? 0 : min(tpt, it.ntok - (tok0 - it.tok0)) * a.G;
+            if (it.ns == 0) continue;
+            const bool apart = !it.shared;
+            const int n0 = it.st[0].n, n1 = it.ns > 1 ? it.st[1].n : 0;
             const unsigned vn0 = vn;
-            vn += dual ? n0 + n1 : n0;
-            if (nrow <= 0) continue;
+            vn += apart ? n0 + n1 : n0;
+            if (s >= it.ns) continue;
+            const PagedStream st = s ? it.st[1] : it.st[0];
+            const int n = st.n, nrow = st.ntok * a.G;
             const bool busy = 32 * wq < nrow;  // a warp without rows only keeps the barriers going
-            const int tok = tok0 + row / a.G;
-            const int lim = min(it.kv_len, tok + it.lim_off);
-            // keys that every row of the warp sees (the first row sees the fewest)
-            const int lim_all = min(it.kv_len, tok0 + 32 * wq / a.G + it.lim_off);
+            const int tok = st.tok0 + row / a.G;
+            // own tokens that the row sees, and that every row of the warp sees (the first sees the fewest)
+            const int lim = min(st.own_len, tok + st.lim_off);
+            const int lim_all = min(st.own_len, st.tok0 + 32 * wq / a.G + st.lim_off);
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; j < n; ++j) {
                 ok = __all_sync(0xffffffffu, fa_wait(&sh.s_full[s], sn & 1, abort));
                 if (!ok) break;
                 ++sn;
-                const int key0 = (kt0 + j) * KT;
-                if (key0 + KT > it.kv_len) {  // the last tile of the list: rows behind the last key
-                    const unsigned v = vn0 + (!dual ? j : s ? j + min(n0, j + 1) : j + min(n1, j)), st = v % kFaStagesV;
-                    ok = __all_sync(0xffffffffu, fa_wait(&sh.v_full[st], (v / kFaStagesV) & 1, abort));
+                const PagedTile t = tile_of(a, z, st, st.kt0 + j);
+                if (t.key0 + KT > t.len) {  // the last tile of a list: rows behind the last key
+                    const unsigned v = vn0 + (!apart ? j : s ? j + min(n0, j + 1) : j + min(n1, j)), vs = v % kFaStagesV;
+                    ok = __all_sync(0xffffffffu, fa_wait(&sh.v_full[vs], (v / kFaStagesV) & 1, abort));
                     if (!ok) break;
-                    const int r0 = it.kv_len - key0;
-                    unsigned char* v_st = mem + (2 + kFaStagesK + st) * kFaTileB;
+                    const int r0 = t.len - t.key0;
+                    unsigned char* v_st = mem + (2 + kFaStagesK + vs) * kFaTileB;
                     for (int x = row; x < (KT - r0) * 16; x += kFaRows)
                         *reinterpret_cast<uint4*>(v_st + ((x >> 3) & 1) * kFaHalfB + (r0 + (x >> 4)) * 128 + (x & 7) * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
@@ -544,8 +567,9 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 fa_wait_ld();
                 fa_ld(t_s + 64, v[2]);
                 fa_ld(t_s + 96, v[3]);
-                const bool cut = key0 + kFaKeys > lim_all || KT < kFaKeys;  // some key is hidden from some row
-                const int c_lim = min(lim - key0, KT);
+                // some key is hidden from some row
+                const bool cut = t.key0 + kFaKeys > (t.own ? lim_all : t.len) || KT < kFaKeys;
+                const int c_lim = min((t.own ? lim : t.len) - t.key0, KT);
                 float mx[4];
                 auto max_of = [&](int k) {
                     if (cut) {
@@ -615,8 +639,8 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             fa_after();
             const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
             const bool mine = row < nrow;
-            const long long part = (long long)(it.slot + (dual ? s : 0)) * a.H + it.h;
-            const int R = tok0 * a.G + row;
+            const long long part = (long long)st.slot * a.H + st.h;
+            const int R = st.tok0 * a.G + row;
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) {
                 unsigned u[32];
@@ -628,10 +652,10 @@ __global__ void __launch_bounds__(kFaThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 32; ++c)  // O was not written where n = 0
                     o[c] = n > 0 && l != 0.0f ? __uint_as_float(u[c]) * inv : 0.0f;
-                if (mine && it.direct) {
+                if (mine && st.direct) {
                     if (tok < valid_tok) {
                         uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)a.out +
-                                                              ((long long)tok * a.H * a.G + it.h * a.G + row % a.G) * kD + 32 * k);
+                                                              ((long long)tok * a.H * a.G + st.h * a.G + row % a.G) * kD + 32 * k);
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
                             dst[c] = make_uint4(fa_pack(o[8 * c], o[8 * c + 1]), fa_pack(o[8 * c + 2], o[8 * c + 3]),
@@ -643,7 +667,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                     for (int c = 0; c < 32; ++c) dst[(long long)c * a.RP] = o[c];
                 }
             }
-            if (mine && !it.direct) a.part_ml[part * a.RP + R] = make_float2(m, l);
+            if (mine && !st.direct) a.part_ml[part * a.RP + R] = make_float2(m, l);
             fa_before();
         }
     }
@@ -689,24 +713,25 @@ static bool fa_map(CUtensorMap* m, const void* p, int rank, const cuuint64_t* di
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-PagedTiles paged_tc_tiles(int P, int G) { return {kFaKeys / P * P, 2 * kFaRows / G, kFaRows / G}; }
+PagedTiles paged_tc_tiles(int P, int G) { return {kFaKeys / P * P, 2 * kFaRows / G, kFaRows / G, kFaRows / G, 0, kFaKeys / P}; }
 
-cudaError_t launch_paged_tc(const PagedAttn& a, int n_sm, cudaStream_t s) {
-    CUtensorMap mq, mk, mv;
+cudaError_t launch_paged_tc(const PagedAttn& a, const PagedTiles& z, int n_sm, cudaStream_t s) {
+    CUtensorMap mq, mf, mk, mv;
     const cuuint64_t qd[3] = {kD, (cuuint64_t)(a.H * a.G), (cuuint64_t)a.n_tokens};
     const cuuint64_t qs[2] = {kD * 2, (cuuint64_t)a.q_stride * 2};
     const cuuint32_t qb[3] = {64, (cuuint32_t)a.G, (cuuint32_t)(kFaRows / a.G)};
+    const cuuint32_t fb[3] = {64, (cuuint32_t)a.G, (cuuint32_t)(kFaFew / a.G)};
     const cuuint64_t kd[2] = {kD, (cuuint64_t)(a.n_pages * a.H * a.P)};
     const cuuint64_t ks[1] = {kD * 2};
     const cuuint32_t kb[2] = {64, (cuuint32_t)a.P};
-    if (!fa_map(&mq, a.q, 3, qd, qs, qb) || !fa_map(&mk, a.k_pages, 2, kd, ks, kb) || !fa_map(&mv, a.v_pages, 2, kd, ks, kb))
+    if (!fa_map(&mq, a.q, 3, qd, qs, qb) || !fa_map(&mf, a.q, 3, qd, qs, fb) || !fa_map(&mk, a.k_pages, 2, kd, ks, kb) || !fa_map(&mv, a.v_pages, 2, kd, ks, kb))
         return cudaErrorNotSupported;
-    return launch_pdl(paged_tc_kernel, dim3(n_sm), dim3(kFaThreads), (size_t)fa_smem(a.n_req), s, a, mq, mk, mv,
-                      paged_tc_tiles(a.P, a.G));
+    return launch_pdl(paged_tc_kernel, dim3(n_sm), dim3(kFaThreads), (size_t)fa_smem(a.n_req), s, a, mq, mf, mk, mv, z);
 }
 
 cudaError_t paged_tc_prepare() {
-    return cudaFuncSetAttribute(paged_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, fa_smem(kPagedMaxRequests));
+    return cudaFuncSetAttribute(paged_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                1024 + (2 + kFaStages) * kFaTileB + (kPagedMaxRequests + 1) * 4);
 }
 
 }  // namespace ice
