@@ -61,16 +61,13 @@ __host__ __device__ constexpr int fa_smem(int n_req) {
     return 1024 + (2 + kFaStages) * kFaTileB + plan_ints(n_req) * 4;  // with slack for the 1 KB alignment
 }
 
-// K-major operand (Q, K), 128-byte swizzle: rows of 128 B, 1024 B between groups of 8.
-__device__ __forceinline__ unsigned long long fa_desc_k(unsigned saddr) {
-    return (unsigned long long)((saddr & 0x3FFFFu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
-// N-major operand (V): 64 dimensions are a row of 128 B, kFaHalfB between the two
-// halves (leading offset), 1024 B between groups of 8 keys (stride offset).
-__device__ __forceinline__ unsigned long long fa_desc_v(unsigned saddr) {
-    return (unsigned long long)((saddr & 0x3FFFFu) >> 4) | ((unsigned long long)(kFaHalfB >> 4) << 16) | (64ull << 32) |
-           (1ull << 46) | (2ull << 61);
-}
+// Shared-memory operand descriptors, 128-byte swizzle: the upper words are constants (1024 B
+// between groups of 8 rows, the fixed bit 46, the swizzle), the lower word holds the address / 16
+// and the leading offset / 16. K-major (Q, K: rows of 128 B): unused, 1. N-major (V: 64
+// dimensions are a row of 128 B): kFaHalfB between the two halves.
+#define FA_DESC_HI "0x40004040"
+__device__ __forceinline__ unsigned fa_desc_k(unsigned saddr) { return (saddr >> 4) | (1u << 16); }
+__device__ __forceinline__ unsigned fa_desc_v(unsigned saddr) { return (saddr >> 4) | ((unsigned)(kFaHalfB >> 4) << 16); }
 // fp32 accumulator, bf16 A and B, M = N = 128; bit 16: B is N-major.
 constexpr unsigned kFaIdescS = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 constexpr unsigned kFaIdescO = kFaIdescS | (1u << 16);
@@ -127,30 +124,64 @@ __device__ __forceinline__ bool fa_elect() {
     return one != 0;
 }
 
-// S = Q K^T of one row tile: 8 steps of 16 dimensions, 32 B along the swizzled rows.
+// S = Q K^T of one row tile: 8 steps of 16 dimensions, 32 B along the swizzled rows, the second
+// 64 dimensions half a tile on. One statement, so that the operands become warp-wide registers
+// once and not at each product.
 __device__ __forceinline__ void fa_mma_s(unsigned tmem, unsigned sq, unsigned sk) {
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks) {
-        const unsigned off = (unsigned)((ks >> 2) * kFaHalfB + (ks & 3) * 32);
-        asm volatile(
-            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem),
-            "l"(fa_desc_k(sq + off)), "l"(fa_desc_k(sk + off)), "r"(kFaIdescS), "r"(ks > 0 ? 1u : 0u)
-            : "memory");
-    }
+    static_assert(kFaHalfB == 16384, "the offsets below");
+    asm volatile(
+        "{\n .reg .pred n, p;\n .reg .b32 q, k;\n .reg .b64 dq, dk;\n setp.ne.b32 n, 0, 0;\n setp.eq.b32 p, 0, 0;\n"
+        " add.u32 q, %1, 0;\n add.u32 k, %2, 0;\n mov.b64 dq, {q, " FA_DESC_HI "};\n mov.b64 dk, {k, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], dq, dk, %3, n;\n"
+        " add.u32 q, %1, 2;\n add.u32 k, %2, 2;\n mov.b64 dq, {q, " FA_DESC_HI "};\n mov.b64 dk, {k, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], dq, dk, %3, p;\n"
+        " add.u32 q, %1, 4;\n add.u32 k, %2, 4;\n mov.b64 dq, {q, " FA_DESC_HI "};\n mov.b64 dk, {k, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], dq, dk, %3, p;\n"
+        " add.u32 q, %1, 6;\n add.u32 k, %2, 6;\n mov.b64 dq, {q, " FA_DESC_HI "};\n mov.b64 dk, {k, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], dq, dk, %3, p;\n"
+        " add.u32 q, %1, 1024;\n add.u32 k, %2, 1024;\n mov.b64 dq, {q, " FA_DESC_HI "};\n mov.b64 dk, {k, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], dq, dk, %3, p;\n"
+        " add.u32 q, %1, 1026;\n add.u32 k, %2, 1026;\n mov.b64 dq, {q, " FA_DESC_HI "};\n mov.b64 dk, {k, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], dq, dk, %3, p;\n"
+        " add.u32 q, %1, 1028;\n add.u32 k, %2, 1028;\n mov.b64 dq, {q, " FA_DESC_HI "};\n mov.b64 dk, {k, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], dq, dk, %3, p;\n"
+        " add.u32 q, %1, 1030;\n add.u32 k, %2, 1030;\n mov.b64 dq, {q, " FA_DESC_HI "};\n mov.b64 dk, {k, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], dq, dk, %3, p;\n"
+        "}\n" ::"r"(tmem),
+        "r"(fa_desc_k(sq)), "r"(fa_desc_k(sk)), "r"(kFaIdescS)
+        : "memory");
 }
-// O (+)= P V over a portion of a key tile, keys 0 .. 95 or 96 .. 127: steps of 16 keys, each 8
-// columns of packed weights and 2048 B of V rows.
-template <int PORTION>
-__device__ __forceinline__ void fa_mma_o(unsigned tmem_o, unsigned tmem_p, unsigned sv, bool add) {
-#pragma unroll
-    for (int ks = PORTION ? 6 : 0; ks < (PORTION ? 8 : 6); ++ks) {
-        asm volatile(
-            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_o),
-            "r"(tmem_p + 8 * ks), "l"(fa_desc_v(sv + 2048 * ks)), "r"(kFaIdescO), "r"(add || ks > 0 ? 1u : 0u)
-            : "memory");
-    }
+// O (+)= P V over keys 0 .. 95 and 96 .. 127 of a tile: steps of 16 keys, each 8 columns of packed
+// weights and 2048 B of V rows.
+__device__ __forceinline__ void fa_mma_o_first(unsigned tmem_o, unsigned tmem_p, unsigned sv, bool add) {
+    asm volatile(
+        "{\n .reg .pred n, p;\n .reg .b32 v, w;\n .reg .b64 dv;\n setp.ne.b32 n, %4, 0;\n setp.eq.b32 p, 0, 0;\n"
+        " add.u32 v, %2, 0;\n add.u32 w, %1, 0;\n mov.b64 dv, {v, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [w], dv, %3, n;\n"
+        " add.u32 v, %2, 128;\n add.u32 w, %1, 8;\n mov.b64 dv, {v, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [w], dv, %3, p;\n"
+        " add.u32 v, %2, 256;\n add.u32 w, %1, 16;\n mov.b64 dv, {v, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [w], dv, %3, p;\n"
+        " add.u32 v, %2, 384;\n add.u32 w, %1, 24;\n mov.b64 dv, {v, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [w], dv, %3, p;\n"
+        " add.u32 v, %2, 512;\n add.u32 w, %1, 32;\n mov.b64 dv, {v, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [w], dv, %3, p;\n"
+        " add.u32 v, %2, 640;\n add.u32 w, %1, 40;\n mov.b64 dv, {v, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [w], dv, %3, p;\n"
+        "}\n" ::"r"(tmem_o),
+        "r"(tmem_p), "r"(fa_desc_v(sv)), "r"(kFaIdescO), "r"(add ? 1u : 0u)
+        : "memory");
+}
+__device__ __forceinline__ void fa_mma_o_rest(unsigned tmem_o, unsigned tmem_p, unsigned sv, bool add) {
+    asm volatile(
+        "{\n .reg .pred n, p;\n .reg .b32 v, w;\n .reg .b64 dv;\n setp.ne.b32 n, %4, 0;\n setp.eq.b32 p, 0, 0;\n"
+        " add.u32 v, %2, 768;\n add.u32 w, %1, 48;\n mov.b64 dv, {v, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [w], dv, %3, n;\n"
+        " add.u32 v, %2, 896;\n add.u32 w, %1, 56;\n mov.b64 dv, {v, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [w], dv, %3, p;\n"
+        "}\n" ::"r"(tmem_o),
+        "r"(tmem_p), "r"(fa_desc_v(sv)), "r"(kFaIdescO), "r"(add ? 1u : 0u)
+        : "memory");
 }
 
 // N columns of the warp's 32 lanes of tensor memory, as register bits.
@@ -494,11 +525,11 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                         ok = ok && fa_wait(&sh.p_ready[s][0], np & 1, abort);
                         if (!ok) break;
                         fa_after();
-                        fa_mma_o<0>(t_o, t_p, sv, j > 0);
+                        fa_mma_o_first(t_o, t_p, sv, j > 0);
                         ok = fa_wait(&sh.p_ready[s][1], np & 1, abort);
                         if (!ok) break;
                         fa_after();
-                        fa_mma_o<1>(t_o, t_p, sv, true);
+                        fa_mma_o_rest(t_o, t_p, sv, true);
                         if (s) ++pn1;
                         else ++pn0;
                         if (j + 1 == ne) fa_commit(&sh.o_done[s]);
