@@ -28,10 +28,8 @@ struct PagedAttn {
     const void* k_pages;
     const void* v_pages;
     void* out;
-    // Parts, by slot and KV head; row R = token * G + head in the group, RP = n_tokens * G
-    // rounded up to 32. Rows are innermost: a warp of the attention holds 32 rows, one a
-    // lane, and writes full lines (as [row][d] the stores of an item took 7 us).
-    float* part_o;   // [slot][H][D][RP]: a part's output, normalised
+    // Parts, by slot and KV head; row R = token * G + head in the group, RP = n_tokens * G.
+    float* part_o;   // [slot][H][RP][D]: a part's output, normalised
     float2* part_ml; // [slot][H][RP]: its maximum (log2 units) and sum
     int* plan;       // kPlanWords, written by the attention kernel for the joining kernel
     int* first_long; // [n_req]: number of each request's first row block x head, if it is long
@@ -117,14 +115,13 @@ __device__ __forceinline__ int plan_items(int nq, int s, int H, int g0, const Pa
 }
 
 struct PlanShared {
-    long long w[32];   // per warp: tiles of the own tokens of requests that share the prefix
-    long long wl[32];  // per warp: tiles of the row blocks of long requests
-    int mx[32];        // per warp: most own tiles of a request that shares the prefix
-    int nl[32];        // per warp: row blocks of long requests
-    int fl[32];        // per warp: 1 bad length, 2 a request that shares the prefix, 4 one with own tokens
-    int sum[32];
-    int sum2[32];
-    int ok, chunk, own, pre, direct;  // items of requests, of the prefix
+    // sums over the requests: tiles of the own tokens of requests that share the prefix, tiles and
+    // number of the row blocks of long ones; the most own tiles of one of the former
+    unsigned long long w, wl;
+    unsigned nl, mx;
+    unsigned fl;  // 1 bad length, 2 a request that shares the prefix, 4 one with own tokens
+    int sum[32], sum2[32];                   // per warp: items, row blocks of long requests
+    int ok, chunk, own, pre, direct;         // items of requests, of the prefix
     int some_long;
     PagedLong f;
     const int *q_start, *seq_len;            // in shared memory where they fit
@@ -137,20 +134,38 @@ __host__ __device__ constexpr int plan_ints(int n_req) {
     return 4 * (n_req + 1) <= kPagedMaxRequests + 1 ? 4 * (n_req + 1) : n_req + 1;
 }
 
+// Sum of the values of the warps before, from their inclusive scan; every thread's exclusive sum.
+__device__ __forceinline__ int block_scan(int mine, int* sums, int& total, int nw) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int inc = mine;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    if (lane == 31) sums[warp] = inc;
+    __syncthreads();
+    const int v = lane < nw ? sums[lane] : 0;
+    total = __reduce_add_sync(0xffffffffu, v);
+    return __reduce_add_sync(0xffffffffu, lane < warp ? v : 0) + inc - mine;
+}
+
 // Fills cum[0 .. n_req] (items before each request) and sh; all threads of the block call
-// it. Block-uniform results after the last barrier.
+// it. Block-uniform results after the last barrier. Every block comes to the same plan (integer
+// sums). Nothing is unrolled: the code runs once, and at the start of a call it comes from memory.
 template <int NT>
 __device__ __forceinline__ void make_plan(const PagedAttn& a, const PagedTiles& z, int* cum, PlanShared& sh) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
     constexpr int NW = NT / 32;
     const int n = a.n_req, per = (n + NT - 1) / NT;
     const int r0 = min(tid * per, n), r1 = min(r0 + per, n);
-    const long long cap = (long long)a.max_blocks * a.P;
-    const int NP = z.NP;
     const bool keep = plan_ints(n) > n + 1;
     int *qs = cum + n + 1, *sl = qs + n + 1, *gl = sl + n + 1;
-    long long w = 0, wl = 0;
-    int mx = 0, nl = 0, fl = 0;
+    if (tid == 0) sh.w = sh.wl = 0, sh.nl = sh.mx = sh.fl = 0;
+    __syncthreads();
+    unsigned long long w = 0, wl = 0;
+    unsigned mx = 0, nl = 0, fl = 0;
+#pragma unroll 1
     for (int r = r0; r < r1; ++r) {
         const int b = a.q_start[r], e = a.q_start[r + 1], s = a.seq_len[r];
         if (keep) {
@@ -158,57 +173,46 @@ __device__ __forceinline__ void make_plan(const PagedAttn& a, const PagedTiles& 
             sl[r] = s;
             if (r == n - 1) qs[n] = e;
         }
-        if (b < 0 || e < b || e > a.n_tokens || s < 0 || s > cap || (r == 0 && b != 0)) {
+        if (b < 0 || e < b || e > a.n_tokens || s < 0 || s > a.max_blocks * a.P || (r == 0 && b != 0)) {
             fl |= 1;
         } else if (e - b > z.TS) {
             const int blocks = long_blocks(e - b, s, z);
             nl += blocks;
-            wl += (long long)blocks * (NP + ceil_div(s, z.KT));
+            wl += (unsigned long long)blocks * (z.NP + ceil_div(s, z.KT));
         } else if (e > b) {
             fl |= s > 0 ? 6 : 2;
-            const int t = ceil_div(s, z.KT);
+            const unsigned t = ceil_div(s, z.KT);
             w += t;
             mx = max(mx, t);
         }
     }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        w += __shfl_xor_sync(0xffffffffu, w, o);
-        wl += __shfl_xor_sync(0xffffffffu, wl, o);
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        nl += __shfl_xor_sync(0xffffffffu, nl, o);
-        fl |= __shfl_xor_sync(0xffffffffu, fl, o);
-    }
+    if (w) atomicAdd(&sh.w, w);
+    if (wl) atomicAdd(&sh.wl, wl);
+    nl = __reduce_add_sync(0xffffffffu, nl);
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    fl = __reduce_or_sync(0xffffffffu, fl);
     if (lane == 0) {
-        sh.w[warp] = w;
-        sh.wl[warp] = wl;
-        sh.mx[warp] = mx;
-        sh.nl[warp] = nl;
-        sh.fl[warp] = fl;
+        if (nl) atomicAdd(&sh.nl, nl);
+        atomicMax(&sh.mx, mx);
+        atomicOr(&sh.fl, fl);
     }
     __syncthreads();
-    w = 0, wl = 0, mx = 0, nl = 0, fl = 0;
-#pragma unroll
-    for (int k = 0; k < NW; ++k) {
-        w += sh.w[k];
-        wl += sh.wl[k];
-        mx = max(mx, sh.mx[k]);
-        nl += sh.nl[k];
-        fl |= sh.fl[k];
-    }
+    nl = sh.nl, mx = sh.mx, fl = sh.fl;
     const bool bad = fl & 1;
-    long long chunk = min(max((w * a.H + a.target_items - 1) / a.target_items, 1LL), (long long)kPagedMaxRange);
-    chunk = max(chunk, (long long)ceil_div(mx, z.TD > 0 ? a.max_splits / 2 : a.max_splits));
-    const int ch = (int)chunk;
+    const float want = (float)sh.w * (float)a.H / (float)a.target_items;
+    const int chunk = max(max((int)fminf(ceilf(want), (float)kPagedMaxRange), 1),
+                          ceil_div((int)mx, z.TD > 0 ? a.max_splits / 2 : a.max_splits));
     // parts of the last wave's: waves x (tiles of a part + the fixed cost of an item, and of
     // joining it, in tiles), the least of 1 to 16
     // (where the lengths do not fit in shared memory, with thousands of requests, all are whole)
     PagedLong f = {INT_MAX, 1};
     if (nl > 0 && keep) {
-        const int all = nl * a.H, rest = all % a.target_items, mean = (int)(wl / nl);
+        const int all = nl * a.H, rest = all % a.target_items, mean = (int)((float)sh.wl / (float)nl);
         f.whole = all - rest;  // the last `rest` are an incomplete wave
         int best = INT_MAX;
-        for (int k = 1; rest > 0 && k <= min(16, min(a.max_splits, max(mean, 1))); ++k) {
+        const int most = rest > 0 ? min(16, min(a.max_splits, max(mean, 1))) : 0;
+#pragma unroll 1
+        for (int k = 1; k <= most; ++k) {
             const int t = ceil_div(rest * k, a.target_items) * (ceil_div(mean, k) + (k > 1 ? 6 : 3));
             if (t < best) {
                 best = t;
@@ -216,61 +220,37 @@ __device__ __forceinline__ void make_plan(const PagedAttn& a, const PagedTiles& 
             }
         }
     }
-    // long row blocks before each request, then items
-    int lmine = 0, linc;
-    if (!bad && nl > 0)
-        for (int r = r0; r < r1; ++r) lmine += long_blocks(a.q_start[r + 1] - a.q_start[r], a.seq_len[r], z);
-    linc = lmine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, linc, o);
-        if (lane >= o) linc += x;
+    // long row blocks before each thread's requests, then items
+    int g0 = 0, total;
+    if (nl > 0) {
+        int mine = 0;
+#pragma unroll 1
+        for (int r = r0; r < r1 && !bad; ++r) mine += long_blocks(a.q_start[r + 1] - a.q_start[r], a.seq_len[r], z);
+        g0 = block_scan(mine, sh.sum2, total, NW) * a.H;
     }
-    if (lane == 31) sh.sum2[warp] = linc;
-    __syncthreads();
-    int g0 = linc - lmine;
-#pragma unroll
-    for (int k = 0; k < NW; ++k)
-        if (k < warp) g0 += sh.sum2[k];
-    g0 *= a.H;
-    int mine = 0, g = g0;
-    if (!bad)
-        for (int r = r0; r < r1; ++r) {
+    int before = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        int g = g0, mine = 0;
+#pragma unroll 1
+        for (int r = r0; r < r1 && !bad; ++r) {
             const int nq = a.q_start[r + 1] - a.q_start[r], s = a.seq_len[r];
-            mine += plan_items(nq, s, a.H, g, z, ch, f);
-            g += long_blocks(nq, s, z) * a.H;
-        }
-    int inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-    }
-    if (lane == 31) sh.sum[warp] = inc;
-    __syncthreads();
-    int before = inc - mine, total = 0;
-#pragma unroll
-    for (int k = 0; k < NW; ++k) {
-        if (k < warp) before += sh.sum[k];
-        total += sh.sum[k];
-    }
-    if (!bad) {
-        g = g0;
-        for (int r = r0; r < r1; ++r) {
-            const int nq = a.q_start[r + 1] - a.q_start[r], s = a.seq_len[r];
-            cum[r] = before;
-            before += plan_items(nq, s, a.H, g, z, ch, f);
-            if (nl > 0 && keep) {
-                gl[r] = g;
-                if (blockIdx.x == 0) a.first_long[r] = g;  // for the joining kernel
+            if (pass) {
+                cum[r] = before + mine;
+                if (nl > 0 && keep) {
+                    gl[r] = g;
+                    if (blockIdx.x == 0) a.first_long[r] = g;  // for the joining kernel
+                }
             }
+            mine += plan_items(nq, s, a.H, g, z, chunk, f);
             g += long_blocks(nq, s, z) * a.H;
         }
+        if (pass == 0) before = block_scan(mine, sh.sum, total, NW);
     }
     if (tid == 0) {
         cum[n] = total;
         sh.ok = !bad;
-        sh.chunk = ch;
+        sh.chunk = chunk;
         sh.f = f;
         sh.own = total;
         sh.some_long = nl > 0;
@@ -283,7 +263,7 @@ __device__ __forceinline__ void make_plan(const PagedAttn& a, const PagedTiles& 
         sh.first_long = gl;
         if (blockIdx.x == 0) {
             a.plan[kPlanOk] = !bad;
-            a.plan[kPlanChunk] = ch;
+            a.plan[kPlanChunk] = chunk;
             a.plan[kPlanWhole] = f.whole;
             a.plan[kPlanSplit] = f.split;
             a.plan[kPlanDirect] = sh.direct;
@@ -416,7 +396,8 @@ __device__ __forceinline__ void get_item(const PagedAttn& a, const PagedTiles& z
         const int seen = min(s, st.tok0 + st.ntok - 1 + st.lim_off);
         nt = NP - base + (seen > 0 ? ceil_div(seen, z.KT) : 0);
     }
-    auto edge = [&](int p) { return base + (int)((long long)nt * p / parts); };
+    // fits 32 bits: at most 2^25 tiles and 16 parts, or 2^24 and 128
+    auto edge = [&](int p) { return base + (int)((unsigned)nt * (unsigned)p / (unsigned)parts); };
     st.kt0 = edge(p0);
     const int kt1 = edge(p0 + 1);
     st.n = kt1 - st.kt0;

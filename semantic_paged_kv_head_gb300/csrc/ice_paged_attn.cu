@@ -1,6 +1,7 @@
 // Attention of a batch that shares a prefix: the fp32 kernel on the CUDA cores, the joining
 // of the parts, and the choice of the parts.
 #include <algorithm>
+#include <cstring>
 
 #include "ice_paged.cuh"
 
@@ -149,170 +150,144 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(PagedAttn a, P
             }
             __syncwarp();
         }
-        __syncthreads();  // the key tile's memory takes the output, [d][row]
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float sum = l[j];
 #pragma unroll
             for (int d = 8; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            const int r = rg * 4 + j;
+            const int r = rg * 4 + j, tok = it.tok0 + r / a.G;
+            if (r >= nrow || (it.direct && tok >= valid_tok)) continue;
             const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+            const long long R = ((long long)it.slot * a.H + it.h) * a.RP + it.tok0 * a.G + r;
+            float* dst = it.direct ? (float*)a.out + ((long long)tok * a.H * a.G + it.h * a.G + r % a.G) * kD
+                                   : a.part_o + R * kD;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                sK[((k >> 2) * 64 + kg * 4 + (k & 3)) * (kSimtRows + 1) + r] = o[j][k] * inv;
-            if (kg == 0 && r < nrow && !it.direct)
-                a.part_ml[((long long)it.slot * a.H + it.h) * a.RP + it.tok0 * a.G + r] = make_float2(m[j], sum);
-        }
-        __syncthreads();
-        if (it.direct) {
-            for (int x = tid; x < nrow * kD; x += kSimtThreads) {
-                const int r = x / kD, c = x % kD, tok = it.tok0 + r / a.G;
-                if (tok < valid_tok)
-                    ((float*)a.out)[((long long)tok * a.H * a.G + it.h * a.G + r % a.G) * kD + c] =
-                        sK[c * (kSimtRows + 1) + r];
-            }
-        } else {
-            float* dst = a.part_o + ((long long)it.slot * a.H + it.h) * kD * a.RP + it.tok0 * a.G;
-            const int r = tid % kSimtRows;
-            if (r < nrow)
-                for (int c = tid / kSimtRows; c < kD; c += kSimtThreads / kSimtRows)
-                    dst[(long long)c * a.RP + r] = sK[c * (kSimtRows + 1) + r];
+            for (int k = 0; k < 2; ++k)
+                *reinterpret_cast<float4*>(dst + 64 * k + kg * 4) =
+                    make_float4(o[j][4 * k] * inv, o[j][4 * k + 1] * inv, o[j][4 * k + 2] * inv, o[j][4 * k + 3] * inv);
+            if (kg == 0 && !it.direct) a.part_ml[R] = make_float2(m[j], sum);
         }
     }
 }
 
 // ---------------------------------------------------------------------------
-// Joining: a block for 32 rows of a KV head, a lane a row. With parts (m_i, l_i, o_i),
-// M = max m_i and w_i = l_i 2^(m_i - M): out = sum w_i o_i / sum w_i, zeros where
+// Joining: PW warps for a row of a KV head, four dimensions a lane. With parts (m_i, l_i,
+// o_i), M = max m_i and w_i = l_i 2^(m_i - M): out = sum w_i o_i / sum w_i, zeros where
 // nothing was seen. Rows with one part were written by the attention kernel. Bound by the
-// parts' bytes, read once, where there are many rows, and by the latency of a
-// chain of loads where there are few. PW of the 8 warps therefore share the parts of 16
-// dimensions (and the block has 8 / PW groups of 16): one where the rows fill the GPU,
-// eight where a row has many parts and little else runs.
+// parts' bytes, read once, where there are many rows (PW = 1), and by the latency of
+// a chain of loads where there are few: the warps of a row then take every PW-th part.
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
-constexpr int kJoinDims = 16;
+
+template <typename T>
+__device__ __forceinline__ void store4(T* p, float4 v) {
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(p) = v;
+    } else {
+        __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
+        uint2 u;
+        memcpy(&u.x, &x, 4);
+        memcpy(&u.y, &y, 4);
+        *reinterpret_cast<uint2*>(p) = u;
+    }
+}
 
 template <typename T, int PW>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttn a, PagedTiles z) {
-    constexpr int kDims = kJoinDims * (kJoinWarps / PW);  // dimensions of the block
-    __shared__ float wt[kPagedMaxSlots][32];  // weights of the parts, by row
-    __shared__ float tile[PW][32][kDims + 1];
-    __shared__ float red[kJoinWarps][32];
-    __shared__ int req_of[32], blk_of[32];    // request of each token, its row block
-    __shared__ int own_of[32], len_of[32];    // new and own tokens of each token's request, then its parts
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int h = blockIdx.y, R0 = blockIdx.x * 32, d0 = blockIdx.z * kDims, G = a.G;
+    __shared__ float4 red[kJoinWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int group = warp / PW, pw = warp % PW, h = blockIdx.y, G = a.G;
+    const int R = blockIdx.x * (kJoinWarps / PW) + group, tok = R / G;
     // Before the wait: q_start and seq_len were complete when the attention kernel's blocks let
     // this one be scheduled (they wait for the kernels before them first).
-    const int valid_tok = a.q_start[a.n_req];
-    for (int t = warp; t < 32 / G; t += kJoinWarps) {
-        const int tok = R0 / G + t;
-        int nq = -1, own_len = 0;
-        if (tok < valid_tok) {
-            int lo = 0, hi = a.n_req;  // q_start[lo] <= tok < q_start[hi]; 32 probes a step
-            while (hi - lo > 1) {
-                const int w = (hi - lo + 31) / 32, probe = lo + lane * w;
-                const unsigned le =
-                    __ballot_sync(0xffffffffu, probe < hi && a.q_start[min(probe, a.n_req)] <= tok);
-                const int k = 31 - __clz(le);  // lane 0 always holds
-                hi = min(hi, lo + (k + 1) * w);
-                lo = lo + k * w;
-            }
-            nq = a.q_start[lo + 1] - a.q_start[lo];
-            own_len = a.seq_len[lo];
-            if (lane == 0) {
-                req_of[t] = lo;
-                blk_of[t] = (tok - a.q_start[lo]) / z.TB;
-            }
+    int req = 0, nq = -1, own = 0, blk = 0;
+    if (tok < a.q_start[a.n_req]) {
+        int lo = 0, hi = a.n_req;  // q_start[lo] <= tok < q_start[hi]; 32 probes a step
+        while (hi - lo > 1) {
+            const int w = (hi - lo + 31) / 32, probe = lo + lane * w;
+            const unsigned le = __ballot_sync(0xffffffffu, probe < hi && a.q_start[min(probe, a.n_req)] <= tok);
+            const int k = 31 - __clz(le);  // lane 0 always holds
+            hi = min(hi, lo + (k + 1) * w);
+            lo = lo + k * w;
         }
-        if (lane == 0) {
-            own_of[t] = nq;
-            len_of[t] = own_len;
-        }
+        const int b = a.q_start[lo];
+        req = lo, nq = a.q_start[lo + 1] - b, own = a.seq_len[lo], blk = (tok - b) / z.TB;
     }
     pdl_wait_then_release();
     if (!a.plan[kPlanOk]) return;
-    const int chunk = a.plan[kPlanChunk], pre_direct = a.plan[kPlanDirect];
-    const PagedLong f = {a.plan[kPlanWhole], a.plan[kPlanSplit]};
-    __syncthreads();
-    if (tid < 32 / G) {
-        // the parts' first slot and number; none where the attention kernel wrote the output itself
-        const int nq = own_of[tid], s = len_of[tid];
-        int first = 0, parts = -1;
-        if (nq > z.TS) {
-            const int blocks = long_blocks(nq, s, z);
-            first = a.prefix_splits;
-            const bool whole = f.whole == INT_MAX || a.first_long[req_of[tid]] + h * blocks + blk_of[tid] < f.whole;
-            parts = blocks == 0 ? 0 : whole || f.split == 1 ? -1 : f.split;
-        } else if (nq > 0) {
-            const int own = plan_parts(s, z, chunk);
-            parts = (a.prefix_splits == 0 && own == 1) || pre_direct ? -1 : a.prefix_splits + own;
-        }
-        own_of[tid] = parts;
-        len_of[tid] = first;
+    int parts = -1, first = 0;  // -1: nothing to write
+    if (nq > z.TS) {
+        const PagedLong f = {a.plan[kPlanWhole], a.plan[kPlanSplit]};
+        const int blocks = long_blocks(nq, own, z);
+        first = a.prefix_splits;
+        const bool whole = f.whole == INT_MAX || a.first_long[req] + h * blocks + blk < f.whole;
+        parts = blocks == 0 ? 0 : whole || f.split == 1 ? -1 : f.split;
+    } else if (nq > 0) {
+        const int n = plan_parts(own, z, a.plan[kPlanChunk]);
+        parts = (a.prefix_splits == 0 && n == 1) || a.plan[kPlanDirect] ? -1 : a.prefix_splits + n;
     }
-    __syncthreads();
-    const int n = max(own_of[lane / G], 0);  // parts of row R0 + lane
-    const int first = len_of[lane / G];
-    const float2* ml = a.part_ml + ((long long)first * a.H + h) * a.RP + R0 + lane;
-    const long long ml_step = (long long)a.H * a.RP;
-    float M = -INFINITY;
-#pragma unroll 4
-    for (int p = warp; p < n; p += kJoinWarps) M = fmaxf(M, ml[p * ml_step].x);
-    red[warp][lane] = M;
-    __syncthreads();
+    if (PW == 1 && parts < 0) return;
+    const long long step = (long long)a.H * a.RP, row = (long long)first * step + (long long)h * a.RP + R;
+    float2 ml[kPagedMaxSlots / 32];  // lane p: parts p, p + 32, ...
+    float M = -INFINITY, W = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kJoinWarps; ++k) M = fmaxf(M, red[k][lane]);
+    for (int k = 0; k < kPagedMaxSlots / 32; ++k) {
+        const int p = lane + 32 * k;
+        ml[k] = p < parts ? a.part_ml[row + p * step] : make_float2(-INFINITY, 0.0f);
+        M = fmaxf(M, ml[k].x);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     if (M == -INFINITY) M = 0.0f;
-    for (int p = warp; p < n; p += kJoinWarps) {
-        const float2 x = ml[p * ml_step];
-        wt[p][lane] = x.y * exp2_approx(x.x - M);
-    }
-    __syncthreads();
-    const int pw = warp % PW, dw = warp / PW;
-    const float* src = a.part_o + (((long long)first * a.H + h) * kD + d0 + dw * kJoinDims) * a.RP + R0 + lane;
-    const long long step = (long long)a.H * kD * a.RP;
-    float W = 0.0f, acc[kJoinDims];
 #pragma unroll
-    for (int k = 0; k < kJoinDims; ++k) acc[k] = 0.0f;
-#pragma unroll 2
-    for (int p = pw; p < n; p += PW) {
-        const float w = wt[p][lane];
-        W += w;
-#pragma unroll
-        for (int k = 0; k < kJoinDims; ++k) acc[k] = fmaf(w, src[p * step + (long long)k * a.RP], acc[k]);
+    for (int k = 0; k < kPagedMaxSlots / 32; ++k) {
+        ml[k].y *= exp2_approx(ml[k].x - M);
+        W += ml[k].y;
     }
-    if (PW > 1) {  // the whole sum of weights
-        red[warp][lane] = W;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
+    const float4* src = reinterpret_cast<const float4*>(a.part_o + row * kD) + lane;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < kPagedMaxSlots / 32; ++k) {
+        const int end = min(parts - 32 * k, 32);
+#pragma unroll 4
+        for (int p = pw; p < end; p += PW) {
+            const float w = __shfl_sync(0xffffffffu, ml[k].y, p);
+            const float4 v = src[(32 * k + p) * step * (kD / 4)];
+            acc.x = fmaf(w, v.x, acc.x);
+            acc.y = fmaf(w, v.y, acc.y);
+            acc.z = fmaf(w, v.z, acc.z);
+            acc.w = fmaf(w, v.w, acc.w);
+        }
+    }
+    if (PW > 1) {
+        red[warp][lane] = acc;
         __syncthreads();
-        W = 0.0f;
+        if (pw > 0 || parts < 0) return;
 #pragma unroll
-        for (int k = 0; k < PW; ++k) W += red[dw * PW + k][lane];
+        for (int k = 1; k < PW; ++k) {
+            const float4 v = red[warp + k][lane];
+            acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+        }
     }
     const float inv = W > 0.0f ? 1.0f / W : (W == 0.0f ? 0.0f : W);
-#pragma unroll
-    for (int k = 0; k < kJoinDims; ++k) tile[pw][lane][dw * kJoinDims + k] = acc[k] * inv;
-    __syncthreads();
-    for (int x = tid; x < 32 * kDims; x += kJoinThreads) {
-        const int r = x / kDims, c = x % kDims;
-        if (own_of[r / G] < 0) continue;
-        float v = 0.0f;
-#pragma unroll
-        for (int k = 0; k < PW; ++k) v += tile[k][r][c];
-        ((T*)a.out)[((long long)((R0 + r) / G) * a.H * G + h * G + (R0 + r) % G) * kD + d0 + c] = from_f<T>(v);
-    }
+    store4<T>((T*)a.out + ((long long)tok * a.H * G + h * G + R % G) * kD + lane * 4,
+              make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
 }
 
 template <typename T>
 static cudaError_t launch_join(const PagedAttn& a, const PagedTiles& z, int n_sm, cudaStream_t s) {
-    // warps that share a row's parts: as many as leave the blocks near two a SM
-    const long long groups = (long long)(a.RP / 32) * a.H;
+    // warps that share a row's parts: as many as bring the warps near 32 a SM
+    const long long rows = (long long)a.RP * a.H;
     const dim3 block(kJoinThreads);
-    auto grid = [&](int pw) { return dim3((unsigned)(a.RP / 32), (unsigned)a.H, (unsigned)pw); };
-    if (groups >= 2 * n_sm) return launch_pdl(paged_join_kernel<T, 1>, grid(1), block, 0, s, a, z);
-    if (groups >= n_sm / 2) return launch_pdl(paged_join_kernel<T, 4>, grid(4), block, 0, s, a, z);
+    auto grid = [&](int pw) {
+        const int per = kJoinWarps / pw;
+        return dim3((unsigned)((a.RP + per - 1) / per), (unsigned)a.H);
+    };
+    if (rows >= 16 * n_sm) return launch_pdl(paged_join_kernel<T, 1>, grid(1), block, 0, s, a, z);
+    if (rows >= 4 * n_sm) return launch_pdl(paged_join_kernel<T, 4>, grid(4), block, 0, s, a, z);
     return launch_pdl(paged_join_kernel<T, 8>, grid(8), block, 0, s, a, z);
 }
 
@@ -354,7 +329,7 @@ cudaError_t launch_paged_attn(PagedAttn a, int dtype, long long rows_cap, int n_
     const bool tc = dtype == ICE_BF16;
     PagedTiles z = tc ? paged_tc_tiles(a.P, a.G) : PagedTiles{kSimtKeys, kSimtRows / a.G, kSimtRows / a.G, 0, 0, 0};
     z.NP = (a.prefix_len + z.KT - 1) / z.KT;
-    a.RP = (a.n_tokens * a.G + 31) / 32 * 32;
+    a.RP = a.n_tokens * a.G;
     const int slots = (int)std::min<long long>(rows_cap / ((long long)a.H * a.RP), kPagedMaxSlots);  // >= 3
     const long long n_base = (long long)((a.n_tokens + z.TB - 1) / z.TB) * a.H;
     a.prefix_splits = 0;

@@ -93,8 +93,7 @@ __device__ __forceinline__ bool fa_try(unsigned bar, unsigned parity) {
 // Waits for phase `parity`, at most kWaitNs; false if it ran out here or elsewhere in the block
 // (then every role leaves its loop). The wall clock is slow to read (a handover between
 // warps would wait for it), so it is read every 64th try only.
-__device__ __forceinline__ bool fa_wait(unsigned long long* b, unsigned parity, volatile int* abort) {
-    const unsigned bar = smem_u32(b);
+__device__ __forceinline__ bool fa_wait_long(unsigned bar, unsigned parity, volatile int* abort) {
     unsigned long long t0 = 0;
     for (unsigned k = 1;; ++k) {
         if (fa_try(bar, parity)) return true;
@@ -107,6 +106,9 @@ __device__ __forceinline__ bool fa_wait(unsigned long long* b, unsigned parity, 
             return false;
         }
     }
+}
+__device__ __forceinline__ bool fa_wait(unsigned long long* b, unsigned parity, volatile int* abort) {
+    return fa_try(smem_u32(b), parity) || fa_wait_long(smem_u32(b), parity, abort);
 }
 __device__ __forceinline__ void fa_commit(unsigned long long* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -258,17 +260,19 @@ __device__ __forceinline__ float2 fa_add2(float2 a, float2 b) {
 // The pages of a key tile as rows of the pool's tensor map, page p in lane p % 32.
 struct FaPages {
     int n, row[4];
-    __device__ __forceinline__ void fetch(const PagedAttn& a, const PagedTiles& z, const PagedStream& st, int x, int lane) {
-        const PagedTile t = tile_of(a, z, st, x);
-        const int page0 = (t.own ? x - z.NP : x) * z.pages;
-        n = min(z.pages, ceil_div(t.len, a.P) - page0);
+    __device__ __forceinline__ void fetch(const PagedAttn& a, const PagedTiles& z, const int* own_table, int own_len,
+                                          int head, int x, int lane) {
+        const bool own = x >= z.NP;
+        const int* table = own ? own_table : a.prefix_table;
+        const int page0 = (own ? x - z.NP : x) * z.pages;
+        n = min(z.pages, ceil_div(own ? own_len : a.prefix_len, a.P) - page0);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int p = lane + 32 * u;
             row[u] = (int)(a.n_pages * a.H * a.P);  // past the pool: reads as zeros
             if (p < n) {
-                const int id = t.table[page0 + p];
-                if (id >= 0 && id < a.n_pages) row[u] = (id * a.H + st.h) * a.P;
+                const int id = table[page0 + p];
+                if (id >= 0 && id < a.n_pages) row[u] = (id * a.H + head) * a.P;
                 else set_status(a.status, ICE_ERR_BOUNDS);
             }
         }
@@ -392,42 +396,46 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                         j = x < turns ? x >> 1 : x - (turns >> 1);
                         second = x < turns ? (x & 1) : n1 > it.st[0].n;
                     }
-                    if (second) next.fetch(a, z, it.st[1], it.st[1].kt0 + j, lane);
-                    else next.fetch(a, z, it.st[0], it.st[0].kt0 + j, lane);
+                    next.fetch(a, z, second ? it.st[1].own_table : it.st[0].own_table,
+                               second ? it.st[1].own_len : it.st[0].own_len, second ? it.st[1].h : it.st[0].h,
+                               (second ? it.st[1].kt0 : it.st[0].kt0) + j, lane);
                 };
-                fetch(0);
-                if (is_k) {
-                    for (int t = 0; ok && t < (it.same_q ? 1 : it.ns); ++t) {
-                        const PagedStream st = t ? it.st[1] : it.st[0];
-                        if (st.n == 0) continue;
-                        // free once the tile before in the slot is used up, or the one before that
-                        // where those in between and this one are of few rows
-                        const bool few = st.ntok * a.G <= kFaFew;
-                        const unsigned back = few && (last_few & 2) ? 4 : 2;
-                        if (qcnt >= back) {
-                            const unsigned w = qcnt - back;
-                            ok = __all_sync(0xffffffffu, fa_wait(&sh.q_empty[w & 3], (w >> 2) & 1, abort));
-                        }
-                        if (ok && fa_elect()) {
-                            unsigned long long* bar = &sh.q_full[qcnt & 3];
-                            fa_expect(bar, few ? kFaFew * kD * 2 : kFaTileB);
-                            for (int h = 0; h < 2; ++h)
-                                asm volatile(
-                                    "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-                                        s_q + fa_q_off(qcnt, few) + h * kFaHalfB),
-                                    "l"(few ? reinterpret_cast<unsigned long long>(&mf) : reinterpret_cast<unsigned long long>(&mq)),
-                                    "r"(h * 64), "r"(st.h * a.G), "r"(st.tok0), "r"(smem_u32(bar))
-                                    : "memory");
-                        }
-                        __syncwarp();
-                        ++qcnt;
-                        last_few = (last_few << 1) | (few ? 1 : 0);
-                    }
-                    if (!ok) break;
-                }
-                for (int x = 0; x < n; ++x) {
+#pragma unroll 1
+                for (int x = -1; x < n; ++x) {
                     const FaPages cur = next;
                     if (x + 1 < n) fetch(x + 1);
+                    if (x < 0) {
+                        if (is_k) {
+                            for (int t = 0; ok && t < (it.same_q ? 1 : it.ns); ++t) {
+                                const PagedStream st = t ? it.st[1] : it.st[0];
+                                if (st.n == 0) continue;
+                                // free once the tile before in the slot is used up, or the one before that
+                                // where those in between and this one are of few rows
+                                const bool few = st.ntok * a.G <= kFaFew;
+                                const unsigned back = few && (last_few & 2) ? 4 : 2;
+                                if (qcnt >= back) {
+                                    const unsigned w = qcnt - back;
+                                    ok = __all_sync(0xffffffffu, fa_wait(&sh.q_empty[w & 3], (w >> 2) & 1, abort));
+                                }
+                                if (ok && fa_elect()) {
+                                    unsigned long long* bar = &sh.q_full[qcnt & 3];
+                                    fa_expect(bar, few ? kFaFew * kD * 2 : kFaTileB);
+                                    for (int h = 0; h < 2; ++h)
+                                        asm volatile(
+                                            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                                                s_q + fa_q_off(qcnt, few) + h * kFaHalfB),
+                                            "l"(few ? reinterpret_cast<unsigned long long>(&mf) : reinterpret_cast<unsigned long long>(&mq)),
+                                            "r"(h * 64), "r"(st.h * a.G), "r"(st.tok0), "r"(smem_u32(bar))
+                                            : "memory");
+                                }
+                                __syncwarp();
+                                ++qcnt;
+                                last_few = (last_few << 1) | (few ? 1 : 0);
+                            }
+                            if (!ok) break;
+                        }
+                        continue;
+                    }
                     if (is_k && n > kFaAhead && x == n - kFaAhead && lane == 0) fa_arrive(&sh.item_want);
                     const unsigned st = cnt % stages;
                     ok = __all_sync(0xffffffffu, fa_wait(&empty[st], ((cnt / stages) & 1) ^ 1, abort));
@@ -670,35 +678,46 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             fa_after();
             const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
             const bool mine = row < nrow;
-            const long long part = (long long)st.slot * a.H + st.h;
-            const int R = st.tok0 * a.G + row;
+            const long long R = ((long long)st.slot * a.H + st.h) * a.RP + st.tok0 * a.G + row;
+            const float f = l > 0.0f || l != l ? inv : 0.0f;  // zeros where nothing was seen
 #pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < kD; k += 32) {
                 unsigned u[32];
-                float o[32];
                 if (n > 0) {
-                    fa_ld(t_o + 32 * k, u);
+                    fa_ld(t_o + k, u);
                     fa_wait_ld();
                 }
+                if (n == 0 || f == 0.0f) {  // O was not written where n = 0
 #pragma unroll
-                for (int c = 0; c < 32; ++c)  // O was not written where n = 0
-                    o[c] = n > 0 && l != 0.0f ? __uint_as_float(u[c]) * inv : 0.0f;
-                if (mine && st.direct) {
+                    for (int c = 0; c < 32; ++c) u[c] = 0;
+                }
+#pragma unroll
+                for (int c = 0; c < 32; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * f);
+                if (!mine) continue;
+                if (st.direct) {
                     if (tok < valid_tok) {
                         uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)a.out +
-                                                              ((long long)tok * a.H * a.G + st.h * a.G + row % a.G) * kD + 32 * k);
+                                                              ((long long)tok * a.H * a.G + st.h * a.G + row % a.G) * kD + k);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            dst[c] = make_uint4(fa_pack(o[8 * c], o[8 * c + 1]), fa_pack(o[8 * c + 2], o[8 * c + 3]),
-                                                fa_pack(o[8 * c + 4], o[8 * c + 5]), fa_pack(o[8 * c + 6], o[8 * c + 7]));
+                        for (int c = 0; c < 4; ++c) {
+                            unsigned w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = fa_pack(__uint_as_float(u[8 * c + 2 * e]), __uint_as_float(u[8 * c + 2 * e + 1]));
+                            dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
                     }
-                } else if (mine) {
-                    float* dst = a.part_o + (part * kD + 32 * k) * a.RP + R;
+                } else {
+                    float* dst = a.part_o + R * kD + k;
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) dst[(long long)c * a.RP] = o[c];
+                    for (int c = 0; c < 32; c += 8)  // whole sectors of 32 B
+                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c), "r"(u[c]),
+                                     "r"(u[c + 1]), "r"(u[c + 2]), "r"(u[c + 3]), "r"(u[c + 4]), "r"(u[c + 5]), "r"(u[c + 6]),
+                                     "r"(u[c + 7])
+                                     : "memory");
                 }
             }
-            if (mine && !st.direct) a.part_ml[part * a.RP + R] = make_float2(m, l);
+            if (mine && !st.direct) a.part_ml[R] = make_float2(m, l);
             fa_before();
         }
     }
