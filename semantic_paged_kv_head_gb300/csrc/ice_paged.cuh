@@ -314,19 +314,24 @@ __device__ __forceinline__ int find_last(const int* v, int n, int i) {
     return lo;
 }
 
-// Item i < sh.pre + sh.own. Prefix items and the others alternate as long as there are both:
-// the former are bound by arithmetic, own tokens of few rows by memory, and they
-// overlap on different SMs.
+// Item i < sh.pre + sh.own. The items of the prefix are the longer ones. Up to one a block they
+// come first; with more of them they are every third item while they last: they are bound by
+// arithmetic and own tokens of few rows by memory, and the two overlap on different SMs.
 __device__ __forceinline__ void get_item(const PagedAttn& a, const PagedTiles& z, const int* cum,
                                          const PlanShared& sh, int i, PagedItem& out) {
-    const int both = 2 * min(sh.pre, sh.own);
+    const int every = min(3, (sh.pre + sh.own) / max(sh.pre, 1));
+    const int span = sh.pre * every;
     bool pre;
-    if (i < both) {
-        pre = !(i & 1);
-        i >>= 1;
+    if (sh.pre <= a.target_items) {
+        pre = i < sh.pre;
+        if (!pre) i -= sh.pre;
+    } else if (i < span) {
+        const int k = i / every;
+        pre = i == k * every;
+        i = pre ? k : i - k - 1;
     } else {
-        pre = sh.pre > sh.own;
-        i -= both >> 1;
+        pre = false;
+        i -= sh.pre;
     }
     const int NP = z.NP;
     const int tpt = z.TD > 0 ? z.TD : z.TB;  // tokens of a row tile

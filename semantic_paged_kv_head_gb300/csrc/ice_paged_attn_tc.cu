@@ -248,13 +248,11 @@ __device__ __forceinline__ float2 fa_fma2(float2 a, float2 b, float2 c) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
     return d;
 }
-__device__ __forceinline__ float2 fa_add2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
-        " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
+// Adds the two bf16 values of u to x and y in fp32.
+__device__ __forceinline__ void fa_add_pair(float& x, float& y, unsigned u) {
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n add.rn.f32.bf16 %0, a, %0;\n add.rn.f32.bf16 %1, b, %1;\n}\n"
+        : "+f"(x), "+f"(y)
+        : "r"(u));
 }
 
 // The pages of a key tile as rows of the pool's tensor map, page p in lane p % 32.
@@ -443,17 +441,22 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                     const unsigned bar = smem_u32(&full[st]), dst = dst0 + st * kFaTileB;
                     if (lane == 0) fa_expect(&full[st], (unsigned)(cur.n * a.P * kD * 2));
                     __syncwarp();
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int p = lane + 32 * u;
-                        if (p >= cur.n) break;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
+                    // one thread issues all boxes (of lanes with a page each, a box took 140 cycles)
+#pragma unroll 1
+                    for (int p = 0; p < cur.n; ++p) {
+                        const int mine = p < 32 ? cur.row[0] : p < 64 ? cur.row[1] : p < 96 ? cur.row[2] : cur.row[3];
+                        const int row = __shfl_sync(0xffffffffu, mine, p & 31);
+                        if (fa_elect()) {
+                            const unsigned to = dst + p * a.P * 128;
                             asm volatile(
-                                "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-                                    dst + h * kFaHalfB + p * a.P * 128),
-                                "l"(map), "r"(h * 64), "r"(cur.row[u]), "r"(bar)
+                                "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(to),
+                                "l"(map), "r"(0), "r"(row), "r"(bar)
                                 : "memory");
+                            asm volatile(
+                                "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(to + kFaHalfB),
+                                "l"(map), "r"(64), "r"(row), "r"(bar)
+                                : "memory");
+                        }
                     }
                     __syncwarp();
                     ++cnt;
@@ -540,12 +543,12 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                         fa_mma_o_rest(t_o, t_p, sv, true);
                         if (s) ++pn1;
                         else ++pn0;
-                        if (j + 1 == ne) fa_commit(&sh.o_done[s]);
+                        if (j + 1 < ne) scores(s, j + 1);  // first: the stream waits for them
+                        else fa_commit(&sh.o_done[s]);
                         if (apart || s == ns - 1) {
                             fa_commit(&sh.v_empty[st]);
                             ++vn;
                         }
-                        if (j + 1 < ne) scores(s, j + 1);
                     }
             }
             // products in flight end (bounded) before the tensor memory is given back
@@ -646,7 +649,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 }
                 const float nm = m == -INFINITY ? 0.0f : -m;
                 const float2 c2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(nm, nm);
-                float2 l2[2] = {make_float2(l, 0.0f), make_float2(0.0f, 0.0f)};
+                float ls[4] = {l, 0.0f, 0.0f, 0.0f};
                 auto ready = [&](int h) {  // portion h of the weights is written
                     fa_wait_st();
                     fa_before();
@@ -660,13 +663,13 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                     for (int c = 0; c < 16; ++c) {
                         const float2 x = fa_fma2(make_float2(__uint_as_float(v[k][2 * c]), __uint_as_float(v[k][2 * c + 1])), c2, nm2);
                         u[c] = fa_pack(exp2_approx(x.x), exp2_approx(x.y));
-                        l2[c & 1] = fa_add2(l2[c & 1], make_float2(__uint_as_float(u[c] << 16), __uint_as_float(u[c] & 0xFFFF0000u)));
+                        fa_add_pair(ls[2 * (c & 1)], ls[2 * (c & 1) + 1], u[c]);
                     }
                     if (k == 3) ready(0);  // keys 0 .. 95, stored while these were made
                     fa_st(t_s + 16 * k, u);
                 }
                 ready(1);
-                l = (l2[0].x + l2[1].x) + (l2[0].y + l2[1].y);
+                l = (ls[0] + ls[1]) + (ls[2] + ls[3]);
             }
             if (!ok) break;
             if (n > 0) {
