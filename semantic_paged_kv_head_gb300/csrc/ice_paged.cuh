@@ -72,11 +72,11 @@ cudaError_t paged_prepare();
 // and have nothing to join, except those of the last, incomplete wave over the GPU, which are cut
 // into `split` parts each. The other requests' rows share the prefix items, and their own tokens
 // are cut into ranges of `chunk` tiles; with TD > 0 one block attends two streams side
-// by side: two parts of a range, or two KV heads where there is one part.
-// chunk gives about target_items items in all, but no range is longer than
+// by side: two KV heads, or the two halves of a range where there is one head.
+// chunk gives about target_items items in all, but no stream is longer than
 // kPagedMaxRange tiles (the last items to end are then short), and keeps the parts
 // within max_splits.
-constexpr int kPagedMaxRange = 48;
+constexpr int kPagedMaxRange = 24;
 
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
@@ -85,12 +85,13 @@ struct PagedTiles {
     int NP, pages;       // tiles of the prefix, pages of a tile (TD > 0)
 };
 
-// Parts of the own tokens of a request that shares the prefix items.
-__device__ __forceinline__ int plan_parts(int s, const PagedTiles& z, int chunk) {
+// Parts of the own tokens of a request that shares the prefix items: one a range, or two.
+__device__ __forceinline__ int plan_parts(int s, int H, const PagedTiles& z, int chunk) {
     if (s <= 0) return 0;
     const int t = ceil_div(s, z.KT), ranges = ceil_div(t, chunk);
-    return z.TD > 0 ? min(t, 2 * ranges) : ranges;
+    return z.TD > 0 && H == 1 ? min(t, 2 * ranges) : ranges;
 }
+
 // Row blocks x heads of long requests are numbered: request by request, head by head. Those
 // below `whole` are one item each, the others `split`.
 struct PagedLong {
@@ -109,9 +110,8 @@ __device__ __forceinline__ int plan_items(int nq, int s, int H, int g0, const Pa
         const int n = long_blocks(nq, s, z) * H, w = long_whole(g0, n, f);
         return w + (n - w) * f.split;
     }
-    const int parts = plan_parts(s, z, chunk);
-    if (z.TD == 0) return parts * H;
-    return parts == 1 ? (H + 1) >> 1 : ((parts + 1) >> 1) * H;
+    const int parts = plan_parts(s, H, z, chunk);
+    return z.TD == 0 ? parts * H : H == 1 ? (parts + 1) >> 1 : parts * ((H + 1) >> 1);
 }
 
 struct PlanShared {
@@ -199,9 +199,10 @@ __device__ __forceinline__ void make_plan(const PagedAttn& a, const PagedTiles& 
     __syncthreads();
     nl = sh.nl, mx = sh.mx, fl = sh.fl;
     const bool bad = fl & 1;
-    const float want = (float)sh.w * (float)a.H / (float)a.target_items;
-    const int chunk = max(max((int)fminf(ceilf(want), (float)kPagedMaxRange), 1),
-                          ceil_div((int)mx, z.TD > 0 ? a.max_splits / 2 : a.max_splits));
+    // a range is 2 chunk tiles of an item with two streams of a head, chunk of each with two heads
+    const float want = (float)sh.w * (float)a.H / (float)(a.target_items * (z.TD > 0 ? 2 : 1));
+    const int chunk = max(max((int)fminf(ceilf(want), (float)kPagedMaxRange), 1), ceil_div((int)mx, a.max_splits)) *
+                      (z.TD > 0 && a.H == 1 ? 2 : 1);
     // parts of the last wave's: waves x (tiles of a part + the fixed cost of an item, and of
     // joining it, in tiles), the least of 1 to 16
     // (where the lengths do not fit in shared memory, with thousands of requests, all are whole)
@@ -387,12 +388,13 @@ __device__ __forceinline__ void get_item(const PagedAttn& a, const PagedTiles& z
             base = 0;
             st.direct = parts == 1;
         } else {
-            parts = plan_parts(s, z, sh.chunk);
+            parts = plan_parts(s, a.H, z, sh.chunk);
             base = NP;
-            twin = z.TD > 0 && parts > 1;
-            two_heads = z.TD > 0 && parts == 1;
-            st.h = two_heads ? 2 * x : x % a.H;
-            p0 = two_heads ? 0 : (x / a.H) << (int)twin;
+            twin = z.TD > 0 && a.H == 1 && parts > 1;
+            two_heads = z.TD > 0 && a.H > 1;
+            const int hs = two_heads ? (a.H + 1) >> 1 : a.H, k = x / hs;
+            st.h = (x - k * hs) << (int)two_heads;
+            p0 = k << (int)twin;
             st.direct = a.prefix_splits == 0 && parts == 1;
         }
         st.tok0 = b + rb * z.TB;

@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttn a, P
         const bool whole = f.whole == INT_MAX || a.first_long[req] + h * blocks + blk < f.whole;
         parts = blocks == 0 ? 0 : whole || f.split == 1 ? -1 : f.split;
     } else if (nq > 0) {
-        const int n = plan_parts(own, z, a.plan[kPlanChunk]);
+        const int n = plan_parts(own, a.H, z, a.plan[kPlanChunk]);
         parts = (a.prefix_splits == 0 && n == 1) || a.plan[kPlanDirect] ? -1 : a.prefix_splits + n;
     }
     if (PW == 1 && parts < 0) return;

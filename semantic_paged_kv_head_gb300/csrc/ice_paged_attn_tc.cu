@@ -504,49 +504,51 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 const unsigned sq0 = s_q + fa_q_off(q0, it.st[0].ntok * a.G <= kFaFew);
                 const unsigned sq1 = s_q + fa_q_off(q1, it.st[1].ntok * a.G <= kFaFew);
                 qn = n1 > 0 ? q1 + 1 : q0 + 1;
-                // scores of stream s against its next key tile, the j-th
-                auto scores = [&](int s, int j) {
-                    const unsigned st = kn % kFaStagesK, q = s ? q1 : q0;
-                    if (j == 0) ok = ok && fa_wait(&sh.q_full[q & 3], (q >> 2) & 1, abort);
-                    if (apart || s == 0) ok = ok && fa_wait(&sh.k_full[st], (kn / kFaStagesK) & 1, abort);
-                    if (!ok) return;
-                    fa_after();
-                    fa_mma_s(tmem + 128 * s, s ? sq1 : sq0, s_k + st * kFaTileB);
-                    fa_commit(&sh.s_full[s]);
-                    if (apart || s == ns - 1) {
-                        fa_commit(&sh.k_empty[st]);
-                        ++kn;
-                    }
-                    // a query tile of both is done with the last scores of the two
-                    if (it.same_q ? j + 1 == n && (s ? n1 >= n0 : n0 > n1) : j + 1 == (s ? n1 : n0))
-                        fa_commit(&sh.q_empty[q & 3]);
-                };
-                if (n0 > 0) scores(0, 0);
-                if (ok && n1 > 0) scores(1, 0);
-                for (int j = 0; ok && j < n; ++j)
+                // round j: each stream's products with its j-th value tile, then its scores against
+                // key tile j + 1 (round -1: the first scores)
+#pragma unroll 1
+                for (int j = -1; ok && j < n; ++j)
+#pragma unroll 1
                     for (int s = 0; ok && s < ns; ++s) {
                         const int ne = s ? n1 : n0;
+                        const unsigned t_p = tmem + 128 * s, vs = vn % kFaStagesV, ks = kn % kFaStagesK;
+                        const bool last = apart || s == ns - 1;  // a shared tile's last user
                         if (j >= ne) continue;
-                        const unsigned st = vn % kFaStagesV;
-                        if (apart || s == 0) ok = fa_wait(&sh.v_full[st], (vn / kFaStagesV) & 1, abort);
-                        // the weights come in two portions: the first one's products run
-                        // while the second is made
-                        const unsigned t_p = tmem + 128 * s, t_o = t_p + 256, sv = s_v + st * kFaTileB;
-                        const unsigned np = s ? pn1 : pn0;
-                        ok = ok && fa_wait(&sh.p_ready[s][0], np & 1, abort);
-                        if (!ok) break;
-                        fa_after();
-                        fa_mma_o_first(t_o, t_p, sv, j > 0);
-                        ok = fa_wait(&sh.p_ready[s][1], np & 1, abort);
-                        if (!ok) break;
-                        fa_after();
-                        fa_mma_o_rest(t_o, t_p, sv, true);
-                        if (s) ++pn1;
-                        else ++pn0;
-                        if (j + 1 < ne) scores(s, j + 1);  // first: the stream waits for them
-                        else fa_commit(&sh.o_done[s]);
-                        if (apart || s == ns - 1) {
-                            fa_commit(&sh.v_empty[st]);
+                        if (j >= 0) {
+                            const unsigned t_o = t_p + 256, sv = s_v + vs * kFaTileB, np = s ? pn1 : pn0;
+                            if (apart || s == 0) ok = fa_wait(&sh.v_full[vs], (vn / kFaStagesV) & 1, abort);
+                            // the weights come in two portions: the first one's products run
+                            // while the second is made
+                            ok = ok && fa_wait(&sh.p_ready[s][0], np & 1, abort);
+                            if (!ok) break;
+                            fa_after();
+                            fa_mma_o_first(t_o, t_p, sv, j > 0);
+                            ok = fa_wait(&sh.p_ready[s][1], np & 1, abort);
+                            if (!ok) break;
+                            fa_after();
+                            fa_mma_o_rest(t_o, t_p, sv, true);
+                            if (s) ++pn1;
+                            else ++pn0;
+                            if (j + 1 == ne) fa_commit(&sh.o_done[s]);
+                        }
+                        if (j + 1 < ne) {
+                            const unsigned q = s ? q1 : q0;
+                            if (j < 0) ok = fa_wait(&sh.q_full[q & 3], (q >> 2) & 1, abort);
+                            if (apart || s == 0) ok = ok && fa_wait(&sh.k_full[ks], (kn / kFaStagesK) & 1, abort);
+                            if (!ok) break;
+                            fa_after();
+                            fa_mma_s(t_p, s ? sq1 : sq0, s_k + ks * kFaTileB);
+                            fa_commit(&sh.s_full[s]);  // the stream waits for it
+                            if (last) {
+                                fa_commit(&sh.k_empty[ks]);
+                                ++kn;
+                            }
+                            // a query tile of both is done with the last scores of the two
+                            if (it.same_q ? j + 2 == n && (s ? n1 >= n0 : n0 > n1) : j + 2 == ne)
+                                fa_commit(&sh.q_empty[q & 3]);
+                        }
+                        if (j >= 0 && last) {
+                            fa_commit(&sh.v_empty[vs]);
                             ++vn;
                         }
                     }
