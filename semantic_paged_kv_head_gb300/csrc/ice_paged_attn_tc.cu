@@ -289,7 +289,7 @@ __device__ __forceinline__ unsigned fa_q_off(unsigned p, bool few) {
 // The items of a block, read by its warps from a ring of two that warp 11 fills. An item is
 // taken when kFaAhead tiles of the one before are left to copy, not earlier: a block in a
 // long item would keep a second one waiting that another block could have begun.
-constexpr int kFaAhead = 8;
+constexpr int kFaAhead = 4;
 constexpr int kFaReaders = 11;  // warps 0 .. 10
 struct FaItems {
     unsigned cnt = 0;
@@ -513,6 +513,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                         const int ne = s ? n1 : n0;
                         const unsigned t_p = tmem + 128 * s, vs = vn % kFaStagesV, ks = kn % kFaStagesK;
                         const bool last = apart || s == ns - 1;  // a shared tile's last user
+                        bool k_here = false;
                         if (j >= ne) continue;
                         if (j >= 0) {
                             const unsigned t_o = t_p + 256, sv = s_v + vs * kFaTileB, np = s ? pn1 : pn0;
@@ -523,6 +524,8 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                             if (!ok) break;
                             fa_after();
                             fa_mma_o_first(t_o, t_p, sv, j > 0);
+                            if (j + 1 < ne && (apart || s == 0))  // off the path of the last weights
+                                k_here = fa_try(smem_u32(&sh.k_full[ks]), (kn / kFaStagesK) & 1);
                             ok = fa_wait(&sh.p_ready[s][1], np & 1, abort);
                             if (!ok) break;
                             fa_after();
@@ -534,7 +537,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                         if (j + 1 < ne) {
                             const unsigned q = s ? q1 : q0;
                             if (j < 0) ok = fa_wait(&sh.q_full[q & 3], (q >> 2) & 1, abort);
-                            if (apart || s == 0) ok = ok && fa_wait(&sh.k_full[ks], (kn / kFaStagesK) & 1, abort);
+                            if ((apart || s == 0) && !k_here) ok = ok && fa_wait(&sh.k_full[ks], (kn / kFaStagesK) & 1, abort);
                             if (!ok) break;
                             fa_after();
                             fa_mma_s(t_p, s ? sq1 : sq0, s_k + ks * kFaTileB);
