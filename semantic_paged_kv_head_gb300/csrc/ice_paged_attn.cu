@@ -8,164 +8,341 @@
 namespace ice {
 
 // ---------------------------------------------------------------------------
-// One block takes items in turn: up to 64 rows (new tokens x G heads) against a
-// range of tiles of 64 keys, in one pass with a running maximum m and sum l a
-// row: m' = max(m, max_t s_t), l' = l 2^(m - m') + sum_t 2^(s_t - m'), and the same
-// factor on the output, with s_t = q . k_t log2(e) / sqrt(d). Threads form a 16 x 16
-// grid: RT rows by 4 keys each of the scores, RT rows by 8 dimensions each of the
-// output, so that a row's 16 threads are half a warp and the statistics need
-// shuffles only.
+// One block takes items in turn: rows (new tokens x G heads) against a range of tiles of 64
+// keys, in one pass with a running maximum m and sum l a row: m' = max(m, max_t s_t),
+// l' = l 2^(m - m') + sum_t 2^(s_t - m'), and the same factor on the output, with
+// s_t = q . k_t log2(e) / sqrt(d). fp32 has no tensor-core form that keeps its 24 bits.
+//
+// More than kFewRows rows (up to 64): bound by arithmetic. The next tile is copied into shared
+// memory while one is worked on. Threads form a 16 x 16 grid: 4 rows by 4 keys each of the
+// scores, 4 rows by 8 dimensions each of the output, so that a row's 16 threads are half a warp
+// and the statistics need shuffles only.
+//
+// Few rows (a decode step's own tokens): bound by memory. The warps take groups of 4 keys in
+// turn, 8 lanes a key for the scores and 4 dimensions a lane for the output, straight from
+// global memory, the next group's loads under way; their parts meet in shared memory at the end.
 // ---------------------------------------------------------------------------
 constexpr int kSimtThreads = 256;
+constexpr int kSimtWarps = kSimtThreads / 32;
 constexpr int kSimtRows = 64;
 constexpr int kSimtKeys = 64;
+constexpr int kFewRows = 8;
 constexpr int kSimtStrideK = kD + 4;          // floats a row: consecutive rows 4 banks apart
 constexpr int kSimtStrideP = kSimtKeys + 4;
-constexpr int kSimtSmem = 4 * (kSimtRows * kSimtStrideK + kSimtKeys * kSimtStrideK + kSimtKeys * kD +
-                               kSimtRows * kSimtStrideP);
+constexpr int kSimtStage = kSimtKeys * (kSimtStrideK + kD);  // floats of a K and a V tile
+constexpr int kSimtSmem = 4 * (kSimtRows * kSimtStrideK + 2 * kSimtStage + kSimtRows * kSimtStrideP);
+static_assert(kFewRows * kD + kSimtWarps * kFewRows * (kD + 2) <= kSimtSmem / 4, "queries and the warps' parts fit");
+
+// Row of the pool of a key of the page list, -1 for a key past its end, -2 for a bad page.
+__device__ __forceinline__ int key_row(const PagedAttn& a, const PagedTile& t, int h, int key) {
+    if (key >= t.len) return -1;
+    const int page = t.table[key / a.P];
+    if (page >= 0 && page < a.n_pages) return (page * a.H + h) * a.P + key % a.P;
+    set_status(a.status, ICE_ERR_BOUNDS);
+    return -2;  // reads as zeros
+}
+
+__device__ __forceinline__ void copy16(void* smem, const void* gmem, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((unsigned)__cvta_generic_to_shared(smem)), "l"(gmem),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
+
+// Where the output of row r of the item goes; null for a row that is not to be written.
+__device__ __forceinline__ float* row_dst(const PagedAttn& a, const PagedStream& it, int r, int valid_tok, float2** ml) {
+    const int tok = it.tok0 + r / a.G;
+    if (r >= it.ntok * a.G || (it.direct && tok >= valid_tok)) return nullptr;
+    const long long R = ((long long)it.slot * a.H + it.h) * a.RP + it.tok0 * a.G + r;
+    *ml = it.direct ? nullptr : a.part_ml + R;
+    return it.direct ? (float*)a.out + ((long long)tok * a.H * a.G + it.h * a.G + r % a.G) * kD : a.part_o + R * kD;
+}
+
+// A row's weight sum as a factor: zeros where nothing was seen.
+__device__ __forceinline__ float inverse(float sum) { return sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum); }
+
+__device__ __forceinline__ float4 load_or_zero(const float* base, int row, int off) {
+    return row >= 0 ? __ldg(reinterpret_cast<const float4*>(base + (long long)row * kD + off)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+}
+
+template <int R>
+__device__ __forceinline__ void few_rows(const PagedAttn& a, const PagedTiles& z, const PagedStream& it, int valid_tok,
+                                         float* smem) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kk = lane >> 3, dd = lane & 7;
+    const int nrow = it.ntok * a.G;
+    float* sq = smem;             // the rows' queries
+    float* parts = smem + R * kD; // the warps' parts: [warp][row][d], then m and l
+    float4 acc[R];
+    float m[R], l[R];
+    int lim[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int tok = it.tok0 + r / a.G;
+        lim[r] = r < nrow ? min(it.own_len, tok + it.lim_off) : 0;
+        m[r] = -INFINITY;
+        l[r] = 0.0f;
+        acc[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    for (int x = threadIdx.x; x < R * (kD / 4); x += kSimtThreads) {
+        const int r = x / (kD / 4), c = (x % (kD / 4)) * 4;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (r < nrow)
+            v = *reinterpret_cast<const float4*>((const float*)a.q + (it.tok0 + r / a.G) * a.q_stride +
+                                                 (it.h * a.G + r % a.G) * kD + c);
+        *reinterpret_cast<float4*>(sq + r * kD + c) = v;
+    }
+    __syncthreads();
+    // groups of 4 keys: 16 a tile; the warp takes every kSimtWarps-th
+    const int g_end = it.n * (kSimtKeys / 4);
+    float4 kv[4] = {}, vv[4] = {};
+    int key = 0, row = -1;
+    bool own = false;
+    int len = 0;
+    auto fetch = [&](int g) {
+        const PagedTile t = tile_of(a, z, it, it.kt0 + g / (kSimtKeys / 4));
+        key = t.key0 + (g % (kSimtKeys / 4)) * 4 + kk;
+        own = t.own;
+        len = t.len;
+        row = key_row(a, t, it.h, key);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) kv[i] = load_or_zero((const float*)a.k_pages, row, 4 * dd + 32 * i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            vv[i] = load_or_zero((const float*)a.v_pages, __shfl_sync(0xffffffffu, row, 8 * i), 4 * lane);
+    };
+#pragma unroll 1
+    for (int g = warp - kSimtWarps; g < g_end; g += kSimtWarps) {
+        float4 k_now[4], v_now[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) k_now[i] = kv[i], v_now[i] = vv[i];
+        const int key_now = key, len_now = len;
+        const bool own_now = own;
+        if (g + kSimtWarps < g_end) fetch(g + kSimtWarps);
+        if (g < 0) continue;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 q = *reinterpret_cast<const float4*>(sq + r * kD + 4 * dd + 32 * i);
+                s += q.x * k_now[i].x + q.y * k_now[i].y + q.z * k_now[i].z + q.w * k_now[i].w;
+            }
+#pragma unroll
+            for (int o = 4; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            s = key_now < (own_now ? lim[r] : len_now) ? s * a.scale_log2 : -INFINITY;
+            float mx = fmaxf(m[r], s);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float mu = mx == -INFINITY ? 0.0f : mx;  // nothing seen yet: all weights 0
+            const float f = exp2_approx(m[r] - mu), p = exp2_approx(s - mu);
+            m[r] = mx;
+            l[r] = l[r] * f + p;  // of this lane's key
+            acc[r].x *= f, acc[r].y *= f, acc[r].z *= f, acc[r].w *= f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float w = __shfl_sync(0xffffffffu, p, 8 * i);
+                acc[r].x = fmaf(w, v_now[i].x, acc[r].x);
+                acc[r].y = fmaf(w, v_now[i].y, acc[r].y);
+                acc[r].z = fmaf(w, v_now[i].z, acc[r].z);
+                acc[r].w = fmaf(w, v_now[i].w, acc[r].w);
+            }
+        }
+    }
+    float* sm = parts + kSimtWarps * R * kD;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        float sum = l[r];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        *reinterpret_cast<float4*>(parts + (warp * R + r) * kD + 4 * lane) = acc[r];
+        if (lane == 0) {
+            sm[(warp * R + r) * 2] = m[r];
+            sm[(warp * R + r) * 2 + 1] = sum;
+        }
+    }
+    __syncthreads();
+    for (int r = warp; r < R; r += kSimtWarps) {
+        float M = -INFINITY, W = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < kSimtWarps; ++w) M = fmaxf(M, sm[(w * R + r) * 2]);
+        const float mu = M == -INFINITY ? 0.0f : M;
+#pragma unroll
+        for (int w = 0; w < kSimtWarps; ++w) {
+            const float f = exp2_approx(sm[(w * R + r) * 2] - mu);
+            const float4 x = *reinterpret_cast<const float4*>(parts + (w * R + r) * kD + 4 * lane);
+            W = fmaf(f, sm[(w * R + r) * 2 + 1], W);
+            o.x = fmaf(f, x.x, o.x), o.y = fmaf(f, x.y, o.y), o.z = fmaf(f, x.z, o.z), o.w = fmaf(f, x.w, o.w);
+        }
+        float2* ml;
+        float* dst = row_dst(a, it, r, valid_tok, &ml);
+        if (dst == nullptr) continue;
+        const float inv = inverse(W);
+        *reinterpret_cast<float4*>(dst + 4 * lane) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (ml != nullptr && lane == 0) *ml = make_float2(M, W);
+    }
+}
+
+__device__ __forceinline__ void many_rows(const PagedAttn& a, const PagedTiles& z, const PagedStream& it, int valid_tok,
+                                          float* smem) {
+    float* sQ = smem;
+    float* sKV = sQ + kSimtRows * kSimtStrideK;
+    float* sP = sKV + 2 * kSimtStage;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rg = tid >> 4, kg = tid & 15;
+    const int nrow = it.ntok * a.G;
+    // a warp copies a row of K and of V at a time
+    auto copy_tile = [&](int kt, int stage) {
+        const PagedTile t = tile_of(a, z, it, kt);
+        float* k = sKV + stage * kSimtStage;
+        float* v = k + kSimtKeys * kSimtStrideK;
+#pragma unroll 2
+        for (int i = 0; i < kSimtKeys / kSimtWarps; ++i) {
+            const int r = warp + kSimtWarps * i, row = key_row(a, t, it.h, t.key0 + r);
+            const long long off = (long long)max(row, 0) * kD + 4 * lane;
+            copy16(k + r * kSimtStrideK + 4 * lane, (const float*)a.k_pages + off, row >= 0);
+            copy16(v + r * kD + 4 * lane, (const float*)a.v_pages + off, row >= 0);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // row r: token tok0 + r / G, head h G + r % G; rows past the item's are zero
+    for (int x = tid; x < kSimtRows * (kD / 4); x += kSimtThreads) {
+        const int r = x / (kD / 4), c = (x % (kD / 4)) * 4;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (r < nrow)
+            v = *reinterpret_cast<const float4*>((const float*)a.q + (it.tok0 + r / a.G) * a.q_stride +
+                                                 (it.h * a.G + r % a.G) * kD + c);
+        *reinterpret_cast<float4*>(sQ + r * kSimtStrideK + c) = v;
+    }
+    float m[4], l[4], o[4][8];
+    int lim[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        m[j] = -INFINITY;
+        l[j] = 0.0f;
+        const int r = rg * 4 + j;
+        lim[j] = r < nrow ? min(it.own_len, it.tok0 + r / a.G + it.lim_off) : 0;  // of own tokens
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[j][k] = 0.0f;
+    }
+#pragma unroll 1
+    for (int i = -1; i < it.n; ++i) {
+        if (i + 1 < it.n) copy_tile(it.kt0 + i + 1, (i + 1) & 1);
+        if (i < 0) continue;
+        const PagedTile t = tile_of(a, z, it, it.kt0 + i);
+        const int key0 = t.key0;
+        const float* sK = sKV + (i & 1) * kSimtStage;
+        const float* sV = sK + kSimtKeys * kSimtStrideK;
+        if (i + 1 < it.n) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        float s[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[j][k] = 0.0f;
+#pragma unroll 4
+        for (int c = 0; c < kD; c += 4) {
+            float4 qv[4], kv[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) qv[j] = *reinterpret_cast<const float4*>(sQ + (rg * 4 + j) * kSimtStrideK + c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) kv[k] = *reinterpret_cast<const float4*>(sK + (kg + 16 * k) * kSimtStrideK + c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    s[j][k] += qv[j].x * kv[k].x + qv[j].y * kv[k].y + qv[j].z * kv[k].z + qv[j].w * kv[k].w;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float mx = m[j];
+            const int end = t.own ? lim[j] : t.len;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                s[j][k] = key0 + kg + 16 * k < end ? s[j][k] * a.scale_log2 : -INFINITY;
+                mx = fmaxf(mx, s[j][k]);
+            }
+#pragma unroll
+            for (int d = 8; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            const float mu = mx == -INFINITY ? 0.0f : mx;  // nothing seen yet: all weights 0
+            const float f = exp2_approx(m[j] - mu);
+            m[j] = mx;
+            l[j] *= f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[j][k] *= f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float p = exp2_approx(s[j][k] - mu);
+                l[j] += p;
+                sP[(rg * 4 + j) * kSimtStrideP + kg + 16 * k] = p;
+            }
+        }
+        __syncwarp();  // a row's weights are written and read by one warp
+#pragma unroll 2
+        for (int k0 = 0; k0 < kSimtKeys; k0 += 4) {
+            float4 pv[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) pv[j] = *reinterpret_cast<const float4*>(sP + (rg * 4 + j) * kSimtStrideP + k0);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float4 v0 = *reinterpret_cast<const float4*>(sV + (k0 + u) * kD + kg * 4);
+                const float4 v1 = *reinterpret_cast<const float4*>(sV + (k0 + u) * kD + 64 + kg * 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float p = u == 0 ? pv[j].x : u == 1 ? pv[j].y : u == 2 ? pv[j].z : pv[j].w;
+                    o[j][0] += p * v0.x; o[j][1] += p * v0.y; o[j][2] += p * v0.z; o[j][3] += p * v0.w;
+                    o[j][4] += p * v1.x; o[j][5] += p * v1.y; o[j][6] += p * v1.z; o[j][7] += p * v1.w;
+                }
+            }
+        }
+        __syncthreads();  // the tile's memory is free for the copy after the next
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float sum = l[j];
+#pragma unroll
+        for (int d = 8; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        float2* ml;
+        float* dst = row_dst(a, it, rg * 4 + j, valid_tok, &ml);
+        if (dst == nullptr) continue;
+        const float inv = inverse(sum);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            *reinterpret_cast<float4*>(dst + 64 * k + kg * 4) =
+                make_float4(o[j][4 * k] * inv, o[j][4 * k + 1] * inv, o[j][4 * k + 2] * inv, o[j][4 * k + 3] * inv);
+        if (ml != nullptr && kg == 0) *ml = make_float2(m[j], sum);
+    }
+}
 
 __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(PagedAttn a, PagedTiles z) {
     extern __shared__ __align__(16) float simt_smem[];
     __shared__ PlanShared sh;
-    float* sQ = simt_smem;
-    float* sK = sQ + kSimtRows * kSimtStrideK;
-    float* sV = sK + kSimtKeys * kSimtStrideK;
-    float* sP = sV + kSimtKeys * kD;
-    int* cum = reinterpret_cast<int*>(sP + kSimtRows * kSimtStrideP);
-    const int tid = threadIdx.x, rg = tid >> 4, kg = tid & 15;
+    __shared__ PagedItem item;
+    __shared__ int s_next;
+    int* cum = reinterpret_cast<int*>(simt_smem + kSimtSmem / 4);
+    const int tid = threadIdx.x;
     pdl_wait_then_release();
     make_plan<kSimtThreads>(a, z, cum, sh);
-    if (!sh.ok) return;
+    const int n_items = sh.ok ? sh.pre + sh.own : 0;
     const int valid_tok = a.q_start[a.n_req];
-    const int n_items = sh.pre + sh.own;
-    PagedItem item;
-    for (int i = blockIdx.x; i < n_items; i += gridDim.x) {
-        get_item(a, z, cum, sh, i, item);
-        if (item.ns == 0) continue;
-        const PagedStream& it = item.st[0];
-        const int nrow = it.ntok * a.G;
+    // the block's first item is its own number, the others are handed out
+    for (int i = blockIdx.x; i < n_items; i = s_next) {
+        if (tid == 0) get_item(a, z, cum, sh, i, item);
         __syncthreads();
-        // row r: token tok0 + r / G, head h G + r % G; rows past the item's are zero
-        for (int x = tid; x < kSimtRows * (kD / 4); x += kSimtThreads) {
-            const int r = x / (kD / 4), c = (x % (kD / 4)) * 4;
-            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (r < nrow)
-                load4((const float*)a.q + (it.tok0 + r / a.G) * a.q_stride + (it.h * a.G + r % a.G) * kD + c, v);
-            *reinterpret_cast<float4*>(sQ + r * kSimtStrideK + c) = make_float4(v[0], v[1], v[2], v[3]);
+        if (tid == 0) s_next = gridDim.x + atomicAdd(&a.next[0], 1u);  // read after the item's last barrier
+        const PagedStream it = item.st[0];
+        if (item.ns > 0) {
+            const int nrow = it.ntok * a.G;
+            if (nrow > kFewRows) many_rows(a, z, it, valid_tok, simt_smem);
+            else if (nrow > 2) few_rows<8>(a, z, it, valid_tok, simt_smem);
+            else few_rows<2>(a, z, it, valid_tok, simt_smem);
         }
-        float m[4], l[4], o[4][8];
-        int lim[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            m[j] = -INFINITY;
-            l[j] = 0.0f;
-            const int r = rg * 4 + j;
-            lim[j] = r < nrow ? min(it.own_len, it.tok0 + r / a.G + it.lim_off) : 0;  // of own tokens
-#pragma unroll
-            for (int k = 0; k < 8; ++k) o[j][k] = 0.0f;
-        }
-        for (int kt = it.kt0; kt < it.kt0 + it.n; ++kt) {
-            const PagedTile t = tile_of(a, z, it, kt);
-            const int key0 = t.key0;
-            __syncthreads();
-            for (int x = tid; x < kSimtKeys * (kD / 4); x += kSimtThreads) {
-                const int r = x / (kD / 4), c = (x % (kD / 4)) * 4, key = key0 + r;
-                float vk[4] = {0.0f, 0.0f, 0.0f, 0.0f}, vv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (key < t.len) {
-                    const int page = t.table[key / a.P];
-                    if (page >= 0 && page < a.n_pages) {
-                        const long long row = ((long long)page * a.H + it.h) * a.P + key % a.P;
-                        load4((const float*)a.k_pages + row * kD + c, vk);
-                        load4((const float*)a.v_pages + row * kD + c, vv);
-                    } else {
-                        set_status(a.status, ICE_ERR_BOUNDS);
-                    }
-                }
-                *reinterpret_cast<float4*>(sK + r * kSimtStrideK + c) = make_float4(vk[0], vk[1], vk[2], vk[3]);
-                *reinterpret_cast<float4*>(sV + r * kD + c) = make_float4(vv[0], vv[1], vv[2], vv[3]);
-            }
-            __syncthreads();
-            float s[4][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) s[j][k] = 0.0f;
-#pragma unroll 4
-            for (int c = 0; c < kD; c += 4) {
-                float4 qv[4], kv[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    qv[j] = *reinterpret_cast<const float4*>(sQ + (rg * 4 + j) * kSimtStrideK + c);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    kv[k] = *reinterpret_cast<const float4*>(sK + (kg + 16 * k) * kSimtStrideK + c);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        s[j][k] += qv[j].x * kv[k].x + qv[j].y * kv[k].y + qv[j].z * kv[k].z + qv[j].w * kv[k].w;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float mx = m[j];
-                const int end = t.own ? lim[j] : t.len;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    s[j][k] = key0 + kg + 16 * k < end ? s[j][k] * a.scale_log2 : -INFINITY;
-                    mx = fmaxf(mx, s[j][k]);
-                }
-#pragma unroll
-                for (int d = 8; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                const float mu = mx == -INFINITY ? 0.0f : mx;  // nothing seen yet: all weights 0
-                const float f = exp2_approx(m[j] - mu);
-                m[j] = mx;
-                l[j] *= f;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) o[j][k] *= f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float p = exp2_approx(s[j][k] - mu);
-                    l[j] += p;
-                    sP[(rg * 4 + j) * kSimtStrideP + kg + 16 * k] = p;
-                }
-            }
-            __syncwarp();  // a row's weights are written and read by one warp
-#pragma unroll 2
-            for (int k0 = 0; k0 < kSimtKeys; k0 += 4) {
-                float4 pv[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    pv[j] = *reinterpret_cast<const float4*>(sP + (rg * 4 + j) * kSimtStrideP + k0);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const float4 v0 = *reinterpret_cast<const float4*>(sV + (k0 + u) * kD + kg * 4);
-                    const float4 v1 = *reinterpret_cast<const float4*>(sV + (k0 + u) * kD + 64 + kg * 4);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float p = u == 0 ? pv[j].x : u == 1 ? pv[j].y : u == 2 ? pv[j].z : pv[j].w;
-                        o[j][0] += p * v0.x; o[j][1] += p * v0.y; o[j][2] += p * v0.z; o[j][3] += p * v0.w;
-                        o[j][4] += p * v1.x; o[j][5] += p * v1.y; o[j][6] += p * v1.z; o[j][7] += p * v1.w;
-                    }
-                }
-            }
-            __syncwarp();
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float sum = l[j];
-#pragma unroll
-            for (int d = 8; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            const int r = rg * 4 + j, tok = it.tok0 + r / a.G;
-            if (r >= nrow || (it.direct && tok >= valid_tok)) continue;
-            const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-            const long long R = ((long long)it.slot * a.H + it.h) * a.RP + it.tok0 * a.G + r;
-            float* dst = it.direct ? (float*)a.out + ((long long)tok * a.H * a.G + it.h * a.G + r % a.G) * kD
-                                   : a.part_o + R * kD;
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                *reinterpret_cast<float4*>(dst + 64 * k + kg * 4) =
-                    make_float4(o[j][4 * k] * inv, o[j][4 * k + 1] * inv, o[j][4 * k + 2] * inv, o[j][4 * k + 3] * inv);
-            if (kg == 0 && !it.direct) a.part_ml[R] = make_float2(m[j], sum);
+        __syncthreads();
+    }
+    if (tid == 0) {  // the last block to end leaves the counters at zero
+        __threadfence();
+        if (atomicAdd(&a.next[1], 1u) == gridDim.x - 1) {
+            a.next[0] = 0;
+            a.next[1] = 0;
         }
     }
 }
