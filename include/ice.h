@@ -414,7 +414,8 @@ typedef struct ice_paged ice_paged; /* opaque */
 typedef struct ice_paged_params {
     int32_t d;            /* head dimension; the kernels support 128                  */
     int32_t n_kv_heads;   /* KV heads (>= 1)                                          */
-    int32_t n_q_heads;    /* query heads; n_q_heads / n_kv_heads = 1, 2, 4 or 8       */
+    int32_t n_q_heads;    /* query heads, up to 4096; n_q_heads / n_kv_heads = 1, 2,   */
+                          /* 4 or 8                                                   */
     int32_t page_size;    /* P: tokens per page, 1..64                                */
     int32_t dtype;        /* ICE_BF16 or ICE_F32                                      */
     int32_t max_requests; /* requests per call, 1..8192                               */
@@ -455,6 +456,7 @@ int ice_paged_get_error(ice_paged* pg, void* stream);
  *   lengths and the ring after the step. Each may be its input (in place).
  * q_start: device int32 [n_req + 1]; receives where each request's new tokens
  *   begin among all new tokens, and their number at the end.
+ * n_slots: room for new tokens, 0 .. 2^30.
  * slot_map: device int64 [n_slots]; receives the slot (page * P + offset) of
  *   each new token, request by request, and -1 behind the last.
  * positions: device int32 [n_slots] or NULL; receives the index of each new token

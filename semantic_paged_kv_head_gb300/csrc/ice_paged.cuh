@@ -63,6 +63,15 @@ cudaError_t launch_paged_append(int n_tokens, int H, int P, int es, long long n_
 cudaError_t launch_paged_attn(PagedAttn a, int dtype, long long rows_cap, int n_sm, cudaStream_t s);
 cudaError_t paged_prepare();
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+        " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
 // ---- the plan of an attention call, made by every block from the lengths ---------
 // Keys per tile KT, new tokens per row block TB. Tiles are numbered through the
 // prefix's NP and on through a request's own.
@@ -199,10 +208,11 @@ __device__ __forceinline__ void make_plan(const PagedAttn& a, const PagedTiles& 
     __syncthreads();
     nl = sh.nl, mx = sh.mx, fl = sh.fl;
     const bool bad = fl & 1;
-    // a range is 2 chunk tiles of an item with two streams of a head, chunk of each with two heads
+    // with two streams of one head a range is two parts: twice the tiles, an even number of parts
+    const int halves = z.TD > 0 && a.H == 1 ? 2 : 1;
     const float want = (float)sh.w * (float)a.H / (float)(a.target_items * (z.TD > 0 ? 2 : 1));
-    const int chunk = max(max((int)fminf(ceilf(want), (float)kPagedMaxRange), 1), ceil_div((int)mx, a.max_splits)) *
-                      (z.TD > 0 && a.H == 1 ? 2 : 1);
+    const int chunk = halves * max(max((int)fminf(ceilf(want), (float)kPagedMaxRange), 1),
+                                   ceil_div((int)mx, a.max_splits / halves * halves));
     // parts of the last wave's: waves x (tiles of a part + the fixed cost of an item, and of
     // joining it, in tiles), the least of 1 to 16
     // (where the lengths do not fit in shared memory, with thousands of requests, all are whole)

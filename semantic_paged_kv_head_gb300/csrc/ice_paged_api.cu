@@ -35,7 +35,7 @@ int check(const ice_paged_params* p) {
     if (p->n_kv_heads < 1 || p->n_q_heads < p->n_kv_heads || p->n_q_heads % p->n_kv_heads)
         return ICE_ERR_INVALID_ARG;
     const int G = p->n_q_heads / p->n_kv_heads;
-    if (!(G == 1 || G == 2 || G == 4 || G == 8) || p->n_q_heads > 65536) return ICE_ERR_UNSUPPORTED;
+    if (!(G == 1 || G == 2 || G == 4 || G == 8) || p->n_q_heads > 4096) return ICE_ERR_UNSUPPORTED;
     if (p->page_size < 1 || p->page_size > kMaxP) return ICE_ERR_INVALID_ARG;
     if (p->dtype != ICE_F32 && p->dtype != ICE_BF16) return ICE_ERR_INVALID_ARG;
     if (p->max_requests < 1 || p->max_requests > kPagedMaxRequests) return ICE_ERR_INVALID_ARG;
@@ -168,7 +168,8 @@ int ice_paged_tables(ice_paged* pg, int32_t n_req, const int32_t* seq_len, const
                      int32_t* seq_len_out, int64_t* free_state_out, int32_t* q_start,
                      int64_t* slot_map, int32_t* positions, int32_t n_slots, void* stream) {
     ApiRange range_("ice_paged_tables");
-    if (!pg || n_req < 1 || n_req > pg->p.max_requests || n_slots < 0) return ICE_ERR_INVALID_ARG;
+    if (!pg || n_req < 1 || n_req > pg->p.max_requests || n_slots < 0 || n_slots > (1 << 30))
+        return ICE_ERR_INVALID_ARG;
     Buffers b(pg, stream);
     b.need(seq_len, 4).need(n_new, 4).need(block_table, 4).need(free_pages, 4).need(free_state, 8);
     b.need(seq_len_out, 4).need(free_state_out, 8).need(q_start, 4);

@@ -212,7 +212,8 @@ __device__ __forceinline__ void many_rows(const PagedAttn& a, const PagedTiles& 
                                                  (it.h * a.G + r % a.G) * kD + c);
         *reinterpret_cast<float4*>(sQ + r * kSimtStrideK + c) = v;
     }
-    float m[4], l[4], o[4][8];
+    float m[4], l[4];
+    float2 o[4][4];  // dimensions 4 kg .. + 3, 64 + 4 kg .. + 3
     int lim[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -221,7 +222,7 @@ __device__ __forceinline__ void many_rows(const PagedAttn& a, const PagedTiles& 
         const int r = rg * 4 + j;
         lim[j] = r < nrow ? min(it.own_len, it.tok0 + r / a.G + it.lim_off) : 0;  // of own tokens
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o[j][k] = 0.0f;
+        for (int k = 0; k < 4; ++k) o[j][k] = make_float2(0.0f, 0.0f);
     }
 #pragma unroll 1
     for (int i = -1; i < it.n; ++i) {
@@ -234,11 +235,11 @@ __device__ __forceinline__ void many_rows(const PagedAttn& a, const PagedTiles& 
         if (i + 1 < it.n) asm volatile("cp.async.wait_group 1;" ::: "memory");
         else asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
-        float s[4][4];
+        float2 s2[4][4];  // even and odd dimensions
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[j][k] = 0.0f;
+            for (int k = 0; k < 4; ++k) s2[j][k] = make_float2(0.0f, 0.0f);
 #pragma unroll 4
         for (int c = 0; c < kD; c += 4) {
             float4 qv[4], kv[4];
@@ -249,17 +250,20 @@ __device__ __forceinline__ void many_rows(const PagedAttn& a, const PagedTiles& 
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    s[j][k] += qv[j].x * kv[k].x + qv[j].y * kv[k].y + qv[j].z * kv[k].z + qv[j].w * kv[k].w;
+                for (int k = 0; k < 4; ++k) {
+                    s2[j][k] = fma2(make_float2(qv[j].x, qv[j].y), make_float2(kv[k].x, kv[k].y), s2[j][k]);
+                    s2[j][k] = fma2(make_float2(qv[j].z, qv[j].w), make_float2(kv[k].z, kv[k].w), s2[j][k]);
+                }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float mx = m[j];
             const int end = t.own ? lim[j] : t.len;
+            float s[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                s[j][k] = key0 + kg + 16 * k < end ? s[j][k] * a.scale_log2 : -INFINITY;
-                mx = fmaxf(mx, s[j][k]);
+                s[k] = key0 + kg + 16 * k < end ? (s2[j][k].x + s2[j][k].y) * a.scale_log2 : -INFINITY;
+                mx = fmaxf(mx, s[k]);
             }
 #pragma unroll
             for (int d = 8; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
@@ -268,10 +272,10 @@ __device__ __forceinline__ void many_rows(const PagedAttn& a, const PagedTiles& 
             m[j] = mx;
             l[j] *= f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) o[j][k] *= f;
+            for (int k = 0; k < 4; ++k) o[j][k].x *= f, o[j][k].y *= f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float p = exp2_approx(s[j][k] - mu);
+                const float p = exp2_approx(s[k] - mu);
                 l[j] += p;
                 sP[(rg * 4 + j) * kSimtStrideP + kg + 16 * k] = p;
             }
@@ -289,8 +293,11 @@ __device__ __forceinline__ void many_rows(const PagedAttn& a, const PagedTiles& 
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float p = u == 0 ? pv[j].x : u == 1 ? pv[j].y : u == 2 ? pv[j].z : pv[j].w;
-                    o[j][0] += p * v0.x; o[j][1] += p * v0.y; o[j][2] += p * v0.z; o[j][3] += p * v0.w;
-                    o[j][4] += p * v1.x; o[j][5] += p * v1.y; o[j][6] += p * v1.z; o[j][7] += p * v1.w;
+                    const float2 p2 = make_float2(p, p);
+                    o[j][0] = fma2(p2, make_float2(v0.x, v0.y), o[j][0]);
+                    o[j][1] = fma2(p2, make_float2(v0.z, v0.w), o[j][1]);
+                    o[j][2] = fma2(p2, make_float2(v1.x, v1.y), o[j][2]);
+                    o[j][3] = fma2(p2, make_float2(v1.z, v1.w), o[j][3]);
                 }
             }
         }
@@ -308,7 +315,7 @@ __device__ __forceinline__ void many_rows(const PagedAttn& a, const PagedTiles& 
 #pragma unroll
         for (int k = 0; k < 2; ++k)
             *reinterpret_cast<float4*>(dst + 64 * k + kg * 4) =
-                make_float4(o[j][4 * k] * inv, o[j][4 * k + 1] * inv, o[j][4 * k + 2] * inv, o[j][4 * k + 3] * inv);
+                make_float4(o[j][2 * k].x * inv, o[j][2 * k].y * inv, o[j][2 * k + 1].x * inv, o[j][2 * k + 1].y * inv);
         if (ml != nullptr && kg == 0) *ml = make_float2(m[j], sum);
     }
 }

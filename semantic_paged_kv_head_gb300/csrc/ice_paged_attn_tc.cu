@@ -239,15 +239,6 @@ __device__ __forceinline__ float fa_max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fa_fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
-        " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
 // Adds the two bf16 values of u to x and y in fp32.
 __device__ __forceinline__ void fa_add_pair(float& x, float& y, unsigned u) {
     asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n add.rn.f32.bf16 %0, a, %0;\n add.rn.f32.bf16 %1, b, %1;\n}\n"
@@ -609,31 +600,26 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 }
                 fa_after();
                 unsigned v[4][32];  // scores, as bits
-                fa_ld(t_s, v[0]);
-                fa_ld(t_s + 32, v[1]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) fa_ld(t_s + 32 * k, v[k]);
                 fa_wait_ld();
-                fa_ld(t_s + 64, v[2]);
-                fa_ld(t_s + 96, v[3]);
                 // some key is hidden from some row
-                const bool cut = t.key0 + kFaKeys > (t.own ? lim_all : t.len) || KT < kFaKeys;
-                const int c_lim = min((t.own ? lim : t.len) - t.key0, KT);
-                float mx[4];
-                auto max_of = [&](int k) {
-                    if (cut) {
+                if (t.key0 + kFaKeys > (t.own ? lim_all : t.len) || KT < kFaKeys) {
+                    const int c_lim = min((t.own ? lim : t.len) - t.key0, KT);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
                             if (32 * k + c >= c_lim) v[k][c] = 0xFF800000u;  // -inf
-                    }
+                }
+                float mx[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
                     mx[k] = fmaxf(__uint_as_float(v[k][0]), __uint_as_float(v[k][1]));
 #pragma unroll
                     for (int c = 2; c < 32; c += 2)
                         mx[k] = fa_max3(mx[k], __uint_as_float(v[k][c]), __uint_as_float(v[k][c + 1]));
-                };
-                max_of(0);
-                max_of(1);
-                fa_wait_ld();
-                max_of(2);
-                max_of(3);
+                }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
                 const bool grow = top > m + kFaSlack;  // also the first finite one
                 if (__any_sync(0xffffffffu, grow)) {
@@ -654,7 +640,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 }
                 const float nm = m == -INFINITY ? 0.0f : -m;
                 const float2 c2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(nm, nm);
-                float ls[4] = {l, 0.0f, 0.0f, 0.0f};
+                float ls[2] = {l, 0.0f};
                 auto ready = [&](int h) {  // portion h of the weights is written
                     fa_wait_st();
                     fa_before();
@@ -666,15 +652,15 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                     unsigned u[16];
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
-                        const float2 x = fa_fma2(make_float2(__uint_as_float(v[k][2 * c]), __uint_as_float(v[k][2 * c + 1])), c2, nm2);
+                        const float2 x = fma2(make_float2(__uint_as_float(v[k][2 * c]), __uint_as_float(v[k][2 * c + 1])), c2, nm2);
                         u[c] = fa_pack(exp2_approx(x.x), exp2_approx(x.y));
-                        fa_add_pair(ls[2 * (c & 1)], ls[2 * (c & 1) + 1], u[c]);
+                        fa_add_pair(ls[0], ls[1], u[c]);
                     }
                     if (k == 3) ready(0);  // keys 0 .. 95, stored while these were made
                     fa_st(t_s + 16 * k, u);
                 }
                 ready(1);
-                l = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                l = ls[0] + ls[1];
             }
             if (!ok) break;
             if (n > 0) {

@@ -17,36 +17,45 @@ namespace ice {
 // state) is written by the last block to have read it, found by a ticket.
 // ---------------------------------------------------------------------------
 constexpr int kTabThreads = 1024;
+constexpr int kTabSlots = 4;  // consecutive slots of a thread: one search for them, wide stores
 
 struct TabSums {
-    long long v[3][32];
+    unsigned v[3][32];
+    float f[3][32];
 };
 
-// Inclusive block scan of three values per thread; total in tot.
-__device__ __forceinline__ void scan3(long long (&x)[3], long long (&tot)[3], TabSums& sh) {
+// Exclusive block scan of three values per thread and their totals. The sums are modulo 2^32;
+// those in fp32 tell whether one has wrapped (every bound that they are held to is below 2^31).
+__device__ __forceinline__ void scan3(unsigned (&x)[3], unsigned (&tot)[3], bool& wrapped, TabSums& sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1)
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            const long long y = __shfl_up_sync(0xffffffffu, x[k], o);
-            if (lane >= o) x[k] += y;
-        }
-    if (lane == 31)
-#pragma unroll
-        for (int k = 0; k < 3; ++k) sh.v[k][warp] = x[k];
-    __syncthreads();
+    float f[3];
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-        long long y = sh.v[k][lane];
+        const unsigned mine = x[k];
+        f[k] = (float)mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long z = __shfl_up_sync(0xffffffffu, y, o);
-            if (lane >= o) y += z;
+            const unsigned y = __shfl_up_sync(0xffffffffu, x[k], o);
+            if (lane >= o) x[k] += y;
+            f[k] += __shfl_xor_sync(0xffffffffu, f[k], o);
         }
-        tot[k] = __shfl_sync(0xffffffffu, y, 31);
-        const long long before = __shfl_sync(0xffffffffu, y, max(warp - 1, 0));
-        if (warp > 0) x[k] += before;
+        if (lane == 31) {
+            sh.v[k][warp] = x[k];
+            sh.f[k][warp] = f[k];
+        }
+        x[k] -= mine;
+    }
+    __syncthreads();
+    wrapped = false;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const unsigned y = sh.v[k][lane];
+        tot[k] = __reduce_add_sync(0xffffffffu, y);
+        x[k] += __reduce_add_sync(0xffffffffu, lane < warp ? y : 0u);
+        float g = sh.f[k][lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) g += __shfl_xor_sync(0xffffffffu, g, o);
+        wrapped |= g > 4.0e9f;
     }
 }
 
@@ -80,7 +89,7 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(
     const int per = (n + kTabThreads - 1) / kTabThreads;
     const int r0 = min(tid * per, n), r1 = min(r0 + per, n);
     const long long cap = (long long)max_blocks * P;
-    long long x[3] = {0, 0, 0}, tot[3];
+    unsigned x[3] = {0, 0, 0}, tot[3];
     int bad = 0;  // 1: an impossible length, 2: the table's columns do not suffice
     for (int r = r0; r < r1; ++r) {
         const long long o = seq_len[r], w = o + n_new[r];
@@ -96,27 +105,24 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(
         }
     }
     if (bad) atomicOr(&s_bad, bad);
-    long long e[3] = {x[0], x[1], x[2]};
-    scan3(x, tot, sums);  // its barrier also orders s_bad
+    bool wrapped;
+    scan3(x, tot, wrapped, sums);  // its barrier also orders s_bad
     // every block comes to the same verdict
     int code = ICE_OK;
-    if ((s_bad & 1) || head < 0 || tail < head || tail - head > n_pages || tail - head + tot[2] > n_pages)
-        code = ICE_ERR_BOUNDS;
-    else if ((s_bad & 2) || tot[1] > tail - head || tot[0] > n_slots)
-        code = ICE_ERR_CAPACITY;
+    if ((s_bad & 1) || head < 0 || tail < head || tail - head > n_pages) code = ICE_ERR_BOUNDS;
+    else if ((s_bad & 2) || wrapped || tot[1] > tail - head || tot[0] > (unsigned)n_slots) code = ICE_ERR_CAPACITY;
+    else if (tail - head + tot[2] > n_pages) code = ICE_ERR_BOUNDS;
     const bool ok = code == ICE_OK;
     const int n_tok = ok ? (int)tot[0] : 0, n_pop = ok ? (int)tot[1] : 0, n_push = ok ? (int)tot[2] : 0;
     if (ok) {
-#pragma unroll
-        for (int k = 0; k < 3; ++k) e[k] = x[k] - e[k];
         for (int r = r0; r < r1; ++r) {
-            tok_cum[r] = (int)e[0];
-            pop_cum[r] = (int)e[1];
-            push_cum[r] = (int)e[2];
+            tok_cum[r] = (int)x[0];
+            pop_cum[r] = (int)x[1];
+            push_cum[r] = (int)x[2];
             const int o = seq_len[r], w = o + n_new[r], had = (o + P - 1) / P, has = (w + P - 1) / P;
-            e[0] += max(w - o, 0);
-            e[1] += max(has - had, 0);
-            e[2] += max(had - has, 0);
+            x[0] += max(w - o, 0);
+            x[1] += max(has - had, 0);
+            x[2] += max(had - has, 0);
         }
     }
     if (tid == 0) {
@@ -132,20 +138,48 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(
     };
     const int first = blockIdx.x * kTabThreads + tid, step = gridDim.x * kTabThreads;
     for (int r = first; r <= n; r += step) q_start[r] = ok ? tok_cum[r] : 0;
-    for (int i = first; i < n_slots; i += step) {
-        long long slot = -1;
-        int pos = 0;
-        if (i < n_tok) {
-            const int r = find_row(tok_cum, n, i);
-            const int o = seq_len[r];
-            pos = o + i - tok_cum[r];
-            const int had = (o + P - 1) / P, pg = pos / P;
-            const int id = pg < had ? block_table[(long long)r * max_blocks + pg]
-                                    : free_pages[ring(hm, pop_cum[r] + pg - had)];
-            slot = (long long)id * P + (pos - pg * P);
+    const bool wide = ((uintptr_t)slot_map & 15) == 0 && ((uintptr_t)positions & 15) == 0;
+    for (long long i4 = (long long)first * kTabSlots; i4 < n_slots; i4 += (long long)step * kTabSlots) {
+        const int i0 = (int)i4;
+        long long slot[kTabSlots];
+        int pos[kTabSlots];
+        int r = 0, next = 0;  // request of the slot before, first slot of the request after
+        int o = 0, b = 0;
+        if (i0 < n_tok) {
+            r = find_row(tok_cum, n, i0);
+            o = seq_len[r], b = tok_cum[r], next = tok_cum[r + 1];
         }
-        slot_map[i] = slot;
-        if (positions) positions[i] = pos;
+#pragma unroll
+        for (int k = 0; k < kTabSlots; ++k) {
+            const int i = i0 + k;
+            slot[k] = -1;
+            pos[k] = 0;
+            if (i < n_tok) {
+                if (i >= next) {
+                    do ++r;
+                    while (tok_cum[r + 1] <= i);
+                    o = seq_len[r], b = tok_cum[r], next = tok_cum[r + 1];
+                }
+                pos[k] = o + i - b;
+                const int had = (o + P - 1) / P, pg = pos[k] / P;
+                const int id = pg < had ? block_table[(long long)r * max_blocks + pg]
+                                        : free_pages[ring(hm, pop_cum[r] + pg - had)];
+                slot[k] = (long long)id * P + (pos[k] - pg * P);
+            }
+        }
+        if (wide && i0 + kTabSlots <= n_slots) {
+            longlong2* d = reinterpret_cast<longlong2*>(slot_map + i0);
+            d[0] = make_longlong2(slot[0], slot[1]);
+            d[1] = make_longlong2(slot[2], slot[3]);
+            if (positions) *reinterpret_cast<int4*>(positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kTabSlots; ++k)
+                if (i0 + k < n_slots) {
+                    slot_map[i0 + k] = slot[k];
+                    if (positions) positions[i0 + k] = pos[k];
+                }
+        }
     }
     for (int j = first; j < n_pop; j += step) {
         const int r = find_row(pop_cum, n, j);
@@ -161,7 +195,7 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(
     __syncthreads();
     if (tid == 0) {
         __threadfence();
-        s_last = atomicAdd(ticket, 1u) == gridDim.x - 1;
+        s_last = gridDim.x == 1 || atomicAdd(ticket, 1u) == gridDim.x - 1;
     }
     __syncthreads();
     if (!s_last) return;
@@ -179,7 +213,7 @@ cudaError_t launch_paged_tables(int n_req, int max_blocks, int P, long long n_pa
                                 const long long* free_state, int* seq_len_out, long long* free_state_out,
                                 int* q_start, long long* slot_map, int* positions, int n_slots,
                                 unsigned* ticket, int* status, cudaStream_t s) {
-    const int blocks = std::max(1, std::min(152, std::max(n_slots / 4096, n_req / 512)));
+    const int blocks = std::max(1, std::min(152, std::max(n_slots / 1024, n_req / 32)));
     return launch_pdl(tables_kernel, dim3(blocks), dim3(kTabThreads), (size_t)(n_req + 1) * 12, s, n_req,
                       max_blocks, P, n_pages, seq_len, n_new, block_table, free_pages, free_state,
                       seq_len_out, free_state_out, q_start, slot_map, positions, n_slots, ticket, status);
@@ -188,33 +222,44 @@ cudaError_t launch_paged_tables(int n_req, int max_blocks, int P, long long n_pa
 // ---------------------------------------------------------------------------
 // Rows of new tokens into their slots: a copy whose destination is looked up.
 // A row (one token, KV head, K or V) is 16 or 32 pieces of 16 bytes; consecutive
-// threads take consecutive pieces.
+// threads take consecutive pieces. Bound by memory.
 // ---------------------------------------------------------------------------
 constexpr int kAppThreads = 256;
+constexpr int kAppBatch = 4;  // pieces of a thread that are under way together
 
 __global__ void __launch_bounds__(kAppThreads) append_kernel(
     int n_tokens, int H, int P, int shift, long long n_slots, const uint4* k, long long k_stride,
     const uint4* v, long long v_stride, const long long* slot_map, uint4* k_pages, uint4* v_pages,
     int* status) {
     pdl_wait_then_release();
-    const int per_kv = H << shift;  // pieces of a token's K
-    const long long total = (long long)n_tokens * 2 * per_kv;
-    const long long step = (long long)gridDim.x * kAppThreads;
-    for (long long i = (long long)blockIdx.x * kAppThreads + threadIdx.x; i < total; i += step) {
-        const long long t = i / (2 * per_kv);
-        int c = (int)(i - t * (2 * per_kv));
-        const long long slot = slot_map[t];
-        if (slot < 0 || slot >= n_slots) {
-            if (slot != -1) set_status(status, ICE_ERR_BOUNDS);
-            continue;
+    const unsigned per_kv = H << shift, per_tok = 2 * per_kv;  // pieces of a token's K, of a token
+    const long long total = (long long)n_tokens * per_tok;
+    for (long long i0 = (long long)blockIdx.x * kAppThreads * kAppBatch + threadIdx.x; i0 < total;
+         i0 += (long long)gridDim.x * kAppThreads * kAppBatch) {
+        uint4 x[kAppBatch];
+        uint4* dst[kAppBatch];
+#pragma unroll
+        for (int u = 0; u < kAppBatch; ++u) {
+            const long long i = i0 + (long long)u * kAppThreads;
+            dst[u] = nullptr;
+            if (i >= total) continue;
+            const long long t = total <= 0xFFFFFFFFll ? (long long)((unsigned)i / per_tok) : i / per_tok;
+            unsigned c = (unsigned)(i - t * per_tok);
+            const long long slot = slot_map[t];
+            if (slot < 0 || slot >= n_slots) {
+                if (slot != -1) set_status(status, ICE_ERR_BOUNDS);
+                continue;
+            }
+            const bool is_v = c >= per_kv;
+            if (is_v) c -= per_kv;
+            const unsigned page = (unsigned)slot / (unsigned)P;  // n_slots < 2^31
+            const int off = (int)((unsigned)slot - page * P), h = c >> shift, piece = c & ((1 << shift) - 1);
+            x[u] = __ldcs(is_v ? v + t * v_stride + c : k + t * k_stride + c);
+            dst[u] = (is_v ? v_pages : k_pages) + (((((long long)page * H + h) * P + off) << shift) + piece);
         }
-        const bool is_v = c >= per_kv;
-        if (is_v) c -= per_kv;
-        const long long page = slot / P;
-        const int off = (int)(slot - page * P), h = c >> shift, piece = c & ((1 << shift) - 1);
-        const uint4 x = is_v ? v[t * v_stride + c] : k[t * k_stride + c];
-        uint4* dst = is_v ? v_pages : k_pages;
-        dst[(((page * H + h) * P + off) << shift) + piece] = x;
+#pragma unroll
+        for (int u = 0; u < kAppBatch; ++u)
+            if (dst[u] != nullptr) *dst[u] = x[u];
     }
 }
 
@@ -224,7 +269,8 @@ cudaError_t launch_paged_append(int n_tokens, int H, int P, int es, long long n_
                                 cudaStream_t s) {
     const int shift = es == 2 ? 4 : 5;  // 16-byte pieces of a row of 128 elements
     const long long total = (long long)n_tokens * 2 * ((long long)H << shift);
-    const int blocks = (int)std::min<long long>((total + kAppThreads - 1) / kAppThreads, 152 * 8);
+    const int per_block = kAppThreads * kAppBatch;
+    const int blocks = (int)std::min<long long>((total + per_block - 1) / per_block, 152 * 8);
     return launch_pdl(append_kernel, dim3(blocks), dim3(kAppThreads), 0, s, n_tokens, H, P, shift,
                       n_pages * P, (const uint4*)k, k_stride * es / 16, (const uint4*)v, v_stride * es / 16,
                       slot_map, (uint4*)k_pages, (uint4*)v_pages, status);

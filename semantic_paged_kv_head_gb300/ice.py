@@ -494,28 +494,27 @@ class PagedCache:
         block_table and free_pages are updated in place; seq_len_out and free_state_out may
         be seq_len and free_state. n_slots: room for new tokens (entries behind the last
         are -1 in slot_map)."""
-        n, i32, i64 = seq_len.shape[0], torch.int32, torch.int64
-        if seq_len_out is None:
-            seq_len_out = torch.empty_like(seq_len)
-        if free_state_out is None:
-            free_state_out = torch.empty_like(free_state)
-        if q_start is None:
-            q_start = torch.empty((n + 1,), dtype=i32, device=self.device)
-        if slot_map is None:
-            slot_map = torch.empty((n_slots,), dtype=i64, device=self.device)
-        if positions is None:
-            positions = torch.empty((n_slots,), dtype=i32, device=self.device)
-        _check(_lib.ice_paged_tables(
-            self._h, n, self._ints(seq_len, i32, (n,), "seq_len"), self._ints(n_new, i32, (n,), "n_new"),
-            self._ints(block_table, i32, (n, self.params.max_blocks), "block_table"),
-            self._ints(free_pages, i32, (self.params.n_pages,), "free_pages"),
-            self._ints(free_state, i64, (2,), "free_state"),
-            self._ints(seq_len_out, i32, (n,), "seq_len_out"),
-            self._ints(free_state_out, i64, (2,), "free_state_out"),
-            self._ints(q_start, i32, (n + 1,), "q_start"),
-            self._ints(slot_map, i64, (n_slots,), "slot_map"),
-            self._ints(positions, i32, (n_slots,), "positions"), n_slots, _stream(stream)),
-            "ice_paged_tables")
+        n, i32, i64, check = seq_len.shape[0], torch.int32, torch.int64, self._ints
+        ins = (check(seq_len, i32, (n,), "seq_len"), check(n_new, i32, (n,), "n_new"),
+               check(block_table, i32, (n, self.params.max_blocks), "block_table"),
+               check(free_pages, i32, (self.params.n_pages,), "free_pages"),
+               check(free_state, i64, (2,), "free_state"))
+        if seq_len_out is free_state_out is q_start is slot_map is positions is None:
+            # two allocations instead of five (a decode step is bound by the host); no checks needed
+            positions, q_start, seq_len_out = torch.empty(
+                (n_slots + 2 * n + 1,), dtype=i32, device=self.device).split((n_slots, n + 1, n))
+            free_state_out, slot_map = torch.empty((2 + n_slots,), dtype=i64, device=self.device).split((2, n_slots))
+            outs = (seq_len_out.data_ptr(), free_state_out.data_ptr(), q_start.data_ptr(), slot_map.data_ptr(),
+                    positions.data_ptr())
+        else:
+            new = lambda t, d, shape: torch.empty(shape, dtype=d, device=self.device) if t is None else t  # noqa: E731
+            seq_len_out, free_state_out = new(seq_len_out, i32, (n,)), new(free_state_out, i64, (2,))
+            q_start, slot_map = new(q_start, i32, (n + 1,)), new(slot_map, i64, (n_slots,))
+            positions = new(positions, i32, (n_slots,))
+            outs = (check(seq_len_out, i32, (n,), "seq_len_out"), check(free_state_out, i64, (2,), "free_state_out"),
+                    check(q_start, i32, (n + 1,), "q_start"), check(slot_map, i64, (n_slots,), "slot_map"),
+                    check(positions, i32, (n_slots,), "positions"))
+        _check(_lib.ice_paged_tables(self._h, n, *ins, *outs, n_slots, _stream(stream)), "ice_paged_tables")
         return seq_len_out, free_state_out, q_start, slot_map, positions
 
     def append(self, k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor,
@@ -540,7 +539,7 @@ class PagedCache:
         p, n = self.params, seq_len.shape[0]
         qp, qs = self._rows(q, p.n_q_heads, "q")
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         elif out.shape != q.shape:
             raise ValueError("out must be shaped like q")
         kg, vg = self._pages(k_pages, v_pages)

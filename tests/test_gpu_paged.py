@@ -224,9 +224,20 @@ MIXED = [(0, 40), (1, 40), (3, 3), (70, 90), (0, 0), (2, 129), (129, 400)]
     (1, 4, 16, 0, [(1, 0), (2, 1), (4, 2)]),    # or nothing: zeros
     (8, 4, 16, 4000, [(1, 60)]), (1, 1, 16, 90, [(300, 300)]), (1, 4, 16, 2000, [(1, 3000), (1, 2), (1, 700)]),
     (1, 2, 16, 64, [(0, 5), (0, 0)]),           # nothing to do
+    (1, 4, 3, 200, DECODE), (2, 4, 48, 300, DECODE), (5, 1, 63, 257, DECODE),  # pages that fill no tile
+    (1, 8, 16, 3000, [(1, 40), (2, 2500), (1, 129)]),  # one KV head: a range's halves side by side
+    (8, 4, 16, 130, [(700, 700), (650, 900), (1, 5), (40, 60)]),  # long requests, whole and in parts
+    (8, 4, 16, 0, [(1300, 1300)]), (4, 8, 32, 1000, [(17, 20), (16, 300), (33, 33)]),
     (1, 4, 16, 320, [(1, 1 + i % 37) for i in range(150)])])
 def test_attn(ice, dtype, H, G, P, L, reqs):
     _attn_check(ice, _attn_case(H * 1000 + L, dtype, H, G, P, L, reqs))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H,G,extra", [(1, 1, []), (2, 2, [(70, 90), (200, 200)])])
+def test_attn_thousands_of_requests(ice, dtype, H, G, extra):
+    """More requests than the kernels keep the lengths of in shared memory."""
+    _attn_check(ice, _attn_case(21, dtype, H, G, 16, 70, [(1 if i % 5 else 0, 1 + i % 3) for i in range(2500)] + extra))
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -276,6 +287,52 @@ def test_attn_repeats_bit_for_bit(ice):
     a, pc = _attn_run(ice, c)
     for _ in range(3):
         assert torch.equal(_attn_run(ice, c, pc=pc)[0], a)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attn_shapes_share_a_handle(ice, dtype):
+    """Calls of other sizes before and after do not show in a result: scratch and counters are left as found."""
+    big = _attn_case(22, dtype, 2, 4, 16, 900, MIXED + DECODE)
+    small = [_attn_case(23 + i, dtype, 2, 4, 16, L, reqs) for i, (L, reqs) in enumerate(
+        [(0, [(1, 1)]), (5000, [(1, 3)]), (17, [(0, 0), (3, 2)]), (300, [(130, 200)])])]
+    pc = _cache(ice, n_kv_heads=2, n_q_heads=8, page_size=16, n_pages=max(c["n_pages"] for c in [big] + small), dtype=dtype,
+                max_requests=len(big["seq_len"]), max_blocks=max(c["table"].shape[1] for c in [big] + small),
+                max_tokens=big["q"].shape[0])
+    n_pages, cols = pc.params.n_pages, pc.params.max_blocks
+    for c in [big] + small:  # one handle: pools and tables of its sizes
+        for x in ("k", "v"):
+            c[x] = torch.cat([c[x], torch.zeros((n_pages - c[x].shape[0], *c[x].shape[1:]), dtype=dtype)])
+        c["table"] = torch.cat([c["table"], torch.full((c["table"].shape[0], cols - c["table"].shape[1]), -1, dtype=torch.int32)], 1)
+    first = [_attn_check(ice, c, pc=pc) for c in [big] + small]
+    for k in (2, 0, 4, 1, 3, 0):
+        assert torch.equal(_attn_run(ice, ([big] + small)[k], pc=pc)[0], first[k])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attn_graphs_share_a_handle(ice, dtype):
+    """Two captured graphs of one handle, replayed in turn on one stream, on buffers whose contents change."""
+    cs = [_attn_case(31, dtype, 2, 4, 16, 200, MIXED), _attn_case(32, dtype, 2, 4, 16, 200, MIXED)]
+    _, pc = _attn_run(ice, cs[0])
+    x = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in cs[0].items()}
+    graphs, outs = [], []
+    for L in (200, 0):
+        out = torch.empty_like(x["q"])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            pc.attn(x["q"], x["q_start"], x["seq_len"], x["table"], x["k"], x["v"], x["prefix"], L, out=out)
+        graphs.append(g)
+        outs.append(out)
+    for c in (cs[1], cs[0], cs[1]):
+        for k, v in x.items():
+            if isinstance(v, torch.Tensor):
+                v.copy_(c[k])
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert pc.get_error() == 0
+        for out, L in zip(outs, (200, 0)):
+            ref, tol = plain_attn(c["q"], c["q_start"], c["seq_len"], c["table"], c["k"], c["v"], c["prefix"], L)
+            assert bool(((out.cpu().double() - ref).abs() <= tol).all())
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
