@@ -499,23 +499,18 @@ class PagedCache:
                check(block_table, i32, (n, self.params.max_blocks), "block_table"),
                check(free_pages, i32, (self.params.n_pages,), "free_pages"),
                check(free_state, i64, (2,), "free_state"))
-        if seq_len_out is free_state_out is q_start is slot_map is positions is None:
-            # two allocations instead of five (a decode step is bound by the host); no checks needed
-            positions, q_start, seq_len_out = torch.empty(
-                (n_slots + 2 * n + 1,), dtype=i32, device=self.device).split((n_slots, n + 1, n))
-            free_state_out, slot_map = torch.empty((2 + n_slots,), dtype=i64, device=self.device).split((2, n_slots))
-            outs = (seq_len_out.data_ptr(), free_state_out.data_ptr(), q_start.data_ptr(), slot_map.data_ptr(),
-                    positions.data_ptr())
-        else:
-            new = lambda t, d, shape: torch.empty(shape, dtype=d, device=self.device) if t is None else t  # noqa: E731
-            seq_len_out, free_state_out = new(seq_len_out, i32, (n,)), new(free_state_out, i64, (2,))
-            q_start, slot_map = new(q_start, i32, (n + 1,)), new(slot_map, i64, (n_slots,))
-            positions = new(positions, i32, (n_slots,))
-            outs = (check(seq_len_out, i32, (n,), "seq_len_out"), check(free_state_out, i64, (2,), "free_state_out"),
-                    check(q_start, i32, (n + 1,), "q_start"), check(slot_map, i64, (n_slots,), "slot_map"),
-                    check(positions, i32, (n_slots,), "positions"))
-        _check(_lib.ice_paged_tables(self._h, n, *ins, *outs, n_slots, _stream(stream)), "ice_paged_tables")
-        return seq_len_out, free_state_out, q_start, slot_map, positions
+        dev, outs = self.device, []
+        for t, dtype, shape, name in ((seq_len_out, i32, (n,), "seq_len_out"), (free_state_out, i64, (2,), "free_state_out"),
+                                      (q_start, i32, (n + 1,), "q_start"), (slot_map, i64, (n_slots,), "slot_map"),
+                                      (positions, i32, (n_slots,), "positions")):
+            if t is None:
+                t = torch.empty(shape, dtype=dtype, device=dev)
+            else:
+                check(t, dtype, shape, name)
+            outs.append(t)
+        _check(_lib.ice_paged_tables(self._h, n, *ins, *[t.data_ptr() for t in outs], n_slots, _stream(stream)),
+               "ice_paged_tables")
+        return tuple(outs)
 
     def append(self, k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor,
                k_pages: torch.Tensor, v_pages: torch.Tensor, stream=None):
