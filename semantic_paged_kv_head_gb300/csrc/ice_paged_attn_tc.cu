@@ -43,7 +43,7 @@ constexpr int kFaRows = 128;              // rows of a tile (the MMA's M)
 constexpr int kFaKeys = 128;              // key rows of a stage (N of S, K of O)
 constexpr int kFaTileB = kFaRows * kD * 2;  // 32 KB: Q tile, K or V stage
 constexpr int kFaHalfB = kFaTileB / 2;    // 64 dimensions
-constexpr int kFaStagesK = 2, kFaStagesV = 2;
+constexpr int kFaStagesK = 2, kFaStagesV = 2;  // two each: the matrix thread counts in bits
 constexpr int kFaStages = kFaStagesK + kFaStagesV;
 constexpr float kFaSlack = 8.0f;          // growth of the maximum (log2) that is let pass
 
@@ -183,6 +183,37 @@ __device__ __forceinline__ void fa_mma_o_rest(unsigned tmem_o, unsigned tmem_p, 
         " tcgen05.mma.cta_group::1.kind::f16 [%0], [w], dv, %3, p;\n"
         "}\n" ::"r"(tmem_o),
         "r"(tmem_p), "r"(fa_desc_v(sv)), "r"(kFaIdescO), "r"(add ? 1u : 0u)
+        : "memory");
+}
+
+// fa_mma_o_rest, then the stream's next scores (their columns hold the weights until then) and the
+// commit of them: the stretch that a stream waits for, in one statement.
+__device__ __forceinline__ void fa_mma_o_rest_s(unsigned tmem_o, unsigned tmem_s, unsigned sv, unsigned sq, unsigned sk,
+                                                unsigned long long* bar) {
+    asm volatile(
+        "{\n .reg .pred n, p;\n .reg .b32 v, w, q, k;\n .reg .b64 dv, dq, dk;\n setp.ne.b32 n, 0, 0;\n setp.eq.b32 p, 0, 0;\n"
+        " add.u32 v, %2, 768;\n add.u32 w, %1, 48;\n mov.b64 dv, {v, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [w], dv, %3, p;\n"
+        " add.u32 v, %2, 896;\n add.u32 w, %1, 56;\n mov.b64 dv, {v, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [w], dv, %3, p;\n"
+        " add.u32 q, %4, 0;\n add.u32 k, %5, 0;\n mov.b64 dq, {q, " FA_DESC_HI "};\n mov.b64 dk, {k, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%1], dq, dk, %6, n;\n"
+        " add.u32 q, %4, 2;\n add.u32 k, %5, 2;\n mov.b64 dq, {q, " FA_DESC_HI "};\n mov.b64 dk, {k, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%1], dq, dk, %6, p;\n"
+        " add.u32 q, %4, 4;\n add.u32 k, %5, 4;\n mov.b64 dq, {q, " FA_DESC_HI "};\n mov.b64 dk, {k, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%1], dq, dk, %6, p;\n"
+        " add.u32 q, %4, 6;\n add.u32 k, %5, 6;\n mov.b64 dq, {q, " FA_DESC_HI "};\n mov.b64 dk, {k, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%1], dq, dk, %6, p;\n"
+        " add.u32 q, %4, 1024;\n add.u32 k, %5, 1024;\n mov.b64 dq, {q, " FA_DESC_HI "};\n mov.b64 dk, {k, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%1], dq, dk, %6, p;\n"
+        " add.u32 q, %4, 1026;\n add.u32 k, %5, 1026;\n mov.b64 dq, {q, " FA_DESC_HI "};\n mov.b64 dk, {k, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%1], dq, dk, %6, p;\n"
+        " add.u32 q, %4, 1028;\n add.u32 k, %5, 1028;\n mov.b64 dq, {q, " FA_DESC_HI "};\n mov.b64 dk, {k, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%1], dq, dk, %6, p;\n"
+        " add.u32 q, %4, 1030;\n add.u32 k, %5, 1030;\n mov.b64 dq, {q, " FA_DESC_HI "};\n mov.b64 dk, {k, " FA_DESC_HI "};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%1], dq, dk, %6, p;\n"
+        " tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%7];\n}\n" ::"r"(tmem_o),
+        "r"(tmem_s), "r"(fa_desc_v(sv)), "r"(kFaIdescO), "r"(fa_desc_k(sq)), "r"(fa_desc_k(sk)), "r"(kFaIdescS), "r"(smem_u32(bar))
         : "memory");
 }
 
@@ -489,12 +520,76 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 const int ns = it.ns, n0 = ns > 0 ? it.st[0].n : 0, n1 = ns > 1 ? it.st[1].n : 0;
                 const int n = max(n0, n1);
                 if (n == 0) continue;
-                const bool apart = !it.shared;  // each stream has key tiles of its own
                 // query tiles: number, address
                 const unsigned q0 = qn, q1 = it.same_q || n0 == 0 ? qn : qn + 1;
                 const unsigned sq0 = s_q + fa_q_off(q0, it.st[0].ntok * a.G <= kFaFew);
                 const unsigned sq1 = s_q + fa_q_off(q1, it.st[1].ntok * a.G <= kFaFew);
                 qn = n1 > 0 ? q1 + 1 : q0 + 1;
+                if (it.shared) {
+                    // two row tiles on the same key tiles: bound by this thread's own instructions, so
+                    // a round is written out (as rounds of the loop below a tile took 3400 cycles)
+                    const unsigned t0 = tmem, t1 = tmem + 128, o0 = tmem + 256, o1 = tmem + 384;
+                    unsigned ks = kn & 1, sk = s_k + ks * kFaTileB;
+                    ok = fa_wait(&sh.q_full[q0 & 3], (q0 >> 2) & 1, abort) &&
+                         fa_wait(&sh.q_full[q1 & 3], (q1 >> 2) & 1, abort) && fa_wait(&sh.k_full[ks], (kn >> 1) & 1, abort);
+                    if (!ok) break;
+                    fa_after();
+                    fa_mma_s(t0, sq0, sk);
+                    fa_commit(&sh.s_full[0]);
+                    fa_mma_s(t1, sq1, sk);
+                    fa_commit(&sh.s_full[1]);
+                    fa_commit(&sh.k_empty[ks]);
+                    ++kn;
+#pragma unroll 1
+                    for (int left = n - 1; left > 0; --left) {
+                        const unsigned vs = vn & 1, sv = s_v + vs * kFaTileB;
+                        ks = kn & 1, sk = s_k + ks * kFaTileB;
+                        if (!fa_wait(&sh.v_full[vs], (vn >> 1) & 1, abort) || !fa_wait(&sh.k_full[ks], (kn >> 1) & 1, abort) ||
+                            !fa_wait(&sh.p_ready[0][0], pn0 & 1, abort))
+                            break;
+                        fa_after();
+                        fa_mma_o_first(o0, t0, sv, left < n - 1);
+                        if (!fa_wait(&sh.p_ready[0][1], pn0 & 1, abort)) break;
+                        fa_after();
+                        fa_mma_o_rest_s(o0, t0, sv, sq0, sk, &sh.s_full[0]);
+                        ++pn0;
+                        if (!fa_wait(&sh.p_ready[1][0], pn1 & 1, abort)) break;
+                        fa_after();
+                        fa_mma_o_first(o1, t1, sv, left < n - 1);
+                        if (!fa_wait(&sh.p_ready[1][1], pn1 & 1, abort)) break;
+                        fa_after();
+                        fa_mma_o_rest_s(o1, t1, sv, sq1, sk, &sh.s_full[1]);
+                        ++pn1;
+                        fa_commit(&sh.k_empty[ks]);
+                        fa_commit(&sh.v_empty[vs]);
+                        ++kn;
+                        ++vn;
+                    }
+                    ok = !*abort;
+                    if (!ok) break;
+                    // the last scores are issued; the last value tile
+                    fa_commit(&sh.q_empty[q0 & 3]);
+                    fa_commit(&sh.q_empty[q1 & 3]);
+                    const unsigned vs = vn & 1, sv = s_v + vs * kFaTileB;
+                    ok = fa_wait(&sh.v_full[vs], (vn >> 1) & 1, abort) && fa_wait(&sh.p_ready[0][0], pn0 & 1, abort) &&
+                         fa_wait(&sh.p_ready[0][1], pn0 & 1, abort);
+                    if (!ok) break;
+                    fa_after();
+                    fa_mma_o_first(o0, t0, sv, n > 1);
+                    fa_mma_o_rest(o0, t0, sv, true);
+                    fa_commit(&sh.o_done[0]);
+                    ++pn0;
+                    ok = fa_wait(&sh.p_ready[1][0], pn1 & 1, abort) && fa_wait(&sh.p_ready[1][1], pn1 & 1, abort);
+                    if (!ok) break;
+                    fa_after();
+                    fa_mma_o_first(o1, t1, sv, n > 1);
+                    fa_mma_o_rest(o1, t1, sv, true);
+                    fa_commit(&sh.o_done[1]);
+                    ++pn1;
+                    fa_commit(&sh.v_empty[vs]);
+                    ++vn;
+                    continue;
+                }
                 // round j: each stream's products with its j-th value tile, then its scores against
                 // key tile j + 1 (round -1: the first scores)
 #pragma unroll 1
@@ -503,19 +598,18 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                     for (int s = 0; ok && s < ns; ++s) {
                         const int ne = s ? n1 : n0;
                         const unsigned t_p = tmem + 128 * s, vs = vn % kFaStagesV, ks = kn % kFaStagesK;
-                        const bool last = apart || s == ns - 1;  // a shared tile's last user
                         bool k_here = false;
                         if (j >= ne) continue;
                         if (j >= 0) {
                             const unsigned t_o = t_p + 256, sv = s_v + vs * kFaTileB, np = s ? pn1 : pn0;
-                            if (apart || s == 0) ok = fa_wait(&sh.v_full[vs], (vn / kFaStagesV) & 1, abort);
+                            ok = fa_wait(&sh.v_full[vs], (vn / kFaStagesV) & 1, abort);
                             // the weights come in two portions: the first one's products run
                             // while the second is made
                             ok = ok && fa_wait(&sh.p_ready[s][0], np & 1, abort);
                             if (!ok) break;
                             fa_after();
                             fa_mma_o_first(t_o, t_p, sv, j > 0);
-                            if (j + 1 < ne && (apart || s == 0))  // off the path of the last weights
+                            if (j + 1 < ne)  // off the path of the last weights
                                 k_here = fa_try(smem_u32(&sh.k_full[ks]), (kn / kFaStagesK) & 1);
                             ok = fa_wait(&sh.p_ready[s][1], np & 1, abort);
                             if (!ok) break;
@@ -528,20 +622,18 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                         if (j + 1 < ne) {
                             const unsigned q = s ? q1 : q0;
                             if (j < 0) ok = fa_wait(&sh.q_full[q & 3], (q >> 2) & 1, abort);
-                            if ((apart || s == 0) && !k_here) ok = ok && fa_wait(&sh.k_full[ks], (kn / kFaStagesK) & 1, abort);
+                            if (!k_here) ok = ok && fa_wait(&sh.k_full[ks], (kn / kFaStagesK) & 1, abort);
                             if (!ok) break;
                             fa_after();
                             fa_mma_s(t_p, s ? sq1 : sq0, s_k + ks * kFaTileB);
                             fa_commit(&sh.s_full[s]);  // the stream waits for it
-                            if (last) {
-                                fa_commit(&sh.k_empty[ks]);
-                                ++kn;
-                            }
+                            fa_commit(&sh.k_empty[ks]);
+                            ++kn;
                             // a query tile of both is done with the last scores of the two
                             if (it.same_q ? j + 2 == n && (s ? n1 >= n0 : n0 > n1) : j + 2 == ne)
                                 fa_commit(&sh.q_empty[q & 3]);
                         }
-                        if (j >= 0 && last) {
+                        if (j >= 0) {
                             fa_commit(&sh.v_empty[vs]);
                             ++vn;
                         }
