@@ -210,6 +210,9 @@ int ice_paged_attn(ice_paged* pg, int32_t n_req, int32_t n_tokens, const void* q
     if (prefix_len < 0 || prefix_len > (1 << 30) || !stride_ok(pg, q_stride, pg->p.n_q_heads))
         return ICE_ERR_INVALID_ARG;
     if (n_tokens == 0) return ICE_OK;
+    const uintptr_t es = es_of(pg), q0 = (uintptr_t)q, o0 = (uintptr_t)out;
+    const uintptr_t row = (uintptr_t)pg->p.n_q_heads * kD * es;
+    if (q0 < o0 + n_tokens * row && o0 < q0 + (n_tokens - 1) * (uintptr_t)q_stride * es + row) return ICE_ERR_INVALID_ARG;
     Buffers b(pg, stream);
     b.need(q, 16).need(q_start, 4).need(seq_len, 4).need(block_table, 4);
     if (prefix_len > 0) b.need(prefix_table, 4);

@@ -11,28 +11,44 @@
 namespace ice {
 
 // ---------------------------------------------------------------------------
-// One block per SM takes items in turn: one or two tiles of 128 rows (new tokens
-// x G heads) against a range of tiles of KT keys (KT = the whole pages in 128
+// One block per SM takes items in turn: one or two streams, each a tile of 128 rows (new
+// tokens x G heads) against a range of tiles of KT keys (KT = the whole pages in 128
 // keys). For each row tile and key tile
 //   S = Q K^T      tcgen05.mma 128 x 128 x 128, accumulator S in tensor memory
 //   P = 2^(S c - m) one thread a row: S read back, maximum, weights rounded to
 //                  bf16 and written over S
 //   O += P V       tcgen05.mma with A = P from tensor memory, V [key][d] as the
 //                  N-major operand, accumulator O in tensor memory
-// Warps 0-3 and 4-7 do the softmax of row tile 0 and 1, warps 8 and 10 issue the
-// copies, one thread of warp 9 the matrix products (11 fills the warpgroup). With two row tiles the tensor cores work
-// on one while the other's weights are made, and both use the key tile that was
-// read once. Tensor memory is full: S0 S1 O0 O1, 128 columns each.
+// Warps 0-3 and 4-7 do the softmax of stream 0 and 1, warps 8 and 10 issue the
+// copies, one thread of warp 9 the matrix products, one of warp 11 hands out the items. The
+// products of one thread run in order: a stream's next scores may follow its
+// last weights into their columns without a wait. Tensor memory is full: S0 S1 O0 O1,
+// 128 columns each.
+//
+// The two streams are two row tiles of one block (they share the key tile, which is read
+// once), or two KV heads, or two halves of a range, so that one's products run while the
+// other's weights are made.
 //
 // The maximum m that the weights refer to moves only when a row's true maximum
-// has grown by more than 8 (weights stay below 2^8, exact enough in bf16, whose
-// rounding is relative); only then O is read back and rescaled. The sum l is of
-// the rounded weights, the ones that meet V.
+// has grown by more than 8 (weights stay below 2^8; bf16 rounds them by 2^-8 of
+// themselves at most, whatever their size); only then O is read back and rescaled. The sum
+// l is of the rounded weights, the ones that meet V, in fp32.
 //
 // Pages are read by the tensor memory accelerator, a box of P rows x 64 dimensions
-// (128-byte swizzle, the layout that the operand descriptors name), into a ring of
+// (128-byte swizzle, the layout that the operand descriptors name), into rings of
 // 32 KB stages. Key tiles end where pages do; rows of a stage behind the last key
 // are zeroed before they meet weights of zero, whatever the page's free slots hold.
+//
+// Every wait is bounded (kWaitNs); when one runs out the block's roles leave their loops,
+// what is in flight ends, and the status word says ICE_ERR_TIMEOUT.
+//
+// Bound by memory with few rows: 4 requests on 250k tokens, 170 us, 6.07 TB/s (89 % of the
+// measured copy rate); 16 requests with 16k own tokens each on average, 177 us, 5.85 TB/s. With 256
+// rows or more a key tile is bound by the softmax of its two streams (2500 cycles for 16.8 MFLOP,
+// of which the products take 2048): chunks of up to 1021 tokens on 8k, 421 us, 1.24 PFLOP/s (66 %
+// of the measured rate). Tried and not kept: key tiles of 64 with two score buffers a stream (twice
+// the commits, 1.6 times the time), part of the exponentials as polynomials (the issue slots are
+// what is short), weights made before the maximum is known (spills).
 // ---------------------------------------------------------------------------
 constexpr int kFaThreads = 384;
 // registers a thread: 168 at launch, moved from the copy and product warps to the softmax warps.
@@ -463,7 +479,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                     const unsigned bar = smem_u32(&full[st]), dst = dst0 + st * kFaTileB;
                     if (lane == 0) fa_expect(&full[st], (unsigned)(cur.n * a.P * kD * 2));
                     __syncwarp();
-                    // one thread issues all boxes (of lanes with a page each, a box took 140 cycles)
+                    // one thread issues all boxes
 #pragma unroll 1
                     for (int p = 0; p < cur.n; ++p) {
                         const int mine = p < 32 ? cur.row[0] : p < 64 ? cur.row[1] : p < 96 ? cur.row[2] : cur.row[3];
@@ -526,8 +542,8 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 const unsigned sq1 = s_q + fa_q_off(q1, it.st[1].ntok * a.G <= kFaFew);
                 qn = n1 > 0 ? q1 + 1 : q0 + 1;
                 if (it.shared) {
-                    // two row tiles on the same key tiles: bound by this thread's own instructions, so
-                    // a round is written out (as rounds of the loop below a tile took 3400 cycles)
+                    // two row tiles on the same key tiles: this thread's own instructions are on the
+                    // path, so a round is written out (rounds of the loop below: 3 % slower)
                     const unsigned t0 = tmem, t1 = tmem + 128, o0 = tmem + 256, o1 = tmem + 384;
                     unsigned ks = kn & 1, sk = s_k + ks * kFaTileB;
                     ok = fa_wait(&sh.q_full[q0 & 3], (q0 >> 2) & 1, abort) &&
@@ -779,21 +795,18 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 }
 #pragma unroll
                 for (int c = 0; c < 32; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * f);
-                if (!mine) continue;
-                if (st.direct) {
-                    if (tok < valid_tok) {
-                        uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)a.out +
-                                                              ((long long)tok * a.H * a.G + st.h * a.G + row % a.G) * kD + k);
+                if (mine && st.direct && tok < valid_tok) {
+                    uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)a.out +
+                                                          ((long long)tok * a.H * a.G + st.h * a.G + row % a.G) * kD + k);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            unsigned w[4];
+                    for (int c = 0; c < 4; ++c) {
+                        unsigned w[4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                w[e] = fa_pack(__uint_as_float(u[8 * c + 2 * e]), __uint_as_float(u[8 * c + 2 * e + 1]));
-                            dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = fa_pack(__uint_as_float(u[8 * c + 2 * e]), __uint_as_float(u[8 * c + 2 * e + 1]));
+                        dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                } else {
+                } else if (mine && !st.direct) {
                     float* dst = a.part_o + R * kD + k;
 #pragma unroll
                     for (int c = 0; c < 32; c += 8)  // whole sectors of 32 B
@@ -802,6 +815,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                                      "r"(u[c + 7])
                                      : "memory");
                 }
+                __syncwarp();  // the next columns are read by the whole warp
             }
             if (mine && !st.direct) a.part_ml[R] = make_float2(m, l);
             fa_before();

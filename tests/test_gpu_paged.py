@@ -409,7 +409,7 @@ def test_refusals_on_a_live_handle(ice):
     for over in (dict(n_req=0), dict(n_req=3), dict(n_tok=-1), dict(n_tok=3), dict(q=None), dict(q=x["q"].data_ptr() + 2),
                  dict(stride=1023), dict(stride=1028), dict(stride=512), dict(q0=None), dict(lens=None), dict(table=None),
                  dict(pre=None), dict(L=-1), dict(L=(1 << 30) + 1), dict(k=None), dict(v=x["v"].data_ptr() + 8), dict(o=None),
-                 dict(o=out.data_ptr() + 4), dict(lens=host.data_ptr()), dict(table=pinned.data_ptr()), dict(o=host.data_ptr())):
+                 dict(o=out.data_ptr() + 4), dict(o=x["q"].data_ptr()), dict(o=x["q"].data_ptr() + 2048), dict(lens=host.data_ptr()), dict(table=pinned.data_ptr()), dict(o=host.data_ptr())):
         assert attn(**over) == E, over
     assert attn(n_tok=0, q=None) == ice.ICE_OK  # nothing to do
     kv = torch.zeros((2, 2, D), dtype=BF16, device="cuda")
