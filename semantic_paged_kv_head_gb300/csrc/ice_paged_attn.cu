@@ -13,14 +13,18 @@ namespace ice {
 // l' = l 2^(m - m') + sum_t 2^(s_t - m'), and the same factor on the output, with
 // s_t = q . k_t log2(e) / sqrt(d). fp32 has no tensor-core form that keeps its 24 bits.
 //
-// More than kFewRows rows (up to 64): bound by arithmetic. The next tile is copied into shared
-// memory while one is worked on. Threads form a 16 x 16 grid: 4 rows by 4 keys each of the
-// scores, 4 rows by 8 dimensions each of the output, so that a row's 16 threads are half a warp
-// and the statistics need shuffles only.
+// More than kFewRows rows (up to 16 RT = 64): bound by the reads of shared memory that feed the
+// products. The next tile is copied into shared memory while one is worked on, and the page ids
+// of the one after are read. Threads form a 16 x 16 grid: RT rows by 4 keys each of the scores,
+// RT rows by 8 dimensions each of the output, so that a row's 16 threads are half a warp
+// and the statistics need shuffles only. 4 requests of up to 512 tokens on 4k: 1.29 ms, 39.7
+// TFLOP/s.
 //
 // Few rows (a decode step's own tokens): bound by memory. The warps take groups of 4 keys in
 // turn, 8 lanes a key for the scores and 4 dimensions a lane for the output, straight from
 // global memory, the next group's loads under way; their parts meet in shared memory at the end.
+// 24 requests of up to 777 own tokens: 15.0 us, of which about 11 us are the call's fixed part
+// (plan, first loads, joining).
 // ---------------------------------------------------------------------------
 constexpr int kSimtThreads = 256;
 constexpr int kSimtWarps = kSimtThreads / 32;
@@ -94,38 +98,44 @@ __device__ __forceinline__ void few_rows(const PagedAttn& a, const PagedTiles& z
     // groups of 4 keys: 16 a tile; the warp takes every kSimtWarps-th
     const int g_end = it.n * (kSimtKeys / 4);
     float4 kv[4] = {}, vv[4] = {};
-    int key = 0, row = -1;
-    bool own = false;
-    int len = 0;
-    auto fetch = [&](int g) {
+    int row = -1, key1 = 0, end1 = 0, key = 0, end = 0;  // located group; loaded group
+    bool own1 = false, own = false;
+    auto locate = [&](int g) {
         const PagedTile t = tile_of(a, z, it, it.kt0 + g / (kSimtKeys / 4));
-        key = t.key0 + (g % (kSimtKeys / 4)) * 4 + kk;
-        own = t.own;
-        len = t.len;
-        row = key_row(a, t, it.h, key);
+        key1 = t.key0 + (g % (kSimtKeys / 4)) * 4 + kk;
+        own1 = t.own;
+        end1 = t.len;
+        row = key_row(a, t, it.h, key1);
+    };
+    auto load = [&]() {
+        key = key1, own = own1, end = end1;
 #pragma unroll
         for (int i = 0; i < 4; ++i) kv[i] = load_or_zero((const float*)a.k_pages, row, 4 * dd + 32 * i);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             vv[i] = load_or_zero((const float*)a.v_pages, __shfl_sync(0xffffffffu, row, 8 * i), 4 * lane);
     };
+    // while a group is worked on, the next one's rows and the page ids of the one after are under way
 #pragma unroll 1
-    for (int g = warp - kSimtWarps; g < g_end; g += kSimtWarps) {
+    for (int g = warp - 2 * kSimtWarps; g < g_end; g += kSimtWarps) {
         float4 k_now[4], v_now[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) k_now[i] = kv[i], v_now[i] = vv[i];
-        const int key_now = key, len_now = len;
+        const int key_now = key, len_now = end;
         const bool own_now = own;
-        if (g + kSimtWarps < g_end) fetch(g + kSimtWarps);
+        if (g + kSimtWarps >= 0 && g + kSimtWarps < g_end) load();
+        if (g + 2 * kSimtWarps < g_end) locate(g + 2 * kSimtWarps);
         if (g < 0) continue;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            float s = 0.0f;
+            float2 s2 = make_float2(0.0f, 0.0f);  // even and odd dimensions
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float4 q = *reinterpret_cast<const float4*>(sq + r * kD + 4 * dd + 32 * i);
-                s += q.x * k_now[i].x + q.y * k_now[i].y + q.z * k_now[i].z + q.w * k_now[i].w;
+                s2 = fma2(make_float2(q.x, q.y), make_float2(k_now[i].x, k_now[i].y), s2);
+                s2 = fma2(make_float2(q.z, q.w), make_float2(k_now[i].z, k_now[i].w), s2);
             }
+            float s = s2.x + s2.y;
 #pragma unroll
             for (int o = 4; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
             s = key_now < (own_now ? lim[r] : len_now) ? s * a.scale_log2 : -INFINITY;
@@ -136,15 +146,14 @@ __device__ __forceinline__ void few_rows(const PagedAttn& a, const PagedTiles& z
             const float f = exp2_approx(m[r] - mu), p = exp2_approx(s - mu);
             m[r] = mx;
             l[r] = l[r] * f + p;  // of this lane's key
-            acc[r].x *= f, acc[r].y *= f, acc[r].z *= f, acc[r].w *= f;
+            float2 lo = make_float2(acc[r].x * f, acc[r].y * f), hi = make_float2(acc[r].z * f, acc[r].w * f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float w = __shfl_sync(0xffffffffu, p, 8 * i);
-                acc[r].x = fmaf(w, v_now[i].x, acc[r].x);
-                acc[r].y = fmaf(w, v_now[i].y, acc[r].y);
-                acc[r].z = fmaf(w, v_now[i].z, acc[r].z);
-                acc[r].w = fmaf(w, v_now[i].w, acc[r].w);
+                lo = fma2(make_float2(w, w), make_float2(v_now[i].x, v_now[i].y), lo);
+                hi = fma2(make_float2(w, w), make_float2(v_now[i].z, v_now[i].w), hi);
             }
+            acc[r] = make_float4(lo.x, lo.y, hi.x, hi.y);
         }
     }
     float* sm = parts + kSimtWarps * R * kD;
@@ -182,6 +191,7 @@ __device__ __forceinline__ void few_rows(const PagedAttn& a, const PagedTiles& z
     }
 }
 
+template <int RT>  // rows a thread: 16 RT rows a block
 __device__ __forceinline__ void many_rows(const PagedAttn& a, const PagedTiles& z, const PagedStream& it, int valid_tok,
                                           float* smem) {
     float* sQ = smem;
@@ -189,14 +199,18 @@ __device__ __forceinline__ void many_rows(const PagedAttn& a, const PagedTiles& 
     float* sP = sKV + 2 * kSimtStage;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rg = tid >> 4, kg = tid & 15;
     const int nrow = it.ntok * a.G;
-    // a warp copies a row of K and of V at a time
-    auto copy_tile = [&](int kt, int stage) {
+    // a warp copies a row of K and of V at a time; lane i finds its i-th row a tile ahead
+    int rows = -1;
+    auto locate = [&](int kt) {
         const PagedTile t = tile_of(a, z, it, kt);
+        if (lane < kSimtKeys / kSimtWarps) rows = key_row(a, t, it.h, t.key0 + warp + kSimtWarps * lane);
+    };
+    auto copy_tile = [&](int stage) {
         float* k = sKV + stage * kSimtStage;
         float* v = k + kSimtKeys * kSimtStrideK;
-#pragma unroll 2
+#pragma unroll
         for (int i = 0; i < kSimtKeys / kSimtWarps; ++i) {
-            const int r = warp + kSimtWarps * i, row = key_row(a, t, it.h, t.key0 + r);
+            const int r = warp + kSimtWarps * i, row = __shfl_sync(0xffffffffu, rows, i);
             const long long off = (long long)max(row, 0) * kD + 4 * lane;
             copy16(k + r * kSimtStrideK + 4 * lane, (const float*)a.k_pages + off, row >= 0);
             copy16(v + r * kD + 4 * lane, (const float*)a.v_pages + off, row >= 0);
@@ -204,7 +218,7 @@ __device__ __forceinline__ void many_rows(const PagedAttn& a, const PagedTiles& 
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     // row r: token tok0 + r / G, head h G + r % G; rows past the item's are zero
-    for (int x = tid; x < kSimtRows * (kD / 4); x += kSimtThreads) {
+    for (int x = tid; x < 16 * RT * (kD / 4); x += kSimtThreads) {
         const int r = x / (kD / 4), c = (x % (kD / 4)) * 4;
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (r < nrow)
@@ -212,21 +226,22 @@ __device__ __forceinline__ void many_rows(const PagedAttn& a, const PagedTiles& 
                                                  (it.h * a.G + r % a.G) * kD + c);
         *reinterpret_cast<float4*>(sQ + r * kSimtStrideK + c) = v;
     }
-    float m[4], l[4];
-    float2 o[4][4];  // dimensions 4 kg .. + 3, 64 + 4 kg .. + 3
-    int lim[4];
+    float m[RT], l[RT];
+    float2 o[RT][4];  // dimensions 4 kg .. + 3, 64 + 4 kg .. + 3
+    int lim[RT];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < RT; ++j) {
         m[j] = -INFINITY;
         l[j] = 0.0f;
-        const int r = rg * 4 + j;
+        const int r = rg * RT + j;
         lim[j] = r < nrow ? min(it.own_len, it.tok0 + r / a.G + it.lim_off) : 0;  // of own tokens
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[j][k] = make_float2(0.0f, 0.0f);
     }
 #pragma unroll 1
-    for (int i = -1; i < it.n; ++i) {
-        if (i + 1 < it.n) copy_tile(it.kt0 + i + 1, (i + 1) & 1);
+    for (int i = -2; i < it.n; ++i) {
+        if (i >= -1 && i + 1 < it.n) copy_tile((i + 1) & 1);
+        if (i + 2 < it.n) locate(it.kt0 + i + 2);
         if (i < 0) continue;
         const PagedTile t = tile_of(a, z, it, it.kt0 + i);
         const int key0 = t.key0;
@@ -235,20 +250,20 @@ __device__ __forceinline__ void many_rows(const PagedAttn& a, const PagedTiles& 
         if (i + 1 < it.n) asm volatile("cp.async.wait_group 1;" ::: "memory");
         else asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
-        float2 s2[4][4];  // even and odd dimensions
+        float2 s2[RT][4];  // even and odd dimensions
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < RT; ++j)
 #pragma unroll
             for (int k = 0; k < 4; ++k) s2[j][k] = make_float2(0.0f, 0.0f);
 #pragma unroll 4
         for (int c = 0; c < kD; c += 4) {
-            float4 qv[4], kv[4];
+            float4 qv[RT], kv[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) qv[j] = *reinterpret_cast<const float4*>(sQ + (rg * 4 + j) * kSimtStrideK + c);
+            for (int j = 0; j < RT; ++j) qv[j] = *reinterpret_cast<const float4*>(sQ + (rg * RT + j) * kSimtStrideK + c);
 #pragma unroll
             for (int k = 0; k < 4; ++k) kv[k] = *reinterpret_cast<const float4*>(sK + (kg + 16 * k) * kSimtStrideK + c);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < RT; ++j)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     s2[j][k] = fma2(make_float2(qv[j].x, qv[j].y), make_float2(kv[k].x, kv[k].y), s2[j][k]);
@@ -256,7 +271,7 @@ __device__ __forceinline__ void many_rows(const PagedAttn& a, const PagedTiles& 
                 }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < RT; ++j) {
             float mx = m[j];
             const int end = t.own ? lim[j] : t.len;
             float s[4];
@@ -277,21 +292,21 @@ __device__ __forceinline__ void many_rows(const PagedAttn& a, const PagedTiles& 
             for (int k = 0; k < 4; ++k) {
                 const float p = exp2_approx(s[k] - mu);
                 l[j] += p;
-                sP[(rg * 4 + j) * kSimtStrideP + kg + 16 * k] = p;
+                sP[(rg * RT + j) * kSimtStrideP + kg + 16 * k] = p;
             }
         }
         __syncwarp();  // a row's weights are written and read by one warp
 #pragma unroll 2
         for (int k0 = 0; k0 < kSimtKeys; k0 += 4) {
-            float4 pv[4];
+            float4 pv[RT];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) pv[j] = *reinterpret_cast<const float4*>(sP + (rg * 4 + j) * kSimtStrideP + k0);
+            for (int j = 0; j < RT; ++j) pv[j] = *reinterpret_cast<const float4*>(sP + (rg * RT + j) * kSimtStrideP + k0);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const float4 v0 = *reinterpret_cast<const float4*>(sV + (k0 + u) * kD + kg * 4);
                 const float4 v1 = *reinterpret_cast<const float4*>(sV + (k0 + u) * kD + 64 + kg * 4);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < RT; ++j) {
                     const float p = u == 0 ? pv[j].x : u == 1 ? pv[j].y : u == 2 ? pv[j].z : pv[j].w;
                     const float2 p2 = make_float2(p, p);
                     o[j][0] = fma2(p2, make_float2(v0.x, v0.y), o[j][0]);
@@ -304,12 +319,12 @@ __device__ __forceinline__ void many_rows(const PagedAttn& a, const PagedTiles& 
         __syncthreads();  // the tile's memory is free for the copy after the next
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < RT; ++j) {
         float sum = l[j];
 #pragma unroll
         for (int d = 8; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         float2* ml;
-        float* dst = row_dst(a, it, rg * 4 + j, valid_tok, &ml);
+        float* dst = row_dst(a, it, rg * RT + j, valid_tok, &ml);
         if (dst == nullptr) continue;
         const float inv = inverse(sum);
 #pragma unroll
@@ -339,7 +354,9 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(PagedAttn a, P
         const PagedStream it = item.st[0];
         if (item.ns > 0) {
             const int nrow = it.ntok * a.G;
-            if (nrow > kFewRows) many_rows(a, z, it, valid_tok, simt_smem);
+            if (nrow > 32) many_rows<4>(a, z, it, valid_tok, simt_smem);
+            else if (nrow > 16) many_rows<2>(a, z, it, valid_tok, simt_smem);
+            else if (nrow > kFewRows) many_rows<1>(a, z, it, valid_tok, simt_smem);
             else if (nrow > 2) few_rows<8>(a, z, it, valid_tok, simt_smem);
             else few_rows<2>(a, z, it, valid_tok, simt_smem);
         }
@@ -359,7 +376,8 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(PagedAttn a, P
 // o_i), M = max m_i and w_i = l_i 2^(m_i - M): out = sum w_i o_i / sum w_i, zeros where
 // nothing was seen. Rows with one part were written by the attention kernel. Bound by the
 // parts' bytes, read once, where there are many rows (PW = 1), and by the latency of
-// a chain of loads where there are few: the warps of a row then take every PW-th part.
+// a chain of loads where there are few: the warps of a row then take every PW-th part. 4 requests
+// of up to 400 tokens on 8k: 24.5 us cold for 52 MB of parts; decode steps 7 to 15 us cold.
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
@@ -509,9 +527,25 @@ static int prefix_ranges(long long n_base, int tiles, int limit, int n_sm) {
     return best;
 }
 
+// f32 blocks of 64 rows, or of 32 or 16 while that many more prefix items still fit one wave
+// (24 requests of 2 heads on 4k: 64 rows 34 us, 32 rows 26.4 us; 64 rows a head on 32k with 4 KV
+// heads, where blocks of 64 fill the waves: 155 us, blocks of 8 435 us).
+static PagedTiles simt_tiles(const PagedAttn& a, long long rows_cap, int n_sm) {
+    const long long slots = std::min<long long>(rows_cap / ((long long)a.H * a.n_tokens * a.G), kPagedMaxSlots);
+    const long long tiles = std::max(1, (a.prefix_len + kSimtKeys - 1) / kSimtKeys);
+    const long long ranges = std::min<long long>(std::min<long long>(slots / 2, kPagedMaxPrefixSplits), tiles);
+    int rows = kSimtRows;
+    while (rows > 16) {
+        const int t = rows / 2 / a.G;
+        if ((long long)((a.n_tokens + t - 1) / t) * a.H * ranges > n_sm) break;
+        rows /= 2;
+    }
+    return PagedTiles{kSimtKeys, rows / a.G, rows / a.G, 0, 0, 0};
+}
+
 cudaError_t launch_paged_attn(PagedAttn a, int dtype, long long rows_cap, int n_sm, cudaStream_t s) {
     const bool tc = dtype == ICE_BF16;
-    PagedTiles z = tc ? paged_tc_tiles(a.P, a.G) : PagedTiles{kSimtKeys, kSimtRows / a.G, kSimtRows / a.G, 0, 0, 0};
+    PagedTiles z = tc ? paged_tc_tiles(a.P, a.G) : simt_tiles(a, rows_cap, n_sm);
     z.NP = (a.prefix_len + z.KT - 1) / z.KT;
     a.RP = a.n_tokens * a.G;
     const int slots = (int)std::min<long long>(rows_cap / ((long long)a.H * a.RP), kPagedMaxSlots);  // >= 3

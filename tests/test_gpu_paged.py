@@ -233,6 +233,15 @@ def test_attn(ice, dtype, H, G, P, L, reqs):
     _attn_check(ice, _attn_case(H * 1000 + L, dtype, H, G, P, L, reqs))
 
 
+@pytest.mark.parametrize("H,G,L,reqs", [
+    (1, 2, 4096, [(1, 30)] * 24), (1, 1, 700, [(1, 9)] * 40), (2, 8, 200, [(3, 20), (2, 2), (1, 70)]), (4, 4, 3000, [(1, 5)] * 16),
+    (1, 1, 9000, [(16, 16), (1, 1)]), (1, 2, 300, [(9, 9), (8, 30), (16, 200), (33, 40)]), (1, 8, 0, [(90, 150), (2, 40), (4, 4)]),
+    (1, 4, 64, [(200, 300)])])
+def test_attn_f32_row_blocks(ice, H, G, L, reqs):
+    """Blocks of 16, 32 and 64 rows, full and not, and requests on both sides of a block's tokens."""
+    _attn_check(ice, _attn_case(L + G, F32, H, G, 16, L, reqs))
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("H,G,extra", [(1, 1, []), (2, 2, [(70, 90), (200, 200)])])
 def test_attn_thousands_of_requests(ice, dtype, H, G, extra):
