@@ -16,7 +16,7 @@ namespace ice {
 // no block waits for another. What a call may replace in place (lengths, ring
 // state) is written by the last block to have read it, found by a ticket.
 // Bound by latency: the launch, the scan and the look-ups in a row, 6.5 us for 16 requests,
-// 8.4 us for 256. 4096 requests with 1.05 million new tokens: 14.9 us, 12.8 MB written; four
+// 8.4 us for 256. 4096 requests with 1.03 million new tokens: 14.9 us, 12.8 MB written; four
 // slots a thread took one search and a wide store (one slot a thread: 21 us).
 // ---------------------------------------------------------------------------
 constexpr int kTabThreads = 1024;
