@@ -108,7 +108,7 @@ int ice_paged_create(const ice_paged_params* params, ice_paged** out) {
     pg->p = *params;
     pg->G = params->n_q_heads / params->n_kv_heads;
     const long long R = (long long)params->max_tokens * params->n_q_heads;
-    pg->rows_cap = std::max(3 * R, std::min(64 * R, 262144LL));
+    pg->rows_cap = std::max(3 * R, std::min(128 * R, 262144LL));
     if (cudaGetDevice(&pg->device) != cudaSuccess ||
         cudaDeviceGetAttribute(&pg->n_sm, cudaDevAttrMultiProcessorCount, pg->device) != cudaSuccess ||
         paged_prepare() != cudaSuccess) {

@@ -509,16 +509,20 @@ cudaError_t paged_prepare() {
                                 kSimtSmem + (kPagedMaxRequests + 1) * 4);
 }
 
-// Ranges of the prefix: n_base row blocks x heads, each range a wave's share of
-// tiles. The time of s ranges is taken as waves x (tiles of a range + the fixed cost of
-// an item, in tiles); the least wins, the fewest ranges among equals.
-static int prefix_ranges(long long n_base, int tiles, int limit, int n_sm) {
-    constexpr int kItemCost = 3;
+// Ranges of the prefix: n_base row blocks x heads, each range a wave's share of tiles, `streams` of
+// them side by side. The time of s ranges is taken as waves x (steps of a range + the fixed cost
+// of an item, in steps), and that of the own items (taken as kOwnCost steps each: their lengths are
+// on the GPU) that do not fit beside the last wave; the least wins, the fewest ranges among equals.
+// Without the own items in the model 16 requests of 500 own tokens at most on 36864 took 48 us (19
+// ranges, a full wave), with them 45 us (16).
+static int prefix_ranges(long long n_base, int tiles, int limit, int n_sm, int streams, int item_cost, long long own) {
+    constexpr int kOwnCost = 4;
     int best = 1;
     long long best_t = -1;
     for (int s = 1; s <= std::min(limit, tiles); ++s) {
-        const long long waves = (n_base * s + n_sm - 1) / n_sm;
-        const long long t = waves * ((tiles + s - 1) / s + kItemCost);
+        const long long waves = (n_base * s + n_sm - 1) / n_sm, item = (tiles + streams * s - 1) / (streams * s) + item_cost;
+        const long long beside = (waves * n_sm - n_base * s) * (item / kOwnCost), rest = std::max(0LL, own - beside);
+        const long long t = waves * item + (rest + n_sm - 1) / n_sm * kOwnCost;
         if (best_t < 0 || t < best_t) {
             best_t = t;
             best = s;
@@ -528,8 +532,8 @@ static int prefix_ranges(long long n_base, int tiles, int limit, int n_sm) {
 }
 
 // f32 blocks of 64 rows, or of 32 or 16 while that many more prefix items still fit one wave
-// (24 requests of 2 heads on 4k: 64 rows 34 us, 32 rows 26.4 us; 64 rows a head on 32k with 4 KV
-// heads, where blocks of 64 fill the waves: 155 us, blocks of 8 435 us).
+// (24 requests of 2 heads on 4k: 64 rows 34 us, 32 rows 24 us; 64 rows a head on 32k with 4 KV
+// heads, where blocks of 64 fill the waves: 139 us, blocks of 8 over 400 us).
 static PagedTiles simt_tiles(const PagedAttn& a, long long rows_cap, int n_sm) {
     const long long slots = std::min<long long>(rows_cap / ((long long)a.H * a.n_tokens * a.G), kPagedMaxSlots);
     const long long tiles = std::max(1, (a.prefix_len + kSimtKeys - 1) / kSimtKeys);
@@ -554,7 +558,11 @@ cudaError_t launch_paged_attn(PagedAttn a, int dtype, long long rows_cap, int n_
     if (a.prefix_len > 0) {
         const int tiles = z.NP, limit = std::min(slots / 2, kPagedMaxPrefixSplits);
         const bool twin = a.n_tokens <= z.TD;  // two parts a range
-        a.prefix_splits = prefix_ranges(n_base, tiles, twin ? std::max(1, limit / 2) : limit, n_sm);
+        // bf16: an item's end takes 7 us with two full row tiles, of 1.25 us a step. f32: own items
+        // are short beside a tile of the prefix's
+        const long long own = tc ? (long long)std::min(a.n_req, a.n_tokens) * ((a.H + 1) / 2) : 0;
+        a.prefix_splits = prefix_ranges(n_base, tiles, twin ? std::max(1, limit / 2) : limit, n_sm, twin ? 2 : 1,
+                                        tc && !twin ? 6 : 3, own);
         if (twin) a.prefix_splits = std::min(std::min(2 * a.prefix_splits, limit), tiles);
     }
     a.max_splits = slots - a.prefix_splits;
