@@ -13,17 +13,17 @@ namespace ice {
 // l' = l 2^(m - m') + sum_t 2^(s_t - m'), and the same factor on the output, with
 // s_t = q . k_t log2(e) / sqrt(d). fp32 has no tensor-core form that keeps its 24 bits.
 //
-// More than kFewRows rows (up to 16 RT = 64): bound by the reads of shared memory that feed the
-// products. The next tile is copied into shared memory while one is worked on, and the page ids
-// of the one after are read. Threads form a 16 x 16 grid: RT rows by 4 keys each of the scores,
-// RT rows by 8 dimensions each of the output, so that a row's 16 threads are half a warp
-// and the statistics need shuffles only. 4 requests of up to 512 tokens on 4k: 1.29 ms, 39.7
-// TFLOP/s.
+// More than kFewRows rows (up to 64): the next tile is copied into shared memory while one is worked
+// on, and the page ids of the one after are read. A warp has RW rows: a lane makes the scores of
+// two keys, and then four dimensions of the output, so that the statistics need shuffles only, and
+// the rows' operands are read once a warp. 4 requests of up to 512 tokens on 4k: 1.28 ms, 40 TFLOP/s,
+// half of what the fp32 units give; neither they (56 %) nor shared memory (about half, by count) are full. 16 warps
+// of half the rows were slower (1.51 ms, spills), operands one step ahead in registers no faster.
 //
 // Few rows (a decode step's own tokens): bound by memory. The warps take groups of 4 keys in
 // turn, 8 lanes a key for the scores and 4 dimensions a lane for the output, straight from
 // global memory, the next group's loads under way; their parts meet in shared memory at the end.
-// 24 requests of up to 777 own tokens: 15.0 us, of which about 11 us are the call's fixed part
+// 24 requests of up to 777 own tokens: 14.0 us, of which about 11 us are the call's fixed part
 // (plan, first loads, joining).
 // ---------------------------------------------------------------------------
 constexpr int kSimtThreads = 256;
@@ -191,13 +191,13 @@ __device__ __forceinline__ void few_rows(const PagedAttn& a, const PagedTiles& z
     }
 }
 
-template <int RT>  // rows a thread: 16 RT rows a block
+template <int RW>  // rows a warp: 8 RW rows a block
 __device__ __forceinline__ void many_rows(const PagedAttn& a, const PagedTiles& z, const PagedStream& it, int valid_tok,
                                           float* smem) {
     float* sQ = smem;
     float* sKV = sQ + kSimtRows * kSimtStrideK;
     float* sP = sKV + 2 * kSimtStage;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rg = tid >> 4, kg = tid & 15;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nrow = it.ntok * a.G;
     // a warp copies a row of K and of V at a time; lane i finds its i-th row a tile ahead
     int rows = -1;
@@ -218,7 +218,7 @@ __device__ __forceinline__ void many_rows(const PagedAttn& a, const PagedTiles& 
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     // row r: token tok0 + r / G, head h G + r % G; rows past the item's are zero
-    for (int x = tid; x < 16 * RT * (kD / 4); x += kSimtThreads) {
+    for (int x = tid; x < kSimtWarps * RW * (kD / 4); x += kSimtThreads) {
         const int r = x / (kD / 4), c = (x % (kD / 4)) * 4;
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (r < nrow)
@@ -226,17 +226,17 @@ __device__ __forceinline__ void many_rows(const PagedAttn& a, const PagedTiles& 
                                                  (it.h * a.G + r % a.G) * kD + c);
         *reinterpret_cast<float4*>(sQ + r * kSimtStrideK + c) = v;
     }
-    float m[RT], l[RT];
-    float2 o[RT][4];  // dimensions 4 kg .. + 3, 64 + 4 kg .. + 3
-    int lim[RT];
+    float m[RW], l[RW];
+    float2 o[RW][2];  // dimensions 4 lane .. + 3
+    int lim[RW];
 #pragma unroll
-    for (int j = 0; j < RT; ++j) {
+    for (int j = 0; j < RW; ++j) {
         m[j] = -INFINITY;
         l[j] = 0.0f;
-        const int r = rg * RT + j;
+        const int r = warp * RW + j;
         lim[j] = r < nrow ? min(it.own_len, it.tok0 + r / a.G + it.lim_off) : 0;  // of own tokens
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[j][k] = make_float2(0.0f, 0.0f);
+        for (int k = 0; k < 2; ++k) o[j][k] = make_float2(0.0f, 0.0f);
     }
 #pragma unroll 1
     for (int i = -2; i < it.n; ++i) {
@@ -250,88 +250,82 @@ __device__ __forceinline__ void many_rows(const PagedAttn& a, const PagedTiles& 
         if (i + 1 < it.n) asm volatile("cp.async.wait_group 1;" ::: "memory");
         else asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
-        float2 s2[RT][4];  // even and odd dimensions
+        float2 s2[RW][2];  // even and odd dimensions
 #pragma unroll
-        for (int j = 0; j < RT; ++j)
+        for (int j = 0; j < RW; ++j)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s2[j][k] = make_float2(0.0f, 0.0f);
+            for (int k = 0; k < 2; ++k) s2[j][k] = make_float2(0.0f, 0.0f);
 #pragma unroll 4
         for (int c = 0; c < kD; c += 4) {
-            float4 qv[RT], kv[4];
+            float4 qv[RW], kv[2];
 #pragma unroll
-            for (int j = 0; j < RT; ++j) qv[j] = *reinterpret_cast<const float4*>(sQ + (rg * RT + j) * kSimtStrideK + c);
+            for (int j = 0; j < RW; ++j) qv[j] = *reinterpret_cast<const float4*>(sQ + (warp * RW + j) * kSimtStrideK + c);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) kv[k] = *reinterpret_cast<const float4*>(sK + (kg + 16 * k) * kSimtStrideK + c);
+            for (int k = 0; k < 2; ++k) kv[k] = *reinterpret_cast<const float4*>(sK + (lane + 32 * k) * kSimtStrideK + c);
 #pragma unroll
-            for (int j = 0; j < RT; ++j)
+            for (int j = 0; j < RW; ++j)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < 2; ++k) {
                     s2[j][k] = fma2(make_float2(qv[j].x, qv[j].y), make_float2(kv[k].x, kv[k].y), s2[j][k]);
                     s2[j][k] = fma2(make_float2(qv[j].z, qv[j].w), make_float2(kv[k].z, kv[k].w), s2[j][k]);
                 }
         }
 #pragma unroll
-        for (int j = 0; j < RT; ++j) {
+        for (int j = 0; j < RW; ++j) {
             float mx = m[j];
             const int end = t.own ? lim[j] : t.len;
-            float s[4];
+            float s[2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                s[k] = key0 + kg + 16 * k < end ? (s2[j][k].x + s2[j][k].y) * a.scale_log2 : -INFINITY;
+            for (int k = 0; k < 2; ++k) {
+                s[k] = key0 + lane + 32 * k < end ? (s2[j][k].x + s2[j][k].y) * a.scale_log2 : -INFINITY;
                 mx = fmaxf(mx, s[k]);
             }
 #pragma unroll
-            for (int d = 8; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            for (int d = 16; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
             const float mu = mx == -INFINITY ? 0.0f : mx;  // nothing seen yet: all weights 0
             const float f = exp2_approx(m[j] - mu);
             m[j] = mx;
             l[j] *= f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) o[j][k].x *= f, o[j][k].y *= f;
+            for (int k = 0; k < 2; ++k) o[j][k].x *= f, o[j][k].y *= f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 2; ++k) {
                 const float p = exp2_approx(s[k] - mu);
                 l[j] += p;
-                sP[(rg * RT + j) * kSimtStrideP + kg + 16 * k] = p;
+                sP[(warp * RW + j) * kSimtStrideP + lane + 32 * k] = p;
             }
         }
         __syncwarp();  // a row's weights are written and read by one warp
 #pragma unroll 2
         for (int k0 = 0; k0 < kSimtKeys; k0 += 4) {
-            float4 pv[RT];
+            float4 pv[RW];
 #pragma unroll
-            for (int j = 0; j < RT; ++j) pv[j] = *reinterpret_cast<const float4*>(sP + (rg * RT + j) * kSimtStrideP + k0);
+            for (int j = 0; j < RW; ++j) pv[j] = *reinterpret_cast<const float4*>(sP + (warp * RW + j) * kSimtStrideP + k0);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const float4 v0 = *reinterpret_cast<const float4*>(sV + (k0 + u) * kD + kg * 4);
-                const float4 v1 = *reinterpret_cast<const float4*>(sV + (k0 + u) * kD + 64 + kg * 4);
+                const float4 v0 = *reinterpret_cast<const float4*>(sV + (k0 + u) * kD + lane * 4);
 #pragma unroll
-                for (int j = 0; j < RT; ++j) {
+                for (int j = 0; j < RW; ++j) {
                     const float p = u == 0 ? pv[j].x : u == 1 ? pv[j].y : u == 2 ? pv[j].z : pv[j].w;
                     const float2 p2 = make_float2(p, p);
                     o[j][0] = fma2(p2, make_float2(v0.x, v0.y), o[j][0]);
                     o[j][1] = fma2(p2, make_float2(v0.z, v0.w), o[j][1]);
-                    o[j][2] = fma2(p2, make_float2(v1.x, v1.y), o[j][2]);
-                    o[j][3] = fma2(p2, make_float2(v1.z, v1.w), o[j][3]);
                 }
             }
         }
         __syncthreads();  // the tile's memory is free for the copy after the next
     }
 #pragma unroll
-    for (int j = 0; j < RT; ++j) {
+    for (int j = 0; j < RW; ++j) {
         float sum = l[j];
 #pragma unroll
-        for (int d = 8; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         float2* ml;
-        float* dst = row_dst(a, it, rg * RT + j, valid_tok, &ml);
+        float* dst = row_dst(a, it, warp * RW + j, valid_tok, &ml);
         if (dst == nullptr) continue;
         const float inv = inverse(sum);
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-            *reinterpret_cast<float4*>(dst + 64 * k + kg * 4) =
-                make_float4(o[j][2 * k].x * inv, o[j][2 * k].y * inv, o[j][2 * k + 1].x * inv, o[j][2 * k + 1].y * inv);
-        if (ml != nullptr && kg == 0) *ml = make_float2(m[j], sum);
+        *reinterpret_cast<float4*>(dst + lane * 4) = make_float4(o[j][0].x * inv, o[j][0].y * inv, o[j][1].x * inv, o[j][1].y * inv);
+        if (ml != nullptr && lane == 0) *ml = make_float2(m[j], sum);
     }
 }
 
@@ -354,9 +348,9 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(PagedAttn a, P
         const PagedStream it = item.st[0];
         if (item.ns > 0) {
             const int nrow = it.ntok * a.G;
-            if (nrow > 32) many_rows<4>(a, z, it, valid_tok, simt_smem);
-            else if (nrow > 16) many_rows<2>(a, z, it, valid_tok, simt_smem);
-            else if (nrow > kFewRows) many_rows<1>(a, z, it, valid_tok, simt_smem);
+            if (nrow > 32) many_rows<8>(a, z, it, valid_tok, simt_smem);
+            else if (nrow > 16) many_rows<4>(a, z, it, valid_tok, simt_smem);
+            else if (nrow > kFewRows) many_rows<2>(a, z, it, valid_tok, simt_smem);
             else if (nrow > 2) few_rows<8>(a, z, it, valid_tok, simt_smem);
             else few_rows<2>(a, z, it, valid_tok, simt_smem);
         }
@@ -510,19 +504,19 @@ cudaError_t paged_prepare() {
 }
 
 // Ranges of the prefix: n_base row blocks x heads, each range a wave's share of tiles, `streams` of
-// them side by side. The time of s ranges is taken as waves x (steps of a range + the fixed cost
-// of an item, in steps), and that of the own items (taken as kOwnCost steps each: their lengths are
-// on the GPU) that do not fit beside the last wave; the least wins, the fewest ranges among equals.
+// them side by side. The time of s ranges, in half steps, is taken as waves x (steps of a range +
+// the fixed cost of an item), and that of the own items (own_cost each: their lengths are on the
+// GPU) that do not fit beside the last wave; the least wins, the fewest ranges among equals.
 // Without the own items in the model 16 requests of 500 own tokens at most on 36864 took 48 us (19
 // ranges, a full wave), with them 45 us (16).
-static int prefix_ranges(long long n_base, int tiles, int limit, int n_sm, int streams, int item_cost, long long own) {
-    constexpr int kOwnCost = 4;
+static int prefix_ranges(long long n_base, int tiles, int limit, int n_sm, int streams, int item_cost, long long own,
+                         int own_cost) {
     int best = 1;
     long long best_t = -1;
     for (int s = 1; s <= std::min(limit, tiles); ++s) {
-        const long long waves = (n_base * s + n_sm - 1) / n_sm, item = (tiles + streams * s - 1) / (streams * s) + item_cost;
-        const long long beside = (waves * n_sm - n_base * s) * (item / kOwnCost), rest = std::max(0LL, own - beside);
-        const long long t = waves * item + (rest + n_sm - 1) / n_sm * kOwnCost;
+        const long long waves = (n_base * s + n_sm - 1) / n_sm, item = 2 * ((tiles + streams * s - 1) / (streams * s)) + item_cost;
+        const long long beside = (waves * n_sm - n_base * s) * (item / own_cost), rest = std::max(0LL, own - beside);
+        const long long t = waves * item + (rest + n_sm - 1) / n_sm * own_cost;
         if (best_t < 0 || t < best_t) {
             best_t = t;
             best = s;
@@ -558,11 +552,11 @@ cudaError_t launch_paged_attn(PagedAttn a, int dtype, long long rows_cap, int n_
     if (a.prefix_len > 0) {
         const int tiles = z.NP, limit = std::min(slots / 2, kPagedMaxPrefixSplits);
         const bool twin = a.n_tokens <= z.TD;  // two parts a range
-        // bf16: an item's end takes 7 us with two full row tiles, of 1.25 us a step. f32: own items
-        // are short beside a tile of the prefix's
+        // bf16: an item's end takes 7 us with two full row tiles, of 1.25 us a step, and an own item 5;
+        // with two parts side by side a step takes 3 us. f32: own items are short beside a tile
         const long long own = tc ? (long long)std::min(a.n_req, a.n_tokens) * ((a.H + 1) / 2) : 0;
         a.prefix_splits = prefix_ranges(n_base, tiles, twin ? std::max(1, limit / 2) : limit, n_sm, twin ? 2 : 1,
-                                        tc && !twin ? 6 : 3, own);
+                                        !tc ? 6 : twin ? 4 : 12, own, twin ? 5 : 8);
         if (twin) a.prefix_splits = std::min(std::min(2 * a.prefix_splits, limit), tiles);
     }
     a.max_splits = slots - a.prefix_splits;

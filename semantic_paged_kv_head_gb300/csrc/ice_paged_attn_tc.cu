@@ -42,7 +42,7 @@ namespace ice {
 // Every wait is bounded (kWaitNs); when one runs out the block's roles leave their loops,
 // what is in flight ends, and the status word says ICE_ERR_TIMEOUT.
 //
-// Bound by memory with few rows: 4 requests on 250k tokens, 170 us, 6.07 TB/s (89 % of the
+// Bound by memory with few rows: 4 requests on 250k tokens, 168 us, 6.13 TB/s (90 % of the
 // measured copy rate); 16 requests with 16k own tokens each on average, 177 us, 5.85 TB/s. With 256
 // rows or more a key tile is bound by the softmax of its two streams (2500 cycles for 16.8 MFLOP,
 // of which the products take 2048): chunks of up to 1021 tokens on 8k, 421 us, 1.24 PFLOP/s (66 %
