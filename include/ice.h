@@ -406,6 +406,8 @@ int ice_key_codes_noalloc(const ice_params* params, const void* keys, int64_t n_
  *    in a CUDA graph and replayed as these change. Values out of range are
  *    reported through ice_paged_get_error; no memory outside the given buffers is
  *    read or written for them.
+ *  - a buffer that a call writes overlaps no other buffer of the call, unless said
+ *    below.
  *  - calls on one handle share its scratch: on different streams (or as captured
  *    graphs) they must be ordered by the caller.
  */

@@ -494,6 +494,10 @@ class PagedCache:
         block_table and free_pages are updated in place; seq_len_out and free_state_out may
         be seq_len and free_state. n_slots: room for new tokens (entries behind the last
         are -1 in slot_map)."""
+        if stream is not None:  # what is allocated here belongs to the stream that writes it
+            with torch.cuda.stream(stream):
+                return self.tables(seq_len, n_new, block_table, free_pages, free_state, n_slots, seq_len_out,
+                                   free_state_out, q_start, slot_map, positions)
         n, i32, i64, check = seq_len.shape[0], torch.int32, torch.int64, self._ints
         ins = (check(seq_len, i32, (n,), "seq_len"), check(n_new, i32, (n,), "n_new"),
                check(block_table, i32, (n, self.params.max_blocks), "block_table"),
@@ -508,7 +512,7 @@ class PagedCache:
             else:
                 check(t, dtype, shape, name)
             outs.append(t)
-        _check(_lib.ice_paged_tables(self._h, n, *ins, *[t.data_ptr() for t in outs], n_slots, _stream(stream)),
+        _check(_lib.ice_paged_tables(self._h, n, *ins, *[t.data_ptr() for t in outs], n_slots, _stream()),
                "ice_paged_tables")
         return tuple(outs)
 
@@ -531,6 +535,9 @@ class PagedCache:
              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """ice_paged_attn of q [tokens, q_heads, d] (a token stride is allowed); returns out,
         contiguous."""
+        if stream is not None:  # what is allocated here belongs to the stream that writes it
+            with torch.cuda.stream(stream):
+                return self.attn(q, q_start, seq_len, block_table, k_pages, v_pages, prefix_table, prefix_len, out)
         p, n = self.params, seq_len.shape[0]
         qp, qs = self._rows(q, p.n_q_heads, "q")
         if out is None:
@@ -547,7 +554,7 @@ class PagedCache:
             self._h, n, q.shape[0], qp, qs, self._ints(q_start, torch.int32, (n + 1,), "q_start"),
             self._ints(seq_len, torch.int32, (n,), "seq_len"),
             self._ints(block_table, torch.int32, (n, p.max_blocks), "block_table"), pt, int(prefix_len),
-            kg, vg, _dev_ptr(out, self.dtype, "out", host_ok=False), _stream(stream)), "ice_paged_attn")
+            kg, vg, _dev_ptr(out, self.dtype, "out", host_ok=False), _stream()), "ice_paged_attn")
         return out
 
     # -- status, teardown ------------------------------------------------------------------

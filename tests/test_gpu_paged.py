@@ -418,7 +418,8 @@ def test_refusals_on_a_live_handle(ice):
     for over in (dict(n_req=0), dict(n_req=3), dict(n_tok=-1), dict(n_tok=3), dict(q=None), dict(q=x["q"].data_ptr() + 2),
                  dict(stride=1023), dict(stride=1028), dict(stride=512), dict(q0=None), dict(lens=None), dict(table=None),
                  dict(pre=None), dict(L=-1), dict(L=(1 << 30) + 1), dict(k=None), dict(v=x["v"].data_ptr() + 8), dict(o=None),
-                 dict(o=out.data_ptr() + 4), dict(o=x["q"].data_ptr()), dict(o=x["q"].data_ptr() + 2048), dict(lens=host.data_ptr()), dict(table=pinned.data_ptr()), dict(o=host.data_ptr())):
+                 dict(o=out.data_ptr() + 4), dict(o=x["q"].data_ptr()), dict(o=x["q"].data_ptr() + 2048),
+                 dict(lens=host.data_ptr()), dict(table=pinned.data_ptr()), dict(o=host.data_ptr())):
         assert attn(**over) == E, over
     assert attn(n_tok=0, q=None) == ice.ICE_OK  # nothing to do
     kv = torch.zeros((2, 2, D), dtype=BF16, device="cuda")
@@ -476,6 +477,32 @@ def test_binding_refusals(ice):
 
 
 # ---- streams, graphs, and the three calls together ------------------------------------------
+
+def test_outputs_belong_to_the_given_stream(ice):
+    """Memory that was freed while the current stream still writes to it is not what a call on another
+    stream gets for its outputs."""
+    c = _attn_case(13, BF16, 2, 4, 16, 100, [(1, 40), (1, 50)])
+    good, pc = _attn_run(ice, c)
+    x = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in c.items()}
+    lens, table, ring, state = pc.new_tables(2)
+    new = torch.tensor([3, 5], dtype=torch.int32, device="cuda")
+    plain = [t.tolist() for t in pc.tables(lens, new, table.clone(), ring.clone(), state, 8)]
+    table2, ring2 = table.clone(), ring.clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    late = [torch.empty_like(good)] + [torch.empty(n, dtype=d, device="cuda") for n, d in
+                                       ((2, torch.int32), (2, torch.int64), (3, torch.int32), (8, torch.int64), (8, torch.int32))]
+    torch.cuda._sleep(100_000_000)  # about 50 ms
+    for t in late:
+        t.fill_(77)
+    del late, t
+    out = pc.attn(x["q"], x["q_start"], x["seq_len"], x["table"], x["k"], x["v"], x["prefix"], x["L"], stream=side)
+    got = pc.tables(lens, new, table2, ring2, state, 8, stream=side)
+    torch.cuda.synchronize()
+    assert pc.get_error() == 0
+    assert torch.equal(out, good)
+    assert [t.tolist() for t in got] == plain
+
 
 def _steps(seed, n_steps, B):
     """Changes of the lengths over a serving loop: prompts, decode steps, rejected drafts, an end and a new
