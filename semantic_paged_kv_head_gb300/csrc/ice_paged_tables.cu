@@ -16,8 +16,9 @@ namespace ice {
 // no block waits for another. What a call may replace in place (lengths, ring
 // state) is written by the last block to have read it, found by a ticket.
 // Bound by latency: the launch, the scan and the look-ups in a row, 6.5 us for 16 requests,
-// 8.4 us for 256. 4096 requests with 1.03 million new tokens: 14.9 us, 12.8 MB written; four
-// slots a thread took one search and a wide store (one slot a thread: 21 us).
+// 8.4 us for 256. 4096 requests with 1.03 million new tokens: 13.8 us, 12.8 MB written; four
+// slots a thread take one search, one divide and a wide store (one slot a thread: 21 us, a divide
+// a slot 14.9, eight slots a thread 14.4 and 1.7 us more for the small calls).
 // ---------------------------------------------------------------------------
 constexpr int kTabThreads = 1024;
 constexpr int kTabSlots = 4;  // consecutive slots of a thread: one search for them, wide stores
@@ -147,28 +148,34 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(
         const int i0 = (int)i4;
         long long slot[kTabSlots];
         int pos[kTabSlots];
-        int r = 0, next = 0;  // request of the slot before, first slot of the request after
-        int o = 0, b = 0;
-        if (i0 < n_tok) {
-            r = find_row(tok_cum, n, i0);
-            o = seq_len[r], b = tok_cum[r], next = tok_cum[r + 1];
-        }
+        // the slot's request, its first slot and that of the one after; page, its id, offset in it; pages
+        // that the request had
+        int r = 0, b = 0, next = 0, pg = 0, id = 0, off = 0, had = 0;
+        auto page_id = [&]() {
+            id = pg < had ? block_table[(long long)r * max_blocks + pg] : free_pages[ring(hm, pop_cum[r] + pg - had)];
+        };
+        if (i0 < n_tok) r = find_row(tok_cum, n, i0);
 #pragma unroll
         for (int k = 0; k < kTabSlots; ++k) {
             const int i = i0 + k;
             slot[k] = -1;
             pos[k] = 0;
             if (i < n_tok) {
-                if (i >= next) {
-                    do ++r;
-                    while (tok_cum[r + 1] <= i);
-                    o = seq_len[r], b = tok_cum[r], next = tok_cum[r + 1];
+                if (k == 0 || i >= next) {
+                    while (tok_cum[r + 1] <= i) ++r;
+                    b = tok_cum[r], next = tok_cum[r + 1];
+                    const int o = seq_len[r], p = o + i - b;
+                    had = (o + P - 1) / P;
+                    pg = p / P;
+                    off = p - pg * P;
+                    page_id();
+                } else if (++off == P) {
+                    off = 0;
+                    ++pg;
+                    page_id();
                 }
-                pos[k] = o + i - b;
-                const int had = (o + P - 1) / P, pg = pos[k] / P;
-                const int id = pg < had ? block_table[(long long)r * max_blocks + pg]
-                                        : free_pages[ring(hm, pop_cum[r] + pg - had)];
-                slot[k] = (long long)id * P + (pos[k] - pg * P);
+                pos[k] = pg * P + off;
+                slot[k] = (long long)id * P + off;
             }
         }
         if (wide && i0 + kTabSlots <= n_slots) {
