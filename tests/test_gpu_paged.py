@@ -83,6 +83,12 @@ def test_tables(ice, n, P, cols, kinds, in_place):
         assert _run_tables(ice, pc, lens, new, table, ring, state, n_slots, in_place) == ref
 
 
+@pytest.mark.parametrize("n,P,cols,kinds", [(256, 16, 30, ["one", "end", "drop", "chunk"]), (200, 16, 100, ["fill"])])
+def test_tables_few_requests(ice, n, P, cols, kinds):
+    """As many requests as the small blocks take, and fewer with more slots than those take."""
+    test_tables(ice, n, P, cols, kinds, False)
+
+
 @pytest.mark.parametrize("fault", ["pages", "columns", "slots", "negative", "too_long", "below_zero", "ring_backwards",
                                    "ring_too_full", "given_twice"])
 def test_tables_all_or_nothing(ice, fault):
