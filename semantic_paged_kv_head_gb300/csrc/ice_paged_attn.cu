@@ -4,6 +4,7 @@
 #include <cstring>
 
 #include "ice_paged.cuh"
+#include "ice_paged_search.h"
 
 namespace ice {
 
@@ -399,16 +400,11 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttn a, P
     // this one be scheduled (they wait for the kernels before them first).
     int req = 0, nq = -1, own = 0, blk = 0;
     if (tok < a.q_start[a.n_req]) {
-        int lo = 0, hi = a.n_req;  // q_start[lo] <= tok < q_start[hi]; 32 probes a step
-        while (hi - lo > 1) {
-            const int w = (hi - lo + 31) / 32, probe = lo + lane * w;
-            const unsigned le = __ballot_sync(0xffffffffu, probe < hi && a.q_start[min(probe, a.n_req)] <= tok);
-            const int k = 31 - __clz(le);  // lane 0 always holds
-            hi = min(hi, lo + (k + 1) * w);
-            lo = lo + k * w;
-        }
-        const int b = a.q_start[lo];
-        req = lo, nq = a.q_start[lo + 1] - b, own = a.seq_len[lo], blk = (tok - b) / z.TB;
+        RowSearch f(a.n_req);  // the lists may be out of range: the verdict on them is read below
+        while (f.open())
+            f.narrow(__ballot_sync(0xffffffffu, f.has_probe(lane) && a.q_start[f.probe(lane)] <= tok));
+        const int b = a.q_start[f.lo];
+        req = f.lo, nq = a.q_start[f.lo + 1] - b, own = a.seq_len[f.lo], blk = (tok - b) / z.TB;
     }
     pdl_wait_then_release();
     if (!a.plan[kPlanOk]) return;

@@ -78,3 +78,76 @@ def test_plain_tables_by_hand():
     assert code == 0 and lens == [6, 2] and state == [5, 8] and q0 == [0, 3, 3]
     assert slots == [11, 20, 21, -1, -1] and pos == [3, 4, 5, 0, 0]
     assert table == [[2, 5, -1], [0, 4, -1]] and ring == [1, 4, -1, -1, 5, 3]
+
+
+SEARCH = r"""
+#include <algorithm>
+#include <climits>
+#include <cstdio>
+#include <cstdlib>
+#include <vector>
+#include "ice_paged_search.h"
+
+static int bad = 0;
+// Entry i of the list, with the index checked first.
+static int at(const std::vector<int>& q, int i) {
+    if (i < 0 || i >= (int)q.size()) { ++bad; return INT_MIN; }
+    return q[i];
+}
+// The search of one row as the kernel makes it, 32 lanes in turn; the request found.
+static int find(const std::vector<int>& q, int tok) {
+    const int n = (int)q.size() - 1;
+    ice::RowSearch f(n);
+    for (int step = 0; f.open(); ++step) {
+        unsigned le = 0;
+        for (int lane = 0; lane < 32; ++lane)
+            if (f.has_probe(lane) && at(q, f.probe(lane)) <= tok) le |= 1u << lane;
+        f.narrow(le);
+        if (f.lo < 0 || f.hi > n || f.lo >= f.hi || step > 4) { ++bad; return -1; }
+    }
+    at(q, f.lo), at(q, f.lo + 1);
+    return f.lo;
+}
+
+int main() {
+    unsigned long long x = 88172645463325252ull;
+    auto rnd = [&](int m) { x ^= x << 13, x ^= x >> 7, x ^= x << 17; return (int)(x % (unsigned long long)m); };
+    for (int n : {1, 2, 3, 31, 32, 33, 64, 65, 1000, 1024, 1025, 2047, 2500, 8191, 8192}) {
+        // in order: a request of its own for every row, however many are empty
+        std::vector<int> q(n + 1, 0);
+        for (int r = 0; r < n; ++r) q[r + 1] = q[r] + (rnd(3) ? rnd(5) : 0);
+        for (int r = 0; r < n; ++r)
+            for (int t = q[r]; t < q[r + 1]; ++t)
+                if (find(q, t) != r) ++bad;
+        // out of order or out of range: some request, and no entry outside the list
+        for (int kind = 0; kind < 7; ++kind)
+            for (int rep = 0; rep < 40; ++rep) {
+                std::vector<int> b = q;
+                if (kind == 0) b[0] = 1 + rnd(1000);
+                if (kind == 1) std::fill(b.begin(), b.end(), INT_MAX);
+                if (kind == 2) std::fill(b.begin(), b.end(), INT_MIN);
+                if (kind == 3) for (int& e : b) e = rnd(2 * n + 2) - n;
+                if (kind == 4) std::reverse(b.begin(), b.end());
+                if (kind == 5) b[rnd(n + 1)] = rnd(2) ? INT_MAX : INT_MIN;
+                if (kind == 6) for (int& e : b) e = 1 + rnd(3);
+                find(b, 0), find(b, rnd(4 * n + 1)), find(b, (1 << 20) - 1);
+            }
+    }
+    std::printf("%d\n", bad);
+    return bad != 0;
+}
+"""
+
+
+def test_row_search_stays_in_the_list(tmp_path):
+    """The joining kernel's search reads q_start before it is known to be in order: every index that it makes lies in the
+    list for any contents, and it finds the right request of a list that is in order."""
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no host C++ compiler")
+    src, exe = tmp_path / "search.cpp", tmp_path / "search"
+    src.write_text(SEARCH)
+    csrc = os.path.join(ROOT, "semantic_paged_kv_head_gb300", "csrc")
+    subprocess.run([cxx, "-std=c++17", "-O1", "-I", csrc, str(src), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
