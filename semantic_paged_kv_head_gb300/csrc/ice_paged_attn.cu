@@ -396,28 +396,29 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttn a, P
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = warp / PW, pw = warp % PW, h = blockIdx.y, G = a.G;
     const int R = blockIdx.x * (kJoinWarps / PW) + group, tok = R / G;
-    // Before the wait: q_start and seq_len were complete when the attention kernel's blocks let
-    // this one be scheduled (they wait for the kernels before them first).
+    // Nothing is read before the wait, not even q_start and seq_len: that the attention kernel waited for
+    // their writer is promised to that kernel's threads only.
+    pdl_wait_then_release();
+    const int ok = a.plan[kPlanOk], chunk = a.plan[kPlanChunk], direct = a.plan[kPlanDirect];
+    const PagedLong f = {a.plan[kPlanWhole], a.plan[kPlanSplit]};
     int req = 0, nq = -1, own = 0, blk = 0;
     if (tok < a.q_start[a.n_req]) {
-        RowSearch f(a.n_req);  // the lists may be out of range: the verdict on them is read below
-        while (f.open())
-            f.narrow(__ballot_sync(0xffffffffu, f.has_probe(lane) && a.q_start[f.probe(lane)] <= tok));
-        const int b = a.q_start[f.lo];
-        req = f.lo, nq = a.q_start[f.lo + 1] - b, own = a.seq_len[f.lo], blk = (tok - b) / z.TB;
+        RowSearch r(a.n_req);  // beside the load of the verdict, which may be that the lists are out of range
+        while (r.open())
+            r.narrow(__ballot_sync(0xffffffffu, r.has_probe(lane) && a.q_start[r.probe(lane)] <= tok));
+        const int b = a.q_start[r.lo];
+        req = r.lo, nq = a.q_start[r.lo + 1] - b, own = a.seq_len[r.lo], blk = (tok - b) / z.TB;
     }
-    pdl_wait_then_release();
-    if (!a.plan[kPlanOk]) return;
+    if (!ok) return;
     int parts = -1, first = 0;  // -1: nothing to write
     if (nq > z.TS) {
-        const PagedLong f = {a.plan[kPlanWhole], a.plan[kPlanSplit]};
         const int blocks = long_blocks(nq, own, z);
         first = a.prefix_splits;
         const bool whole = f.whole == INT_MAX || a.first_long[req] + h * blocks + blk < f.whole;
         parts = blocks == 0 ? 0 : whole || f.split == 1 ? -1 : f.split;
     } else if (nq > 0) {
-        const int n = plan_parts(own, a.H, z, a.plan[kPlanChunk]);
-        parts = (a.prefix_splits == 0 && n == 1) || a.plan[kPlanDirect] ? -1 : a.prefix_splits + n;
+        const int n = plan_parts(own, a.H, z, chunk);
+        parts = (a.prefix_splits == 0 && n == 1) || direct ? -1 : a.prefix_splits + n;
     }
     if (PW == 1 && parts < 0) return;
     const long long step = (long long)a.H * a.RP, row = (long long)first * step + (long long)h * a.RP + R;

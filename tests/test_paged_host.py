@@ -2,6 +2,7 @@
 the plain statement of the tables that the GPU tests compare with."""
 import ctypes
 import os
+import re
 import shutil
 import subprocess
 
@@ -151,3 +152,23 @@ def test_row_search_stays_in_the_list(tmp_path):
     subprocess.run([cxx, "-std=c++17", "-O1", "-I", csrc, str(src), "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
+
+
+def test_kernels_wait_before_they_read():
+    """The paged kernels are launched before the kernels ahead of them have ended: what comes before the wait touches no
+    buffer of the call."""
+    csrc = os.path.join(ROOT, "semantic_paged_kv_head_gb300", "csrc")
+    seen = []
+    for name in ("ice_paged_attn.cu", "ice_paged_attn_tc.cu", "ice_paged_tables.cu"):
+        text = open(os.path.join(csrc, name)).read()
+        for m in re.finditer(r"__global__ void __launch_bounds__\([^)]*\)\s*(\w+)\((.*?)\) \{", text, re.S):
+            kernel, params = m.group(1), m.group(2)
+            before = text[m.end():text.index("pdl_wait_then_release();", m.end())]
+            assert "__global__" not in before, kernel
+            before = re.sub(r"//[^\n]*", "", before)
+            # PagedAttn's pointers, and pointer parameters
+            pointers = [r"a\.\w+"] if "PagedAttn a" in params else re.findall(r"\*\s*(\w+)", params)
+            for p in pointers:
+                assert not re.search(r"\b" + p + r"\s*\[|\*\s*" + p + r"\b(?!\s*[\w(])", before), (kernel, p)
+            seen.append(kernel)
+    assert sorted(seen) == ["append_kernel", "paged_join_kernel", "paged_simt_kernel", "paged_tc_kernel", "tables_kernel"]
