@@ -379,6 +379,74 @@ def test_attn_bad_lengths_leave_out(ice, dtype, which, at, value):
     assert bool((out == 7.0).all())
 
 
+def _long_prefix_call(ice, dtype, H, G, P, nq, L, table, k, v, q):
+    """One request of nq new tokens that see the prefix only."""
+    pc = _cache(ice, n_kv_heads=H, n_q_heads=H * G, page_size=P, n_pages=k.shape[0], max_requests=1, max_blocks=1, max_tokens=nq,
+                dtype=dtype)
+    out = pc.attn(q.cuda(), torch.tensor([0, nq], dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda"),
+                  torch.zeros((1, 1), dtype=torch.int32, device="cuda"), k.cuda(), v.cuda(), table.cuda(), L)
+    assert pc.get_error() == 0
+    return out.cpu()
+
+
+def test_attn_equal_weights_of_millions_of_keys(ice):
+    """Sums of one sign over 2^22 keys in one pass: q = 0, so that every weight is 1 and only sums round.
+
+    Tolerance: the output's rounding, 2^-8; O's additions between two folds, 8192 x 2^-23 = 2^-10 of the mean of |v|; the
+    sums of the folds and l, 1024 tiles and 32 folds a 2^-24 each, twice: 2^-12."""
+    P, L, nq = 64, 1 << 22, 152 * 32  # a block of rows for every SM: none is cut into ranges
+    g = torch.Generator().manual_seed(41)
+    k = torch.randn((2, 1, P, D), generator=g).to(BF16)
+    v = (1 + torch.rand((2, 1, P, D), generator=g)).to(BF16)
+    table = torch.tensor([0, 1], dtype=torch.int32).repeat(L // P // 2)
+    got = _long_prefix_call(ice, BF16, 1, 8, P, nq, L, table, k, v, torch.zeros((nq, 8, D), dtype=BF16)).double()
+    mean = v.double().mean((0, 1, 2))
+    err = (got / mean - 1).abs().max()
+    assert float(err) <= 2.0 ** -8 + 2.0 ** -10 + 2.0 ** -12
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rise", [0.0, 1.0])
+def test_attn_long_passes(ice, dtype, rise):
+    """Several thousand tiles in one pass, scores that rise along the context among them."""
+    H, G, P, L, nq = 2, 4, 64, 2 * 131072 + 5000, 76 * 64
+    n = pages_of(L, P)
+    g = torch.Generator().manual_seed(42)
+    k, v = (torch.randn((n, H, P, D), generator=g) for _ in range(2))
+    q = torch.randn((nq, H * G, D), generator=g)
+    if rise:
+        k, q = k.abs() * (torch.arange(n) / n * rise).view(-1, 1, 1, 1), q.abs()
+    k, v, q = (x.to(dtype) for x in (k, v, q))
+    table = torch.randperm(n, generator=g).int() if not rise else torch.arange(n, dtype=torch.int32)
+    got = _long_prefix_call(ice, dtype, H, G, P, nq, L, table, k, v, q).double()
+    some = [0, 33, 64, 2000, nq - 1]
+    ref, tol = plain_attn(q[some], torch.tensor([0, len(some)]), torch.zeros(1), torch.zeros((1, 1), dtype=torch.int32), k, v, table, L)
+    err = (got[some] - ref).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H,G", [(1, 8), (2, 4)])
+def test_attn_long_parts_are_joined(ice, dtype, H, G):
+    """So many rows that the scratch holds one part of the prefix and two of own tokens, both of over a thousand tiles."""
+    P, L, TS = 64, 150000, 128 // G
+    reqs = [(2, 290000), (1, 50), (2, 300)] + [(TS, TS + 3)] * (89600 // (H * G) // TS)
+    g = torch.Generator().manual_seed(43)
+    n = pages_of(L, P)
+    k, v = (torch.randn((n, H, P, D), generator=g).to(dtype) for _ in range(2))
+    table = torch.randint(0, n, (len(reqs), pages_of(290000, P)), generator=g).int()  # pages may serve several requests
+    prefix = torch.randperm(n, generator=g).int()
+    q_start = torch.tensor([0] + [x for x, _ in reqs]).cumsum(0).int()
+    lens = torch.tensor([s for _, s in reqs], dtype=torch.int32)
+    q = torch.randn((int(q_start[-1]), H * G, D), generator=g).to(dtype)
+    c = dict(q=q, q_start=q_start, seq_len=lens, table=table, k=k, v=v, prefix=prefix, L=L, P=P, H=H, G=G, n_pages=n)
+    got, pc = _attn_run(ice, c)
+    assert pc.get_error() == 0
+    ref, tol = plain_attn(q[:5], q_start[:4], lens[:3], table, k, v, prefix, L)
+    err = (got[:5].cpu().double() - ref).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+
+
 def test_attn_long_own_part_in_a_large_pool(ice):
     """Offsets past 2^31 elements: the last pages of a pool of 20 GB in all."""
     P, H = 64, 8
