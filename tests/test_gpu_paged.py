@@ -405,6 +405,30 @@ def test_attn_equal_weights_of_millions_of_keys(ice):
     assert float(err) <= 2.0 ** -8 + 2.0 ** -10 + 2.0 ** -12
 
 
+def test_attn_f32_equal_weights_of_a_million_keys(ice):
+    """The same for fp32: a prefix under blocks of 64 rows, and own tokens under blocks of 8.
+
+    Tolerance: the sums of a tile's 64 products, and 16 more roundings (carried sums, joining of lanes, warps and parts,
+    division, output): 80 x 2^-24 of the mean of |v|."""
+    P, L, nq = 64, 1 << 20, 152 * 8
+    g = torch.Generator().manual_seed(44)
+    k, v = torch.randn((2, 1, P, D), generator=g), 1 + torch.rand((2, 1, P, D), generator=g)
+    mean = v.double().mean((0, 1, 2))
+    got = _long_prefix_call(ice, F32, 1, 8, P, nq, L, torch.tensor([0, 1], dtype=torch.int32).repeat(L // P // 2), k, v,
+                            torch.zeros((nq, 8, D))).double()
+    assert float((got / mean - 1).abs().max()) <= 80 * 2.0 ** -24
+    # so many rows that the scratch holds three parts a row: the first request's own tokens are three long ranges
+    reqs = [(1, L)] + [(8, 8)] * 1400
+    table = torch.zeros((len(reqs), L // P), dtype=torch.int32)
+    table[0, 1::2] = 1
+    q_start = torch.tensor([0] + [x for x, _ in reqs]).cumsum(0).int()
+    c = dict(q=torch.zeros((int(q_start[-1]), 8, D)), q_start=q_start, seq_len=torch.tensor([s for _, s in reqs], dtype=torch.int32),
+             table=table, k=k, v=v, prefix=None, L=0, P=P, H=1, G=8, n_pages=2)
+    got, pc = _attn_run(ice, c)
+    assert pc.get_error() == 0
+    assert float((got[0].cpu().double() / mean - 1).abs().max()) <= 80 * 2.0 ** -24
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("rise", [0.0, 1.0])
 def test_attn_long_passes(ice, dtype, rise):

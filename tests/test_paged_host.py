@@ -161,7 +161,7 @@ def test_kernels_wait_before_they_read():
     seen = []
     for name in ("ice_paged_attn.cu", "ice_paged_attn_tc.cu", "ice_paged_tables.cu"):
         text = open(os.path.join(csrc, name)).read()
-        for m in re.finditer(r"__global__ void __launch_bounds__\([^)]*\)\s*(\w+)\((.*?)\) \{", text, re.S):
+        for m in re.finditer(r"__global__ void __\w+__\([^)]*\)\s*(\w+)\((.*?)\) \{", text, re.S):
             kernel, params = m.group(1), m.group(2)
             before = text[m.end():text.index("pdl_wait_then_release();", m.end())]
             assert "__global__" not in before, kernel
