@@ -45,7 +45,7 @@ namespace ice {
 // 32 KB stages. Key tiles end where pages do; rows of a stage behind the last key
 // are zeroed before they meet weights of zero, whatever the page's free slots hold.
 //
-// Every wait is bounded (kWaitNs); when one runs out the block's roles leave their loops,
+// Every wait is bounded (kWaitNs; those for a next item, kWaitNs without progress); when one runs out the block's roles leave their loops,
 // what is in flight ends, and the status word says ICE_ERR_TIMEOUT.
 //
 // Bound by memory with few rows: 4 requests on 250k tokens, 168 us, 6.13 TB/s (90 % of the
@@ -70,12 +70,18 @@ constexpr int kFaStages = kFaStagesK + kFaStagesV;
 constexpr float kFaSlack = 8.0f;          // growth of the maximum (log2) that is let pass
 constexpr int kFaFold = 1024;             // tiles after which O and l are added to the sums of the tiles before
 
+// What every wait of the block watches: whether one has run out, and the key tiles copied so far.
+struct FaWatch {
+    int abort;
+    unsigned tiles;
+};
 struct FaShared {
     unsigned long long q_full[4], q_empty[4], k_full[kFaStagesK], k_empty[kFaStagesK], v_full[kFaStagesV], v_empty[kFaStagesV];
     unsigned long long s_full[2], p_ready[2][2], o_done[2], drain;  // p_ready: portions of a tile's weights
     unsigned long long item_full[2], item_empty[2], item_want;
     unsigned tmem;
-    int abort, left[2];  // left: whether the item exists
+    FaWatch watch;
+    int left[2];  // whether the item exists
     PagedItem item[2];
     PlanShared plan;
 };
@@ -116,22 +122,33 @@ __device__ __forceinline__ bool fa_try(unsigned bar, unsigned parity) {
 // Waits for phase `parity`, at most kWaitNs; false if it ran out here or elsewhere in the block
 // (then every role leaves its loop). The wall clock is slow to read (a handover between
 // warps would wait for it), so it is read every 64th try only.
-__device__ __forceinline__ bool fa_wait_long(unsigned bar, unsigned parity, volatile int* abort) {
+// item: a wait for the next item or for room for one. A stream without rows and the thread that hands the items
+// out wait for as long as an item takes (0.4 s with 30 million keys), so kWaitNs counts from the key tile that
+// the block copied last. All others are handovers within a few tiles.
+template <bool item>
+__device__ __forceinline__ bool fa_wait_long(unsigned bar, unsigned parity, volatile FaWatch* watch) {
     unsigned long long t0 = 0;
+    unsigned tiles = 0;
     for (unsigned k = 1;; ++k) {
         if (fa_try(bar, parity)) return true;
         if (k % 64) continue;
-        if (*abort) return false;
+        if (watch->abort) return false;
         const unsigned long long t = global_ns();
-        if (t0 == 0) t0 = t;
+        if (t0 == 0 || (item && watch->tiles != tiles)) {
+            t0 = t;
+            if (item) tiles = watch->tiles;
+        }
         if (t - t0 > kWaitNs) {
-            *abort = 1;
+            watch->abort = 1;
             return false;
         }
     }
 }
-__device__ __forceinline__ bool fa_wait(unsigned long long* b, unsigned parity, volatile int* abort) {
-    return fa_try(smem_u32(b), parity) || fa_wait_long(smem_u32(b), parity, abort);
+__device__ __forceinline__ bool fa_wait(unsigned long long* b, unsigned parity, volatile FaWatch* watch) {
+    return fa_try(smem_u32(b), parity) || fa_wait_long<false>(smem_u32(b), parity, watch);
+}
+__device__ __forceinline__ bool fa_wait_item(unsigned long long* b, unsigned parity, volatile FaWatch* watch) {
+    return fa_try(smem_u32(b), parity) || fa_wait_long<true>(smem_u32(b), parity, watch);
 }
 __device__ __forceinline__ void fa_commit(unsigned long long* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -380,7 +397,7 @@ struct FaItems {
     // One warp, or its one active thread (whole = false). False at the end or when a wait ran out (ok = false).
     __device__ __forceinline__ bool next(FaShared& sh, PagedItem& it, bool& ok, bool whole) {
         const unsigned k = cnt & 1;
-        bool got = fa_wait(&sh.item_full[k], (cnt >> 1) & 1, &sh.abort);
+        bool got = fa_wait_item(&sh.item_full[k], (cnt >> 1) & 1, &sh.watch);
         if (whole) got = __all_sync(0xffffffffu, got);
         if (!got) {
             ok = false;
@@ -408,7 +425,8 @@ __global__ void __launch_bounds__(kFaThreads, 1)
     int* cum = reinterpret_cast<int*>(mem + (2 + kFaStages) * kFaTileB);
     const int KT = z.KT;
     if (tid == 0) {
-        sh.abort = 0;
+        sh.watch.abort = 0;
+        sh.watch.tiles = 0;
         for (int k = 0; k < 4; ++k) {
             fa_bar_init(&sh.q_full[k], 1);
             fa_bar_init(&sh.q_empty[k], 1);
@@ -447,7 +465,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
     make_plan<kFaThreads>(a, z, cum, sh.plan);  // its barriers also publish the setup
     fa_after();
     const unsigned tmem = sh.tmem;
-    volatile int* abort = &sh.abort;
+    volatile FaWatch* watch = &sh.watch;
     PagedItem it;
     FaItems items;
     bool ok = true;
@@ -497,7 +515,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                                 const unsigned back = few && (last_few & 2) ? 4 : 2;
                                 if (qcnt >= back) {
                                     const unsigned w = qcnt - back;
-                                    ok = __all_sync(0xffffffffu, fa_wait(&sh.q_empty[w & 3], (w >> 2) & 1, abort));
+                                    ok = __all_sync(0xffffffffu, fa_wait(&sh.q_empty[w & 3], (w >> 2) & 1, watch));
                                 }
                                 if (ok && fa_elect()) {
                                     unsigned long long* bar = &sh.q_full[qcnt & 3];
@@ -520,10 +538,13 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                     }
                     if (is_k && n > kFaAhead && x == n - kFaAhead && lane == 0) fa_arrive(&sh.item_want);
                     const unsigned st = cnt % stages;
-                    ok = __all_sync(0xffffffffu, fa_wait(&empty[st], ((cnt / stages) & 1) ^ 1, abort));
+                    ok = __all_sync(0xffffffffu, fa_wait(&empty[st], ((cnt / stages) & 1) ^ 1, watch));
                     if (!ok) break;
                     const unsigned bar = smem_u32(&full[st]), dst = dst0 + st * kFaTileB;
-                    if (lane == 0) fa_expect(&full[st], (unsigned)(cur.n * a.P * kD * 2));
+                    if (lane == 0) {
+                        fa_expect(&full[st], (unsigned)(cur.n * a.P * kD * 2));
+                        if (is_k) watch->tiles = cnt + 1;
+                    }
                     __syncwarp();
                     // one thread issues all boxes
 #pragma unroll 1
@@ -561,8 +582,8 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 int i = blockIdx.x;
                 for (unsigned c = 0;; ++c) {
                     const unsigned k = c & 1;
-                    if ((c > 0 && !fa_wait(&sh.item_want, (c - 1) & 1, abort)) ||
-                        !fa_wait(&sh.item_empty[k], ((c >> 1) & 1) ^ 1, abort)) {
+                    if ((c > 0 && !fa_wait_item(&sh.item_want, (c - 1) & 1, watch)) ||
+                        !fa_wait_item(&sh.item_empty[k], ((c >> 1) & 1) ^ 1, watch)) {
                         set_status(a.status, ICE_ERR_TIMEOUT);
                         break;
                     }
@@ -592,8 +613,8 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                     // path, so a round is written out (rounds of the loop below: 3 % slower)
                     const unsigned t0 = tmem, t1 = tmem + 128, o0 = tmem + 256, o1 = tmem + 384;
                     unsigned ks = kn & 1, sk = s_k + ks * kFaTileB;
-                    ok = fa_wait(&sh.q_full[q0 & 3], (q0 >> 2) & 1, abort) &&
-                         fa_wait(&sh.q_full[q1 & 3], (q1 >> 2) & 1, abort) && fa_wait(&sh.k_full[ks], (kn >> 1) & 1, abort);
+                    ok = fa_wait(&sh.q_full[q0 & 3], (q0 >> 2) & 1, watch) &&
+                         fa_wait(&sh.q_full[q1 & 3], (q1 >> 2) & 1, watch) && fa_wait(&sh.k_full[ks], (kn >> 1) & 1, watch);
                     if (!ok) break;
                     fa_after();
                     fa_mma_s(t0, sq0, sk);
@@ -606,19 +627,19 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                     for (int left = n - 1; left > 0; --left) {
                         const unsigned vs = vn & 1, sv = s_v + vs * kFaTileB;
                         ks = kn & 1, sk = s_k + ks * kFaTileB;
-                        if (!fa_wait(&sh.v_full[vs], (vn >> 1) & 1, abort) || !fa_wait(&sh.k_full[ks], (kn >> 1) & 1, abort) ||
-                            !fa_wait(&sh.p_ready[0][0], pn0 & 1, abort))
+                        if (!fa_wait(&sh.v_full[vs], (vn >> 1) & 1, watch) || !fa_wait(&sh.k_full[ks], (kn >> 1) & 1, watch) ||
+                            !fa_wait(&sh.p_ready[0][0], pn0 & 1, watch))
                             break;
                         fa_after();
                         fa_mma_o_first(o0, t0, sv, (n - 1 - left) % kFaFold != 0);
-                        if (!fa_wait(&sh.p_ready[0][1], pn0 & 1, abort)) break;
+                        if (!fa_wait(&sh.p_ready[0][1], pn0 & 1, watch)) break;
                         fa_after();
                         fa_mma_o_rest_s(o0, t0, sv, sq0, sk, &sh.s_full[0]);
                         ++pn0;
-                        if (!fa_wait(&sh.p_ready[1][0], pn1 & 1, abort)) break;
+                        if (!fa_wait(&sh.p_ready[1][0], pn1 & 1, watch)) break;
                         fa_after();
                         fa_mma_o_first(o1, t1, sv, (n - 1 - left) % kFaFold != 0);
-                        if (!fa_wait(&sh.p_ready[1][1], pn1 & 1, abort)) break;
+                        if (!fa_wait(&sh.p_ready[1][1], pn1 & 1, watch)) break;
                         fa_after();
                         fa_mma_o_rest_s(o1, t1, sv, sq1, sk, &sh.s_full[1]);
                         ++pn1;
@@ -627,21 +648,21 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                         ++kn;
                         ++vn;
                     }
-                    ok = !*abort;
+                    ok = !watch->abort;
                     if (!ok) break;
                     // the last scores are issued; the last value tile
                     fa_commit(&sh.q_empty[q0 & 3]);
                     fa_commit(&sh.q_empty[q1 & 3]);
                     const unsigned vs = vn & 1, sv = s_v + vs * kFaTileB;
-                    ok = fa_wait(&sh.v_full[vs], (vn >> 1) & 1, abort) && fa_wait(&sh.p_ready[0][0], pn0 & 1, abort) &&
-                         fa_wait(&sh.p_ready[0][1], pn0 & 1, abort);
+                    ok = fa_wait(&sh.v_full[vs], (vn >> 1) & 1, watch) && fa_wait(&sh.p_ready[0][0], pn0 & 1, watch) &&
+                         fa_wait(&sh.p_ready[0][1], pn0 & 1, watch);
                     if (!ok) break;
                     fa_after();
                     fa_mma_o_first(o0, t0, sv, (n - 1) % kFaFold != 0);
                     fa_mma_o_rest(o0, t0, sv, true);
                     fa_commit(&sh.o_done[0]);
                     ++pn0;
-                    ok = fa_wait(&sh.p_ready[1][0], pn1 & 1, abort) && fa_wait(&sh.p_ready[1][1], pn1 & 1, abort);
+                    ok = fa_wait(&sh.p_ready[1][0], pn1 & 1, watch) && fa_wait(&sh.p_ready[1][1], pn1 & 1, watch);
                     if (!ok) break;
                     fa_after();
                     fa_mma_o_first(o1, t1, sv, (n - 1) % kFaFold != 0);
@@ -664,16 +685,16 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                         if (j >= ne) continue;
                         if (j >= 0) {
                             const unsigned t_o = t_p + 256, sv = s_v + vs * kFaTileB, np = s ? pn1 : pn0;
-                            ok = fa_wait(&sh.v_full[vs], (vn / kFaStagesV) & 1, abort);
+                            ok = fa_wait(&sh.v_full[vs], (vn / kFaStagesV) & 1, watch);
                             // the weights come in two portions: the first one's products run
                             // while the second is made
-                            ok = ok && fa_wait(&sh.p_ready[s][0], np & 1, abort);
+                            ok = ok && fa_wait(&sh.p_ready[s][0], np & 1, watch);
                             if (!ok) break;
                             fa_after();
                             fa_mma_o_first(t_o, t_p, sv, j % kFaFold != 0);
                             if (j + 1 < ne)  // off the path of the last weights
                                 k_here = fa_try(smem_u32(&sh.k_full[ks]), (kn / kFaStagesK) & 1);
-                            ok = fa_wait(&sh.p_ready[s][1], np & 1, abort);
+                            ok = fa_wait(&sh.p_ready[s][1], np & 1, watch);
                             if (!ok) break;
                             fa_after();
                             fa_mma_o_rest(t_o, t_p, sv, true);
@@ -683,8 +704,8 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                         }
                         if (j + 1 < ne) {
                             const unsigned q = s ? q1 : q0;
-                            if (j < 0) ok = fa_wait(&sh.q_full[q & 3], (q >> 2) & 1, abort);
-                            if (!k_here) ok = ok && fa_wait(&sh.k_full[ks], (kn / kFaStagesK) & 1, abort);
+                            if (j < 0) ok = fa_wait(&sh.q_full[q & 3], (q >> 2) & 1, watch);
+                            if (!k_here) ok = ok && fa_wait(&sh.k_full[ks], (kn / kFaStagesK) & 1, watch);
                             if (!ok) break;
                             fa_after();
                             fa_mma_s(t_p, s ? sq1 : sq0, s_k + ks * kFaTileB);
@@ -734,13 +755,13 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             auto part = [&]() { return ((long long)st.slot * a.H + st.h) * a.RP + st.tok0 * a.G + row; };
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; j < n; ++j) {
-                ok = __all_sync(0xffffffffu, fa_wait(&sh.s_full[s], sn & 1, abort));
+                ok = __all_sync(0xffffffffu, fa_wait(&sh.s_full[s], sn & 1, watch));
                 if (!ok) break;
                 ++sn;
                 const PagedTile t = tile_of(a, z, st, st.kt0 + j);
                 if (t.key0 + KT > t.len) {  // the last tile of a list: rows behind the last key
                     const unsigned v = vn0 + (!apart ? j : s ? j + min(n0, j + 1) : j + min(n1, j)), vs = v % kFaStagesV;
-                    ok = __all_sync(0xffffffffu, fa_wait(&sh.v_full[vs], (v / kFaStagesV) & 1, abort));
+                    ok = __all_sync(0xffffffffu, fa_wait(&sh.v_full[vs], (v / kFaStagesV) & 1, watch));
                     if (!ok) break;
                     const int r0 = t.len - t.key0;
                     unsigned char* v_st = mem + (2 + kFaStagesK + vs) * kFaTileB;
@@ -824,7 +845,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             }
             if (!ok) break;
             if (n > 0) {
-                ok = __all_sync(0xffffffffu, fa_wait(&sh.o_done[s], on & 1, abort));
+                ok = __all_sync(0xffffffffu, fa_wait(&sh.o_done[s], on & 1, watch));
                 if (!ok) break;
                 ++on;
             }

@@ -405,6 +405,19 @@ def test_attn_equal_weights_of_millions_of_keys(ice):
     assert float(err) <= 2.0 ** -8 + 2.0 ** -10 + 2.0 ** -12
 
 
+def test_attn_items_longer_than_a_wait(ice):
+    """2^25 keys in one pass: an item takes twice as long as a wait may without progress, and the last block's second
+    stream has no rows and waits all that time. The tolerance as above, with 256 folds."""
+    P, L, nq = 64, 1 << 25, 152 * 32 - 16
+    g = torch.Generator().manual_seed(45)
+    k = torch.randn((2, 1, P, D), generator=g).to(BF16)
+    v = (1 + torch.rand((2, 1, P, D), generator=g)).to(BF16)
+    table = torch.tensor([0, 1], dtype=torch.int32).repeat(L // P // 2)
+    got = _long_prefix_call(ice, BF16, 1, 8, P, nq, L, table, k, v, torch.zeros((nq, 8, D), dtype=BF16)).double()
+    mean = v.double().mean((0, 1, 2))
+    assert float((got / mean - 1).abs().max()) <= 2.0 ** -8 + 2.0 ** -10 + 2.0 ** -12
+
+
 def test_attn_f32_equal_weights_of_a_million_keys(ice):
     """The same for fp32: a prefix under blocks of 64 rows, and own tokens under blocks of 8.
 
