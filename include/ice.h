@@ -524,12 +524,23 @@ int ice_paged_append(ice_paged* pg, int32_t n_tokens, const void* k, int64_t k_s
  *
  * A page id outside the pool reads as a page of zeros and is reported
  * (ICE_ERR_BOUNDS); q_start or seq_len out of range are reported and out is left
- * as it was.
+ * as it was. With bf16 the GPU's waits for its own copies and products are bounded
+ * (200 ms without progress): ICE_ERR_TIMEOUT says that one ran out, and out is then
+ * not to be used.
  */
 int ice_paged_attn(ice_paged* pg, int32_t n_req, int32_t n_tokens, const void* q, int64_t q_stride,
                    const int32_t* q_start, const int32_t* seq_len, const int32_t* block_table,
                    const int32_t* prefix_table, int32_t prefix_len, const void* k_pages,
                    const void* v_pages, void* out, void* stream);
+
+/*
+ * ice_paged_debug_set_flags - test hooks (0 = normal operation).
+ * ICE_DEBUG_STALL_ATTN: in ice_paged_attn with bf16 one copy of keys expects 16 bytes
+ * more than it delivers, so the bounded waits for it run out and the call reports
+ * ICE_ERR_TIMEOUT. Nothing is left in flight, and later calls on the handle (with the
+ * flag off) are exact. Used to test the timeout path.
+ */
+int ice_paged_debug_set_flags(ice_paged* pg, int32_t flags);
 
 #ifdef __cplusplus
 }

@@ -43,6 +43,7 @@ struct PagedAttn {
                         // tile where two are attended side by side)
     int max_splits;     // most parts of a request's own tokens (slots after the prefix's), >= 2
     int target_items;   // items of own tokens aimed at where they are few
+    int debug;          // ICE_DEBUG_* flags (tests only), 0 in normal use
 };
 constexpr int kPagedMaxSlots = 128;
 

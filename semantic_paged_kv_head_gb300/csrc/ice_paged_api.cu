@@ -11,7 +11,7 @@ using namespace ice;
 
 struct ice_paged {
     ice_paged_params p;
-    int G = 0, device = 0, n_sm = 0;
+    int G = 0, device = 0, n_sm = 0, debug = 0;
     long long rows_cap = 0;    // rows of partial results
     float* part_o = nullptr;   // rows_cap x D
     float2* part_ml = nullptr; // rows_cap
@@ -163,6 +163,12 @@ int ice_paged_get_error(ice_paged* pg, void* stream) {
     return code;
 }
 
+int ice_paged_debug_set_flags(ice_paged* pg, int32_t flags) {
+    if (!pg || (flags & ~ICE_DEBUG_STALL_ATTN)) return ICE_ERR_INVALID_ARG;
+    pg->debug = flags;
+    return ICE_OK;
+}
+
 int ice_paged_tables(ice_paged* pg, int32_t n_req, const int32_t* seq_len, const int32_t* n_new,
                      int32_t* block_table, int32_t* free_pages, const int64_t* free_state,
                      int32_t* seq_len_out, int64_t* free_state_out, int32_t* q_start,
@@ -243,6 +249,7 @@ int ice_paged_attn(ice_paged* pg, int32_t n_req, int32_t n_tokens, const void* q
     a.max_blocks = pg->p.max_blocks;
     a.prefix_len = prefix_len;
     a.n_pages = pg->p.n_pages;
+    a.debug = pg->debug;
     const cudaError_t e = launch_paged_attn(a, pg->p.dtype, pg->rows_cap, pg->n_sm, (cudaStream_t)stream);
     if (e != cudaSuccess) {
         cudaGetLastError();

@@ -542,7 +542,10 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                     if (!ok) break;
                     const unsigned bar = smem_u32(&full[st]), dst = dst0 + st * kFaTileB;
                     if (lane == 0) {
-                        fa_expect(&full[st], (unsigned)(cur.n * a.P * kD * 2));
+                        // ICE_DEBUG_STALL_ATTN: the last key tile of the first block's first item with any expects 16 bytes that no
+                        // copy delivers, so that the waits for it run out
+                        const bool stall = a.debug && is_k && blockIdx.x == 0 && x == n - 1 && cnt == (unsigned)x;
+                        fa_expect(&full[st], (unsigned)(cur.n * a.P * kD * 2) + (stall ? 16u : 0u));
                         if (is_k) watch->tiles = cnt + 1;
                     }
                     __syncwarp();

@@ -40,7 +40,7 @@ EXPORTS = ["ice_build", "ice_insert", "ice_select", "ice_select_attn", "ice_spar
            "ice_key_codes_noalloc", "ice_select_attn_reuse", "ice_reuse_reset",
            "ice_debug_set_flags", "ice_select_heads", "ice_decode_step", "ice_set_cluster_size",
            "ice_paged_create", "ice_paged_destroy", "ice_paged_get_error", "ice_paged_tables",
-           "ice_paged_append", "ice_paged_attn"]
+           "ice_paged_append", "ice_paged_attn", "ice_paged_debug_set_flags"]
 
 
 class ice_params(ctypes.Structure):
@@ -136,6 +136,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ice_paged_append.restype = ctypes.c_int
     lib.ice_paged_attn.argtypes = [vp, i32, i32, vp, i64, vp, vp, vp, vp, i32, vp, vp, vp, vp]
     lib.ice_paged_attn.restype = ctypes.c_int
+    lib.ice_paged_debug_set_flags.argtypes = [vp, i32]
+    lib.ice_paged_debug_set_flags.restype = ctypes.c_int
     return lib
 
 
@@ -558,6 +560,11 @@ class PagedCache:
         return out
 
     # -- status, teardown ------------------------------------------------------------------
+    def debug_set_flags(self, flags: int):
+        """ice_paged_debug_set_flags (tests only): DEBUG_STALL_ATTN forces the bounded waits of a
+        bf16 attn call to run out."""
+        _check(_lib.ice_paged_debug_set_flags(self._h, int(flags)), "ice_paged_debug_set_flags")
+
     def get_error(self, stream=None) -> int:
         return int(_lib.ice_paged_get_error(self._h, _stream(stream)))
 

@@ -508,6 +508,33 @@ def test_attn_long_own_part_in_a_large_pool(ice):
     assert bool(((got.cpu().double() - ref).abs() <= tol).all())
 
 
+# ---- the bounded waits ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("H,G,L,reqs", [
+    (2, 4, 3000, [(1, 20)] * 100),     # two row tiles on one key tile
+    (2, 4, 60000, [(1, 20)] * 3),      # two parts of the prefix side by side
+    (2, 4, 0, [(1, 2500), (2, 700)]),  # two heads side by side
+    (1, 4, 0, [(1, 2500), (1, 1)]),    # two halves of one head's range
+    (3, 2, 0, [(1, 100)]),             # one tile
+    (2, 4, 1000, [(300, 400), (1, 5)])])  # a request of its own
+def test_forced_timeout_reports_and_recovers(ice, H, G, L, reqs):
+    """A copy that never completes: the call ends with ICE_ERR_TIMEOUT, and the handle's next calls are exact."""
+    c = _attn_case(51, BF16, H, G, 16, L, reqs)
+    good, pc = _attn_run(ice, c)
+    assert pc.get_error() == 0
+    pc.debug_set_flags(ice.DEBUG_STALL_ATTN)
+    _attn_run(ice, c, pc=pc)
+    assert pc.get_error() == ice.ICE_ERR_TIMEOUT
+    assert pc.get_error() == 0
+    pc.debug_set_flags(0)
+    for _ in range(3):
+        got, _ = _attn_run(ice, c, pc=pc)
+        assert pc.get_error() == 0
+        assert torch.equal(got, good)
+    with pytest.raises(ice.IceError):
+        pc.debug_set_flags(1 << 5)
+
+
 # ---- refusals ----------------------------------------------------------------------------
 
 def test_refusals_on_a_live_handle(ice):

@@ -81,6 +81,10 @@ def test_plain_tables_by_hand():
     assert table == [[2, 5, -1], [0, 4, -1]] and ring == [1, 4, -1, -1, 5, 3]
 
 
+def test_debug_flags_need_a_handle(lib):
+    assert lib.raw_library().ice_paged_debug_set_flags(None, 0) == lib.ICE_ERR_INVALID_ARG
+
+
 SEARCH = r"""
 #include <algorithm>
 #include <climits>
