@@ -256,6 +256,38 @@ def test_attn_thousands_of_requests(ice, dtype, H, G, extra):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attn_most_requests(ice, dtype):
+    _attn_check(ice, _attn_case(24, dtype, 1, 1, 16, 70, [(1 if i % 3 else 0, 1 + i % 3) for i in range(8190)] + [(150, 160), (3, 40)]))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H,G", [(4096, 1), (512, 8)])
+def test_attn_most_heads(ice, dtype, H, G):
+    _attn_check(ice, _attn_case(25, dtype, H, G, 4, 9, [(1, 5), (0, 3), (2, 2)]))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attn_most_tokens(ice, dtype):
+    """2^20 tokens of 8192 requests and 16 heads: 2^31 elements of queries and of outputs, more of parts."""
+    B, nq, H, P, L, s = 8192, 128, 16, 16, 100, 130
+    g = torch.Generator().manual_seed(26)
+    n, cols = 60, pages_of(s, P)
+    k, v = (torch.randn((n, H, P, D), generator=g).to(dtype) for _ in range(2))
+    table = torch.randint(0, n, (B, cols), generator=g).int()
+    prefix = torch.randperm(n, generator=g)[:pages_of(L, P)].int()
+    q_start, lens = torch.arange(B + 1, dtype=torch.int32) * nq, torch.full((B,), s, dtype=torch.int32)
+    q = torch.randn((B * nq, H, D), generator=torch.Generator(device="cuda").manual_seed(27), device="cuda", dtype=dtype)
+    pc = _cache(ice, n_kv_heads=H, n_q_heads=H, page_size=P, n_pages=n, max_requests=B, max_blocks=cols, max_tokens=B * nq, dtype=dtype)
+    got = pc.attn(q, q_start.cuda(), lens.cuda(), table.cuda(), k.cuda(), v.cuda(), prefix.cuda(), L)
+    assert pc.get_error() == 0
+    for r in (0, 1, 4099, B - 1):
+        rows = slice(r * nq, (r + 1) * nq)
+        ref, tol = plain_attn(q[rows].cpu(), torch.tensor([0, nq]), lens[r:r + 1], table[r:r + 1], k, v, prefix, L)
+        err = (got[rows].cpu().double() - ref).abs()
+        assert bool((err <= tol).all()), (r, float((err / tol).max()))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("scale", [0.0, 0.01, 30.0])
 def test_attn_score_ranges(ice, dtype, scale):
     """Equal scores, near-equal ones, and ones so far apart that a key has nearly all the weight."""
