@@ -460,7 +460,16 @@ class PagedCache:
                 torch.tensor([0, n_pages], dtype=torch.int64, device=self.device))
 
     # -- checks ------------------------------------------------------------------------
+    @staticmethod
+    def _count(t, name):
+        """Entries of a list."""
+        if not isinstance(t, torch.Tensor) or t.dim() != 1:
+            raise ValueError(f"{name} must be a CUDA tensor of one dimension")
+        return t.shape[0]
+
     def _ints(self, t, dtype, shape, name):
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a CUDA tensor")
         if t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous():
             return t.data_ptr()
         if t.shape != shape:
@@ -500,7 +509,7 @@ class PagedCache:
             with torch.cuda.stream(stream):
                 return self.tables(seq_len, n_new, block_table, free_pages, free_state, n_slots, seq_len_out,
                                    free_state_out, q_start, slot_map, positions)
-        n, i32, i64, check = seq_len.shape[0], torch.int32, torch.int64, self._ints
+        n, i32, i64, check = self._count(seq_len, "seq_len"), torch.int32, torch.int64, self._ints
         ins = (check(seq_len, i32, (n,), "seq_len"), check(n_new, i32, (n,), "n_new"),
                check(block_table, i32, (n, self.params.max_blocks), "block_table"),
                check(free_pages, i32, (self.params.n_pages,), "free_pages"),
@@ -521,7 +530,7 @@ class PagedCache:
     def append(self, k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor,
                k_pages: torch.Tensor, v_pages: torch.Tensor, stream=None):
         """ice_paged_append of k, v [tokens, kv_heads, d] (a token stride is allowed)."""
-        n = slot_map.shape[0]
+        n = self._count(slot_map, "slot_map")
         kp, ks = self._rows(k, self.params.n_kv_heads, "k")
         vp, vs = self._rows(v, self.params.n_kv_heads, "v")
         if k.shape[0] != n or v.shape[0] != n:
@@ -540,16 +549,16 @@ class PagedCache:
         if stream is not None:  # what is allocated here belongs to the stream that writes it
             with torch.cuda.stream(stream):
                 return self.attn(q, q_start, seq_len, block_table, k_pages, v_pages, prefix_table, prefix_len, out)
-        p, n = self.params, seq_len.shape[0]
+        p, n = self.params, self._count(seq_len, "seq_len")
         qp, qs = self._rows(q, p.n_q_heads, "q")
         if out is None:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        elif out.shape != q.shape:
+        elif not isinstance(out, torch.Tensor) or out.shape != q.shape:
             raise ValueError("out must be shaped like q")
         kg, vg = self._pages(k_pages, v_pages)
         pt = None
         if prefix_len:
-            if prefix_table is None or prefix_table.numel() * p.page_size < prefix_len:
+            if not isinstance(prefix_table, torch.Tensor) or prefix_table.numel() * p.page_size < prefix_len:
                 raise ValueError("prefix_table must hold the pages of prefix_len tokens")
             pt = _dev_ptr(prefix_table, torch.int32, "prefix_table", host_ok=False)
         _check(_lib.ice_paged_attn(

@@ -646,6 +646,31 @@ def test_binding_refusals(ice):
             pc.tables(*a, 4)
 
 
+@pytest.mark.parametrize("wrong", [None, 3, [1, 2], "number"])
+def test_binding_refuses_what_is_no_tensor(ice, wrong):
+    """Every tensor argument in turn: ValueError, as for a tensor of the wrong kind ("number": a tensor of no dimension)."""
+    wrong = torch.tensor(1, dtype=torch.int32, device="cuda") if wrong == "number" else wrong
+    c = _attn_case(12, BF16, 2, 4, 16, 100, [(1, 40), (1, 50)])
+    good, pc = _attn_run(ice, c)
+    x = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in c.items()}
+    kv, slots = torch.zeros((2, 2, D), dtype=BF16, device="cuda"), torch.full((2,), -1, dtype=torch.int64, device="cuda")
+    lens, table, ring, state = pc.new_tables(2)
+    calls = [(pc.attn, [x["q"], x["q_start"], x["seq_len"], x["table"], x["k"], x["v"], x["prefix"], x["L"], good.clone()], (7, )),
+             (pc.append, [kv, kv, slots, x["k"], x["v"]], ()),
+             (pc.tables, [lens, lens, table, ring, state, 2] + [t.clone() for t in (lens, state)]
+              + [torch.zeros(n, dtype=t, device="cuda") for n, t in ((3, torch.int32), (2, torch.int64), (2, torch.int32))], (5, ))]
+    for call, args, numbers in calls:
+        call(*args)
+        for i in range(len(args)):
+            # outputs may be None: they are then made by the call
+            if i in numbers or (wrong is None and i > {pc.attn: 7, pc.append: 9, pc.tables: 5}[call]):
+                continue
+            with pytest.raises(ValueError):
+                call(*args[:i], wrong, *args[i + 1:])
+    torch.cuda.synchronize()
+    assert pc.get_error() == 0
+
+
 # ---- streams, graphs, and the three calls together ------------------------------------------
 
 def test_outputs_belong_to_the_given_stream(ice):
