@@ -16,6 +16,7 @@ import of this module raises.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 import numpy as np
@@ -420,6 +421,14 @@ class IceIndex:
         return hk, hv
 
 
+def _int(x, name: str, bits: int = 32) -> int:
+    """x as a C integer argument; ctypes would cut a larger number to its low bits."""
+    x = operator.index(x)
+    if not -(1 << (bits - 1)) <= x < 1 << (bits - 1):
+        raise ValueError(f"{name} = {x} does not fit {bits} bits")
+    return x
+
+
 class PagedCache:
     """The plain paged cache of a batch whose requests share a prefix (an ice_paged
     handle: geometry, scratch and status word; the pages and tables are the caller's
@@ -433,10 +442,10 @@ class PagedCache:
     def __init__(self, *, n_kv_heads: int, n_q_heads: int, page_size: int, n_pages: int,
                  max_requests: int, max_blocks: int, max_tokens: int,
                  dtype: torch.dtype = torch.bfloat16, d: int = 128):
-        self.params = ice_paged_params(d=d, n_kv_heads=n_kv_heads, n_q_heads=n_q_heads,
-                                       page_size=page_size, dtype=_code(dtype),
-                                       max_requests=max_requests, max_blocks=max_blocks,
-                                       max_tokens=max_tokens, n_pages=n_pages)
+        sizes = dict(d=d, n_kv_heads=n_kv_heads, n_q_heads=n_q_heads, page_size=page_size,
+                     max_requests=max_requests, max_blocks=max_blocks, max_tokens=max_tokens)
+        self.params = ice_paged_params(dtype=_code(dtype), n_pages=_int(n_pages, "n_pages", 64),
+                                       **{k: _int(x, k) for k, x in sizes.items()})
         self.dtype = dtype
         self._h = ctypes.c_void_p()
         self.device = torch.device("cuda", torch.cuda.current_device())
@@ -509,6 +518,9 @@ class PagedCache:
             with torch.cuda.stream(stream):
                 return self.tables(seq_len, n_new, block_table, free_pages, free_state, n_slots, seq_len_out,
                                    free_state_out, q_start, slot_map, positions)
+        n_slots = _int(n_slots, "n_slots")
+        if n_slots < 0:
+            raise ValueError("n_slots must not be negative")
         n, i32, i64, check = self._count(seq_len, "seq_len"), torch.int32, torch.int64, self._ints
         ins = (check(seq_len, i32, (n,), "seq_len"), check(n_new, i32, (n,), "n_new"),
                check(block_table, i32, (n, self.params.max_blocks), "block_table"),
@@ -549,7 +561,7 @@ class PagedCache:
         if stream is not None:  # what is allocated here belongs to the stream that writes it
             with torch.cuda.stream(stream):
                 return self.attn(q, q_start, seq_len, block_table, k_pages, v_pages, prefix_table, prefix_len, out)
-        p, n = self.params, self._count(seq_len, "seq_len")
+        p, n, prefix_len = self.params, self._count(seq_len, "seq_len"), _int(int(prefix_len), "prefix_len")
         qp, qs = self._rows(q, p.n_q_heads, "q")
         if out is None:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
@@ -564,7 +576,7 @@ class PagedCache:
         _check(_lib.ice_paged_attn(
             self._h, n, q.shape[0], qp, qs, self._ints(q_start, torch.int32, (n + 1,), "q_start"),
             self._ints(seq_len, torch.int32, (n,), "seq_len"),
-            self._ints(block_table, torch.int32, (n, p.max_blocks), "block_table"), pt, int(prefix_len),
+            self._ints(block_table, torch.int32, (n, p.max_blocks), "block_table"), pt, prefix_len,
             kg, vg, _dev_ptr(out, self.dtype, "out", host_ok=False), _stream()), "ice_paged_attn")
         return out
 

@@ -7,6 +7,7 @@ import shutil
 import subprocess
 
 import pytest
+import torch
 
 from tests import paged_helpers as H
 
@@ -79,6 +80,27 @@ def test_plain_tables_by_hand():
     assert code == 0 and lens == [6, 2] and state == [5, 8] and q0 == [0, 3, 3]
     assert slots == [11, 20, 21, -1, -1] and pos == [3, 4, 5, 0, 0]
     assert table == [[2, 5, -1], [0, 4, -1]] and ring == [1, 4, -1, -1, 5, 3]
+
+
+@pytest.mark.parametrize("field", ["d", "n_kv_heads", "n_q_heads", "page_size", "max_requests", "max_blocks", "max_tokens", "n_pages"])
+def test_binding_refuses_sizes_that_do_not_fit(lib, field):
+    """A size whose low bits would be a valid one."""
+    sizes = dict(d=128, n_kv_heads=8, n_q_heads=32, page_size=16, max_requests=4, max_blocks=8, max_tokens=16, n_pages=64)
+    sizes[field] += 1 << (64 if field == "n_pages" else 32)
+    with pytest.raises(ValueError, match=field):
+        lib.PagedCache(**sizes)
+
+
+def test_binding_refuses_counts_that_do_not_fit(lib):
+    pc = lib.PagedCache.__new__(lib.PagedCache)
+    pc.params = _params(lib)
+    lens = torch.zeros(1, dtype=torch.int32)
+    for n in (1 << 32, -(1 << 31) - 1, -1):
+        with pytest.raises(ValueError, match="n_slots"):
+            pc.tables(lens, lens, lens, lens, lens, n)
+    for n in (1 << 32, (1 << 32) + 5, 1 << 31):
+        with pytest.raises(ValueError, match="prefix_len"):
+            pc.attn(lens, lens, lens, lens, lens, lens, lens, n)
 
 
 def test_debug_flags_need_a_handle(lib):
