@@ -86,6 +86,14 @@ void free_all(ice_paged* pg) {
     cudaFree(pg->words);
 }
 
+// A launch's result as a status. A failed one leaves no error behind that the caller's next, unrelated check of
+// the runtime would find.
+int launched(cudaError_t e) {
+    if (e == cudaSuccess) return ICE_OK;
+    cudaGetLastError();
+    return ICE_ERR_CUDA;
+}
+
 int es_of(const ice_paged* pg) { return pg->p.dtype == ICE_BF16 ? 2 : 4; }
 
 // A token stride in elements: at least the row, a multiple of 16 bytes.
@@ -185,7 +193,7 @@ int ice_paged_tables(ice_paged* pg, int32_t n_req, const int32_t* seq_len, const
         n_req, pg->p.max_blocks, pg->p.page_size, pg->p.n_pages, seq_len, n_new, block_table, free_pages,
         (const long long*)free_state, seq_len_out, (long long*)free_state_out, q_start, (long long*)slot_map,
         positions, n_slots, (unsigned*)pg->words + kWordTicket, pg->words + kWordStatus, (cudaStream_t)stream);
-    return e == cudaSuccess ? ICE_OK : ICE_ERR_CUDA;
+    return launched(e);
 }
 
 int ice_paged_append(ice_paged* pg, int32_t n_tokens, const void* k, int64_t k_stride, const void* v,
@@ -203,7 +211,7 @@ int ice_paged_append(ice_paged* pg, int32_t n_tokens, const void* k, int64_t k_s
         launch_paged_append(n_tokens, pg->p.n_kv_heads, pg->p.page_size, es_of(pg), pg->p.n_pages, k, k_stride, v,
                             v_stride, (const long long*)slot_map, k_pages, v_pages, pg->words + kWordStatus,
                             (cudaStream_t)stream);
-    return e == cudaSuccess ? ICE_OK : ICE_ERR_CUDA;
+    return launched(e);
 }
 
 int ice_paged_attn(ice_paged* pg, int32_t n_req, int32_t n_tokens, const void* q, int64_t q_stride,
@@ -251,11 +259,7 @@ int ice_paged_attn(ice_paged* pg, int32_t n_req, int32_t n_tokens, const void* q
     a.n_pages = pg->p.n_pages;
     a.debug = pg->debug;
     const cudaError_t e = launch_paged_attn(a, pg->p.dtype, pg->rows_cap, pg->n_sm, (cudaStream_t)stream);
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return ICE_ERR_CUDA;
-    }
-    return ICE_OK;
+    return launched(e);
 }
 
 }  // extern "C"

@@ -1,6 +1,7 @@
 """The plain paged cache on the GPU against its definition in 64 bits: block tables and slot
 maps, the append by slot map, the attention over a shared prefix and own tokens; refusals,
 streams, graphs, and a run of all three as a decode loop uses them."""
+import ctypes
 import random
 
 import pytest
@@ -644,6 +645,41 @@ def test_binding_refusals(ice):
               (lens, lens, table, ring[1:], state), (lens, lens, table, ring, state.int())):
         with pytest.raises(ValueError):
             pc.tables(*a, 4)
+
+
+def test_failed_launches_leave_no_error_behind(ice):
+    """Launches into a capture that has become invalid (by a wait for its stream) fail; the status says so, and the
+    runtime's last error, which the caller's next check would take for its own, is clear."""
+    c = _attn_case(12, BF16, 2, 4, 16, 100, [(1, 40), (1, 50)])
+    good, pc = _attn_run(ice, c)
+    x = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in c.items()}
+    kv, slots = torch.zeros((2, 2, D), dtype=BF16, device="cuda"), torch.full((2,), -1, dtype=torch.int64, device="cuda")
+    lens, table, ring, state = pc.new_tables(2)
+    outs = pc.tables(lens, lens, table, ring, state, 2)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    rt, s = ctypes.CDLL("libcudart.so.13"), ctypes.c_void_p(side.cuda_stream)
+    codes, left = [], []
+    assert rt.cudaStreamBeginCapture(s, 0) == 0
+    try:
+        assert rt.cudaStreamSynchronize(s) != 0
+        rt.cudaGetLastError()
+        for call in (lambda: pc.attn(x["q"], x["q_start"], x["seq_len"], x["table"], x["k"], x["v"], x["prefix"], x["L"],
+                                     out=good, stream=side),
+                     lambda: pc.append(kv, kv, slots, x["k"], x["v"], stream=side),
+                     lambda: pc.tables(lens, lens, table, ring, state, 2, *outs, stream=side)):
+            try:
+                call()
+                codes.append(0)
+            except ice.IceError as e:
+                codes.append(e.code)
+            left.append(rt.cudaGetLastError())
+    finally:
+        graph = ctypes.c_void_p()
+        assert rt.cudaStreamEndCapture(s, ctypes.byref(graph)) != 0
+        rt.cudaGetLastError()
+    assert codes == [ice.ICE_ERR_CUDA] * 3 and left == [0, 0, 0]
+    assert torch.equal(_attn_run(ice, c, pc=pc)[0], good) and pc.get_error() == 0
 
 
 @pytest.mark.parametrize("wrong", [None, 3, [1, 2], "number"])
