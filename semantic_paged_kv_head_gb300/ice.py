@@ -472,15 +472,18 @@ class PagedCache:
     @staticmethod
     def _count(t, name):
         """Entries of a list."""
-        if not isinstance(t, torch.Tensor) or t.dim() != 1:
-            raise ValueError(f"{name} must be a CUDA tensor of one dimension")
-        return t.shape[0]
+        try:
+            n, = t.shape
+        except (AttributeError, ValueError):
+            raise ValueError(f"{name} must be a CUDA tensor of one dimension") from None
+        return n
 
     def _ints(self, t, dtype, shape, name):
-        if not isinstance(t, torch.Tensor):
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous():
-            return t.data_ptr()
+        try:
+            if t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+                return t.data_ptr()
+        except AttributeError:
+            raise ValueError(f"{name} must be a CUDA tensor") from None
         if t.shape != shape:
             raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
         return _dev_ptr(t, dtype, name, host_ok=False)
@@ -518,9 +521,8 @@ class PagedCache:
             with torch.cuda.stream(stream):
                 return self.tables(seq_len, n_new, block_table, free_pages, free_state, n_slots, seq_len_out,
                                    free_state_out, q_start, slot_map, positions)
-        n_slots = _int(n_slots, "n_slots")
-        if n_slots < 0:
-            raise ValueError("n_slots must not be negative")
+        if not 0 <= n_slots <= 1 << 30:
+            raise ValueError(f"n_slots = {n_slots} must be from 0 to 2^30")
         n, i32, i64, check = self._count(seq_len, "seq_len"), torch.int32, torch.int64, self._ints
         ins = (check(seq_len, i32, (n,), "seq_len"), check(n_new, i32, (n,), "n_new"),
                check(block_table, i32, (n, self.params.max_blocks), "block_table"),
