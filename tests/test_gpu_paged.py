@@ -475,6 +475,17 @@ def test_attn_f32_equal_weights_of_a_million_keys(ice):
     assert float((got[0].cpu().double() / mean - 1).abs().max()) <= 80 * 2.0 ** -24
 
 
+@pytest.mark.parametrize("dtype,tol", [(BF16, 2.0 ** -8 + 2.0 ** -10 + 2.0 ** -12), (F32, 80 * 2.0 ** -24)])
+def test_attn_one_token_on_millions_of_keys(ice, dtype, tol):
+    """The same for a decode step, whose few rows take the prefix in 64 parts of thousands of tiles. The tolerances as above."""
+    P, L = 64, 1 << 24
+    g = torch.Generator().manual_seed(46)
+    k, v = torch.randn((2, 1, P, D), generator=g).to(dtype), (1 + torch.rand((2, 1, P, D), generator=g)).to(dtype)
+    table = torch.tensor([0, 1], dtype=torch.int32).repeat(L // P // 2)
+    got = _long_prefix_call(ice, dtype, 1, 8, P, 1, L, table, k, v, torch.zeros((1, 8, D), dtype=dtype)).double()
+    assert float((got / v.double().mean((0, 1, 2)) - 1).abs().max()) <= tol
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("rise", [0.0, 1.0])
 def test_attn_long_passes(ice, dtype, rise):
