@@ -497,19 +497,22 @@ int ice_paged_append(ice_paged* pg, int32_t n_tokens, const void* k, int64_t k_s
                      void* stream);
 
 /*
- * ice_paged_attn - attention of the batch's new tokens over the shared prefix,
- * whose keys and values are read once for the whole batch, and over each request's
- * own tokens.
+ * ice_paged_attn - attention of the batch's new tokens over the shared prefix and over
+ * each request's own tokens. The prefix's keys and values are read once for all requests
+ * of few new tokens (up to 128 * n_kv_heads / n_q_heads with bf16; up to 16 to 64 times
+ * that ratio with f32); a request of more goes through the prefix by itself.
  *
  * q: device, n_tokens x [n_q_heads][d], dtype; q_stride as k_stride above.
  * q_start: device int32 [n_req + 1]; request r's new tokens are q_start[r] ..
  *   q_start[r + 1] - 1 of q, in order (one for a decode step, more for draft
  *   tokens or a chunk of a prompt, none for a request that waits). q_start[0] = 0,
- *   q_start[n_req] <= n_tokens.
+ *   q_start[n_req] <= n_tokens. Rows behind q_start[n_req] take the time of others: the
+ *   work on the prefix goes by n_tokens.
  * seq_len: device int32 [n_req], each request's own tokens, the new ones among them.
  * block_table: device int32 [n_req][max_blocks].
  * prefix_table: device int32 [ceil(prefix_len / P)], the prefix's pages; NULL when
- *   prefix_len is 0. prefix_len may end inside a page.
+ *   prefix_len is 0. prefix_len (up to 2^30) may end inside a page; like n_tokens it is a
+ *   host argument, so a captured graph keeps it.
  * out: device, [n_tokens][n_q_heads][d], dtype, not overlapping q.
  *
  * Query head g of KV head h is h * G + g. The i-th new token of request r sees every
@@ -519,8 +522,9 @@ int ice_paged_append(ice_paged* pg, int32_t n_tokens, const void* k, int64_t k_s
  * were. Slots of the pages behind a length are not used, whatever they hold;
  * values of tokens that exist are finite (a token hidden from some rows of its tile
  * has weight zero there, and zero times an infinity would be NaN).
- * Sums, softmax statistics and the parts' joining are in fp32; with bf16 the
- * weights are rounded to bf16 before they meet the values, as the values are.
+ * Sums, softmax statistics and the parts' joining are in fp32, and their error does not
+ * grow with the length; with bf16 the weights are rounded to bf16 before they meet the
+ * values, as the values are.
  *
  * A page id outside the pool reads as a page of zeros and is reported
  * (ICE_ERR_BOUNDS); q_start or seq_len out of range are reported and out is left

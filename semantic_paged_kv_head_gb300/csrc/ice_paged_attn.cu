@@ -12,19 +12,20 @@ namespace ice {
 // One block takes items in turn: rows (new tokens x G heads) against a range of tiles of 64
 // keys, in one pass with a running maximum m and sum l a row: m' = max(m, max_t s_t),
 // l' = l 2^(m - m') + sum_t 2^(s_t - m'), and the same factor on the output, with
-// s_t = q . k_t log2(e) / sqrt(d). fp32 has no tensor-core form that keeps its 24 bits.
+// s_t = q . k_t log2(e) / sqrt(d). On the CUDA cores: a tensor-core form that keeps fp32's 24 bits takes three
+// bf16 terms a value and six products.
 //
 // More than kFewRows rows (up to 64): the next tile is copied into shared memory while one is worked
 // on, and the page ids of the one after are read. A warp has RW rows: a lane makes the scores of
 // two keys, and then four dimensions of the output, so that the statistics need shuffles only, and
-// the rows' operands are read once a warp. 4 requests of up to 512 tokens on 4k: 1.28 ms, 40 TFLOP/s,
+// the rows' operands are read once a warp. 4 requests of up to 512 tokens on 4k: 1.29 ms, 40 TFLOP/s,
 // half of what the fp32 units give; neither they (56 %) nor shared memory (about half, by count) are full. 16 warps
 // of half the rows were slower (1.51 ms, spills), operands one step ahead in registers no faster.
 //
 // Few rows (a decode step's own tokens): bound by memory. The warps take groups of 4 keys in
 // turn, 8 lanes a key for the scores and 4 dimensions a lane for the output, straight from
 // global memory, the next group's loads under way; their parts meet in shared memory at the end.
-// 24 requests of up to 777 own tokens: 14.0 us, of which about 11 us are the call's fixed part
+// 24 requests of up to 777 own tokens: 14.4 us, of which about 11 us are the call's fixed part
 // (plan, first loads, joining).
 // ---------------------------------------------------------------------------
 constexpr int kSimtThreads = 256;
@@ -444,7 +445,7 @@ __global__ void __maxnreg__(208) paged_simt_kernel(PagedAttn a, PagedTiles z) {
 // nothing was seen. Rows with one part were written by the attention kernel. Bound by the
 // parts' bytes, read once, where there are many rows (PW = 1), and by the latency of
 // a chain of loads where there are few: the warps of a row then take every PW-th part. 4 requests
-// of up to 400 tokens on 8k: 24.5 us cold for 52 MB of parts; decode steps 7 to 15 us cold.
+// of up to 400 tokens on 8k: 24.2 us cold for 52 MB of parts; decode steps 7 to 14 us cold.
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;

@@ -32,7 +32,9 @@ namespace ice {
 // The maximum m that the weights refer to moves only when a row's true maximum
 // has grown by more than 8 (weights stay below 2^8; bf16 rounds them by 2^-8 of
 // themselves at most, whatever their size); only then O is read back and rescaled. The sum
-// l is of the rounded weights, the ones that meet V, in fp32.
+// l is of the rounded weights, the ones that meet V, in fp32. (The product takes both operands in one type, and V is
+// bf16; weights in two terms would double it. Error of the output against 64 bits, as norms: 2.3e-3, with
+// fp32 weights 1.7e-3, the output's own rounding.)
 //
 // A product's addition to O cuts off what does not fit O's 24 bits, and the cuts of sums of one sign add up:
 // with equal weights O lost 0.4 % over a million keys, 3 % over four. So every kFaFold tiles O and l are
@@ -48,8 +50,8 @@ namespace ice {
 // Every wait is bounded (kWaitNs; those for a next item, kWaitNs without progress); when one runs out the block's roles leave their loops,
 // what is in flight ends, and the status word says ICE_ERR_TIMEOUT.
 //
-// Bound by memory with few rows: 4 requests on 250k tokens, 168 us, 6.13 TB/s (90 % of the
-// measured copy rate); 16 requests with 16k own tokens each on average, 177 us, 5.85 TB/s. With 256
+// Bound by memory with few rows: 4 requests on 250k tokens, 167 us, 6.17 TB/s (91 % of the
+// measured copy rate); 16 requests with 16k own tokens each, 178 us, 6.03 TB/s. With 256
 // rows or more a key tile is bound by the softmax of its two streams (2500 cycles for 16.8 MFLOP,
 // of which the products take 2048): chunks of up to 1021 tokens on 8k, 421 us, 1.24 PFLOP/s (66 %
 // of the measured rate). Tried and not kept: key tiles of 64 with two score buffers a stream (twice

@@ -16,7 +16,7 @@ namespace ice {
 // no block waits for another. What a call may replace in place (lengths, ring
 // state) is written by the last block to have read it, found by a ticket.
 // Bound by latency: the launch, the scan and the look-ups in a row, 5.5 us for 16 requests,
-// 7.6 us for 256. 4096 requests with 1.03 million new tokens: 13.8 us, 12.8 MB written; four
+// 7.8 us for 256. 4096 requests with 1.03 million new tokens: 13.8 us, 12.8 MB written; four
 // slots a thread take one search, one divide and a wide store (one slot a thread: 21 us, a divide
 // a slot 14.9, eight slots a thread 14.4 and 1.7 us more for the small calls).
 // ---------------------------------------------------------------------------
