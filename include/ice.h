@@ -522,9 +522,9 @@ int ice_paged_append(ice_paged* pg, int32_t n_tokens, const void* k, int64_t k_s
  * were. Slots of the pages behind a length are not used, whatever they hold;
  * values of tokens that exist are finite (a token hidden from some rows of its tile
  * has weight zero there, and zero times an infinity would be NaN).
- * Sums, softmax statistics and the parts' joining are in fp32, and their error does not
- * grow with the length; with bf16 the weights are rounded to bf16 before they meet the
- * values, as the values are.
+ * Sums, softmax statistics and the parts' joining are in fp32, sums over many keys
+ * compensated or made in steps; with bf16 the weights are rounded to bf16 before they meet
+ * the values, as the values are.
  *
  * A page id outside the pool reads as a page of zeros and is reported
  * (ICE_ERR_BOUNDS); q_start or seq_len out of range are reported and out is left
