@@ -537,6 +537,170 @@ int ice_paged_attn(ice_paged* pg, int32_t n_req, int32_t n_tokens, const void* q
                    const int32_t* prefix_table, int32_t prefix_len, const void* k_pages,
                    const void* v_pages, void* out, void* stream);
 
+/* ---- around the attention of a serving step ------------------------------ */
+
+/*
+ * Rotary positions of a model. Pair i < n_pairs of a head turns by freq[i] times the
+ * token's position on axis axis[i], in radians: (a, b) -> (a cos - b sin, b cos + a sin).
+ * One axis is a text's position; images and video have several (time, height, width).
+ */
+typedef struct ice_rope {
+    int32_t n_axes;      /* 1..4                                                     */
+    int32_t n_pairs;     /* 8..64, a multiple of 8; elements behind them stay         */
+    int32_t interleaved; /* 0: pair i is elements i, i + n_pairs; 1: 2i, 2i + 1       */
+    int32_t reserved;    /* 0                                                        */
+    double freq[64];     /* radians a position; finite, any sign                      */
+    int32_t axis[64];    /* 0 .. n_axes - 1                                          */
+} ice_rope;
+
+/*
+ * ice_paged_rope_append - ice_paged_append with the keys (and, beside it, the queries)
+ * rotated by their positions on the way.
+ *
+ * rope: host.
+ * positions: device int32, n_axes rows of n_tokens, row x at positions + x * pos_stride
+ *   (pos_stride >= n_tokens where n_axes > 1). pos_offset is added to each (for the positions
+ *   that ice_paged_tables writes, the length of the shared prefix). Angles are right at every
+ *   position of 32 bits.
+ * q, q_out: device, n_tokens x [n_q_heads][d]; token i starts q_stride (q_out_stride)
+ *   elements after token i - 1. q_out receives the rotated queries. It is q itself (same
+ *   address and stride) or does not overlap it. Both NULL: keys and values alone.
+ * The rest as in ice_paged_append. A token whose slot is -1, or out of range, is skipped
+ * altogether: its row of q_out stays as it was.
+ */
+int ice_paged_rope_append(ice_paged* pg, int32_t n_tokens, const ice_rope* rope, const int32_t* positions,
+                          int64_t pos_stride, int64_t pos_offset, const void* q, int64_t q_stride, void* q_out,
+                          int64_t q_out_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                          const int64_t* slot_map, void* k_pages, void* v_pages, void* stream);
+
+/*
+ * Pages that several requests hold. page_refs, device int32 [n_pages], counts for each
+ * page the block tables (and lists of the caller's own, such as a prefix's) that name it; 0
+ * is a free page. The caller starts with zeros, and adds what its own lists hold. A request's row
+ * names a page once. Requests that share pages are forked by ice_paged_fork and moved
+ * on by ice_paged_tables_shared; ice_paged_tables knows nothing of counts and is not to be
+ * used with such a pool.
+ *
+ * The first of these calls on a handle allocates their scratch (8 bytes a page, 4 a request;
+ * ICE_ERR_CAPACITY if that fails). A call that would have to allocate while its stream is
+ * captured returns ICE_ERR_INVALID_ARG: make one eager call before.
+ */
+
+/*
+ * ice_paged_fork - new requests that continue others: parallel samples, beams, branches.
+ *
+ * src, dst: device int32 [n_fork]. Request dst[i] becomes request src[i] (or its first
+ *   fork_len[i] tokens) by sharing its pages; nothing is copied. A source may be given
+ *   many times. Destinations are distinct, hold no tokens (seq_len 0) and are no sources.
+ * fork_len: device int32 [n_fork] or NULL (all tokens).
+ * seq_len, seq_len_out: device int32 [n_req]; seq_len_out may be seq_len.
+ * block_table: device int32 [n_req][max_blocks], in and out: the destinations' rows.
+ * page_refs: in and out.
+ *
+ * All or nothing: with an index, length or destination that is not as said nothing changes,
+ * seq_len_out is seq_len, and the status word says ICE_ERR_BOUNDS. (A page id out of range in
+ * a source's row is copied as it is, and reported.)
+ */
+int ice_paged_fork(ice_paged* pg, int32_t n_fork, const int32_t* src, const int32_t* dst,
+                   const int32_t* fork_len, int32_t n_req, const int32_t* seq_len, int32_t* block_table,
+                   int32_t* page_refs, int32_t* seq_len_out, void* stream);
+
+/*
+ * ice_paged_tables_shared - ice_paged_tables for requests that share pages.
+ *
+ * As ice_paged_tables, and:
+ *  - a page that a request no longer touches goes back to the ring when no other holds it. One that several
+ *    requests let go of in a call is given back once, in the place of the last of them.
+ *  - a request that grows writes into its last page if that is incomplete. Where others hold that
+ *    page too, the request takes a new page in its place (before the others that it takes), and
+ *    copy_src[r], copy_dst[r] say that the old one is to be copied (ice_paged_copy, in every layer,
+ *    before rows are written). If all holders of a page let go of it in one call, the last of those
+ *    that write into it keeps it.
+ * copy_src, copy_dst: device int32 [n_req]; -1 where nothing is to be copied.
+ * page_refs: in and out. A count below the number of a page's holders that let go of it is reported as
+ *   ICE_ERR_BOUNDS, as is a page id out of range; as with any other failure nothing changes then, and
+ *   copy_src and copy_dst are all -1.
+ */
+int ice_paged_tables_shared(ice_paged* pg, int32_t n_req, const int32_t* seq_len, const int32_t* n_new,
+                            int32_t* block_table, int32_t* free_pages, const int64_t* free_state,
+                            int32_t* page_refs, int32_t* seq_len_out, int64_t* free_state_out, int32_t* q_start,
+                            int64_t* slot_map, int32_t* positions, int32_t n_slots, int32_t* copy_src,
+                            int32_t* copy_dst, void* stream);
+
+/*
+ * ice_paged_copy - pages copied by a list, K and V, in every layer.
+ *
+ * src, dst: device int32 [n]; page dst[i] becomes a copy of page src[i]. Entries with a -1 are
+ *   skipped; other ids outside the pool are skipped and reported (ICE_ERR_BOUNDS). The destinations
+ *   of a call are distinct, and none is a source of it.
+ * k_pages, v_pages: the first layer's; layer y's begin y * layer_stride elements later
+ *   (layer_stride a multiple of 16 bytes, at least a layer's pages; not used with one layer).
+ */
+int ice_paged_copy(ice_paged* pg, int32_t n, const int32_t* src, const int32_t* dst, int32_t n_layers,
+                   int64_t layer_stride, void* k_pages, void* v_pages, void* stream);
+
+/*
+ * ice_paged_compact - the pages in use (page_refs > 0) moved to the front of the pool, so that its end
+ * is free: to hand memory back, or before a pool is saved.
+ *
+ * With L pages in use, those at L and behind go, in order, to the free ones before L; the others stay.
+ * move_src, move_dst: device int32 [n_moves]; receive the moves in order, for ice_paged_copy, and -1
+ *   behind the last. n_moves = n_pages / 2 always suffices.
+ * seq_len: device int32 [n_req]. block_table, block_table_out: device int32 [n_req][max_blocks]; the
+ *   entries of each request's pages are rewritten, others in block_table_out stay as they were.
+ * extra, extra_out: device int32 [n_extra], further page ids of the caller's (prefixes); NULL when
+ *   n_extra is 0.
+ * page_refs, page_refs_out: device int32 [n_pages].
+ *   Each of the three outputs may be its input.
+ * free_pages, free_state_out: out: a ring of the pages L .. n_pages - 1 from head 0 on; entries of free_pages
+ *   behind those stay as they were.
+ *
+ * All or nothing: where n_moves does not suffice (ICE_ERR_CAPACITY), or a length, a count below 0, a page id
+ * out of range or of a page that is not in use is found (ICE_ERR_BOUNDS), move_src and move_dst are all -1, the outputs are
+ * the inputs, and free_pages and free_state_out stay as they were.
+ */
+int ice_paged_compact(ice_paged* pg, int32_t n_req, const int32_t* seq_len, const int32_t* block_table,
+                      int32_t n_extra, const int32_t* extra, const int32_t* page_refs, int32_t* free_pages,
+                      int64_t* free_state_out, int32_t n_moves, int32_t* move_src, int32_t* move_dst,
+                      int32_t* block_table_out, int32_t* extra_out, int32_t* page_refs_out, void* stream);
+
+/*
+ * ice_paged_verify - drafted tokens against the target model (speculative decoding): how many of
+ * each request's drafts stay, and the token after them.
+ *
+ * Request r has n_draft[r] drafts, 0 .. n_draft_max; -1 for a request that takes no part (its
+ * tokens are all -1, n_accepted and n_new 0).
+ * draft_tokens: device int32 [n_req][n_draft_max]; not used where n_draft_max is 0.
+ * target: device, dtype (ICE_F32 or ICE_BF16), rows of `vocab` entries: row i of request r, at
+ *   target + r * target_req_stride + i * target_row_stride elements, belongs to the place of draft i, and row
+ *   n_draft[r] to the place behind the last draft.
+ * draft: as target, the probabilities that the draft i was drawn from; NULL for drafts that were not drawn
+ *   (looked up in the prompt, or greedy): q is then 1 at the draft and 0 elsewhere.
+ * uniform: device float32 [n_req][n_draft_max + 1], random numbers from [0, 1) (others count as the nearest
+ *   of these): entry i for draft i, the last for the token behind the drafts that stay.
+ *   With them target and draft are probabilities p and q, not necessarily of sum 1. Draft x stays if u q(x) < p(x)
+ *   and all before it stay. After the first that does not, the token is drawn from max(p - q, 0) of that place (from p if
+ *   that is 0 everywhere); if all stay, from p of the last row: it is the first j with
+ *   w_0 + .. + w_j > u (w_0 + .. + w_{vocab - 1}). The sums are held in more than 40 bits. NaN, negative entries and
+ *   those above 2^100 count as 0.
+ * uniform NULL: greedy. target may be logits; draft is not used. Draft x stays if it is the index of
+ *   its row's largest entry (of equal ones the lowest index; NaN is passed over), and the token is that of the first
+ *   row whose draft does not stay.
+ * tokens: device int32 [n_req][n_draft_max + 1]; receives the drafts that stay, the token, then -1.
+ * n_accepted: device int32 [n_req]; receives the drafts that stay.
+ * n_new: device int32 [n_req]; receives n_accepted - n_draft, by how many tokens the request changes in the next
+ *   ice_paged_tables or ice_paged_tables_shared call: the rejected ones.
+ *
+ * A draft outside the vocabulary does not stay, and is reported (ICE_ERR_BOUNDS), as is an n_draft out of
+ * range (the request takes no part) and a deciding row that leaves nothing (all entries 0 or NaN; the token is then
+ * -1). n_draft_max <= 63, vocab <= 2^22 (ICE_ERR_UNSUPPORTED above).
+ */
+int ice_paged_verify(ice_paged* pg, int32_t n_req, int32_t n_draft_max, int32_t vocab, int32_t dtype,
+                     const int32_t* draft_tokens, const int32_t* n_draft, const void* target,
+                     int64_t target_req_stride, int64_t target_row_stride, const void* draft,
+                     int64_t draft_req_stride, int64_t draft_row_stride, const float* uniform, int32_t* tokens,
+                     int32_t* n_accepted, int32_t* n_new, void* stream);
+
 /*
  * ice_paged_debug_set_flags - test hooks (0 = normal operation).
  * ICE_DEBUG_STALL_ATTN: in ice_paged_attn with bf16 one copy of keys expects 16 bytes

@@ -1,0 +1,635 @@
+// Pages that several requests hold: forking, block tables with copy on write, compaction of the pool, copies of pages.
+#include <algorithm>
+
+#include "ice_paged_scan.cuh"
+#include "ice_paged_share.cuh"
+
+namespace ice {
+
+// ---------------------------------------------------------------------------
+// Forking: a row of page ids copied and each page's count raised. Every block checks the whole call by itself (the
+// destinations as a bitmap in shared memory) and does its share of pieces of 256 columns; the lengths, which may be replaced
+// in place, are written by the last block to have read them.
+// ---------------------------------------------------------------------------
+constexpr int kForkThreads = 256, kForkPiece = 256;
+
+__global__ void __launch_bounds__(kForkThreads) fork_kernel(Fork a) {
+    __shared__ unsigned s_dst[kPagedMaxRequests / 32];
+    __shared__ int s_last;
+    const int tid = threadIdx.x, lane = tid & 31;
+    for (int i = tid; i < kPagedMaxRequests / 32; i += kForkThreads) s_dst[i] = 0;
+    __syncthreads();
+    pdl_wait_then_release();
+    const long long cap = (long long)a.max_blocks * a.P;
+    auto length = [&](int i) { return a.fork_len ? a.fork_len[i] : a.seq_len[a.src[i]]; };
+    bool bad = false;
+    for (int i = tid; i < a.n_fork; i += kForkThreads) {
+        const int s = a.src[i], d = a.dst[i];
+        if (s < 0 || s >= a.n || d < 0 || d >= a.n) {
+            bad = true;
+            continue;
+        }
+        const int have = a.seq_len[s], len = length(i);
+        bad |= (atomicOr(&s_dst[d >> 5], 1u << (d & 31)) >> (d & 31)) & 1;  // a destination given twice
+        bad |= have < 0 || have > cap || len < 0 || len > have || a.seq_len[d] != 0;
+    }
+    __syncthreads();
+    for (int i = tid; i < a.n_fork; i += kForkThreads) {
+        const int s = a.src[i];
+        bad |= s >= 0 && s < a.n && ((s_dst[s >> 5] >> (s & 31)) & 1);
+    }
+    const bool ok = !__syncthreads_or(bad);
+    if (ok) {
+        const int pieces = (a.max_blocks + kForkPiece - 1) / kForkPiece;
+        const long long items = (long long)a.n_fork * pieces;
+        const int step = gridDim.x * (kForkThreads / 32);
+        bool range = false;
+        for (long long x = blockIdx.x * (kForkThreads / 32) + (tid >> 5); x < items; x += step) {
+            const int i = (int)(x / pieces), c0 = (int)(x - (long long)i * pieces) * kForkPiece;
+            const int n = min((length(i) + a.P - 1) / a.P, c0 + kForkPiece);
+            const int* from = a.block_table + (long long)a.src[i] * a.max_blocks;
+            int* to = a.block_table + (long long)a.dst[i] * a.max_blocks;
+#pragma unroll 4
+            for (int c = c0 + lane; c < n; c += 32) {
+                const int p = from[c];
+                to[c] = p;
+                if (p >= 0 && p < a.n_pages) atomicAdd(a.page_refs + p, 1);
+                else range = true;
+            }
+        }
+        if (range) set_status(a.status, ICE_ERR_BOUNDS);
+    }
+    __syncthreads();
+    if (tid == 0) {
+        __threadfence();
+        s_last = gridDim.x == 1 || atomicAdd(&a.head->ticket, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!s_last) return;
+    if (a.seq_len_out != a.seq_len)
+        for (int r = tid; r < a.n; r += kForkThreads)
+            if (!ok || !((s_dst[r >> 5] >> (r & 31)) & 1)) a.seq_len_out[r] = a.seq_len[r];
+    if (ok)
+        for (int i = tid; i < a.n_fork; i += kForkThreads) a.seq_len_out[a.dst[i]] = length(i);  // no source is a destination
+    if (tid == 0) {
+        if (!ok) set_status(a.status, ICE_ERR_BOUNDS);
+        a.head->ticket = 0;
+    }
+}
+
+cudaError_t launch_fork(const Fork& a, cudaStream_t s) {
+    const long long items = (long long)a.n_fork * ((a.max_blocks + kForkPiece - 1) / kForkPiece);
+    const int blocks = (int)std::max<long long>(1, std::min<long long>(152, (items + 7) / 8));
+    return launch_pdl(fork_kernel, dim3(blocks), dim3(kForkThreads), 0, s, a);
+}
+
+// ---------------------------------------------------------------------------
+// One step's block tables where pages may have several holders. Three phases:
+//
+// claim  A request lets go of the pages that it no longer touches, and of the page that it is about to write
+//        into (its last, incomplete one): each lowers the page's count by one, and leaves its name with the page.
+//        The largest name stays: a request that writes goes before one that leaves, then the later request before
+//        the earlier. A name carries the call's number, so that names of earlier calls lose and are never cleared.
+// count  A page whose count came to 0 has lost all its holders. If its name is of one that writes, that request
+//        keeps it; else the named request gives it back to the ring. A request that writes and does not keep its page
+//        takes a new one and copies. So each request knows how many pages it takes and gives back.
+// fill   As without sharing: sums over the requests, after which every entry is a function of what is there.
+//
+// Names make the result independent of the order in which the blocks run; the counts are whole numbers. If the step cannot be
+// carried out the claims are taken back by adding them again.
+//
+// Bound by latency. Small steps run the phases in one block, others as three launches.
+// ---------------------------------------------------------------------------
+constexpr int kShrThreads = 1024, kShrGridThreads = 256;
+constexpr int kShrSlots = 4;  // consecutive slots of a thread
+
+__device__ __forceinline__ unsigned long long claim_name(unsigned long long epoch, bool writes, int r) {
+    // above every word that a compaction leaves in the claims (below 2^31)
+    return (epoch + (1ull << 20)) << 16 | (writes ? 1u << 15 : 0u) | (unsigned)(r + 1);
+}
+
+// A request's lengths in tokens and pages. grows: it writes into a page that is there.
+struct ShareReq {
+    int old_len, new_len, had, has;
+    int bad;
+    bool grows;
+};
+__device__ __forceinline__ ShareReq share_req(const SharedTables& a, int r) {
+    ShareReq q;
+    const long long cap = (long long)a.max_blocks * a.P, o = a.seq_len[r], w = o + a.n_new[r];
+    q.bad = o < 0 || o > cap || w < 0 ? kBadBounds : w > cap ? kBadCapacity : 0;
+    q.old_len = (int)o, q.new_len = (int)w;
+    q.had = q.has = 0;
+    q.grows = false;
+    if (q.bad) return q;
+    q.had = (int)((o + a.P - 1) / a.P), q.has = (int)((w + a.P - 1) / a.P);
+    q.grows = w > o && (int)o % a.P != 0;
+    return q;
+}
+
+// Calls f(page) for the pages that the request lets go of, a lane each; returns whether an id was out of range.
+template <typename F>
+__device__ __forceinline__ bool for_claims(const SharedTables& a, int r, const ShareReq& q, F f) {
+    const int lane = threadIdx.x & 31;
+    const int* row = a.block_table + (long long)r * a.max_blocks;
+    bool bad = false;
+    if (q.grows) {
+        if (lane == 0) {
+            const int p = row[q.had - 1];
+            if (p >= 0 && p < a.n_pages) f(p);
+            else bad = true;
+        }
+        return bad;
+    }
+    for (int c = q.has + lane; c < q.had; c += 32) {
+        const int p = row[c];
+        if (p >= 0 && p < a.n_pages) f(p);
+        else bad = true;
+    }
+    return bad;
+}
+
+__device__ __forceinline__ void share_claim(const SharedTables& a, int warp, int warps) {
+    const unsigned long long epoch = a.w.head->epoch;
+    for (int r = warp; r < a.n; r += warps) {
+        const ShareReq q = share_req(a, r);
+        const unsigned long long name = claim_name(epoch, q.grows, r);
+        int bad = q.bad;
+        if (for_claims(a, r, q, [&](int p) {
+                atomicSub(a.page_refs + p, 1);
+                atomicMax(a.w.claim + p, name);
+            }))
+            bad |= kBadBounds;
+        if (bad) atomicOr(&a.w.head->flags, bad);
+    }
+}
+
+// Whether the request is the one that decides on a page that it has let go of, and that nobody holds.
+__device__ __forceinline__ bool share_mine(const SharedTables& a, int p, unsigned long long name) {
+    return __ldcg(a.page_refs + p) == 0 && __ldcg(a.w.claim + p) == name;
+}
+
+__device__ __forceinline__ void share_count(const SharedTables& a, int warp, int warps) {
+    const unsigned long long epoch = a.w.head->epoch;
+    for (int r = warp; r < a.n; r += warps) {
+        const ShareReq q = share_req(a, r);
+        const unsigned long long name = claim_name(epoch, q.grows, r);
+        int mine = 0;
+        bool bad = false;
+        for_claims(a, r, q, [&](int p) {
+            mine += share_mine(a, p, name);
+            bad |= __ldcg(a.page_refs + p) < 0;  // more holders than the page's count
+        });
+        if (bad) atomicOr(&a.w.head->flags, kBadBounds);
+        mine = __reduce_add_sync(0xffffffffu, mine);
+        if ((threadIdx.x & 31) == 0) a.w.req[r] = q.grows ? (mine ? 0 : 1) : 2 * mine;
+    }
+}
+
+template <int NT>
+__device__ __forceinline__ void share_fill(const SharedTables& a) {
+    extern __shared__ int shr_smem[];
+    __shared__ TabSums sums;
+    __shared__ int s_last;
+    const int tid = threadIdx.x, lane = tid & 31, n = a.n, P = a.P;
+    int* tok_cum = shr_smem;           // [n + 1] new tokens before each request
+    int* pop_cum = tok_cum + n + 1;    // [n + 1] pages taken
+    int* push_cum = pop_cum + n + 1;   // [n + 1] pages given back
+    const long long head = a.free_state[0], tail = a.free_state[1], n_pages = a.n_pages;
+    const int flags = __ldcg(&a.w.head->flags);
+    const int per = (n + NT - 1) / NT, r0 = min(tid * per, n), r1 = min(r0 + per, n);
+    unsigned x[3] = {0, 0, 0}, tot[3];
+    auto add = [&](int r) {
+        const ShareReq q = share_req(a, r);
+        const int c = __ldcg(a.w.req + r);
+        x[0] += max(q.new_len - q.old_len, 0);
+        x[1] += max(q.has - q.had, 0) + (c & 1);
+        x[2] += c >> 1;
+    };
+    bool over = false;
+    if (!flags) {
+        for (int r = r0; r < r1; ++r) {
+            add(r);
+            over |= (x[0] | x[1] | x[2]) >> 31;  // each term is below 2^31: seen before a sum can wrap
+        }
+    }
+    bool wrapped;
+    scan3<NT>(x, tot, wrapped, sums);
+    over = __syncthreads_or(over);
+    // every block comes to the same verdict
+    int code = ICE_OK;
+    if ((flags & kBadBounds) || head < 0 || tail < head || tail - head > n_pages) code = ICE_ERR_BOUNDS;
+    else if ((flags & kBadCapacity) || over || wrapped || tot[1] > tail - head || tot[0] > (unsigned)a.n_slots) code = ICE_ERR_CAPACITY;
+    else if (tail - head + tot[2] > n_pages) code = ICE_ERR_BOUNDS;
+    const bool ok = code == ICE_OK;
+    const int n_tok = ok ? (int)tot[0] : 0, n_pop = ok ? (int)tot[1] : 0, n_push = ok ? (int)tot[2] : 0;
+    if (ok) {
+        for (int r = r0; r < r1; ++r) {
+            tok_cum[r] = (int)x[0];
+            pop_cum[r] = (int)x[1];
+            push_cum[r] = (int)x[2];
+            add(r);
+        }
+    }
+    if (tid == 0) {
+        tok_cum[n] = n_tok;
+        pop_cum[n] = n_pop;
+        push_cum[n] = n_push;
+    }
+    __syncthreads();
+    const int hm = ok ? (int)(head % n_pages) : 0, tm = ok ? (int)(tail % n_pages) : 0;
+    auto ring = [&](int base, int j) {  // base, j < n_pages < 2^31: the sum may pass 2^31
+        const long long p = (long long)base + j;
+        return (int)(p < n_pages ? p : p - n_pages);
+    };
+    const int first = blockIdx.x * NT + tid, step = gridDim.x * NT;
+    for (int r = first; r <= n; r += step) a.q_start[r] = ok ? tok_cum[r] : 0;
+    for (int r = first; r < n; r += step) {
+        const bool copies = ok && (__ldcg(a.w.req + r) & 1);
+        if (!copies) a.copy_src[r] = a.copy_dst[r] = -1;
+        if (ok && !copies) {
+            const ShareReq q = share_req(a, r);
+            if (q.grows) a.page_refs[a.block_table[(long long)r * a.max_blocks + q.had - 1]] = 1;  // kept, nobody else's
+        }
+    }
+    const bool wide = ((uintptr_t)a.slot_map & 15) == 0 && ((uintptr_t)a.positions & 15) == 0;
+    for (long long i4 = (long long)first * kShrSlots; i4 < a.n_slots; i4 += (long long)step * kShrSlots) {
+        const int i0 = (int)i4;
+        long long slot[kShrSlots];
+        int pos[kShrSlots];
+        // the slot's request, its first slot and that of the one after; page, its id, offset in it; pages that the
+        // request keeps
+        int r = 0, b = 0, next = 0, pg = 0, id = 0, off = 0, held = 0;
+        auto page_id = [&]() {
+            id = pg < held ? a.block_table[(long long)r * a.max_blocks + pg] : a.free_pages[ring(hm, pop_cum[r] + pg - held)];
+        };
+        if (i0 < n_tok) r = find_row(tok_cum, n, i0);
+#pragma unroll
+        for (int k = 0; k < kShrSlots; ++k) {
+            const int i = i0 + k;
+            slot[k] = -1;
+            pos[k] = 0;
+            if (i < n_tok) {
+                if (k == 0 || i >= next) {
+                    while (tok_cum[r + 1] <= i) ++r;
+                    b = tok_cum[r], next = tok_cum[r + 1];
+                    const int o = a.seq_len[r], p = o + i - b;
+                    // a page that is copied is the first of those taken
+                    held = (o + P - 1) / P - (__ldcg(a.w.req + r) & 1);
+                    pg = p / P;
+                    off = p - pg * P;
+                    page_id();
+                } else if (++off == P) {
+                    off = 0;
+                    ++pg;
+                    page_id();
+                }
+                pos[k] = pg * P + off;
+                slot[k] = (long long)id * P + off;
+            }
+        }
+        if (wide && i0 + kShrSlots <= a.n_slots) {
+            longlong2* d = reinterpret_cast<longlong2*>(a.slot_map + i0);
+            d[0] = make_longlong2(slot[0], slot[1]);
+            d[1] = make_longlong2(slot[2], slot[3]);
+            if (a.positions) *reinterpret_cast<int4*>(a.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kShrSlots; ++k)
+                if (i0 + k < a.n_slots) {
+                    a.slot_map[i0 + k] = slot[k];
+                    if (a.positions) a.positions[i0 + k] = pos[k];
+                }
+        }
+    }
+    for (int j = first; j < n_pop; j += step) {
+        const int r = find_row(pop_cum, n, j), k = j - pop_cum[r], copies = __ldcg(a.w.req + r) & 1;
+        const int had = (a.seq_len[r] + P - 1) / P, p = a.free_pages[ring(hm, j)];
+        int* e = a.block_table + (long long)r * a.max_blocks + had - copies + k;
+        if (copies && k == 0) {
+            a.copy_src[r] = *e;
+            a.copy_dst[r] = p;
+        }
+        *e = p;
+        if (p >= 0 && p < n_pages) a.page_refs[p] = 1;
+        else set_status(a.status, ICE_ERR_BOUNDS);  // an id in the ring that is no page's
+    }
+    // pages given back, and on failure the claims: a warp a request
+    const unsigned long long epoch = a.w.head->epoch;
+    for (int r = first >> 5; r < n; r += step >> 5) {
+        if (!ok) {
+            for_claims(a, r, share_req(a, r), [&](int p) { atomicAdd(a.page_refs + p, 1); });
+        } else if (push_cum[r + 1] > push_cum[r]) {
+            const ShareReq q = share_req(a, r);
+            const unsigned long long name = claim_name(epoch, false, r);
+            const int* row = a.block_table + (long long)r * a.max_blocks;
+            int at = push_cum[r];
+            for (int c0 = q.has; c0 < q.had; c0 += 32) {
+                const int p = c0 + lane < q.had ? row[c0 + lane] : -1;
+                const bool mine = p >= 0 && share_mine(a, p, name);
+                const unsigned m = __ballot_sync(0xffffffffu, mine);
+                if (mine) a.free_pages[ring(tm, at + __popc(m & ((1u << lane) - 1)))] = p;
+                at += __popc(m);
+            }
+        }
+    }
+    // the last block to come here: every block has read the lengths, the ring's state and the flags
+    __syncthreads();
+    if (tid == 0) {
+        __threadfence();
+        s_last = gridDim.x == 1 || atomicAdd(&a.w.head->ticket, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!s_last) return;
+    for (int r = tid; r < n; r += NT) a.seq_len_out[r] = ok ? a.seq_len[r] + a.n_new[r] : a.seq_len[r];
+    if (tid == 0) {
+        a.free_state_out[0] = head + n_pop;
+        a.free_state_out[1] = tail + n_push;
+        if (!ok) set_status(a.status, code);
+        a.w.head->ticket = 0;
+        a.w.head->flags = 0;
+        a.w.head->epoch = epoch + 1;
+    }
+}
+
+__global__ void __launch_bounds__(kShrGridThreads) share_claim_kernel(SharedTables a) {
+    pdl_wait_then_release();
+    share_claim(a, (blockIdx.x * kShrGridThreads + threadIdx.x) >> 5, gridDim.x * kShrGridThreads >> 5);
+}
+
+__global__ void __launch_bounds__(kShrGridThreads) share_count_kernel(SharedTables a) {
+    pdl_wait_then_release();
+    share_count(a, (blockIdx.x * kShrGridThreads + threadIdx.x) >> 5, gridDim.x * kShrGridThreads >> 5);
+}
+
+__global__ void __launch_bounds__(kShrThreads) share_fill_kernel(SharedTables a) {
+    pdl_wait_then_release();
+    share_fill<kShrThreads>(a);
+}
+
+__global__ void __launch_bounds__(kShrThreads) share_step_kernel(SharedTables a) {
+    pdl_wait_then_release();
+    share_claim(a, threadIdx.x >> 5, kShrThreads >> 5);
+    __threadfence();
+    __syncthreads();
+    share_count(a, threadIdx.x >> 5, kShrThreads >> 5);
+    __threadfence();
+    __syncthreads();
+    share_fill<kShrThreads>(a);
+}
+
+cudaError_t launch_shared_tables(const SharedTables& a, cudaStream_t s) {
+    const size_t smem = (size_t)(a.n + 1) * 12;
+    // One block where its 32 warps have few requests each, few slots, and few pages to give back whatever the lengths
+    if (a.n <= 128 && a.n_slots <= 4096 && (long long)a.n * a.max_blocks <= 65536)
+        return launch_pdl(share_step_kernel, dim3(1), dim3(kShrThreads), smem, s, a);
+    const int per = kShrGridThreads / 32;
+    const dim3 grid(std::min(152 * 4, (a.n + per - 1) / per));
+    cudaError_t e = launch_pdl(share_claim_kernel, grid, dim3(kShrGridThreads), 0, s, a);
+    if (e == cudaSuccess) e = launch_pdl(share_count_kernel, grid, dim3(kShrGridThreads), 0, s, a);
+    const int blocks = std::max(1, std::min(152, std::max(a.n_slots / 1024, a.n / 32)));
+    if (e == cudaSuccess) e = launch_pdl(share_fill_kernel, dim3(blocks), dim3(kShrThreads), smem, s, a);
+    return e;
+}
+
+// ---------------------------------------------------------------------------
+// Compaction: with L pages in use, the pages in use at L and behind go to the free ones before L, in order: the k-th of
+// the former to the k-th of the latter. Ranks are sums of flags, so three passes do it: flags counted by
+// chunk (and every list checked), ranks and lists of moves, then the tables. A page that moves leaves its
+// number k in its claim, where the tables' pass finds it.
+// ---------------------------------------------------------------------------
+constexpr int kCmpThreads = 256, kCmpPer = kCmpChunk / kCmpThreads;
+
+__device__ __forceinline__ int block_sum(int x, int* s_sum) {  // 8 warps
+    x = __reduce_add_sync(0xffffffffu, x);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = x;
+    __syncthreads();
+    int t = 0;
+#pragma unroll
+    for (int i = 0; i < kCmpThreads / 32; ++i) t += s_sum[i];
+    return t;
+}
+
+__global__ void __launch_bounds__(kCmpThreads) compact_count_kernel(Compact a) {
+    __shared__ int s_sum[kCmpThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31;
+    pdl_wait_then_release();
+    const int chunks = (int)((a.n_pages + kCmpChunk - 1) / kCmpChunk);
+    bool bad = false;
+    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+        int live = 0;
+#pragma unroll
+        for (int k = 0; k < kCmpPer; ++k) {
+            const long long p = (long long)c * kCmpChunk + k * kCmpThreads + tid;
+            const int f = p < a.n_pages ? a.page_refs[p] : 0;
+            live += f > 0;
+            bad |= f < 0;
+        }
+        live = block_sum(live, s_sum);
+        if (tid == 0) a.w.count[c] = live;
+    }
+    // every page that is named is one in use
+    auto named = [&](int p) { return p >= 0 && p < a.n_pages && a.page_refs[p] > 0; };
+    const long long cap = (long long)a.max_blocks * a.P;
+    const int warps = gridDim.x * (kCmpThreads / 32), warp = blockIdx.x * (kCmpThreads / 32) + (tid >> 5);
+    for (int r = warp; r < a.n; r += warps) {
+        const int len = a.seq_len[r];
+        if (len < 0 || len > cap) {
+            bad = true;
+            continue;
+        }
+        const int pages = (len + a.P - 1) / a.P;
+#pragma unroll 4
+        for (int c = lane; c < pages; c += 32) bad |= !named(a.block_table[(long long)r * a.max_blocks + c]);
+    }
+    for (int i = blockIdx.x * kCmpThreads + tid; i < a.n_extra; i += gridDim.x * kCmpThreads) bad |= !named(a.extra[i]);
+    if (bad) atomicOr(&a.w.head->flags, kBadBounds);
+}
+
+__global__ void __launch_bounds__(kCmpThreads) compact_move_kernel(Compact a) {
+    __shared__ int s_sum[kCmpThreads / 32], s_warp[kCmpThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait_then_release();
+    const int chunks = (int)((a.n_pages + kCmpChunk - 1) / kCmpChunk);
+    // this block's chunks, the pages in use before them and in all
+    const int c0 = (int)((long long)chunks * blockIdx.x / gridDim.x), c1 = (int)((long long)chunks * (blockIdx.x + 1) / gridDim.x);
+    int before = 0, all = 0;
+    for (int c = tid; c < chunks; c += kCmpThreads) {
+        const int x = a.w.count[c];
+        all += x;
+        if (c < c0) before += x;
+    }
+    before = block_sum(before, s_sum);
+    const int L = block_sum(all, s_sum);
+    // those in use before page L
+    int low = 0;
+    for (int c = tid; c < L / kCmpChunk; c += kCmpThreads) low += a.w.count[c];
+    for (int p = L / kCmpChunk * kCmpChunk + tid; p < L; p += kCmpThreads) low += a.page_refs[p] > 0;
+    low = block_sum(low, s_sum);
+    const int moves = L - low;
+    const int code = a.w.head->flags ? ICE_ERR_BOUNDS : moves > a.n_moves ? ICE_ERR_CAPACITY : ICE_OK;
+    const bool ok = code == ICE_OK;
+    for (int c = c0; ok && c < c1; ++c) {
+        // neighbouring pages a thread: ranks in order
+        const long long p0 = (long long)c * kCmpChunk + tid * kCmpPer;
+        int f[kCmpPer], mine = 0;
+#pragma unroll
+        for (int k = 0; k < kCmpPer; ++k) {
+            f[k] = p0 + k < a.n_pages && a.page_refs[p0 + k] > 0;
+            mine += f[k];
+        }
+        int inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        __syncthreads();
+        if (lane == 31) s_warp[warp] = inc;
+        __syncthreads();
+        int rank = before + inc - mine;
+#pragma unroll
+        for (int i = 0; i < kCmpThreads / 32; ++i) {
+            if (i < warp) rank += s_warp[i];
+            before += s_warp[i];
+        }
+#pragma unroll
+        for (int k = 0; k < kCmpPer; ++k) {
+            const long long p = p0 + k;
+            if (p >= a.n_pages) break;
+            if (p >= L) {
+                a.free_pages[p - L] = (int)p;
+                if (f[k]) {
+                    a.move_src[rank - low] = (int)p;
+                    a.w.claim[p] = (unsigned long long)(rank - low);
+                }
+            } else if (!f[k]) {
+                a.move_dst[p - rank] = (int)p;
+            }
+            rank += f[k];
+        }
+    }
+    for (int k = (ok ? moves : 0) + blockIdx.x * kCmpThreads + tid; k < a.n_moves; k += gridDim.x * kCmpThreads)
+        a.move_src[k] = a.move_dst[k] = -1;
+    if (blockIdx.x == 0 && tid == 0) {
+        a.w.head->plan[0] = ok;
+        a.w.head->plan[1] = L;
+        a.w.head->plan[2] = moves;
+        if (ok) {
+            a.free_state_out[0] = 0;
+            a.free_state_out[1] = a.n_pages - L;
+        } else {
+            set_status(a.status, code);
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kCmpThreads) compact_apply_kernel(Compact a) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    pdl_wait_then_release();
+    const bool ok = a.w.head->plan[0];
+    const int L = a.w.head->plan[1], moves = a.w.head->plan[2];
+    const int first = blockIdx.x * kCmpThreads + tid, step = gridDim.x * kCmpThreads;
+    if (first == 0) a.w.head->flags = 0;
+    auto goes = [&](int p) { return ok && p >= L ? a.move_dst[(int)a.w.claim[p]] : p; };
+    const long long cap = (long long)a.max_blocks * a.P;
+    for (int r = first >> 5; r < a.n; r += step >> 5) {
+        const int len = a.seq_len[r];
+        const int pages = len < 0 || len > cap ? 0 : (len + a.P - 1) / a.P;
+        const long long row = (long long)r * a.max_blocks;
+#pragma unroll 4
+        for (int c = lane; c < pages; c += 32) a.block_table_out[row + c] = goes(a.block_table[row + c]);
+    }
+    for (int i = first; i < a.n_extra; i += step) a.extra_out[i] = goes(a.extra[i]);
+    // counts: a page that moves takes its own along
+    if (ok) {
+        for (int k = first; k < moves; k += step) {
+            const int s = a.move_src[k], f = a.page_refs[s];
+            a.page_refs_out[a.move_dst[k]] = f;
+            a.page_refs_out[s] = 0;
+        }
+    }
+    if (a.page_refs_out != a.page_refs) {
+        for (long long p = first; p < a.n_pages; p += step) {
+            const int f = a.page_refs[p];
+            if (!ok) a.page_refs_out[p] = f;
+            else if (p >= L) a.page_refs_out[p] = 0;
+            else if (f > 0) a.page_refs_out[p] = f;
+        }
+    }
+}
+
+cudaError_t launch_compact(const Compact& a, cudaStream_t s) {
+    const int chunks = (int)((a.n_pages + kCmpChunk - 1) / kCmpChunk);
+    const dim3 block(kCmpThreads);
+    const dim3 wide(std::max(1, std::min(152 * 4, std::max(chunks, std::max(a.n, a.n_extra / kCmpThreads) / 8))));
+    cudaError_t e = launch_pdl(compact_count_kernel, wide, block, 0, s, a);
+    if (e == cudaSuccess) e = launch_pdl(compact_move_kernel, dim3(std::min(152 * 4, chunks)), block, 0, s, a);
+    if (e == cudaSuccess) e = launch_pdl(compact_apply_kernel, wide, block, 0, s, a);
+    return e;
+}
+
+// ---------------------------------------------------------------------------
+// Pages copied by a list of pairs, in every layer, K and V. A warp takes pieces of 2 KB, four 16-byte loads a lane
+// under way together. A block looks up the entries of its share of the list at once and goes on with those that are
+// pairs: most entries of a step's list are -1. Where the list is short, blocks in y share an entry.
+// ---------------------------------------------------------------------------
+constexpr int kCpyThreads = 256, kCpyBatch = 4;
+
+__global__ void __launch_bounds__(kCpyThreads) page_copy_kernel(int n, const int* src, const int* dst, int n_layers, long long layer_vecs,
+                                                                int page_vecs, long long n_pages, uint4* k_pages, uint4* v_pages,
+                                                                int* status) {
+    __shared__ int2 s_pair[kCpyThreads];
+    __shared__ int s_n;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int w = blockIdx.y * (kCpyThreads / 32) + (tid >> 5), warps = gridDim.y * (kCpyThreads / 32);
+    const int pieces = (page_vecs + 32 * kCpyBatch - 1) / (32 * kCpyBatch), units = n_layers * 2 * pieces;
+    pdl_wait_then_release();
+    for (long long e0 = blockIdx.x; e0 < n; e0 += (long long)gridDim.x * kCpyThreads) {
+        __syncthreads();
+        if (tid == 0) s_n = 0;
+        __syncthreads();
+        const long long e = e0 + (long long)tid * gridDim.x;
+        if (e < n) {
+            const int s = src[e], d = dst[e];
+            if (s >= 0 && s < n_pages && d >= 0 && d < n_pages) s_pair[atomicAdd(&s_n, 1)] = make_int2(s, d);
+            else if (!(s == -1 || d == -1)) set_status(status, ICE_ERR_BOUNDS);
+        }
+        __syncthreads();
+        const int m = s_n;
+        // pieces of all pairs in turn
+        for (long long x = w; x < (long long)m * units; x += warps) {
+            const int i = (int)(x / units), u = (int)(x - (long long)i * units);
+            const int y = u / pieces, at = (u - y * pieces) * 32 * kCpyBatch + lane;
+            uint4* pool = (y & 1 ? v_pages : k_pages) + (long long)(y >> 1) * layer_vecs;
+            const int2 p = s_pair[i];
+            const uint4* from = pool + (long long)p.x * page_vecs;
+            uint4* to = pool + (long long)p.y * page_vecs;
+            uint4 v[kCpyBatch];
+#pragma unroll
+            for (int k = 0; k < kCpyBatch; ++k)
+                if (at + 32 * k < page_vecs) v[k] = __ldcs(from + at + 32 * k);
+#pragma unroll
+            for (int k = 0; k < kCpyBatch; ++k)
+                if (at + 32 * k < page_vecs) to[at + 32 * k] = v[k];
+        }
+    }
+}
+
+cudaError_t launch_page_copy(int n, const int* src, const int* dst, int n_layers, long long layer_bytes, long long page_bytes,
+                             long long n_pages, void* k_pages, void* v_pages, int* status, cudaStream_t s) {
+    const int page_vecs = (int)(page_bytes / 16);
+    const long long pieces = (page_vecs + 32 * kCpyBatch - 1) / (32 * kCpyBatch), units = n_layers * 2 * pieces;
+    const int x = std::min(n, 152 * 8);
+    const int y = (int)std::max<long long>(1, std::min<long long>(152 * 8 / x, (units + 7) / 8));
+    return launch_pdl(page_copy_kernel, dim3(x, y), dim3(kCpyThreads), 0, s, n, src, dst, n_layers, layer_bytes / 16, page_vecs,
+                      n_pages, (uint4*)k_pages, (uint4*)v_pages, status);
+}
+
+cudaError_t share_prepare() {
+    cudaError_t e = cudaFuncSetAttribute(share_fill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kPagedMaxRequests + 1) * 12);
+    return e;
+}
+
+}  // namespace ice

@@ -16,6 +16,7 @@ import of this module raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import operator
 import os
 
@@ -41,7 +42,9 @@ EXPORTS = ["ice_build", "ice_insert", "ice_select", "ice_select_attn", "ice_spar
            "ice_key_codes_noalloc", "ice_select_attn_reuse", "ice_reuse_reset",
            "ice_debug_set_flags", "ice_select_heads", "ice_decode_step", "ice_set_cluster_size",
            "ice_paged_create", "ice_paged_destroy", "ice_paged_get_error", "ice_paged_tables",
-           "ice_paged_append", "ice_paged_attn", "ice_paged_debug_set_flags"]
+           "ice_paged_append", "ice_paged_attn", "ice_paged_debug_set_flags", "ice_paged_rope_append",
+           "ice_paged_fork", "ice_paged_tables_shared", "ice_paged_copy", "ice_paged_compact",
+           "ice_paged_verify"]
 
 
 class ice_params(ctypes.Structure):
@@ -74,6 +77,12 @@ class ice_paged_params(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("max_requests", ctypes.c_int32),
                 ("max_blocks", ctypes.c_int32), ("max_tokens", ctypes.c_int32),
                 ("n_pages", ctypes.c_int64)]
+
+
+class ice_rope(ctypes.Structure):
+    _fields_ = [("n_axes", ctypes.c_int32), ("n_pairs", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("freq", ctypes.c_double * 64), ("axis", ctypes.c_int32 * 64)]
 
 
 class IceError(RuntimeError):
@@ -139,6 +148,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ice_paged_attn.restype = ctypes.c_int
     lib.ice_paged_debug_set_flags.argtypes = [vp, i32]
     lib.ice_paged_debug_set_flags.restype = ctypes.c_int
+    lib.ice_paged_rope_append.argtypes = [vp, i32, P(ice_rope), vp, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp]
+    lib.ice_paged_rope_append.restype = ctypes.c_int
+    lib.ice_paged_fork.argtypes = [vp, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp]
+    lib.ice_paged_fork.restype = ctypes.c_int
+    lib.ice_paged_tables_shared.argtypes = [vp, i32] + [vp] * 11 + [i32, vp, vp, vp]
+    lib.ice_paged_tables_shared.restype = ctypes.c_int
+    lib.ice_paged_copy.argtypes = [vp, i32, vp, vp, i32, i64, vp, vp, vp]
+    lib.ice_paged_copy.restype = ctypes.c_int
+    lib.ice_paged_compact.argtypes = [vp, i32, vp, vp, i32, vp, vp, vp, vp, i32] + [vp] * 6
+    lib.ice_paged_compact.restype = ctypes.c_int
+    lib.ice_paged_verify.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp, i64, i64, vp, i64, i64] + [vp] * 5
+    lib.ice_paged_verify.restype = ctypes.c_int
     return lib
 
 
@@ -429,6 +450,27 @@ def _int(x, name: str, bits: int = 32) -> int:
     return x
 
 
+class Rope:
+    """Rotary positions of a model (an ice_rope): pair i of a head turns by freq[i] radians a
+    position on axis axis[i] (None: one axis for all). Pair i is elements i and i + len(freq), or
+    2i and 2i + 1 if interleaved; len(freq) is a multiple of 8, up to 64."""
+
+    def __init__(self, freq, axis=None, interleaved: bool = False):
+        freq = [float(f) for f in freq]
+        axis = [0] * len(freq) if axis is None else [_int(a, "axis") for a in axis]
+        if len(freq) > 64 or len(freq) < 8 or len(freq) % 8:
+            raise ValueError(f"{len(freq)} frequencies: must be a multiple of 8, 8 to 64")
+        if not all(math.isfinite(f) for f in freq):
+            raise ValueError("freq must be finite")
+        if len(axis) != len(freq) or min(axis) < 0 or max(axis) > 3:
+            raise ValueError("axis must hold an axis of 0 to 3 for each frequency")
+        self.n_axes = max(axis) + 1
+        self.params = ice_rope(n_axes=self.n_axes, n_pairs=len(freq), interleaved=int(bool(interleaved)))
+        self.params.freq[:len(freq)] = freq
+        self.params.axis[:len(axis)] = axis
+        self._ref = ctypes.byref(self.params)
+
+
 class PagedCache:
     """The plain paged cache of a batch whose requests share a prefix (an ice_paged
     handle: geometry, scratch and status word; the pages and tables are the caller's
@@ -437,6 +479,11 @@ class PagedCache:
         seq_len, state, q_start, slots, pos = pc.tables(seq_len, n_new, table, ring, state, n)
         pc.append(k, v, slots, k_pages, v_pages)
         out = pc.attn(q, q_start, seq_len, table, k_pages, v_pages, prefix_table, prefix_len)
+
+    rope_append is append with rotary positions, on the queries too. Requests that share pages by
+    reference counts (fork) are moved on by tables_shared and copy instead of tables; compact moves
+    the pages in use to the front of the pool; verify says how many drafted tokens stay, and by
+    how many tokens the next tables call changes each request.
     """
 
     def __init__(self, *, n_kv_heads: int, n_q_heads: int, page_size: int, n_pages: int,
@@ -467,6 +514,10 @@ class PagedCache:
                 torch.full((n_req, self.params.max_blocks), -1, dtype=torch.int32, device=self.device),
                 torch.arange(n_pages, dtype=torch.int32, device=self.device),
                 torch.tensor([0, n_pages], dtype=torch.int64, device=self.device))
+
+    def new_refs(self):
+        """page_refs of a pool whose pages are all free."""
+        return torch.zeros((self.params.n_pages,), dtype=torch.int32, device=self.device)
 
     # -- checks ------------------------------------------------------------------------
     @staticmethod
@@ -581,6 +632,195 @@ class PagedCache:
             self._ints(block_table, torch.int32, (n, p.max_blocks), "block_table"), pt, prefix_len,
             kg, vg, _dev_ptr(out, self.dtype, "out", host_ok=False), _stream()), "ice_paged_attn")
         return out
+
+    # -- around the attention ----------------------------------------------------------------
+    def _out(self, t, dtype, shape, name):
+        """An output: the given tensor, or a new one."""
+        if t is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        self._ints(t, dtype, shape, name)
+        return t
+
+    def rope_append(self, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                    rope: Rope, slot_map: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                    pos_offset: int = 0, q_out: torch.Tensor | None = None, stream=None):
+        """ice_paged_rope_append of q [tokens, q_heads, d] and k, v [tokens, kv_heads, d] (a token
+        stride is allowed); returns q_out, which may be q.
+
+        positions: int32 [axes, tokens] (rows contiguous), or [tokens] with one axis. q None: keys
+        and values alone; returns None. Rows of q_out whose token has slot -1 are not written."""
+        if stream is not None:  # what is allocated here belongs to the stream that writes it
+            with torch.cuda.stream(stream):
+                return self.rope_append(q, k, v, positions, rope, slot_map, k_pages, v_pages, pos_offset, q_out)
+        if not isinstance(rope, Rope):
+            raise ValueError("rope must be a Rope")
+        n, p = self._count(slot_map, "slot_map"), self.params
+        sp = self._ints(slot_map, torch.int64, (n,), "slot_map")
+        kp, ks = self._rows(k, p.n_kv_heads, "k")
+        vp, vs = self._rows(v, p.n_kv_heads, "v")
+        if k.shape[0] != n or v.shape[0] != n:
+            raise ValueError("k, v and slot_map must have as many tokens")
+        if not isinstance(positions, torch.Tensor) or not positions.is_cuda or positions.dtype != torch.int32:
+            raise ValueError("positions must be a CUDA tensor of torch.int32")
+        if positions.shape != (rope.n_axes, n) and not (rope.n_axes == 1 and positions.shape == (n,)):
+            raise ValueError(f"positions must be [{rope.n_axes}, {n}], got {tuple(positions.shape)}")
+        if n > 1 and positions.stride(-1) != 1:
+            raise ValueError("positions: the tokens of an axis must be contiguous")
+        ps = max(positions.stride(0), n) if positions.dim() == 2 and rope.n_axes > 1 else n
+        if rope.n_axes > 1 and positions.stride(0) < n:
+            raise ValueError("positions: the axes must not overlap")
+        kg, vg = self._pages(k_pages, v_pages)
+        qp = qs = op = os_ = 0
+        if q is not None:
+            qp, qs = self._rows(q, p.n_q_heads, "q")
+            if q.shape[0] != n:
+                raise ValueError("q and slot_map must have as many tokens")
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=self.dtype, device=q.device)
+            op, os_ = self._rows(q_out, p.n_q_heads, "q_out")
+            if q_out.shape[0] != n:
+                raise ValueError("q_out must be shaped like q")
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        _check(_lib.ice_paged_rope_append(self._h, n, rope._ref, positions.data_ptr(), ps, _int(pos_offset, "pos_offset"),
+                                          qp, qs, op, os_, kp, ks, vp, vs, sp, kg, vg, _stream()), "ice_paged_rope_append")
+        return q_out
+
+    def fork(self, src: torch.Tensor, dst: torch.Tensor, seq_len: torch.Tensor, block_table: torch.Tensor,
+             page_refs: torch.Tensor, fork_len: torch.Tensor | None = None, seq_len_out: torch.Tensor | None = None,
+             stream=None) -> torch.Tensor:
+        """ice_paged_fork; returns seq_len_out (which may be seq_len). block_table and page_refs are
+        updated in place. src, dst, fork_len: int32 [forks]."""
+        if stream is not None:  # what is allocated here belongs to the stream that writes it
+            with torch.cuda.stream(stream):
+                return self.fork(src, dst, seq_len, block_table, page_refs, fork_len, seq_len_out)
+        f, n, i32, check = self._count(src, "src"), self._count(seq_len, "seq_len"), torch.int32, self._ints
+        sp, dp = check(src, i32, (f,), "src"), check(dst, i32, (f,), "dst")
+        lp = None if fork_len is None else check(fork_len, i32, (f,), "fork_len")
+        lens, table = check(seq_len, i32, (n,), "seq_len"), check(block_table, i32, (n, self.params.max_blocks), "block_table")
+        refs = check(page_refs, i32, (self.params.n_pages,), "page_refs")
+        out = self._out(seq_len_out, i32, (n,), "seq_len_out")
+        _check(_lib.ice_paged_fork(self._h, f, sp, dp, lp, n, lens, table, refs, out.data_ptr(), _stream()), "ice_paged_fork")
+        return out
+
+    def tables_shared(self, seq_len: torch.Tensor, n_new: torch.Tensor, block_table: torch.Tensor,
+                      free_pages: torch.Tensor, free_state: torch.Tensor, page_refs: torch.Tensor, n_slots: int,
+                      seq_len_out: torch.Tensor | None = None, free_state_out: torch.Tensor | None = None,
+                      q_start: torch.Tensor | None = None, slot_map: torch.Tensor | None = None,
+                      positions: torch.Tensor | None = None, copy_src: torch.Tensor | None = None,
+                      copy_dst: torch.Tensor | None = None, stream=None):
+        """ice_paged_tables_shared; returns (seq_len_out, free_state_out, q_start, slot_map, positions,
+        copy_src, copy_dst). As tables; page_refs is updated in place, and the pages copy_src are to
+        be copied to copy_dst (copy) before rows are written."""
+        if stream is not None:  # what is allocated here belongs to the stream that writes it
+            with torch.cuda.stream(stream):
+                return self.tables_shared(seq_len, n_new, block_table, free_pages, free_state, page_refs, n_slots, seq_len_out,
+                                          free_state_out, q_start, slot_map, positions, copy_src, copy_dst)
+        if not 0 <= n_slots <= 1 << 30:
+            raise ValueError(f"n_slots = {n_slots} must be from 0 to 2^30")
+        n, i32, i64, check, out = self._count(seq_len, "seq_len"), torch.int32, torch.int64, self._ints, self._out
+        ins = (check(seq_len, i32, (n,), "seq_len"), check(n_new, i32, (n,), "n_new"),
+               check(block_table, i32, (n, self.params.max_blocks), "block_table"),
+               check(free_pages, i32, (self.params.n_pages,), "free_pages"),
+               check(free_state, i64, (2,), "free_state"), check(page_refs, i32, (self.params.n_pages,), "page_refs"))
+        outs = (out(seq_len_out, i32, (n,), "seq_len_out"), out(free_state_out, i64, (2,), "free_state_out"),
+                out(q_start, i32, (n + 1,), "q_start"), out(slot_map, i64, (n_slots,), "slot_map"),
+                out(positions, i32, (n_slots,), "positions"), out(copy_src, i32, (n,), "copy_src"),
+                out(copy_dst, i32, (n,), "copy_dst"))
+        ptr = [t.data_ptr() for t in outs]
+        _check(_lib.ice_paged_tables_shared(self._h, n, *ins, *ptr[:5], n_slots, ptr[5], ptr[6], _stream()),
+               "ice_paged_tables_shared")
+        return outs
+
+    def copy(self, src: torch.Tensor, dst: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, stream=None):
+        """ice_paged_copy of the pages src to dst, int32 [n], -1 for none. k_pages, v_pages: one
+        layer's, or several layers' [layers, ...] (a layer stride is allowed)."""
+        n = self._count(src, "src")
+        sp, dp = self._ints(src, torch.int32, (n,), "src"), self._ints(dst, torch.int32, (n,), "dst")
+        layers, stride = 1, 0
+        if isinstance(k_pages, torch.Tensor) and isinstance(v_pages, torch.Tensor) and k_pages.dim() == 5:
+            layers, stride = k_pages.shape[0], k_pages.stride(0)
+            if v_pages.shape != k_pages.shape or (layers > 1 and v_pages.stride(0) != stride):
+                raise ValueError("k_pages and v_pages must have the same layers and layer stride")
+            if layers < 1:
+                raise ValueError("k_pages and v_pages must hold a layer")
+            k_pages, v_pages = k_pages[0], v_pages[0]
+        kg, vg = self._pages(k_pages, v_pages)
+        _check(_lib.ice_paged_copy(self._h, n, sp, dp, layers, stride, kg, vg, _stream(stream)), "ice_paged_copy")
+
+    def compact(self, seq_len: torch.Tensor, block_table: torch.Tensor, page_refs: torch.Tensor,
+                free_pages: torch.Tensor, free_state: torch.Tensor, extra_pages: torch.Tensor | None = None,
+                n_moves: int | None = None, block_table_out: torch.Tensor | None = None,
+                page_refs_out: torch.Tensor | None = None, extra_pages_out: torch.Tensor | None = None,
+                move_src: torch.Tensor | None = None, move_dst: torch.Tensor | None = None, stream=None):
+        """ice_paged_compact; returns (move_src, move_dst, block_table_out, page_refs_out,
+        extra_pages_out). free_pages and free_state receive the ring of the free end; the three
+        others are updated in place where no output is given. The moves are to be carried out by
+        copy, in every layer. n_moves: room for moves (n_pages / 2, which always suffices)."""
+        if stream is not None:  # what is allocated here belongs to the stream that writes it
+            with torch.cuda.stream(stream):
+                return self.compact(seq_len, block_table, page_refs, free_pages, free_state, extra_pages, n_moves, block_table_out,
+                                    page_refs_out, extra_pages_out, move_src, move_dst)
+        n, i32, check, out = self._count(seq_len, "seq_len"), torch.int32, self._ints, self._out
+        n_pages, columns = self.params.n_pages, self.params.max_blocks
+        n_moves = n_pages // 2 if n_moves is None else _int(n_moves, "n_moves")
+        if n_moves < 0:
+            raise ValueError(f"n_moves = {n_moves} must not be below 0")
+        lens, table = check(seq_len, i32, (n,), "seq_len"), check(block_table, i32, (n, columns), "block_table")
+        refs, ring = check(page_refs, i32, (n_pages,), "page_refs"), check(free_pages, i32, (n_pages,), "free_pages")
+        state = check(free_state, torch.int64, (2,), "free_state")
+        x, xp, xo = 0, None, None
+        if extra_pages is not None:
+            x = self._count(extra_pages, "extra_pages")
+            xp = check(extra_pages, i32, (x,), "extra_pages")
+            extra_pages_out = extra_pages if extra_pages_out is None else extra_pages_out
+            xo = check(extra_pages_out, i32, (x,), "extra_pages_out")
+        elif extra_pages_out is not None:
+            raise ValueError("extra_pages_out without extra_pages")
+        block_table_out = block_table if block_table_out is None else block_table_out
+        page_refs_out = page_refs if page_refs_out is None else page_refs_out
+        to = check(block_table_out, i32, (n, columns), "block_table_out")
+        ro = check(page_refs_out, i32, (n_pages,), "page_refs_out")
+        move_src, move_dst = out(move_src, i32, (n_moves,), "move_src"), out(move_dst, i32, (n_moves,), "move_dst")
+        _check(_lib.ice_paged_compact(self._h, n, lens, table, x, xp, refs, ring, state, n_moves, move_src.data_ptr(),
+                                      move_dst.data_ptr(), to, xo, ro, _stream()), "ice_paged_compact")
+        return move_src, move_dst, block_table_out, page_refs_out, extra_pages_out
+
+    def verify(self, draft_tokens: torch.Tensor, n_draft: torch.Tensor, target: torch.Tensor,
+               draft: torch.Tensor | None = None, uniform: torch.Tensor | None = None, tokens: torch.Tensor | None = None,
+               n_accepted: torch.Tensor | None = None, n_new: torch.Tensor | None = None, stream=None):
+        """ice_paged_verify; returns (tokens [requests, drafts + 1], n_accepted, n_new).
+
+        draft_tokens: int32 [requests, drafts]; n_draft: int32 [requests]. target: [requests,
+        drafts + 1, vocab], bf16 or f32 (whatever the cache's type), rows contiguous; draft: [requests,
+        drafts, vocab] or None; uniform: f32 [requests, drafts + 1], or None for greedy decoding."""
+        if stream is not None:  # what is allocated here belongs to the stream that writes it
+            with torch.cuda.stream(stream):
+                return self.verify(draft_tokens, n_draft, target, draft, uniform, tokens, n_accepted, n_new)
+        n, i32 = self._count(n_draft, "n_draft"), torch.int32
+        if not isinstance(target, torch.Tensor) or not target.is_cuda or target.dim() != 3:
+            raise ValueError("target must be a CUDA tensor [requests, drafts + 1, vocab]")
+        have, rows, vocab = target.shape
+        k = rows - 1
+        if have != n or k < 0 or vocab < 1 or (target.stride(2) != 1 and vocab > 1):
+            raise ValueError(f"target must be [{n}, drafts + 1, vocab] with contiguous rows, got {tuple(target.shape)}")
+        code, (ts, tr, _) = _code(target.dtype), target.stride()
+        dp, ds, dr = None, 0, 0
+        if draft is not None:
+            if not isinstance(draft, torch.Tensor) or not draft.is_cuda or draft.dtype != target.dtype:
+                raise ValueError(f"draft must be a CUDA tensor of {target.dtype}")
+            if draft.shape != (n, k, vocab) or (draft.stride(2) != 1 and vocab > 1):
+                raise ValueError(f"draft must be [{n}, {k}, {vocab}] with contiguous rows, got {tuple(draft.shape)}")
+            if k > 0:
+                dp, (ds, dr, _) = draft.data_ptr(), draft.stride()
+        check, out = self._ints, self._out
+        tok, nd = check(draft_tokens, i32, (n, k), "draft_tokens"), check(n_draft, i32, (n,), "n_draft")
+        up = None if uniform is None else check(uniform, torch.float32, (n, k + 1), "uniform")
+        outs = (out(tokens, i32, (n, k + 1), "tokens"), out(n_accepted, i32, (n,), "n_accepted"), out(n_new, i32, (n,), "n_new"))
+        a, b, c = (t.data_ptr() for t in outs)
+        _check(_lib.ice_paged_verify(self._h, n, k, vocab, code, tok, nd, target.data_ptr(), ts, tr, dp, ds, dr, up, a, b, c,
+                                     _stream()), "ice_paged_verify")
+        return outs
 
     # -- status, teardown ------------------------------------------------------------------
     def debug_set_flags(self, flags: int):
