@@ -5,6 +5,7 @@
 
 #include "ice_paged_handle.cuh"
 #include "ice_paged_share.cuh"
+#include "ice_paged_verify.cuh"
 
 using namespace ice;
 
@@ -31,6 +32,7 @@ void free_all(ice_paged* pg) {
     cudaFree(pg->part_o);
     cudaFree(pg->part_ml);
     cudaFree(pg->words);
+    cudaFree(pg->verify);
     cudaFree(pg->share);
 }
 
@@ -59,14 +61,17 @@ int ice_paged_create(const ice_paged_params* params, ice_paged** out) {
     }
     if (cudaMalloc(&pg->part_o, (size_t)pg->rows_cap * kD * 4) != cudaSuccess ||
         cudaMalloc(&pg->part_ml, (size_t)pg->rows_cap * 8) != cudaSuccess ||
-        cudaMalloc(&pg->words, (kWords + params->max_requests) * 4) != cudaSuccess) {
+        cudaMalloc(&pg->words, (kWords + params->max_requests) * 4) != cudaSuccess ||
+        cudaMalloc(&pg->verify, sizeof(VerifyScratch) * params->max_requests) != cudaSuccess) {
         cudaGetLastError();
         free_all(pg);
         delete pg;
         return ICE_ERR_CAPACITY;
     }
     // complete before the call returns, whatever stream is used first
-    if (cudaMemset(pg->words, 0, kWords * 4) != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess) {
+    if (cudaMemset(pg->words, 0, kWords * 4) != cudaSuccess ||
+        cudaMemset(pg->verify, 0, sizeof(VerifyScratch) * params->max_requests) != cudaSuccess ||
+        cudaStreamSynchronize(nullptr) != cudaSuccess) {
         cudaGetLastError();
         free_all(pg);
         delete pg;

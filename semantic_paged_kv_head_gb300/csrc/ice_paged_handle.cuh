@@ -12,6 +12,7 @@ struct ice_paged {
     float* part_o = nullptr;   // rows_cap x D
     float2* part_ml = nullptr; // rows_cap
     int* words = nullptr;      // status word, ticket, item counters, plan, then [max_requests] of the plan
+    void* verify = nullptr;    // scratch of ice_paged_verify, VerifyScratch [max_requests]
     char* share = nullptr;     // scratch of the calls on shared pages, made by the first of them
 };
 

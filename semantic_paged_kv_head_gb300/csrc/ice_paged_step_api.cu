@@ -249,6 +249,7 @@ int ice_paged_verify(ice_paged* pg, int32_t n_req, int32_t n_draft_max, int32_t 
     a.accepted = n_accepted;
     a.n_new = n_new;
     a.status = pg->words + kWordStatus;
+    a.scratch = (VerifyScratch*)pg->verify;
     a.n_req = n_req;
     a.K = n_draft_max;
     a.V = vocab;

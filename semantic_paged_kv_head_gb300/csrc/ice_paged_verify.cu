@@ -1,11 +1,7 @@
 // Drafted tokens against the target model's probabilities, or its logits.
-#include <cooperative_groups.h>
-
 #include <algorithm>
 
 #include "ice_paged_verify.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace ice {
 
@@ -13,28 +9,37 @@ namespace ice {
 // Speculative sampling (Leviathan et al. 2023, Chen et al. 2023): draft i with token x stays if u_i q_i(x) < p_i(x). The
 // first that does not is replaced by a token drawn from max(p - q, 0); behind the last one that stays a token is drawn
 // from p. Drawing is by the inverse of the cumulative sum: the first j with w_0 + ... + w_j > u W, W the sum of all.
+// Greedy: draft i stays if it is the largest entry's index of row i; the token is that index of the first row where it is not.
 //
 // A border between two tokens may lie anywhere, so sums have to be near those of exact arithmetic: with 2^17 tokens of
-// like weight fp32 sums would move one draw in ten. A thread's sums carry what each addition and each p - q cut off (two-sum,
-// Knuth 1969; 46 bits or more), and are added over the lanes and tiles in fp64, whose units do a 32nd of
-// the additions that way.
+// like weight fp32 sums would move one draw in ten. Sums therefore carry what each addition and each p - q cuts off (two-sum,
+// Knuth 1969): pairs of fp32, 46 bits or more.
 //
-// One thread-block cluster a request. Its blocks find the first rejected draft by themselves (K gathers), each sums its
-// share of the vocabulary, tile by tile; after one exchange of the blocks' sums through distributed shared memory one
-// of them holds the drawn token: it looks up the tile by the tiles' sums, and reads that tile again.
-// Only the rows that decide are read: two of the 2 K + 1.
+// No block waits for another in either case. Sampling: several blocks a request. Each finds the first rejected draft by
+// itself (K gathers), so that only the one or two rows that decide are read; each warp sums a part of the vocabulary and leaves
+// the sum in the handle's scratch, and the last block of a request to have done so draws the token: the part by the
+// sums, then that part again, its tiles and at last the elements of a tile.
+//
+// Greedy: a row is cut into groups of tiles, a warp each; it leaves its group's best entry
+// in the scratch and counts it; the warp that counts the last group of a request's last row ends the request. Groups are
+// handed out row by row, all requests' first rows first; a warp skips its group when a draft before that row is
+// known not to stay, which changes what is read but not the result.
 // ---------------------------------------------------------------------------
-constexpr int kVerThreads = 512, kVerWarps = kVerThreads / 32;
-constexpr int kVerTile = 1024;                          // elements of a row that a warp takes at once
-constexpr int kVerTiles = kVerMaxVocab / kVerTile;
+constexpr int kSmpThreads = 256, kSmpWarps = kSmpThreads / 32;
+constexpr int kGrdThreads = 128, kGrdWarps = kGrdThreads / 32;
+constexpr int kVerVecs = 4;  // 16-byte words of a lane in a tile
 
-// What an entry counts for: NaN, negative and huge ones nothing (2^22 of 2^100 have a sum in fp32).
-__device__ __forceinline__ float clean(float x) { return x <= 1.2676506e30f ? fmaxf(x, 0.0f) : 0.0f; }
+template <typename T> constexpr int kVec = 16 / sizeof(T);               // elements of 16 bytes
+template <typename T> constexpr int kTile = 32 * kVerVecs * kVec<T>;     // elements of a tile
+
+// What an entry counts for: NaN, negative and huge ones nothing (2^22 of 2^100 have a sum in fp32). As an unsigned number each
+// of those is above the bits of 2^100.
+__device__ __forceinline__ float clean(float x) { return __float_as_uint(x) <= 0x71800000u ? x : 0.0f; }
 
 __device__ __forceinline__ float clamp_uniform(float u) { return fminf(fmaxf(u, 0.0f), 0.99999994f); }
 
-// 16 bytes at p, which is aligned to an element only: from one or two aligned words. The caller has checked that
-// both lie in the row.
+// 16 bytes at p. Not ALIGNED: p is aligned to an element only, and the 16-byte words around it, which the caller has checked
+// to lie in the row, are put together.
 template <bool ALIGNED>
 __device__ __forceinline__ uint4 load16(const char* p) {
     if (ALIGNED) return __ldcs(reinterpret_cast<const uint4*>(p));
@@ -55,8 +60,6 @@ __device__ __forceinline__ uint4 load16(const char* p) {
                       __funnelshift_r(w[3], w[4], bits));
 }
 
-template <typename T> constexpr int kVec = 16 / sizeof(T);  // elements of 16 bytes
-
 template <typename T> __device__ __forceinline__ void unpack(const uint4& w, float (&v)[kVec<T>]);
 template <> __device__ __forceinline__ void unpack<float>(const uint4& w, float (&v)[4]) {
     v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y), v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
@@ -67,98 +70,368 @@ template <> __device__ __forceinline__ void unpack<__nv_bfloat16>(const uint4& w
     for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(u[i] << 16), v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
 }
 
-// Whether a tile's 16-byte loads stay in the row.
-template <typename T>
-__device__ __forceinline__ bool whole_tile(const T* row, int V, int e0) {
-    const unsigned sh = (unsigned)(uintptr_t)row & 15;  // a tile is a multiple of 16 bytes
-    return e0 + kVerTile + (sh ? kVec<T> : 0) <= V && (sh == 0 || e0 > 0);
-}
-
-// A sum of terms >= 0 with the parts that its additions cut off.
-struct Sum2 {
+// A number as a sum of two of fp32, |lo| at most half a step of hi: 48 bits. The fp64 units would bound the kernel: they make two
+// additions a cycle and SM.
+struct Wide {
     float hi = 0.0f, lo = 0.0f;
-    __device__ __forceinline__ void add(float d, float e) {
-        const float s = hi + d, b = s - hi;
-        lo += ((hi - (s - b)) + (d - b)) + e;
-        hi = s;
-    }
-    // max(p - q, 0), exactly: where p > q >= 0 the difference's own error is (p - d) - q
-    __device__ __forceinline__ void add_above(float p, float q) {
-        const float d = p - q;
-        if (d > 0.0f) add(d, (p - d) - q);
-    }
 };
-
-__device__ __forceinline__ double warp_sum(double x) {
+__device__ __forceinline__ Wide wide_add(Wide a, Wide b) {
+    const float s = a.hi + b.hi, t = s - a.hi;
+    const float e = ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo);
+    Wide r;
+    r.hi = s + e;
+    r.lo = e - (r.hi - s);
+    return r;
+}
+__device__ __forceinline__ Wide wide_sub(Wide a, Wide b) {
+    b.hi = -b.hi, b.lo = -b.lo;
+    return wide_add(a, b);
+}
+__device__ __forceinline__ Wide wide_mul(float u, Wide a) {
+    const float p = u * a.hi, e = fmaf(u, a.hi, -p) + u * a.lo;
+    Wide r;
+    r.hi = p + e;
+    r.lo = e - (r.hi - p);
+    return r;
+}
+__device__ __forceinline__ bool wide_less(Wide a, Wide b) { return a.hi < b.hi || (a.hi == b.hi && a.lo < b.lo); }
+__device__ __forceinline__ Wide wide_xor(Wide a, int o) {
+    Wide r;
+    r.hi = __shfl_xor_sync(0xffffffffu, a.hi, o), r.lo = __shfl_xor_sync(0xffffffffu, a.lo, o);
+    return r;
+}
+__device__ __forceinline__ Wide wide_at(Wide a, int lane) {
+    Wide r;
+    r.hi = __shfl_sync(0xffffffffu, a.hi, lane), r.lo = __shfl_sync(0xffffffffu, a.lo, lane);
+    return r;
+}
+// Sum of the lanes up to each, and (before) up to the one before.
+__device__ __forceinline__ Wide wide_scan(Wide a, Wide& before) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    for (int o = 1; o < 32; o <<= 1) {
+        Wide y;
+        y.hi = __shfl_up_sync(0xffffffffu, a.hi, o), y.lo = __shfl_up_sync(0xffffffffu, a.lo, o);
+        if (lane >= o) a = wide_add(y, a);
+    }
+    before.hi = __shfl_up_sync(0xffffffffu, a.hi, 1), before.lo = __shfl_up_sync(0xffffffffu, a.lo, 1);
+    if (lane == 0) before.hi = before.lo = 0.0f;
+    return a;
+}
+__device__ __forceinline__ Wide warp_sum(Wide x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = wide_add(x, wide_xor(x, o));
     return x;
 }
 
-// Sum of a tile's weights, the same in every lane. q: the draft's row or NULL; sure: the token that the draft was certain of,
-// or -1.
-template <typename T, bool ALIGNED, bool HAS_Q>
-__device__ __forceinline__ double sum_whole_tile(const T* p, const T* q, int e0) {
-    constexpr int N = kVerTile / 32 / kVec<T>;
-    const int at = e0 + (threadIdx.x & 31) * kVec<T>;
-    uint4 x[N], y[HAS_Q ? N : 1];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        x[i] = load16<ALIGNED>(reinterpret_cast<const char*>(p + at + i * 32 * kVec<T>));
-        if (HAS_Q) y[i] = load16<ALIGNED>(reinterpret_cast<const char*>(q + at + i * 32 * kVec<T>));
+// Two fp32 additions in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+
+// Two sums of terms >= 0 with the parts that their additions cut off.
+struct Sum2 {
+    float2 hi = {0.0f, 0.0f}, lo = {0.0f, 0.0f};
+    __device__ __forceinline__ float2 cut(float2 d) {
+        const float2 s = add2(hi, d), t = add2(s, neg2(hi));
+        const float2 e = add2(add2(hi, neg2(add2(s, neg2(t)))), add2(d, neg2(t)));
+        hi = s;
+        return e;
     }
-    Sum2 s;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        float a[kVec<T>], b[kVec<T>];
-        unpack<T>(x[i], a);
-        if (HAS_Q) unpack<T>(y[i], b);
-#pragma unroll
-        for (int j = 0; j < kVec<T>; ++j) {
-            if (HAS_Q) s.add_above(clean(a[j]), clean(b[j]));
-            else s.add(clean(a[j]), 0.0f);
-        }
+    __device__ __forceinline__ void add(float2 p) { lo = add2(lo, cut(p)); }
+    // max(p - q, 0) for p, q >= 0, exactly: the difference's own error is (p - d) - q where p >= q
+    __device__ __forceinline__ void add_above(float2 p, float2 q) {
+        p.x = fmaxf(p.x, q.x), p.y = fmaxf(p.y, q.y);
+        const float2 d = add2(p, neg2(q)), e = add2(add2(p, neg2(d)), neg2(q));
+        lo = add2(lo, add2(cut(d), e));
     }
-    return warp_sum((double)s.hi + (double)s.lo);
-}
-
-template <typename T>
-__device__ __forceinline__ double weight(const T* p, const T* q, int sure, int j) {
-    const double b = q != nullptr ? (double)clean(to_f<T>(q[j])) : j == sure ? 1.0 : 0.0;
-    return fmax((double)clean(to_f<T>(p[j])) - b, 0.0);
-}
-
-template <typename T>
-__device__ __forceinline__ double sum_tile(const T* p, const T* q, int sure, int V, int e0) {
-    const bool whole = whole_tile(p, V, e0) && (q == nullptr || whole_tile(q, V, e0)) && !(sure >= e0 && sure < e0 + kVerTile);
-    if (whole) {
-        const bool aligned = (((uintptr_t)p | (uintptr_t)q) & 15) == 0;
-        if (q != nullptr) return aligned ? sum_whole_tile<T, true, true>(p, q, e0) : sum_whole_tile<T, false, true>(p, q, e0);
-        return aligned ? sum_whole_tile<T, true, false>(p, q, e0) : sum_whole_tile<T, false, false>(p, q, e0);
+    __device__ __forceinline__ Wide value() const {
+        Wide a, b;
+        a.hi = hi.x + lo.x, a.lo = lo.x - (a.hi - hi.x);
+        b.hi = hi.y + lo.y, b.lo = lo.y - (b.hi - hi.y);
+        return wide_add(a, b);
     }
-    double s = 0.0;
-    const int end = min(e0 + kVerTile, V);
-#pragma unroll 8
-    for (int j = e0 + (threadIdx.x & 31); j < end; j += 32) s += weight(p, q, sure, j);
-    return warp_sum(s);
-}
-
-// Block's share of the tiles.
-__device__ __forceinline__ void share_of(int tiles, int rank, int size, int& t0, int& t1) {
-    t0 = (int)((long long)tiles * rank / size);
-    t1 = (int)((long long)tiles * (rank + 1) / size);
-}
-
-struct VerifyShared {
-    double total;                 // of this block's tiles; read by the cluster
-    unsigned long long best[2][kVerMaxDrafts + 1];  // greedy: this block's best of each row of a group; read by the cluster
-    double warp[kVerWarps];
-    double x;                     // what is left of u W before the tile
-    unsigned keep[2];
-    int tile, token;
 };
 
-// Entry j of the greedy comparison: larger is better, of equal values the lower index. NaN is nothing.
+__device__ __forceinline__ Wide above(float p, float q) {
+    p = fmaxf(p, q);
+    Wide w;
+    w.hi = p - q, w.lo = (p - w.hi) - q;
+    return w;
+}
+
+template <typename T>
+__device__ __forceinline__ Wide weight(const T* p, const T* q, int sure, int j) {
+    return above(clean(to_f<T>(p[j])), q != nullptr ? clean(to_f<T>(q[j])) : j == sure ? 1.0f : 0.0f);
+}
+
+// The tiles of a row begin at a 16-byte boundary of p, at or before the row's first element: tile t is elements
+// t kTile - s and on.
+template <typename T>
+__device__ __forceinline__ int row_shift(const T* p) { return (int)(((uintptr_t)p & 15) / sizeof(T)); }
+
+// What is taken off the target's entries: nothing, a draft's row, or 1 at the token that the draft was certain of.
+enum { kOffNone = 0, kOffRow = 1, kOffSure = 2 };
+
+template <typename T, int OFF, bool ALIGNED>
+__device__ __forceinline__ void add_whole_tile(const T* p, const T* q, int sure, int e0, Sum2& s) {
+    const int at = e0 + (threadIdx.x & 31) * kVec<T>;
+    uint4 x[kVerVecs], y[OFF == kOffRow ? kVerVecs : 1];
+#pragma unroll
+    for (int i = 0; i < kVerVecs; ++i) {
+        x[i] = load16<true>(reinterpret_cast<const char*>(p + at + i * 32 * kVec<T>));
+        if (OFF == kOffRow) y[i] = load16<ALIGNED>(reinterpret_cast<const char*>(q + at + i * 32 * kVec<T>));
+    }
+#pragma unroll
+    for (int i = 0; i < kVerVecs; ++i) {
+        float a[kVec<T>], b[kVec<T>];
+        unpack<T>(x[i], a);
+        if (OFF == kOffRow) unpack<T>(y[i], b);
+#pragma unroll
+        for (int j = 0; j < kVec<T>; j += 2) {
+            const float2 v = make_float2(clean(a[j]), clean(a[j + 1]));
+            const int k = at + i * 32 * kVec<T> + j;
+            if (OFF == kOffRow) s.add_above(v, make_float2(clean(b[j]), clean(b[j + 1])));
+            else if (OFF == kOffSure) s.add_above(v, make_float2(k == sure ? 1.0f : 0.0f, k + 1 == sure ? 1.0f : 0.0f));
+            else s.add(v);
+        }
+    }
+}
+
+// Adds the lane's weights of a tile.
+template <typename T>
+__device__ __forceinline__ void add_tile(const T* p, const T* q, int sure, int V, int e0, Sum2& s) {
+    const bool inside = e0 >= 0 && e0 + kTile<T> <= V;
+    if (q != nullptr) {
+        if (inside && ((uintptr_t)(q + e0) & 15) == 0) return add_whole_tile<T, kOffRow, true>(p, q, sure, e0, s);
+        if (e0 >= kVec<T> && e0 + kTile<T> + kVec<T> <= V) return add_whole_tile<T, kOffRow, false>(p, q, sure, e0, s);
+    } else if (inside) {
+        if (sure >= e0 && sure < e0 + kTile<T>) return add_whole_tile<T, kOffSure, true>(p, q, sure, e0, s);
+        return add_whole_tile<T, kOffNone, true>(p, q, sure, e0, s);
+    }
+    // a row's ends: element by element, 16 loads of a row under way (at a place that is there, wherever the element is)
+    const int j0 = e0 + (threadIdx.x & 31);
+#pragma unroll 1
+    for (int h = 0; h < kTile<T> / 32; h += 16) {
+        T x[16], y[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = p[min(max(j0 + 32 * (h + i), 0), V - 1)];
+        if (q != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = q[min(max(j0 + 32 * (h + i), 0), V - 1)];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = from_f<T>(j0 + 32 * (h + i) == sure ? 1.0f : 0.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            const int j = j0 + 32 * (h + i);
+            s.add_above(make_float2(j >= 0 && j < V ? clean(to_f<T>(x[i])) : 0.0f, j + 32 >= 0 && j + 32 < V ? clean(to_f<T>(x[i + 1])) : 0.0f),
+                        make_float2(clean(to_f<T>(y[i])), clean(to_f<T>(y[i + 1]))));
+        }
+    }
+}
+
+// Tiles of part g of a row.
+__device__ __forceinline__ void part_of(int tiles, int g, int parts, int& t0, int& t1) {
+    t0 = (int)((long long)tiles * g / parts);
+    t1 = (int)((long long)tiles * (g + 1) / parts);
+}
+
+// The tokens, counts and lengths of a request that has ended, by a warp.
+__device__ __forceinline__ void write_request(const Verify& a, int r, int nd, int kept, int token) {
+    const int K = a.K;
+    const bool part = nd >= 0 && nd <= K;
+    for (int i = threadIdx.x & 31; i <= K; i += 32)
+        a.out[(long long)r * (K + 1) + i] = !part || i > kept ? -1 : i < kept ? a.tokens[(long long)r * K + i] : token;
+    if ((threadIdx.x & 31) == 0) {
+        a.accepted[r] = part ? kept : 0;
+        a.n_new[r] = part ? kept - nd : 0;
+        if (part ? token < 0 : nd != -1) set_status(a.status, ICE_ERR_BOUNDS);
+    }
+}
+
+struct SampleShared {
+    float2 warp[kSmpWarps];  // sums, as two numbers
+    unsigned some[kSmpWarps], over[kSmpWarps];
+    unsigned keep[2];
+    int last;
+};
+
+// Over the block: the first thread whose sum reaches beyond x, else the last that has any weight; -1: none has. `before`
+// becomes the sum up to that thread, and `all` of all.
+struct BlockFind {
+    int at;
+    Wide before, all;
+};
+template <typename X>
+__device__ __forceinline__ BlockFind block_find(Wide w, X want, SampleShared& sh) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Wide before, base;
+    const Wide end = wide_scan(w, before);
+    __syncthreads();
+    if (lane == 31) sh.warp[warp] = make_float2(end.hi, end.lo);
+    __syncthreads();
+    BlockFind f;
+    Wide of_warp;
+    if (lane < kSmpWarps) of_warp.hi = sh.warp[lane].x, of_warp.lo = sh.warp[lane].y;
+    const Wide upto = wide_scan(of_warp, base);
+    f.all = wide_at(upto, 31);
+    base = wide_at(base, warp);
+    const Wide x = want(f.all);
+    const unsigned some = __ballot_sync(0xffffffffu, w.hi > 0.0f);
+    const unsigned over = some & __ballot_sync(0xffffffffu, wide_less(x, wide_add(base, end)));
+    if (lane == 0) sh.some[warp] = some, sh.over[warp] = over;
+    __syncthreads();
+    f.at = -1;
+    for (int k = kSmpWarps - 1; k >= 0; --k)
+        if (f.at < 0 && sh.some[k]) f.at = 32 * k + 31 - __clz(sh.some[k]);
+    for (int k = kSmpWarps - 1; k >= 0; --k)
+        if (sh.over[k]) f.at = 32 * k + __ffs(sh.over[k]) - 1;
+    before = wide_add(base, before);
+    if ((int)threadIdx.x == f.at) sh.warp[0] = make_float2(before.hi, before.lo);
+    __syncthreads();
+    f.before.hi = sh.warp[0].x, f.before.lo = sh.warp[0].y;
+    return f;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kSmpThreads, 4) verify_sample_kernel(Verify a) {
+    __shared__ SampleShared sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int blocks = a.groups / kSmpWarps, r = blockIdx.x / blocks, chunk = blockIdx.x - r * blocks;
+    pdl_wait_then_release();
+    const int K = a.K, V = a.V, nd = a.n_draft[r];
+    const float* const uniform = a.uniform + (long long)r * (K + 1);
+    // asked for together with n_draft
+    const int my_token = tid < K ? a.tokens[(long long)r * K + tid] : 0;
+    const float my_u = tid < K ? uniform[tid] : 0.0f, u = clamp_uniform(uniform[K]);
+    if (nd < 0 || nd > K) {  // a request that takes no part
+        if (chunk == 0 && warp == 0) write_request(a, r, nd, 0, -1);
+        return;
+    }
+    const T *const target = (const T*)a.target + r * a.t_req, *const draft = (const T*)a.draft + r * a.d_req;
+    if (warp < 2) {  // the drafts that stay: one a lane
+        bool stays = false;
+        if (tid < nd) {
+            const int x = my_token;
+            if (x >= 0 && x < V) {
+                const float px = clean(to_f<T>(target[tid * a.t_row + x]));
+                const float qx = a.draft ? clean(to_f<T>(draft[tid * a.d_row + x])) : 1.0f;
+                stays = (double)clamp_uniform(my_u) * (double)qx < (double)px;  // 48 bits: exact
+            } else if (chunk == 0) {
+                set_status(a.status, ICE_ERR_BOUNDS);
+            }
+        }
+        const unsigned m = __ballot_sync(0xffffffffu, stays);
+        if (lane == 0) sh.keep[warp] = m;
+    }
+    __syncthreads();
+    const int kept = __ffsll((long long)~((unsigned long long)sh.keep[1] << 32 | sh.keep[0])) - 1;  // bit 63 is never set
+    const T *const p = target + kept * a.t_row, *q = nullptr;
+    int sure = -1;
+    if (kept < nd) {
+        if (a.draft) q = draft + kept * a.d_row;
+        else sure = a.tokens[(long long)r * K + kept];
+    }
+    const int shift = row_shift(p), tiles = (V + shift + kTile<T> - 1) / kTile<T>;
+    VerifyScratch* const w = a.scratch + r;
+    auto part_sum = [&](int g) {
+        int t0, t1;
+        part_of(tiles, g, a.groups, t0, t1);
+        Sum2 s;
+        for (int t = t0; t < t1; ++t) add_tile(p, q, sure, V, t * kTile<T> - shift, s);
+        const Wide x = warp_sum(s.value());
+        if (lane == 0) __stcg(&w->sum[g], make_float2(x.hi, x.lo));
+    };
+    part_sum(chunk * kSmpWarps + warp);
+    __syncthreads();
+    if (tid == 0) {
+        __threadfence();
+        sh.last = atomicAdd(&w->count[0], 1) == blocks - 1;
+        __threadfence();
+    }
+    __syncthreads();
+    if (!sh.last) return;
+    // the last block of the request. At most twice: where the target is nowhere above the draft, a token of the target's own
+    int token = -1;
+    for (;;) {
+        static_assert(kVerGroups == kSmpThreads, "a part a thread");
+        Wide mine;
+        if (tid < a.groups) {
+            const float2 x = __ldcg(&w->sum[tid]);
+            mine.hi = x.x, mine.lo = x.y;
+        }
+        Wide x;
+        BlockFind f = block_find(mine, [&](Wide all) { return x = wide_mul(u, all); }, sh);
+        if (f.at >= 0) {
+            x = wide_sub(x, f.before);
+            int t0, t1;
+            part_of(tiles, f.at, a.groups, t0, t1);
+            // the part's tiles, a warp each
+            while (t1 - t0 > 1) {
+                const int n = min(t1 - t0, kSmpWarps);
+                Wide s;
+                if (warp < n) {
+                    Sum2 c;
+                    add_tile(p, q, sure, V, (t0 + warp) * kTile<T> - shift, c);
+                    s = warp_sum(c.value());
+                    if (lane != 0) s = Wide();
+                }
+                f = block_find(s, [&](Wide) { return x; }, sh);
+                if (t1 - t0 == n || wide_less(x, f.all)) {
+                    if (f.at >= 0) {
+                        x = wide_sub(x, f.before);
+                        t0 += f.at / 32;
+                    }
+                    t1 = t0 + 1;
+                } else {
+                    x = wide_sub(x, f.all);
+                    t0 += n;
+                }
+            }
+            // the tile's elements, neighbouring ones a thread
+            constexpr int E = kTile<T> / kSmpThreads;
+            const int j = t0 * kTile<T> - shift + E * tid;
+            Wide e[E], c;
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+                if (j + k >= 0 && j + k < V) e[k] = weight(p, q, sure, j + k);
+                c = wide_add(c, e[k]);
+            }
+            f = block_find(c, [&](Wide) { return x; }, sh);
+            if (tid == f.at) {
+                Wide low = f.before;
+#pragma unroll
+                for (int k = 0; k < E; ++k) {
+                    if (e[k].hi > 0.0f && !(token >= 0 && wide_less(x, low))) {
+                        token = j + k;
+                        low = wide_add(low, e[k]);
+                    }
+                }
+                sh.last = token;
+            }
+            if (f.at < 0 && tid == 0) sh.last = -1;
+            __syncthreads();
+            token = sh.last;
+            break;
+        }
+        if (q == nullptr && sure < 0) break;
+        q = nullptr, sure = -1;
+        for (int g = warp; g < a.groups; g += kSmpWarps) part_sum(g);
+        __threadfence_block();
+        __syncthreads();
+    }
+    if (warp == 0) write_request(a, r, nd, kept, token);
+    if (tid == 0) w->count[0] = 0;
+}
+
+// Entry j of the greedy comparison: larger is better, of equal values the lower index. 0: nothing (NaN).
 __device__ __forceinline__ unsigned long long greedy_key(float x, int j) {
     const unsigned b = __float_as_uint(x + 0.0f);  // -0 as 0
     const unsigned o = b & 0x80000000u ? ~b : b | 0x80000000u;
@@ -173,259 +446,129 @@ struct Best {
     }
 };
 
-template <typename T, bool ALIGNED>
-__device__ __forceinline__ void best_of_whole_tile(const T* p, int e0, Best& best) {
-    constexpr int N = kVerTile / 32 / kVec<T>;
-    const int at = e0 + (threadIdx.x & 31) * kVec<T>;
-    uint4 w[N];
+// The largest of 16 bytes of entries; a NaN is passed over.
+template <typename T> __device__ __forceinline__ float largest(const uint4& w);
+template <> __device__ __forceinline__ float largest<float>(const uint4& w) {
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+}
+template <> __device__ __forceinline__ float largest<__nv_bfloat16>(const uint4& w) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
+    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+
+template <typename T>
+__device__ __forceinline__ void best_of_tile(const T* p, int V, int e0, Best& best) {
+    const int lane = threadIdx.x & 31;
+    if (e0 >= 0 && e0 + kTile<T> <= V) {
+        const int at = e0 + lane * kVec<T>;
+        uint4 w[kVerVecs];
 #pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = load16<ALIGNED>(reinterpret_cast<const char*>(p + at + i * 32 * kVec<T>));
+        for (int i = 0; i < kVerVecs; ++i) w[i] = load16<true>(reinterpret_cast<const char*>(p + at + i * 32 * kVec<T>));
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        float v[kVec<T>];
-        unpack<T>(w[i], v);
-        float m = v[0];
+        for (int i = 0; i < kVerVecs; ++i) {
+            const float m = largest<T>(w[i]);
+            if (m > best.x || (best.j < 0 && m == best.x)) {  // rare: the index only where there is a new best
+                float v[kVec<T>];
+                unpack<T>(w[i], v);
 #pragma unroll
-        for (int j = 1; j < kVec<T>; ++j) m = fmaxf(m, v[j]);  // a NaN is passed over
-        if (m > best.x || (best.j < 0 && m == best.x)) {  // rare: the index only where there is a new best
+                for (int j = 0; j < kVec<T>; ++j) best.look(v[j], at + i * 32 * kVec<T> + j);
+            }
+        }
+        return;
+    }
+    // a row's ends, as in add_tile
+#pragma unroll 1
+    for (int h = 0; h < kTile<T> / 32; h += 8) {
+        T v[8];
 #pragma unroll
-            for (int j = 0; j < kVec<T>; ++j) best.look(v[j], at + i * 32 * kVec<T> + j);
+        for (int i = 0; i < 8; ++i) v[i] = p[min(max(e0 + lane + 32 * (h + i), 0), V - 1)];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = e0 + lane + 32 * (h + i);
+            if (j >= 0 && j < V) best.look(to_f<T>(v[i]), j);
         }
     }
 }
 
 template <typename T>
-__device__ __forceinline__ unsigned long long best_of_tile(const T* p, int V, int e0) {
-    Best best;
-    if (whole_tile(p, V, e0)) {
-        if (((uintptr_t)p & 15) == 0) best_of_whole_tile<T, true>(p, e0, best);
-        else best_of_whole_tile<T, false>(p, e0, best);
-    } else {
-        const int end = min(e0 + kVerTile, V);
-#pragma unroll 8
-        for (int j = e0 + (threadIdx.x & 31); j < end; j += 32) best.look(to_f<T>(p[j]), j);
-    }
-    unsigned long long k = best.j < 0 ? 0ull : greedy_key(best.x, best.j);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const unsigned long long y = __shfl_xor_sync(0xffffffffu, k, o);
-        k = y > k ? y : k;
-    }
-    return k;
-}
-
-template <typename T, bool GREEDY>
-__global__ void __launch_bounds__(kVerThreads) verify_kernel(Verify a) {
-    __shared__ VerifyShared sh;
-    __shared__ double s_tile[GREEDY ? 1 : kVerTiles];
-    cg::cluster_group cl = cg::this_cluster();
-    const int rank = (int)cl.block_rank(), size = (int)cl.num_blocks();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int r = blockIdx.x / size;
+__global__ void __launch_bounds__(kGrdThreads, sizeof(T) == 2 ? 12 : 8) verify_greedy_kernel(Verify a) {
+    const int lane = threadIdx.x & 31, K = a.K, V = a.V, G = a.groups;
+    const long long warps = (long long)gridDim.x * kGrdWarps, level = (long long)a.n_req * G, items = level * (K + 1);
     pdl_wait_then_release();
-    const int K = a.K, V = a.V, nd = a.n_draft[r];
-    int* const out = a.out + (long long)r * (K + 1);
-    if (nd < 0 || nd > K) {  // a request that waits; the whole cluster comes here
-        if (rank == 0) {
-            for (int i = tid; i <= K; i += kVerThreads) out[i] = -1;
-            if (tid == 0) {
-                a.accepted[r] = a.n_new[r] = 0;
-                if (nd != -1) set_status(a.status, ICE_ERR_BOUNDS);
-            }
-        }
-        return;
-    }
-    const T* const target = (const T*)a.target + r * a.t_req;
-    const int* const tokens = a.tokens + (long long)r * K;
-    const int tiles = (V + kVerTile - 1) / kVerTile;
-    int t0, t1;
-    share_of(tiles, rank, size, t0, t1);
-    int kept = 0, token = -1;  // sampling: token in the block that owns the drawn one
-    bool none = false;         // the deciding row leaves nothing
-    if (rank == 0 && tid < nd && (tokens[tid] < 0 || tokens[tid] >= V)) set_status(a.status, ICE_ERR_BOUNDS);
-    if (GREEDY) {
-        bool done = false;
-        for (int g0 = 0, buf = 0; !done; g0 += a.group, buf ^= 1) {
-            const int rows = min(a.group, nd + 1 - g0), n = t1 - t0;
-            if (tid < rows) sh.best[buf][tid] = 0;
-            __syncthreads();
-            for (int i = warp; i < rows * n; i += kVerWarps) {
-                const int y = i / n, t = t0 + i - y * n;
-                const unsigned long long k = best_of_tile(target + (g0 + y) * a.t_row, V, t * kVerTile);
-                if (lane == 0 && k) atomicMax(&sh.best[buf][y], k);
-            }
-            cl.sync();
-            for (int y = 0; y < rows && !done; ++y) {
-                unsigned long long k = lane < size ? cl.map_shared_rank(&sh.best[buf][y], lane)[0] : 0ull;
+    for (long long item = (long long)blockIdx.x * kGrdWarps + (threadIdx.x >> 5); item < items; item += warps) {
+        const int i = (int)(item / level);
+        const long long rest = item - i * level;
+        const int r = (int)(rest / G), g = (int)(rest - (long long)r * G);
+        VerifyScratch* const w = a.scratch + r;
+        const int nd = a.n_draft[r], wrong = *(volatile int*)&w->wrong;
+        const bool part = nd >= 0 && nd <= K && i <= nd;
+        if (part && i <= kVerMaxDrafts + 1 - wrong) {
+            const T* p = (const T*)a.target + r * a.t_req + i * a.t_row;
+            Best best;
+            int t0, t1;
+            const int shift = row_shift(p);
+            part_of((V + shift + kTile<T> - 1) / kTile<T>, g, G, t0, t1);
+            for (int t = t0; t < t1; ++t) best_of_tile(p, V, t * kTile<T> - shift, best);
+            unsigned long long k = best.j < 0 ? 0ull : greedy_key(best.x, best.j);
 #pragma unroll
-                for (int o = 8; o > 0; o >>= 1) {
-                    const unsigned long long z = __shfl_xor_sync(0xffffffffu, k, o);
-                    k = z > k ? z : k;
+            for (int o = 16; o > 0; o >>= 1) {
+                const unsigned long long y = __shfl_xor_sync(0xffffffffu, k, o);
+                k = y > k ? y : k;
+            }
+            if (lane == 0 && k) atomicMax(&w->best[i], k);
+        }
+        int last = 0;
+        if (lane == 0) {
+            __threadfence();
+            if (atomicAdd(&w->count[i], 1) == G - 1) {  // the row is complete, or does not matter
+                __threadfence();
+                if (part) {
+                    const unsigned long long k = __ldcg(&w->best[i]);
+                    const int x = i < nd ? a.tokens[(long long)r * K + i] : -1;
+                    if (i < nd && (x < 0 || x >= V)) set_status(a.status, ICE_ERR_BOUNDS);
+                    // a row that some of whose groups were skipped lies behind a wrong one: that stays the first
+                    if (k == 0 || x != (int)(0xffffffffu - (unsigned)k)) atomicMax(&w->wrong, kVerMaxDrafts + 1 - i);
                 }
-                k = __shfl_sync(0xffffffffu, k, 0);
-                none = k == 0;
-                token = none ? -1 : (int)(0xffffffffu - (unsigned)k);
-                if (kept < nd && !none && tokens[kept] == token) ++kept;
-                else done = true;
+                __threadfence();
+                last = atomicAdd(&w->rows, 1) == K;
+                __threadfence();
             }
         }
-    } else {
-        if (warp < 2) {  // the drafts that stay: one a lane
-            bool keep = false;
-            if (tid < nd) {
-                const int x = tokens[tid];
-                if (x >= 0 && x < V) {
-                    const float p = clean(to_f<T>(target[tid * a.t_row + x]));
-                    const float q = a.draft ? clean(to_f<T>(((const T*)a.draft + r * a.d_req)[tid * a.d_row + x])) : 1.0f;
-                    // 48 bits: exact
-                    keep = (double)clamp_uniform(a.uniform[(long long)r * (K + 1) + tid]) * (double)q < (double)p;
-                }
-            }
-            const unsigned m = __ballot_sync(0xffffffffu, keep);
-            if (lane == 0) sh.keep[warp] = m;
-        }
-        const double u = clamp_uniform(a.uniform[(long long)r * (K + 1) + K]);
-        __syncthreads();
-        const unsigned long long m = (unsigned long long)sh.keep[1] << 32 | sh.keep[0];
-        kept = __ffsll((long long)~m) - 1;  // bit 63 is never set
-        const T* const p = target + kept * a.t_row;
-        const T* q = nullptr;
-        int sure = -1;
-        if (kept < nd) {
-            if (a.draft) q = (const T*)a.draft + r * a.d_req + kept * a.d_row;
-            else sure = tokens[kept];
-        }
-        // at most twice: where the target is nowhere above the draft, a token of the target's own
-        for (int pass = 0; pass < 2; ++pass) {
-            for (int t = t0 + warp; t < t1; t += kVerWarps) {
-                const double s = sum_tile(p, q, sure, V, t * kVerTile);
-                if (lane == 0) s_tile[t - t0] = s;
-            }
-            __syncthreads();
-            // sums up to each lane's range of tiles
-            const int n = t1 - t0, per = (n + 31) >> 5, b = min(lane * per, n), e = min(b + per, n);
-            double mine = 0.0, upto = 0.0;
-            if (warp == 0) {
-                for (int t = b; t < e; ++t) mine += s_tile[t];
-                upto = mine;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const double y = __shfl_up_sync(0xffffffffu, upto, o);
-                    if (lane >= o) upto += y;
-                }
-                if (lane == 31) sh.total = upto;
-            }
-            cl.sync();
-            // every block comes to the same owner of the drawn token
-            double before = 0.0, all = 0.0, start = 0.0;
-            int owner = -1;
-            for (int k = 0; k < size; ++k) all += *cl.map_shared_rank(&sh.total, k);
-            const double want = u * all;
-            for (int k = 0; k < size; ++k) {
-                const double s = *cl.map_shared_rank(&sh.total, k);
-                if (s > 0.0 && !(owner >= 0 && want < start + *cl.map_shared_rank(&sh.total, owner))) {
-                    owner = k;  // the first whose end lies beyond `want`, else the last that has any weight
-                    start = before;
-                }
-                before += s;
-            }
-            cl.sync();  // the sums have been read
-            if (owner < 0) {
-                none = true;
-                if (q == nullptr && sure < 0) break;
-                q = nullptr, sure = -1;
-                continue;
-            }
-            none = false;
-            if (owner == rank) {
-                if (warp == 0) {
-                    double x = want - start, low = __shfl_up_sync(0xffffffffu, upto, 1);
-                    if (lane == 0) low = 0.0;
-                    const unsigned some = __ballot_sync(0xffffffffu, mine > 0.0), over = some & __ballot_sync(0xffffffffu, upto > x);
-                    if (lane == (over ? __ffs(over) - 1 : 31 - __clz(some))) {
-                        int found = b;
-                        double base = low;
-                        for (int t = b; t < e; ++t) {
-                            if (s_tile[t] > 0.0) {
-                                found = t;
-                                base = low;
-                                if (low + s_tile[t] > x) break;
-                            }
-                            low += s_tile[t];
-                        }
-                        sh.tile = found;
-                        sh.x = x - base;
-                        sh.token = INT_MAX;
-                    }
-                }
-                __syncthreads();
-                // the tile again, two neighbouring elements a thread, and their sums up to each
-                const int j = (t0 + sh.tile) * kVerTile + 2 * tid;
-                const double w0 = j < V ? weight(p, q, sure, j) : 0.0, w1 = j + 1 < V ? weight(p, q, sure, j + 1) : 0.0;
-                double c = w0 + w1;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const double y = __shfl_up_sync(0xffffffffu, c, o);
-                    if (lane >= o) c += y;
-                }
-                if (lane == 31) sh.warp[warp] = c;
-                __syncthreads();
-                double base = 0.0;
-                for (int k = 0; k < warp; ++k) base += sh.warp[k];
-                double c1 = __shfl_up_sync(0xffffffffu, c, 1);
-                if (lane == 0) c1 = 0.0;
-                if (w0 > 0.0 && base + c1 + w0 > sh.x) atomicMin(&sh.token, j);
-                else if (w1 > 0.0 && base + c > sh.x) atomicMin(&sh.token, j + 1);
-                __syncthreads();
-                if (sh.token == INT_MAX) {  // by the roundings none: the last that has any weight
-                    __syncthreads();
-                    if (tid == 0) sh.token = -1;
-                    __syncthreads();
-                    if (w1 > 0.0) atomicMax(&sh.token, j + 1);
-                    else if (w0 > 0.0) atomicMax(&sh.token, j);
-                    __syncthreads();
-                }
-                token = sh.token;
-                if (tid == 0) out[kept] = token;
-            }
-            break;
-        }
-    }
-    if (GREEDY) cl.sync();  // the blocks' bests have been read
-    if (rank != 0) return;
-    for (int i = tid; i <= K; i += kVerThreads) {
-        if (i < kept) out[i] = tokens[i];
-        else if (i > kept) out[i] = -1;
-        else if (GREEDY || none) out[i] = token;
-    }
-    if (tid == 0) {
-        a.accepted[r] = kept;
-        a.n_new[r] = kept - nd;
-        if (none) set_status(a.status, ICE_ERR_BOUNDS);
+        if (!__shfl_sync(0xffffffffu, last, 0)) continue;
+        const int kept = kVerMaxDrafts + 1 - __ldcg(&w->wrong);
+        const unsigned long long k = nd >= 0 && nd <= K ? __ldcg(&w->best[kept]) : 0ull;
+        write_request(a, r, nd, kept, k ? (int)(0xffffffffu - (unsigned)k) : -1);
+        __syncwarp();
+        for (int x = lane; x <= K; x += 32) w->best[x] = 0, w->count[x] = 0;
+        if (lane == 0) w->wrong = w->rows = 0;
     }
 }
 
-cudaError_t launch_verify(Verify a, int dtype, cudaStream_t s) {
-    const int tiles = (a.V + kVerTile - 1) / kVerTile;
-    int size = 8;
-    while (size > 1 && size > tiles) size >>= 1;
-    a.group = a.n_req * size <= 2 * 152 ? kVerMaxDrafts + 1 : 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.n_req * size);
-    cfg.blockDim = dim3(kVerThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = size;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see pdl_wait_then_release
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 2;
-    const bool greedy = a.uniform == nullptr;
-    if (dtype == ICE_BF16)
-        return cudaLaunchKernelEx(&cfg, greedy ? verify_kernel<__nv_bfloat16, true> : verify_kernel<__nv_bfloat16, false>, a);
-    return cudaLaunchKernelEx(&cfg, greedy ? verify_kernel<float, true> : verify_kernel<float, false>, a);
+template <typename T>
+static cudaError_t launch_sample(Verify a, cudaStream_t s) {
+    const int tiles = (a.V + kTile<T> - 1) / kTile<T>;
+    // a tile a warp while that fills the GPU at most once, else four
+    const int per = (long long)a.n_req * tiles > 152 * 32 ? 4 : 1;
+    a.groups = std::min(kVerGroups, (tiles + per * kSmpWarps - 1) / (per * kSmpWarps) * kSmpWarps);
+    return launch_pdl(verify_sample_kernel<T>, dim3(a.n_req * (a.groups / kSmpWarps)), dim3(kSmpThreads), 0, s, a);
+}
+
+template <typename T>
+static cudaError_t launch_greedy(Verify a, cudaStream_t s) {
+    const int tiles = (a.V + kTile<T> - 1) / kTile<T>;
+    // groups of four tiles where they are many; the shortest way for few
+    const int per = (long long)a.n_req * (a.K + 1) * tiles > 152 * 64 ? 4 : 1;
+    a.groups = (tiles + per - 1) / per;
+    const long long items = (long long)a.n_req * a.groups * (a.K + 1);
+    // a block in turn for each group: what is handed out late can still be skipped
+    const dim3 grid((unsigned)std::min<long long>((items + kGrdWarps - 1) / kGrdWarps, 0x7FFFFFFF));
+    return launch_pdl(verify_greedy_kernel<T>, grid, dim3(kGrdThreads), 0, s, a);
+}
+
+cudaError_t launch_verify(const Verify& a, int dtype, cudaStream_t s) {
+    if (dtype == ICE_BF16) return a.uniform ? launch_sample<__nv_bfloat16>(a, s) : launch_greedy<__nv_bfloat16>(a, s);
+    return a.uniform ? launch_sample<float>(a, s) : launch_greedy<float>(a, s);
 }
 
 }  // namespace ice
