@@ -1,29 +1,54 @@
 // Pages that several requests hold: forking, block tables with copy on write, compaction of the pool, copies of pages.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "ice_paged_scan.cuh"
 #include "ice_paged_share.cuh"
 
+namespace cg = cooperative_groups;
+
 namespace ice {
+
+// One cluster of blocks.
+template <typename Arg>
+static cudaError_t launch_cluster(void (*kern)(Arg), int blocks, int threads, size_t smem, cudaStream_t s, const Arg& a) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = blocks;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see pdl_wait_then_release
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
 
 // ---------------------------------------------------------------------------
 // Forking: a row of page ids copied and each page's count raised. Every block checks the whole call by itself (the
 // destinations as a bitmap in shared memory) and does its share of pieces of 256 columns; the lengths, which may be replaced
 // in place, are written by the last block to have read them.
 // ---------------------------------------------------------------------------
-constexpr int kForkThreads = 256, kForkPiece = 256;
+constexpr int kForkThreads = 1024, kForkFewThreads = 256;  // the latter for few forks
+constexpr int kForkPiece = 256;
 
-__global__ void __launch_bounds__(kForkThreads) fork_kernel(Fork a) {
+template <int NT>
+__global__ void __launch_bounds__(NT) fork_kernel(Fork a) {
     __shared__ unsigned s_dst[kPagedMaxRequests / 32];
     __shared__ int s_last;
     const int tid = threadIdx.x, lane = tid & 31;
-    for (int i = tid; i < kPagedMaxRequests / 32; i += kForkThreads) s_dst[i] = 0;
+    for (int i = tid; i < kPagedMaxRequests / 32; i += NT) s_dst[i] = 0;
     __syncthreads();
     pdl_wait_then_release();
     const long long cap = (long long)a.max_blocks * a.P;
     auto length = [&](int i) { return a.fork_len ? a.fork_len[i] : a.seq_len[a.src[i]]; };
     bool bad = false;
-    for (int i = tid; i < a.n_fork; i += kForkThreads) {
+    for (int i = tid; i < a.n_fork; i += NT) {
         const int s = a.src[i], d = a.dst[i];
         if (s < 0 || s >= a.n || d < 0 || d >= a.n) {
             bad = true;
@@ -34,7 +59,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(Fork a) {
         bad |= have < 0 || have > cap || len < 0 || len > have || a.seq_len[d] != 0;
     }
     __syncthreads();
-    for (int i = tid; i < a.n_fork; i += kForkThreads) {
+    for (int i = tid; i < a.n_fork; i += NT) {
         const int s = a.src[i];
         bad |= s >= 0 && s < a.n && ((s_dst[s >> 5] >> (s & 31)) & 1);
     }
@@ -42,9 +67,9 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(Fork a) {
     if (ok) {
         const int pieces = (a.max_blocks + kForkPiece - 1) / kForkPiece;
         const long long items = (long long)a.n_fork * pieces;
-        const int step = gridDim.x * (kForkThreads / 32);
+        const int step = gridDim.x * (NT / 32);
         bool range = false;
-        for (long long x = blockIdx.x * (kForkThreads / 32) + (tid >> 5); x < items; x += step) {
+        for (long long x = blockIdx.x * (NT / 32) + (tid >> 5); x < items; x += step) {
             const int i = (int)(x / pieces), c0 = (int)(x - (long long)i * pieces) * kForkPiece;
             const int n = min((length(i) + a.P - 1) / a.P, c0 + kForkPiece);
             const int* from = a.block_table + (long long)a.src[i] * a.max_blocks;
@@ -67,10 +92,10 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(Fork a) {
     __syncthreads();
     if (!s_last) return;
     if (a.seq_len_out != a.seq_len)
-        for (int r = tid; r < a.n; r += kForkThreads)
+        for (int r = tid; r < a.n; r += NT)
             if (!ok || !((s_dst[r >> 5] >> (r & 31)) & 1)) a.seq_len_out[r] = a.seq_len[r];
     if (ok)
-        for (int i = tid; i < a.n_fork; i += kForkThreads) a.seq_len_out[a.dst[i]] = length(i);  // no source is a destination
+        for (int i = tid; i < a.n_fork; i += NT) a.seq_len_out[a.dst[i]] = length(i);  // no source is a destination
     if (tid == 0) {
         if (!ok) set_status(a.status, ICE_ERR_BOUNDS);
         a.head->ticket = 0;
@@ -78,9 +103,11 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(Fork a) {
 }
 
 cudaError_t launch_fork(const Fork& a, cudaStream_t s) {
+    const bool few = a.n_fork <= kForkFewThreads;
+    const int threads = few ? kForkFewThreads : kForkThreads;
     const long long items = (long long)a.n_fork * ((a.max_blocks + kForkPiece - 1) / kForkPiece);
-    const int blocks = (int)std::max<long long>(1, std::min<long long>(152, (items + 7) / 8));
-    return launch_pdl(fork_kernel, dim3(blocks), dim3(kForkThreads), 0, s, a);
+    const int blocks = (int)std::max<long long>(1, std::min<long long>(152, (items + threads / 32 - 1) / (threads / 32)));
+    return launch_pdl(few ? fork_kernel<kForkFewThreads> : fork_kernel<kForkThreads>, dim3(blocks), dim3(threads), 0, s, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -98,10 +125,13 @@ cudaError_t launch_fork(const Fork& a, cudaStream_t s) {
 // Names make the result independent of the order in which the blocks run; the counts are whole numbers. If the step cannot be
 // carried out the claims are taken back by adding them again.
 //
-// Bound by latency. Small steps run the phases in one block, others as three launches.
+// Bound by latency. One thread-block cluster runs the phases of most steps, with its barrier between them; large steps are three
+// launches.
 // ---------------------------------------------------------------------------
 constexpr int kShrThreads = 1024, kShrGridThreads = 256;
-constexpr int kShrSlots = 4;  // consecutive slots of a thread
+constexpr int kShrCluster = 8;
+constexpr int kShrSlots = 4;    // consecutive slots of a thread
+constexpr int kShrPiece = 256;  // columns that a warp takes at once
 
 __device__ __forceinline__ unsigned long long claim_name(unsigned long long epoch, bool writes, int r) {
     // above every word that a compaction leaves in the claims (below 2^31)
@@ -127,21 +157,24 @@ __device__ __forceinline__ ShareReq share_req(const SharedTables& a, int r) {
     return q;
 }
 
-// Calls f(page) for the pages that the request lets go of, a lane each; returns whether an id was out of range.
+// Calls f(page) for the pages among a piece's columns that the request lets go of, a lane each; returns whether an id was out of
+// range.
 template <typename F>
-__device__ __forceinline__ bool for_claims(const SharedTables& a, int r, const ShareReq& q, F f) {
+__device__ __forceinline__ bool for_claims(const SharedTables& a, int r, const ShareReq& q, int piece, F f) {
     const int lane = threadIdx.x & 31;
     const int* row = a.block_table + (long long)r * a.max_blocks;
     bool bad = false;
     if (q.grows) {
-        if (lane == 0) {
+        if (piece == 0 && lane == 0) {
             const int p = row[q.had - 1];
             if (p >= 0 && p < a.n_pages) f(p);
             else bad = true;
         }
         return bad;
     }
-    for (int c = q.has + lane; c < q.had; c += 32) {
+    const int c0 = max(q.has, piece * kShrPiece), c1 = min(q.had, (piece + 1) * kShrPiece);
+#pragma unroll 4
+    for (int c = c0 + lane; c < c1; c += 32) {
         const int p = row[c];
         if (p >= 0 && p < a.n_pages) f(p);
         else bad = true;
@@ -149,18 +182,23 @@ __device__ __forceinline__ bool for_claims(const SharedTables& a, int r, const S
     return bad;
 }
 
+__device__ __forceinline__ int share_pieces(const SharedTables& a) { return (a.max_blocks + kShrPiece - 1) / kShrPiece; }
+
 __device__ __forceinline__ void share_claim(const SharedTables& a, int warp, int warps) {
     const unsigned long long epoch = a.w.head->epoch;
-    for (int r = warp; r < a.n; r += warps) {
+    const int pieces = share_pieces(a);
+    for (long long x = warp; x < (long long)a.n * pieces; x += warps) {
+        const int r = (int)(x / pieces), piece = (int)(x - (long long)r * pieces);
         const ShareReq q = share_req(a, r);
         const unsigned long long name = claim_name(epoch, q.grows, r);
         int bad = q.bad;
-        if (for_claims(a, r, q, [&](int p) {
+        if (for_claims(a, r, q, piece, [&](int p) {
                 atomicSub(a.page_refs + p, 1);
                 atomicMax(a.w.claim + p, name);
             }))
             bad |= kBadBounds;
         if (bad) atomicOr(&a.w.head->flags, bad);
+        if (piece == 0 && (threadIdx.x & 31) == 0) a.w.req[r] = make_int4(max(q.new_len - q.old_len, 0), max(q.has - q.had, 0), 0, 0);
     }
 }
 
@@ -171,18 +209,23 @@ __device__ __forceinline__ bool share_mine(const SharedTables& a, int p, unsigne
 
 __device__ __forceinline__ void share_count(const SharedTables& a, int warp, int warps) {
     const unsigned long long epoch = a.w.head->epoch;
-    for (int r = warp; r < a.n; r += warps) {
+    const int pieces = share_pieces(a);
+    for (long long x = warp; x < (long long)a.n * pieces; x += warps) {
+        const int r = (int)(x / pieces), piece = (int)(x - (long long)r * pieces);
         const ShareReq q = share_req(a, r);
         const unsigned long long name = claim_name(epoch, q.grows, r);
         int mine = 0;
         bool bad = false;
-        for_claims(a, r, q, [&](int p) {
+        for_claims(a, r, q, piece, [&](int p) {
             mine += share_mine(a, p, name);
             bad |= __ldcg(a.page_refs + p) < 0;  // more holders than the page's count
         });
         if (bad) atomicOr(&a.w.head->flags, kBadBounds);
         mine = __reduce_add_sync(0xffffffffu, mine);
-        if ((threadIdx.x & 31) == 0) a.w.req[r] = q.grows ? (mine ? 0 : 1) : 2 * mine;
+        if ((threadIdx.x & 31) == 0) {
+            if (q.grows && piece == 0 && !mine) a.w.req[r].w = 1;
+            if (!q.grows && mine) atomicAdd(&a.w.req[r].z, mine);
+        }
     }
 }
 
@@ -199,15 +242,16 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
     const int flags = __ldcg(&a.w.head->flags);
     const int per = (n + NT - 1) / NT, r0 = min(tid * per, n), r1 = min(r0 + per, n);
     unsigned x[3] = {0, 0, 0}, tot[3];
+    auto copied = [&](int r) { return __ldcg(&a.w.req[r].w); };
     auto add = [&](int r) {
-        const ShareReq q = share_req(a, r);
-        const int c = __ldcg(a.w.req + r);
-        x[0] += max(q.new_len - q.old_len, 0);
-        x[1] += max(q.has - q.had, 0) + (c & 1);
-        x[2] += c >> 1;
+        const int4 c = __ldcg(a.w.req + r);
+        x[0] += c.x;
+        x[1] += c.y + c.w;
+        x[2] += c.z;
     };
     bool over = false;
     if (!flags) {
+#pragma unroll 4
         for (int r = r0; r < r1; ++r) {
             add(r);
             over |= (x[0] | x[1] | x[2]) >> 31;  // each term is below 2^31: seen before a sum can wrap
@@ -224,6 +268,7 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
     const bool ok = code == ICE_OK;
     const int n_tok = ok ? (int)tot[0] : 0, n_pop = ok ? (int)tot[1] : 0, n_push = ok ? (int)tot[2] : 0;
     if (ok) {
+#pragma unroll 4
         for (int r = r0; r < r1; ++r) {
             tok_cum[r] = (int)x[0];
             pop_cum[r] = (int)x[1];
@@ -245,7 +290,7 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
     const int first = blockIdx.x * NT + tid, step = gridDim.x * NT;
     for (int r = first; r <= n; r += step) a.q_start[r] = ok ? tok_cum[r] : 0;
     for (int r = first; r < n; r += step) {
-        const bool copies = ok && (__ldcg(a.w.req + r) & 1);
+        const bool copies = ok && copied(r);
         if (!copies) a.copy_src[r] = a.copy_dst[r] = -1;
         if (ok && !copies) {
             const ShareReq q = share_req(a, r);
@@ -275,7 +320,7 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
                     b = tok_cum[r], next = tok_cum[r + 1];
                     const int o = a.seq_len[r], p = o + i - b;
                     // a page that is copied is the first of those taken
-                    held = (o + P - 1) / P - (__ldcg(a.w.req + r) & 1);
+                    held = (o + P - 1) / P - copied(r);
                     pg = p / P;
                     off = p - pg * P;
                     page_id();
@@ -303,7 +348,7 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
         }
     }
     for (int j = first; j < n_pop; j += step) {
-        const int r = find_row(pop_cum, n, j), k = j - pop_cum[r], copies = __ldcg(a.w.req + r) & 1;
+        const int r = find_row(pop_cum, n, j), k = j - pop_cum[r], copies = copied(r);
         const int had = (a.seq_len[r] + P - 1) / P, p = a.free_pages[ring(hm, j)];
         int* e = a.block_table + (long long)r * a.max_blocks + had - copies + k;
         if (copies && k == 0) {
@@ -314,12 +359,16 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
         if (p >= 0 && p < n_pages) a.page_refs[p] = 1;
         else set_status(a.status, ICE_ERR_BOUNDS);  // an id in the ring that is no page's
     }
-    // pages given back, and on failure the claims: a warp a request
     const unsigned long long epoch = a.w.head->epoch;
-    for (int r = first >> 5; r < n; r += step >> 5) {
-        if (!ok) {
-            for_claims(a, r, share_req(a, r), [&](int p) { atomicAdd(a.page_refs + p, 1); });
-        } else if (push_cum[r + 1] > push_cum[r]) {
+    const int pieces = share_pieces(a);
+    if (!ok) {  // the claims taken back
+        for (long long y = first >> 5; y < (long long)n * pieces; y += step >> 5) {
+            const int r = (int)(y / pieces);
+            for_claims(a, r, share_req(a, r), (int)(y - (long long)r * pieces), [&](int p) { atomicAdd(a.page_refs + p, 1); });
+        }
+    } else if (pieces == 1) {  // pages given back, in order: a warp a request, or where rows are long a block
+        for (int r = first >> 5; r < n; r += step >> 5) {
+            if (push_cum[r + 1] == push_cum[r]) continue;
             const ShareReq q = share_req(a, r);
             const unsigned long long name = claim_name(epoch, false, r);
             const int* row = a.block_table + (long long)r * a.max_blocks;
@@ -330,6 +379,28 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
                 const unsigned m = __ballot_sync(0xffffffffu, mine);
                 if (mine) a.free_pages[ring(tm, at + __popc(m & ((1u << lane) - 1)))] = p;
                 at += __popc(m);
+            }
+        }
+    } else {
+        __shared__ int s_warp[NT / 32];
+        const int warp = tid >> 5;
+        for (int r = blockIdx.x; r < n; r += gridDim.x) {
+            if (push_cum[r + 1] == push_cum[r]) continue;
+            const ShareReq q = share_req(a, r);
+            const unsigned long long name = claim_name(epoch, false, r);
+            const int* row = a.block_table + (long long)r * a.max_blocks;
+            int at = push_cum[r];
+            for (int c0 = q.has; c0 < q.had; c0 += NT) {
+                const int p = c0 + tid < q.had ? row[c0 + tid] : -1;
+                const bool mine = p >= 0 && share_mine(a, p, name);
+                const unsigned m = __ballot_sync(0xffffffffu, mine);
+                __syncthreads();
+                if (lane == 0) s_warp[warp] = __popc(m);
+                __syncthreads();
+                const int c = lane < NT / 32 ? s_warp[lane] : 0;
+                const int before = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
+                if (mine) a.free_pages[ring(tm, at + before + __popc(m & ((1u << lane) - 1)))] = p;
+                at += __reduce_add_sync(0xffffffffu, c);
             }
         }
     }
@@ -367,27 +438,29 @@ __global__ void __launch_bounds__(kShrThreads) share_fill_kernel(SharedTables a)
     share_fill<kShrThreads>(a);
 }
 
+// The blocks of one cluster; its barrier orders their writes.
 __global__ void __launch_bounds__(kShrThreads) share_step_kernel(SharedTables a) {
     pdl_wait_then_release();
-    share_claim(a, threadIdx.x >> 5, kShrThreads >> 5);
-    __threadfence();
-    __syncthreads();
-    share_count(a, threadIdx.x >> 5, kShrThreads >> 5);
-    __threadfence();
-    __syncthreads();
+    const cg::cluster_group cl = cg::this_cluster();
+    const int warp = (blockIdx.x * kShrThreads + threadIdx.x) >> 5, warps = gridDim.x * kShrThreads >> 5;
+    share_claim(a, warp, warps);
+    cl.sync();
+    share_count(a, warp, warps);
+    cl.sync();
     share_fill<kShrThreads>(a);
 }
 
 cudaError_t launch_shared_tables(const SharedTables& a, cudaStream_t s) {
     const size_t smem = (size_t)(a.n + 1) * 12;
-    // One block where its 32 warps have few requests each, few slots, and few pages to give back whatever the lengths
-    if (a.n <= 128 && a.n_slots <= 4096 && (long long)a.n * a.max_blocks <= 65536)
-        return launch_pdl(share_step_kernel, dim3(1), dim3(kShrThreads), smem, s, a);
+    // one cluster where its 256 warps have few requests each, few slots, and few pages to give back whatever the lengths
+    if (a.n <= 1024 && a.n_slots <= 65536 && (long long)a.n * a.max_blocks <= 1 << 19)
+        return launch_cluster(share_step_kernel, kShrCluster, kShrThreads, smem, s, a);
     const int per = kShrGridThreads / 32;
-    const dim3 grid(std::min(152 * 4, (a.n + per - 1) / per));
+    const long long items = (long long)a.n * ((a.max_blocks + kShrPiece - 1) / kShrPiece);
+    const dim3 grid((unsigned)std::min<long long>(152 * 8, (items + per - 1) / per));
     cudaError_t e = launch_pdl(share_claim_kernel, grid, dim3(kShrGridThreads), 0, s, a);
     if (e == cudaSuccess) e = launch_pdl(share_count_kernel, grid, dim3(kShrGridThreads), 0, s, a);
-    const int blocks = std::max(1, std::min(152, std::max(a.n_slots / 1024, a.n / 32)));
+    const int blocks = std::max(1, std::min(152, std::max(a.n_slots / 1024, a.max_blocks > kShrPiece ? a.n : a.n / 32)));
     if (e == cudaSuccess) e = launch_pdl(share_fill_kernel, dim3(blocks), dim3(kShrThreads), smem, s, a);
     return e;
 }
@@ -398,41 +471,43 @@ cudaError_t launch_shared_tables(const SharedTables& a, cudaStream_t s) {
 // chunk (and every list checked), ranks and lists of moves, then the tables. A page that moves leaves its
 // number k in its claim, where the tables' pass finds it.
 // ---------------------------------------------------------------------------
-constexpr int kCmpThreads = 256, kCmpPer = kCmpChunk / kCmpThreads;
+constexpr int kCmpThreads = 256, kCmpStepThreads = 1024;
+constexpr int kCmpPer = 4;  // pages of a thread; a block's chunk is one pass over them
+static_assert(kCmpChunk == kCmpThreads * kCmpPer, "the smaller chunk decides how many counts there are");
 
-__device__ __forceinline__ int block_sum(int x, int* s_sum) {  // 8 warps
+template <int NT>
+__device__ __forceinline__ int block_sum(int x, int* s_sum) {
     x = __reduce_add_sync(0xffffffffu, x);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = x;
     __syncthreads();
-    int t = 0;
-#pragma unroll
-    for (int i = 0; i < kCmpThreads / 32; ++i) t += s_sum[i];
-    return t;
+    const int lane = threadIdx.x & 31;
+    return __reduce_add_sync(0xffffffffu, lane < NT / 32 ? s_sum[lane] : 0);
 }
 
-__global__ void __launch_bounds__(kCmpThreads) compact_count_kernel(Compact a) {
-    __shared__ int s_sum[kCmpThreads / 32];
+template <int NT>
+__device__ __forceinline__ void compact_count(const Compact& a) {
+    constexpr int kChunk = NT * kCmpPer;
+    __shared__ int s_sum[NT / 32];
     const int tid = threadIdx.x, lane = tid & 31;
-    pdl_wait_then_release();
-    const int chunks = (int)((a.n_pages + kCmpChunk - 1) / kCmpChunk);
+    const int chunks = (int)((a.n_pages + kChunk - 1) / kChunk);
     bool bad = false;
     for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
         int live = 0;
 #pragma unroll
         for (int k = 0; k < kCmpPer; ++k) {
-            const long long p = (long long)c * kCmpChunk + k * kCmpThreads + tid;
+            const long long p = (long long)c * kChunk + k * NT + tid;
             const int f = p < a.n_pages ? a.page_refs[p] : 0;
             live += f > 0;
             bad |= f < 0;
         }
-        live = block_sum(live, s_sum);
+        live = block_sum<NT>(live, s_sum);
         if (tid == 0) a.w.count[c] = live;
     }
     // every page that is named is one in use
     auto named = [&](int p) { return p >= 0 && p < a.n_pages && a.page_refs[p] > 0; };
     const long long cap = (long long)a.max_blocks * a.P;
-    const int warps = gridDim.x * (kCmpThreads / 32), warp = blockIdx.x * (kCmpThreads / 32) + (tid >> 5);
+    const int warps = gridDim.x * (NT / 32), warp = blockIdx.x * (NT / 32) + (tid >> 5);
     for (int r = warp; r < a.n; r += warps) {
         const int len = a.seq_len[r];
         if (len < 0 || len > cap) {
@@ -443,36 +518,37 @@ __global__ void __launch_bounds__(kCmpThreads) compact_count_kernel(Compact a) {
 #pragma unroll 4
         for (int c = lane; c < pages; c += 32) bad |= !named(a.block_table[(long long)r * a.max_blocks + c]);
     }
-    for (int i = blockIdx.x * kCmpThreads + tid; i < a.n_extra; i += gridDim.x * kCmpThreads) bad |= !named(a.extra[i]);
+    for (int i = blockIdx.x * NT + tid; i < a.n_extra; i += gridDim.x * NT) bad |= !named(a.extra[i]);
     if (bad) atomicOr(&a.w.head->flags, kBadBounds);
 }
 
-__global__ void __launch_bounds__(kCmpThreads) compact_move_kernel(Compact a) {
-    __shared__ int s_sum[kCmpThreads / 32], s_warp[kCmpThreads / 32];
+template <int NT>
+__device__ __forceinline__ void compact_move(const Compact& a) {
+    constexpr int kChunk = NT * kCmpPer;
+    __shared__ int s_sum[NT / 32], s_warp[NT / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    pdl_wait_then_release();
-    const int chunks = (int)((a.n_pages + kCmpChunk - 1) / kCmpChunk);
+    const int chunks = (int)((a.n_pages + kChunk - 1) / kChunk);
     // this block's chunks, the pages in use before them and in all
     const int c0 = (int)((long long)chunks * blockIdx.x / gridDim.x), c1 = (int)((long long)chunks * (blockIdx.x + 1) / gridDim.x);
     int before = 0, all = 0;
-    for (int c = tid; c < chunks; c += kCmpThreads) {
-        const int x = a.w.count[c];
+    for (int c = tid; c < chunks; c += NT) {
+        const int x = __ldcg(a.w.count + c);
         all += x;
         if (c < c0) before += x;
     }
-    before = block_sum(before, s_sum);
-    const int L = block_sum(all, s_sum);
+    before = block_sum<NT>(before, s_sum);
+    const int L = block_sum<NT>(all, s_sum);
     // those in use before page L
     int low = 0;
-    for (int c = tid; c < L / kCmpChunk; c += kCmpThreads) low += a.w.count[c];
-    for (int p = L / kCmpChunk * kCmpChunk + tid; p < L; p += kCmpThreads) low += a.page_refs[p] > 0;
-    low = block_sum(low, s_sum);
+    for (int c = tid; c < L / kChunk; c += NT) low += __ldcg(a.w.count + c);
+    for (int p = L / kChunk * kChunk + tid; p < L; p += NT) low += a.page_refs[p] > 0;
+    low = block_sum<NT>(low, s_sum);
     const int moves = L - low;
-    const int code = a.w.head->flags ? ICE_ERR_BOUNDS : moves > a.n_moves ? ICE_ERR_CAPACITY : ICE_OK;
+    const int code = __ldcg(&a.w.head->flags) ? ICE_ERR_BOUNDS : moves > a.n_moves ? ICE_ERR_CAPACITY : ICE_OK;
     const bool ok = code == ICE_OK;
     for (int c = c0; ok && c < c1; ++c) {
         // neighbouring pages a thread: ranks in order
-        const long long p0 = (long long)c * kCmpChunk + tid * kCmpPer;
+        const long long p0 = (long long)c * kChunk + tid * kCmpPer;
         int f[kCmpPer], mine = 0;
 #pragma unroll
         for (int k = 0; k < kCmpPer; ++k) {
@@ -488,12 +564,9 @@ __global__ void __launch_bounds__(kCmpThreads) compact_move_kernel(Compact a) {
         __syncthreads();
         if (lane == 31) s_warp[warp] = inc;
         __syncthreads();
-        int rank = before + inc - mine;
-#pragma unroll
-        for (int i = 0; i < kCmpThreads / 32; ++i) {
-            if (i < warp) rank += s_warp[i];
-            before += s_warp[i];
-        }
+        const int of_warp = lane < NT / 32 ? s_warp[lane] : 0;
+        int rank = before + inc - mine + __reduce_add_sync(0xffffffffu, lane < warp ? of_warp : 0);
+        before += __reduce_add_sync(0xffffffffu, of_warp);
 #pragma unroll
         for (int k = 0; k < kCmpPer; ++k) {
             const long long p = p0 + k;
@@ -510,7 +583,7 @@ __global__ void __launch_bounds__(kCmpThreads) compact_move_kernel(Compact a) {
             rank += f[k];
         }
     }
-    for (int k = (ok ? moves : 0) + blockIdx.x * kCmpThreads + tid; k < a.n_moves; k += gridDim.x * kCmpThreads)
+    for (int k = (ok ? moves : 0) + blockIdx.x * NT + tid; k < a.n_moves; k += gridDim.x * NT)
         a.move_src[k] = a.move_dst[k] = -1;
     if (blockIdx.x == 0 && tid == 0) {
         a.w.head->plan[0] = ok;
@@ -525,14 +598,14 @@ __global__ void __launch_bounds__(kCmpThreads) compact_move_kernel(Compact a) {
     }
 }
 
-__global__ void __launch_bounds__(kCmpThreads) compact_apply_kernel(Compact a) {
+template <int NT>
+__device__ __forceinline__ void compact_apply(const Compact& a) {
     const int tid = threadIdx.x, lane = tid & 31;
-    pdl_wait_then_release();
-    const bool ok = a.w.head->plan[0];
-    const int L = a.w.head->plan[1], moves = a.w.head->plan[2];
-    const int first = blockIdx.x * kCmpThreads + tid, step = gridDim.x * kCmpThreads;
+    const bool ok = __ldcg(&a.w.head->plan[0]);
+    const int L = __ldcg(&a.w.head->plan[1]), moves = __ldcg(&a.w.head->plan[2]);
+    const int first = blockIdx.x * NT + tid, step = gridDim.x * NT;
     if (first == 0) a.w.head->flags = 0;
-    auto goes = [&](int p) { return ok && p >= L ? a.move_dst[(int)a.w.claim[p]] : p; };
+    auto goes = [&](int p) { return ok && p >= L ? __ldcg(a.move_dst + (int)__ldcg(a.w.claim + p)) : p; };
     const long long cap = (long long)a.max_blocks * a.P;
     for (int r = first >> 5; r < a.n; r += step >> 5) {
         const int len = a.seq_len[r];
@@ -545,8 +618,8 @@ __global__ void __launch_bounds__(kCmpThreads) compact_apply_kernel(Compact a) {
     // counts: a page that moves takes its own along
     if (ok) {
         for (int k = first; k < moves; k += step) {
-            const int s = a.move_src[k], f = a.page_refs[s];
-            a.page_refs_out[a.move_dst[k]] = f;
+            const int s = __ldcg(a.move_src + k), f = a.page_refs[s];
+            a.page_refs_out[__ldcg(a.move_dst + k)] = f;
             a.page_refs_out[s] = 0;
         }
     }
@@ -560,8 +633,38 @@ __global__ void __launch_bounds__(kCmpThreads) compact_apply_kernel(Compact a) {
     }
 }
 
+__global__ void __launch_bounds__(kCmpThreads) compact_count_kernel(Compact a) {
+    pdl_wait_then_release();
+    compact_count<kCmpThreads>(a);
+}
+
+__global__ void __launch_bounds__(kCmpThreads) compact_move_kernel(Compact a) {
+    pdl_wait_then_release();
+    compact_move<kCmpThreads>(a);
+}
+
+__global__ void __launch_bounds__(kCmpThreads) compact_apply_kernel(Compact a) {
+    pdl_wait_then_release();
+    compact_apply<kCmpThreads>(a);
+}
+
+// The blocks of one cluster; its barrier orders their writes.
+__global__ void __launch_bounds__(kCmpStepThreads) compact_step_kernel(Compact a) {
+    pdl_wait_then_release();
+    const cg::cluster_group cl = cg::this_cluster();
+    compact_count<kCmpStepThreads>(a);
+    cl.sync();
+    compact_move<kCmpStepThreads>(a);
+    cl.sync();
+    compact_apply<kCmpStepThreads>(a);
+}
+
 cudaError_t launch_compact(const Compact& a, cudaStream_t s) {
     const int chunks = (int)((a.n_pages + kCmpChunk - 1) / kCmpChunk);
+    // one cluster for small pools (1000 pages 8.3 us, as three launches 8.6 and 5 us more on the host); 32768 pages: 17.2 us, 14.3 as
+    // three launches
+    if (a.n_pages <= 16384 && (long long)a.n * a.max_blocks <= 1 << 19 && a.n_extra <= 65536)
+        return launch_cluster(compact_step_kernel, kShrCluster, kCmpStepThreads, 0, s, a);
     const dim3 block(kCmpThreads);
     const dim3 wide(std::max(1, std::min(152 * 4, std::max(chunks, std::max(a.n, a.n_extra / kCmpThreads) / 8))));
     cudaError_t e = launch_pdl(compact_count_kernel, wide, block, 0, s, a);

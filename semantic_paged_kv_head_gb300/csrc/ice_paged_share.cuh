@@ -20,7 +20,7 @@ constexpr int kCmpChunk = 1024;  // pages that a block of a compaction counts at
 struct ShareScratch {
     ShareHead* head;
     unsigned long long* claim;  // [n_pages]
-    int* req;                   // [max_requests] of a step: pages given back * 2 + 1 if the request's last page is copied
+    int4* req;                  // [max_requests] of a step: new tokens, pages more, pages given back, 1 if its last page is copied
     int* count;                 // [ceil(n_pages / kCmpChunk)] of a compaction: pages in use
 };
 

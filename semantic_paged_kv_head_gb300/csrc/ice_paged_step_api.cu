@@ -22,7 +22,8 @@ bool rope_ok(const ice_rope* r) {
 // The handle's scratch for shared pages, allocated and cleared (on `stream`) the first time.
 int share_scratch(ice_paged* pg, const Buffers& b, void* stream, ShareScratch* w) {
     const size_t chunks = (size_t)((pg->p.n_pages + kCmpChunk - 1) / kCmpChunk);
-    const size_t claims = sizeof(ShareHead), req = claims + 8 * (size_t)pg->p.n_pages, count = req + 4 * (size_t)pg->p.max_requests;
+    const size_t req = sizeof(ShareHead), claims = req + sizeof(int4) * (size_t)pg->p.max_requests;
+    const size_t count = claims + 8 * (size_t)pg->p.n_pages;
     const size_t bytes = count + 4 * chunks;
     if (!pg->share) {
         if (b.capturing) return ICE_ERR_INVALID_ARG;
@@ -40,7 +41,7 @@ int share_scratch(ice_paged* pg, const Buffers& b, void* stream, ShareScratch* w
     }
     w->head = (ShareHead*)pg->share;
     w->claim = (unsigned long long*)(pg->share + claims);
-    w->req = (int*)(pg->share + req);
+    w->req = (int4*)(pg->share + req);
     w->count = (int*)(pg->share + count);
     return ICE_OK;
 }

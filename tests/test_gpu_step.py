@@ -257,7 +257,7 @@ def _pool_lists(p):
 
 @pytest.mark.parametrize("n,P,cols,n_pages,rounds", [
     (3, 4, 6, 20, 30), (9, 1, 12, 60, 25), (40, 16, 10, 160, 20), (128, 5, 12, 700, 10), (129, 16, 10, 500, 10), (300, 3, 40, 5000, 6),
-    (20, 2, 4000, 30000, 5)])
+    (20, 2, 4000, 30000, 5), (140, 2, 4000, 60000, 4), (1100, 4, 20, 9000, 4)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_shared_tables_and_forks(ice, n, P, cols, n_pages, rounds, in_place):
     """A loop of forks and steps, moved on by the kernels and by the definition."""
@@ -363,7 +363,7 @@ def test_shared_tables_by_hand(ice, new, many):
     P = 4
     lens, table, ring, state, refs = _three_holders(P)
     if many:
-        lens, new, table = lens + [0] * 200, new + [0] * 200, table + [[-1] * 3 for _ in range(200)]
+        lens, new, table = lens + [0] * 1100, new + [0] * 1100, table + [[-1] * 3 for _ in range(1100)]
     pc = _cache(ice, n_kv_heads=1, n_q_heads=1, page_size=P, n_pages=8, max_requests=len(lens), max_blocks=3, max_tokens=1)
     ref = plain_tables_shared(lens, new, table, ring, state, refs, 20, P)
     assert ref[0] == 0
@@ -409,7 +409,7 @@ def test_shared_tables_all_or_nothing(ice, fault, many):
         state = [0, 8]
         new = [0, 0, 0, -2, 0]
     if many:
-        lens, new, table = lens + [0] * 200, new + [0] * 200, table + [[-1] * 3 for _ in range(200)]
+        lens, new, table = lens + [0] * 1100, new + [0] * 1100, table + [[-1] * 3 for _ in range(1100)]
     ref = plain_tables_shared(lens, new, table, ring, state, refs, n_slots, P)
     assert ref[0] != 0
     pc = _cache(ice, n_kv_heads=1, n_q_heads=1, page_size=P, n_pages=8, max_requests=len(lens), max_blocks=3, max_tokens=1)
@@ -423,7 +423,7 @@ def test_shared_tables_all_or_nothing(ice, fault, many):
     lens, table, ring, state, refs = _three_holders(P)
     new = [1, 1, 1, 0, 0]
     if many:
-        lens, new, table = lens + [0] * 200, new + [0] * 200, table + [[-1] * 3 for _ in range(200)]
+        lens, new, table = lens + [0] * 1100, new + [0] * 1100, table + [[-1] * 3 for _ in range(1100)]
     ref = plain_tables_shared(lens, new, table, ring, state, refs, 20, P)
     t = [_i32(x) for x in (lens, new, table, ring)]
     st, rf = torch.tensor(state, dtype=torch.int64, device="cuda"), _i32(refs)
@@ -502,11 +502,13 @@ def test_compact_all_or_nothing(ice, fault):
         assert rg.tolist() == ring and st.tolist() == state
 
 
-@pytest.mark.parametrize("n_pages,fill", [(1, 0), (1, 1), (1023, 0.5), (1024, 0.3), (1025, 0.9), (5000, 0.02), (200000, 0.4), (4097, 1.0)])
-def test_compact_pools(ice, n_pages, fill):
-    """Pools of one and of many chunks, empty and full, with a list of the caller's own."""
+@pytest.mark.parametrize("n_pages,fill,n,cols", [
+    (1, 0, 37, 50), (1, 1, 37, 50), (1023, 0.5, 37, 50), (4096, 0.3, 37, 50), (4097, 1.0, 37, 50), (5000, 0.02, 37, 50), (200000, 0.4, 37, 50),
+    (1, 1, 300, 3600), (1025, 0.9, 300, 3600), (30000, 0.5, 300, 3600), (1100000, 0.3, 37, 50)])
+def test_compact_pools(ice, n_pages, fill, n, cols):
+    """Pools of one and of many chunks, empty and full, with a list of the caller's own; one cluster and three launches."""
     rng = random.Random(n_pages)
-    P, cols, n = 2, 50, 37
+    P = 2
     used = rng.sample(range(n_pages), int(n_pages * fill))
     refs = [0] * n_pages
     for p in used:
