@@ -187,6 +187,11 @@ def _stream(stream=None) -> int:
     return _raw_stream(torch.cuda.current_device())
 
 
+def _stream_on(index: int) -> int:
+    """The current stream of a device whose number is known."""
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 def _dev_ptr(t: torch.Tensor, dtype=None, name="tensor", host_ok=True) -> int:
     """Address of a buffer argument: a CUDA tensor or, where the call allows it,
     a page-locked CPU tensor that the kernels read or write in place."""
@@ -499,6 +504,8 @@ class PagedCache:
         _check(_lib.ice_paged_create(ctypes.byref(self.params), ctypes.byref(self._h)),
                "ice_paged_create")
         self._page_shape = (n_pages, n_kv_heads, page_size, d)
+        self._d, self._n_pages, self._columns = d, n_pages, max_blocks
+        self._index = self.device.index
 
     # -- tensors of the shapes that the calls take -----------------------------------
     def new_pages(self):
@@ -541,7 +548,14 @@ class PagedCache:
 
     def _rows(self, t, heads, name):
         """Pointer and token stride of [tokens, heads, d] whose rows of heads are contiguous."""
-        d = self.params.d
+        d = self._d
+        try:
+            n, h, e = t.shape
+            stride, head, one = t.stride()
+            if h == heads and e == d and one == 1 and (head == d or heads == 1) and t.dtype is self.dtype and t.is_cuda:
+                return t.data_ptr(), stride if n > 1 else heads * d
+        except (AttributeError, TypeError, ValueError):
+            pass
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
         if t.dtype != self.dtype:
@@ -660,14 +674,16 @@ class PagedCache:
         vp, vs = self._rows(v, p.n_kv_heads, "v")
         if k.shape[0] != n or v.shape[0] != n:
             raise ValueError("k, v and slot_map must have as many tokens")
-        if not isinstance(positions, torch.Tensor) or not positions.is_cuda or positions.dtype != torch.int32:
+        axes = rope.n_axes
+        if not isinstance(positions, torch.Tensor) or not positions.is_cuda or positions.dtype is not torch.int32:
             raise ValueError("positions must be a CUDA tensor of torch.int32")
-        if positions.shape != (rope.n_axes, n) and not (rope.n_axes == 1 and positions.shape == (n,)):
-            raise ValueError(f"positions must be [{rope.n_axes}, {n}], got {tuple(positions.shape)}")
-        if n > 1 and positions.stride(-1) != 1:
+        if positions.shape != (axes, n) and not (axes == 1 and positions.shape == (n,)):
+            raise ValueError(f"positions must be [{axes}, {n}], got {tuple(positions.shape)}")
+        strides = positions.stride()
+        if n > 1 and strides[-1] != 1:
             raise ValueError("positions: the tokens of an axis must be contiguous")
-        ps = max(positions.stride(0), n) if positions.dim() == 2 and rope.n_axes > 1 else n
-        if rope.n_axes > 1 and positions.stride(0) < n:
+        ps = strides[0] if axes > 1 else n
+        if ps < n:
             raise ValueError("positions: the axes must not overlap")
         kg, vg = self._pages(k_pages, v_pages)
         qp = qs = op = os_ = 0
@@ -683,7 +699,7 @@ class PagedCache:
         elif q_out is not None:
             raise ValueError("q_out without q")
         _check(_lib.ice_paged_rope_append(self._h, n, rope._ref, positions.data_ptr(), ps, _int(pos_offset, "pos_offset"),
-                                          qp, qs, op, os_, kp, ks, vp, vs, sp, kg, vg, _stream()), "ice_paged_rope_append")
+                                          qp, qs, op, os_, kp, ks, vp, vs, sp, kg, vg, _stream_on(self._index)), "ice_paged_rope_append")
         return q_out
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, seq_len: torch.Tensor, block_table: torch.Tensor,
@@ -697,10 +713,10 @@ class PagedCache:
         f, n, i32, check = self._count(src, "src"), self._count(seq_len, "seq_len"), torch.int32, self._ints
         sp, dp = check(src, i32, (f,), "src"), check(dst, i32, (f,), "dst")
         lp = None if fork_len is None else check(fork_len, i32, (f,), "fork_len")
-        lens, table = check(seq_len, i32, (n,), "seq_len"), check(block_table, i32, (n, self.params.max_blocks), "block_table")
-        refs = check(page_refs, i32, (self.params.n_pages,), "page_refs")
+        lens, table = check(seq_len, i32, (n,), "seq_len"), check(block_table, i32, (n, self._columns), "block_table")
+        refs = check(page_refs, i32, (self._n_pages,), "page_refs")
         out = self._out(seq_len_out, i32, (n,), "seq_len_out")
-        _check(_lib.ice_paged_fork(self._h, f, sp, dp, lp, n, lens, table, refs, out.data_ptr(), _stream()), "ice_paged_fork")
+        _check(_lib.ice_paged_fork(self._h, f, sp, dp, lp, n, lens, table, refs, out.data_ptr(), _stream_on(self._index)), "ice_paged_fork")
         return out
 
     def tables_shared(self, seq_len: torch.Tensor, n_new: torch.Tensor, block_table: torch.Tensor,
@@ -720,15 +736,15 @@ class PagedCache:
             raise ValueError(f"n_slots = {n_slots} must be from 0 to 2^30")
         n, i32, i64, check, out = self._count(seq_len, "seq_len"), torch.int32, torch.int64, self._ints, self._out
         ins = (check(seq_len, i32, (n,), "seq_len"), check(n_new, i32, (n,), "n_new"),
-               check(block_table, i32, (n, self.params.max_blocks), "block_table"),
-               check(free_pages, i32, (self.params.n_pages,), "free_pages"),
-               check(free_state, i64, (2,), "free_state"), check(page_refs, i32, (self.params.n_pages,), "page_refs"))
+               check(block_table, i32, (n, self._columns), "block_table"),
+               check(free_pages, i32, (self._n_pages,), "free_pages"),
+               check(free_state, i64, (2,), "free_state"), check(page_refs, i32, (self._n_pages,), "page_refs"))
         outs = (out(seq_len_out, i32, (n,), "seq_len_out"), out(free_state_out, i64, (2,), "free_state_out"),
                 out(q_start, i32, (n + 1,), "q_start"), out(slot_map, i64, (n_slots,), "slot_map"),
                 out(positions, i32, (n_slots,), "positions"), out(copy_src, i32, (n,), "copy_src"),
                 out(copy_dst, i32, (n,), "copy_dst"))
         ptr = [t.data_ptr() for t in outs]
-        _check(_lib.ice_paged_tables_shared(self._h, n, *ins, *ptr[:5], n_slots, ptr[5], ptr[6], _stream()),
+        _check(_lib.ice_paged_tables_shared(self._h, n, *ins, *ptr[:5], n_slots, ptr[5], ptr[6], _stream_on(self._index)),
                "ice_paged_tables_shared")
         return outs
 
@@ -737,16 +753,29 @@ class PagedCache:
         layer's, or several layers' [layers, ...] (a layer stride is allowed)."""
         n = self._count(src, "src")
         sp, dp = self._ints(src, torch.int32, (n,), "src"), self._ints(dst, torch.int32, (n,), "dst")
-        layers, stride = 1, 0
+        layers, stride, shape = 1, 0, self._page_shape
         if isinstance(k_pages, torch.Tensor) and isinstance(v_pages, torch.Tensor) and k_pages.dim() == 5:
             layers, stride = k_pages.shape[0], k_pages.stride(0)
-            if v_pages.shape != k_pages.shape or (layers > 1 and v_pages.stride(0) != stride):
-                raise ValueError("k_pages and v_pages must have the same layers and layer stride")
             if layers < 1:
                 raise ValueError("k_pages and v_pages must hold a layer")
-            k_pages, v_pages = k_pages[0], v_pages[0]
-        kg, vg = self._pages(k_pages, v_pages)
-        _check(_lib.ice_paged_copy(self._h, n, sp, dp, layers, stride, kg, vg, _stream(stream)), "ice_paged_copy")
+            shape = (layers, *shape)
+            for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+                if t.shape != shape:
+                    raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+                if t.dtype is not self.dtype or not t.is_cuda:
+                    raise ValueError(f"{name} must be a CUDA tensor of {self.dtype}")
+                if not t.is_contiguous() and not t[0].is_contiguous():
+                    raise ValueError(f"{name}: a layer must be contiguous")
+            if layers > 1 and v_pages.stride(0) != stride:
+                raise ValueError("k_pages and v_pages must have the same layer stride")
+            kg, vg = k_pages.data_ptr(), v_pages.data_ptr()
+        else:
+            kg, vg = self._pages(k_pages, v_pages)
+        if stream is not None:
+            stream = stream.cuda_stream
+        else:
+            stream = _stream_on(self._index)
+        _check(_lib.ice_paged_copy(self._h, n, sp, dp, layers, stride, kg, vg, stream), "ice_paged_copy")
 
     def compact(self, seq_len: torch.Tensor, block_table: torch.Tensor, page_refs: torch.Tensor,
                 free_pages: torch.Tensor, free_state: torch.Tensor, extra_pages: torch.Tensor | None = None,
@@ -762,7 +791,7 @@ class PagedCache:
                 return self.compact(seq_len, block_table, page_refs, free_pages, free_state, extra_pages, n_moves, block_table_out,
                                     page_refs_out, extra_pages_out, move_src, move_dst)
         n, i32, check, out = self._count(seq_len, "seq_len"), torch.int32, self._ints, self._out
-        n_pages, columns = self.params.n_pages, self.params.max_blocks
+        n_pages, columns = self._n_pages, self._columns
         n_moves = n_pages // 2 if n_moves is None else _int(n_moves, "n_moves")
         if n_moves < 0:
             raise ValueError(f"n_moves = {n_moves} must not be below 0")
@@ -783,7 +812,7 @@ class PagedCache:
         ro = check(page_refs_out, i32, (n_pages,), "page_refs_out")
         move_src, move_dst = out(move_src, i32, (n_moves,), "move_src"), out(move_dst, i32, (n_moves,), "move_dst")
         _check(_lib.ice_paged_compact(self._h, n, lens, table, x, xp, refs, ring, state, n_moves, move_src.data_ptr(),
-                                      move_dst.data_ptr(), to, xo, ro, _stream()), "ice_paged_compact")
+                                      move_dst.data_ptr(), to, xo, ro, _stream_on(self._index)), "ice_paged_compact")
         return move_src, move_dst, block_table_out, page_refs_out, extra_pages_out
 
     def verify(self, draft_tokens: torch.Tensor, n_draft: torch.Tensor, target: torch.Tensor,
@@ -800,26 +829,28 @@ class PagedCache:
         n, i32 = self._count(n_draft, "n_draft"), torch.int32
         if not isinstance(target, torch.Tensor) or not target.is_cuda or target.dim() != 3:
             raise ValueError("target must be a CUDA tensor [requests, drafts + 1, vocab]")
-        have, rows, vocab = target.shape
+        (have, rows, vocab), (ts, tr, one) = target.shape, target.stride()
         k = rows - 1
-        if have != n or k < 0 or vocab < 1 or (target.stride(2) != 1 and vocab > 1):
+        if have != n or k < 0 or vocab < 1 or (one != 1 and vocab > 1):
             raise ValueError(f"target must be [{n}, drafts + 1, vocab] with contiguous rows, got {tuple(target.shape)}")
-        code, (ts, tr, _) = _code(target.dtype), target.stride()
-        dp, ds, dr = None, 0, 0
+        code, dp, ds, dr = _code(target.dtype), None, 0, 0
         if draft is not None:
-            if not isinstance(draft, torch.Tensor) or not draft.is_cuda or draft.dtype != target.dtype:
+            if not isinstance(draft, torch.Tensor) or not draft.is_cuda or draft.dtype is not target.dtype:
                 raise ValueError(f"draft must be a CUDA tensor of {target.dtype}")
-            if draft.shape != (n, k, vocab) or (draft.stride(2) != 1 and vocab > 1):
-                raise ValueError(f"draft must be [{n}, {k}, {vocab}] with contiguous rows, got {tuple(draft.shape)}")
+            if draft.shape != (n, k, vocab):
+                raise ValueError(f"draft must be [{n}, {k}, {vocab}], got {tuple(draft.shape)}")
+            ds, dr, one = draft.stride()
+            if one != 1 and vocab > 1:
+                raise ValueError("draft: the entries of a row must be contiguous")
             if k > 0:
-                dp, (ds, dr, _) = draft.data_ptr(), draft.stride()
+                dp = draft.data_ptr()
         check, out = self._ints, self._out
         tok, nd = check(draft_tokens, i32, (n, k), "draft_tokens"), check(n_draft, i32, (n,), "n_draft")
         up = None if uniform is None else check(uniform, torch.float32, (n, k + 1), "uniform")
         outs = (out(tokens, i32, (n, k + 1), "tokens"), out(n_accepted, i32, (n,), "n_accepted"), out(n_new, i32, (n,), "n_new"))
         a, b, c = (t.data_ptr() for t in outs)
         _check(_lib.ice_paged_verify(self._h, n, k, vocab, code, tok, nd, target.data_ptr(), ts, tr, dp, ds, dr, up, a, b, c,
-                                     _stream()), "ice_paged_verify")
+                                     _stream_on(self._index)), "ice_paged_verify")
         return outs
 
     # -- status, teardown ------------------------------------------------------------------
