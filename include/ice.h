@@ -633,7 +633,7 @@ int ice_paged_tables_shared(ice_paged* pg, int32_t n_req, const int32_t* seq_len
  * src, dst: device int32 [n]; page dst[i] becomes a copy of page src[i]. Entries with a -1 are
  *   skipped; other ids outside the pool are skipped and reported (ICE_ERR_BOUNDS). The destinations
  *   of a call are distinct, and none is a source of it.
- * k_pages, v_pages: the first layer's; layer y's begin y * layer_stride elements later
+ * k_pages, v_pages: the first layer's (of 1 to 4096); layer y's begin y * layer_stride elements later
  *   (layer_stride a multiple of 16 bytes, at least a layer's pages; not used with one layer).
  */
 int ice_paged_copy(ice_paged* pg, int32_t n, const int32_t* src, const int32_t* dst, int32_t n_layers,

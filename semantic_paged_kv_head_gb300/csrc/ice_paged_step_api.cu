@@ -168,7 +168,7 @@ int ice_paged_tables_shared(ice_paged* pg, int32_t n_req, const int32_t* seq_len
 int ice_paged_copy(ice_paged* pg, int32_t n, const int32_t* src, const int32_t* dst, int32_t n_layers,
                    int64_t layer_stride, void* k_pages, void* v_pages, void* stream) {
     ApiRange range_("ice_paged_copy");
-    if (!pg || n < 0 || n_layers < 1 || n_layers > (1 << 16)) return ICE_ERR_INVALID_ARG;
+    if (!pg || n < 0 || n_layers < 1 || n_layers > 4096) return ICE_ERR_INVALID_ARG;
     const int64_t es = es_of(pg), page = (int64_t)pg->p.n_kv_heads * pg->p.page_size * kD;
     if (n_layers == 1) layer_stride = 0;
     else if (layer_stride < page * pg->p.n_pages || layer_stride > (1LL << 45) || layer_stride * es % 16) return ICE_ERR_INVALID_ARG;
