@@ -132,14 +132,15 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
-__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+// a - b, rounded once: b times -1 is exact.
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.0f, -1.0f), a); }
 
 // Two sums of terms >= 0 with the parts that their additions cut off.
 struct Sum2 {
     float2 hi = {0.0f, 0.0f}, lo = {0.0f, 0.0f};
     __device__ __forceinline__ float2 cut(float2 d) {
-        const float2 s = add2(hi, d), t = add2(s, neg2(hi));
-        const float2 e = add2(add2(hi, neg2(add2(s, neg2(t)))), add2(d, neg2(t)));
+        const float2 s = add2(hi, d), t = sub2(s, hi);
+        const float2 e = add2(sub2(hi, sub2(s, t)), sub2(d, t));
         hi = s;
         return e;
     }
@@ -147,7 +148,7 @@ struct Sum2 {
     // max(p - q, 0) for p, q >= 0, exactly: the difference's own error is (p - d) - q where p >= q
     __device__ __forceinline__ void add_above(float2 p, float2 q) {
         p.x = fmaxf(p.x, q.x), p.y = fmaxf(p.y, q.y);
-        const float2 d = add2(p, neg2(q)), e = add2(add2(p, neg2(d)), neg2(q));
+        const float2 d = sub2(p, q), e = sub2(sub2(p, d), q);
         lo = add2(lo, add2(cut(d), e));
     }
     __device__ __forceinline__ Wide value() const {
@@ -431,20 +432,11 @@ __global__ void __launch_bounds__(kSmpThreads, 4) verify_sample_kernel(Verify a)
     if (tid == 0) w->count[0] = 0;
 }
 
-// Entry j of the greedy comparison: larger is better, of equal values the lower index. 0: nothing (NaN).
-__device__ __forceinline__ unsigned long long greedy_key(float x, int j) {
-    const unsigned b = __float_as_uint(x + 0.0f);  // -0 as 0
-    const unsigned o = b & 0x80000000u ? ~b : b | 0x80000000u;
-    return (unsigned long long)o << 32 | (0xffffffffu - (unsigned)j);
+// Order of the greedy comparison: larger is better, -0 is 0, 0 is nothing (NaN).
+__device__ __forceinline__ unsigned greedy_order(float x) {
+    const unsigned b = __float_as_uint(x + 0.0f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
-
-struct Best {
-    float x = -INFINITY;
-    int j = -1;  // none yet
-    __device__ __forceinline__ void look(float y, int at) {
-        if (y > x || (j < 0 && y == x)) x = y, j = at;
-    }
-};
 
 // The largest of 16 bytes of entries; a NaN is passed over.
 template <typename T> __device__ __forceinline__ float largest(const uint4& w);
@@ -457,6 +449,12 @@ template <> __device__ __forceinline__ float largest<__nv_bfloat16>(const uint4&
     return fmaxf(__low2float(m), __high2float(m));
 }
 
+// A lane's best entry of the tiles that it has seen: of a row's inner tiles the first 16 bytes that hold it, of its ends the index.
+struct Best {
+    float x = -INFINITY, y = -INFINITY;
+    int word = -1, j = -1;  // none yet
+};
+
 template <typename T>
 __device__ __forceinline__ void best_of_tile(const T* p, int V, int e0, Best& best) {
     const int lane = threadIdx.x & 31;
@@ -468,12 +466,7 @@ __device__ __forceinline__ void best_of_tile(const T* p, int V, int e0, Best& be
 #pragma unroll
         for (int i = 0; i < kVerVecs; ++i) {
             const float m = largest<T>(w[i]);
-            if (m > best.x || (best.j < 0 && m == best.x)) {  // rare: the index only where there is a new best
-                float v[kVec<T>];
-                unpack<T>(w[i], v);
-#pragma unroll
-                for (int j = 0; j < kVec<T>; ++j) best.look(v[j], at + i * 32 * kVec<T> + j);
-            }
+            if (m > best.x || (best.word < 0 && m == best.x)) best.x = m, best.word = at + i * 32 * kVec<T>;
         }
         return;
     }
@@ -486,9 +479,29 @@ __device__ __forceinline__ void best_of_tile(const T* p, int V, int e0, Best& be
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int j = e0 + lane + 32 * (h + i);
-            if (j >= 0 && j < V) best.look(to_f<T>(v[i]), j);
+            const float x = to_f<T>(v[i]);
+            if (j >= 0 && j < V && (x > best.y || (best.j < 0 && x == best.y))) best.y = x, best.j = j;
         }
     }
+}
+
+// The warp's best entry, order and index (the lower is the larger), 0: none. The words that hold it are looked at again for the
+// index: most words are not, and a comparison for each entry would cost more than the loads.
+template <typename T>
+__device__ __forceinline__ unsigned long long warp_best(const T* p, const Best& best) {
+    const unsigned x = best.word < 0 ? 0u : greedy_order(best.x), y = best.j < 0 ? 0u : greedy_order(best.y);
+    const unsigned top = __reduce_max_sync(0xffffffffu, max(x, y));
+    if (top == 0) return 0;
+    unsigned j = y == top ? (unsigned)best.j : 0xffffffffu;
+    if (x == top) {
+        float v[kVec<T>];
+        unpack<T>(load16<true>(reinterpret_cast<const char*>(p + best.word)), v);
+#pragma unroll
+        for (int i = kVec<T> - 1; i >= 0; --i)
+            if (v[i] == best.x && (unsigned)(best.word + i) < j) j = (unsigned)(best.word + i);
+    }
+    j = __reduce_min_sync(0xffffffffu, j);
+    return (unsigned long long)top << 32 | (0xffffffffu - j);
 }
 
 template <typename T>
@@ -510,12 +523,7 @@ __global__ void __launch_bounds__(kGrdThreads, sizeof(T) == 2 ? 12 : 8) verify_g
             const int shift = row_shift(p);
             part_of((V + shift + kTile<T> - 1) / kTile<T>, g, G, t0, t1);
             for (int t = t0; t < t1; ++t) best_of_tile(p, V, t * kTile<T> - shift, best);
-            unsigned long long k = best.j < 0 ? 0ull : greedy_key(best.x, best.j);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const unsigned long long y = __shfl_xor_sync(0xffffffffu, k, o);
-                k = y > k ? y : k;
-            }
+            const unsigned long long k = warp_best(p, best);
             if (lane == 0 && k) atomicMax(&w->best[i], k);
         }
         int last = 0;
