@@ -430,7 +430,8 @@ typedef struct ice_paged_params {
 
 /* ice_paged_create - a handle for the current device. Allocates the scratch of
  * the attention: 520 bytes for each of max(3 R, min(128 R, 262144)) partial rows
- * with R = max_tokens * n_q_heads (ICE_ERR_CAPACITY if that fails). */
+ * with R = max_tokens * n_q_heads, and 2824 bytes a request for ice_paged_verify
+ * (ICE_ERR_CAPACITY if that fails). */
 int ice_paged_create(const ice_paged_params* params, ice_paged** out);
 
 /* ice_paged_destroy - waits for the device, then frees the handle. */

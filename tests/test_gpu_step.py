@@ -173,6 +173,29 @@ def test_rope_bad_slots(ice):
     _rope_check(c, False, 0, *got)
 
 
+def test_rope_in_a_large_pool(ice):
+    """Rows whose offsets in the pages pass 2^32 elements, and rows of q, k and v that far apart."""
+    n_pages, stride = 131500, 1 << 30
+    pc = _cache(ice, n_kv_heads=4, n_q_heads=4, page_size=64, n_pages=n_pages)
+    kp, vp = pc.new_pages()
+    c = _rope_case(1, BF16, 6, 4, 1, 64, 64, 1)
+    c["slots"] = torch.tensor([n_pages * 64 - 1, 0, 131072 * 64 + 5, -1, 7, 9])
+    rows = torch.empty(5 * stride + 3 * 512, dtype=BF16, device="cuda")
+    q, k, v = (torch.as_strided(rows, (6, 4, D), (stride, D, 1), i * 512) for i in range(3))
+    for name, x in (("q", q), ("k", k), ("v", v)):
+        x.copy_(c[name])
+    assert pc.rope_append(q, k, v, c["pos"].cuda(), ice.Rope(c["freq"]), c["slots"].cuda(), kp, vp, q_out=q) is q
+    assert pc.get_error() == 0
+    for i, slot in enumerate(c["slots"].tolist()):
+        for x, name, pool in ((q, "q", None), (k, "k", kp), (v, "v", vp)):
+            got = x[i] if pool is None else pool[slot // 64, :, slot % 64]
+            if slot < 0:
+                assert torch.equal(x[i].cpu(), c[name][i])  # as it was
+                continue
+            want, tol = plain_rope(c[name][i:i + 1], c["pos"][:, i:i + 1], 0, c["freq"], c["axis"], False)
+            assert torch.equal(got.cpu(), c[name][i]) if name == "v" else bool(((got.cpu().double() - want[0]).abs() <= tol[0]).all())
+
+
 def test_rope_without_turns_is_append(ice):
     c = _rope_case(9, BF16, 100, 8, 4, 16, 64, 1)
     c["freq"] = [0.0] * 64
@@ -674,6 +697,20 @@ def test_verify_strided(ice, mode, dtype, shift):
     c[2], c[3] = spread(c[2], V + 3, (K + 1) * (V + 3) + 1), spread(c[3], V + 1, K * (V + 1) + 2)
     pc, got = _verify_run(ice, c)
     _verify_check(ice, c, got, pc.get_error())
+
+
+@pytest.mark.parametrize("mode", ["sample", "greedy"])
+def test_verify_rows_far_apart(ice, mode):
+    """Rows whose offsets pass 2^32 elements."""
+    n, K, V = 2, 1, 3001
+    c = _verify_case(9, mode, BF16, n, K, V)
+    c[1][:] = 1
+    big = torch.empty((1 << 32) + (1 << 30) + 4 * V, dtype=BF16, device="cuda")
+    far = torch.as_strided(big, (n, K + 1, V), (1 << 32, (1 << 30) + 1, 1), 3)
+    far.copy_(c[2])
+    pc = _cache(ice, n_kv_heads=1, n_q_heads=1, n_pages=1, max_requests=n, max_blocks=1, max_tokens=1)
+    got = pc.verify(c[0].cuda(), c[1].cuda(), far, None if c[3] is None else c[3].cuda(), None if c[4] is None else c[4].cuda())
+    _verify_check(ice, c, [x.cpu() for x in got], pc.get_error())
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
