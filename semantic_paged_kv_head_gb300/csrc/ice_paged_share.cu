@@ -198,7 +198,7 @@ __device__ __forceinline__ void share_claim(const SharedTables& a, int warp, int
             }))
             bad |= kBadBounds;
         if (bad) atomicOr(&a.w.head->flags, bad);
-        if (piece == 0 && (threadIdx.x & 31) == 0) a.w.req[r] = make_int4(max(q.new_len - q.old_len, 0), max(q.has - q.had, 0), 0, 0);
+        if (piece == 0 && (threadIdx.x & 31) == 0) a.w.req[r] = make_int4(max(q.new_len - q.old_len, 0), max(q.has - q.had, 0), 0, q.grows ? kReqKeeps : 0);
     }
 }
 
@@ -223,7 +223,7 @@ __device__ __forceinline__ void share_count(const SharedTables& a, int warp, int
         if (bad) atomicOr(&a.w.head->flags, kBadBounds);
         mine = __reduce_add_sync(0xffffffffu, mine);
         if ((threadIdx.x & 31) == 0) {
-            if (q.grows && piece == 0 && !mine) a.w.req[r].w = 1;
+            if (q.grows && piece == 0 && !mine) a.w.req[r].w = kReqCopies;
             if (!q.grows && mine) atomicAdd(&a.w.req[r].z, mine);
         }
     }
@@ -242,18 +242,22 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
     const int flags = __ldcg(&a.w.head->flags);
     const int per = (n + NT - 1) / NT, r0 = min(tid * per, n), r1 = min(r0 + per, n);
     unsigned x[3] = {0, 0, 0}, tot[3];
-    auto copied = [&](int r) { return __ldcg(&a.w.req[r].w); };
-    auto add = [&](int r) {
-        const int4 c = __ldcg(a.w.req + r);
-        x[0] += c.x;
-        x[1] += c.y + c.w;
-        x[2] += c.z;
-    };
+    auto copied = [&](int r) { return (int)(__ldcg(&a.w.req[r].w) == kReqCopies); };
+    constexpr int kPer = kPagedMaxRequests / NT;
+    int4 c[kPer];  // this thread's requests, all asked for at once
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int r = r0 + k;
+        c[k] = make_int4(0, 0, 0, 0);
+        if (r < r1) c[k] = __ldcg(a.w.req + r);
+    }
     bool over = false;
     if (!flags) {
-#pragma unroll 4
-        for (int r = r0; r < r1; ++r) {
-            add(r);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            x[0] += c[k].x;
+            x[1] += c[k].y + (c[k].w == kReqCopies);
+            x[2] += c[k].z;
             over |= (x[0] | x[1] | x[2]) >> 31;  // each term is below 2^31: seen before a sum can wrap
         }
     }
@@ -268,12 +272,16 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
     const bool ok = code == ICE_OK;
     const int n_tok = ok ? (int)tot[0] : 0, n_pop = ok ? (int)tot[1] : 0, n_push = ok ? (int)tot[2] : 0;
     if (ok) {
-#pragma unroll 4
-        for (int r = r0; r < r1; ++r) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int r = r0 + k;
+            if (r >= r1) break;
             tok_cum[r] = (int)x[0];
             pop_cum[r] = (int)x[1];
             push_cum[r] = (int)x[2];
-            add(r);
+            x[0] += c[k].x;
+            x[1] += c[k].y + (c[k].w == kReqCopies);
+            x[2] += c[k].z;
         }
     }
     if (tid == 0) {
@@ -290,12 +298,9 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
     const int first = blockIdx.x * NT + tid, step = gridDim.x * NT;
     for (int r = first; r <= n; r += step) a.q_start[r] = ok ? tok_cum[r] : 0;
     for (int r = first; r < n; r += step) {
-        const bool copies = ok && copied(r);
-        if (!copies) a.copy_src[r] = a.copy_dst[r] = -1;
-        if (ok && !copies) {
-            const ShareReq q = share_req(a, r);
-            if (q.grows) a.page_refs[a.block_table[(long long)r * a.max_blocks + q.had - 1]] = 1;  // kept, nobody else's
-        }
+        const int kind = ok ? __ldcg(&a.w.req[r].w) : 0;
+        if (kind != kReqCopies) a.copy_src[r] = a.copy_dst[r] = -1;
+        if (kind == kReqKeeps) a.page_refs[a.block_table[(long long)r * a.max_blocks + (a.seq_len[r] - 1) / P]] = 1;  // nobody else's
     }
     const bool wide = ((uintptr_t)a.slot_map & 15) == 0 && ((uintptr_t)a.positions & 15) == 0;
     for (long long i4 = (long long)first * kShrSlots; i4 < a.n_slots; i4 += (long long)step * kShrSlots) {
@@ -712,7 +717,7 @@ __global__ void __launch_bounds__(kCpyThreads) page_copy_kernel(int n, const int
             uint4 v[kCpyBatch];
 #pragma unroll
             for (int k = 0; k < kCpyBatch; ++k)
-                if (at + 32 * k < page_vecs) v[k] = __ldcs(from + at + 32 * k);
+                if (at + 32 * k < page_vecs) v[k] = __ldg(from + at + 32 * k);
 #pragma unroll
             for (int k = 0; k < kCpyBatch; ++k)
                 if (at + 32 * k < page_vecs) to[at + 32 * k] = v[k];
@@ -724,8 +729,9 @@ cudaError_t launch_page_copy(int n, const int* src, const int* dst, int n_layers
                              long long n_pages, void* k_pages, void* v_pages, int* status, cudaStream_t s) {
     const int page_vecs = (int)(page_bytes / 16);
     const long long pieces = (page_vecs + 32 * kCpyBatch - 1) / (32 * kCpyBatch), units = n_layers * 2 * pieces;
-    const int x = std::min(n, 152 * 8);
-    const int y = (int)std::max<long long>(1, std::min<long long>(152 * 8 / x, (units + 7) / 8));
+    const int most = 152 * 64;  // blocks of few pieces: the last ones end together (152 * 8: 32768 pages' moves 172 us, with these 158)
+    const int x = std::min(n, most);
+    const int y = (int)std::max<long long>(1, std::min<long long>(most / x, (units + 7) / 8));
     return launch_pdl(page_copy_kernel, dim3(x, y), dim3(kCpyThreads), 0, s, n, src, dst, n_layers, layer_bytes / 16, page_vecs,
                       n_pages, (uint4*)k_pages, (uint4*)v_pages, status);
 }

@@ -17,10 +17,13 @@ static_assert(sizeof(ShareHead) == 64, "claims begin at a multiple of 8 bytes");
 enum { kBadBounds = 1, kBadCapacity = 2 };
 constexpr int kCmpChunk = 1024;  // pages that a block of a compaction counts at once
 
+// what becomes of the page that a request writes into: kept, or copied
+enum { kReqKeeps = 2, kReqCopies = 1 };
+
 struct ShareScratch {
     ShareHead* head;
     unsigned long long* claim;  // [n_pages]
-    int4* req;                  // [max_requests] of a step: new tokens, pages more, pages given back, 1 if its last page is copied
+    int4* req;                  // [max_requests] of a step: new tokens, pages more, pages given back, kReq*
     int* count;                 // [ceil(n_pages / kCmpChunk)] of a compaction: pages in use
 };
 
