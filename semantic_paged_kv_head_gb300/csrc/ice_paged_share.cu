@@ -229,7 +229,10 @@ __device__ __forceinline__ void share_count(const SharedTables& a, int warp, int
     }
 }
 
-template <int NT>
+__host__ __device__ constexpr size_t share_smem(int n) { return (size_t)(n + 1) * 17; }
+
+// CLUSTER: the grid is one cluster
+template <int NT, bool CLUSTER>
 __device__ __forceinline__ void share_fill(const SharedTables& a) {
     extern __shared__ int shr_smem[];
     __shared__ TabSums sums;
@@ -238,19 +241,25 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
     int* tok_cum = shr_smem;           // [n + 1] new tokens before each request
     int* pop_cum = tok_cum + n + 1;    // [n + 1] pages taken
     int* push_cum = pop_cum + n + 1;   // [n + 1] pages given back
+    int* old_len = push_cum + n + 1;   // [n] tokens
+    unsigned char* kinds = reinterpret_cast<unsigned char*>(old_len + n);  // [n] kReq*
     const long long head = a.free_state[0], tail = a.free_state[1], n_pages = a.n_pages;
+    const unsigned long long epoch = a.w.head->epoch;
     const int flags = __ldcg(&a.w.head->flags);
     const int per = (n + NT - 1) / NT, r0 = min(tid * per, n), r1 = min(r0 + per, n);
     unsigned x[3] = {0, 0, 0}, tot[3];
-    auto copied = [&](int r) { return (int)(__ldcg(&a.w.req[r].w) == kReqCopies); };
+    int turns = 0;
+    auto copied = [&](int r) { return (int)(kinds[r] == kReqCopies); };
     constexpr int kPer = kPagedMaxRequests / NT;
     int4 c[kPer];  // this thread's requests, all asked for at once
+    int had[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const int r = r0 + k;
         c[k] = make_int4(0, 0, 0, 0);
-        if (r < r1) c[k] = __ldcg(a.w.req + r);
+        if (r < r1) c[k] = __ldcg(a.w.req + r), had[k] = a.seq_len[r];
     }
+    const int hm = head >= 0 ? (int)(head % n_pages) : 0, tm = tail >= 0 ? (int)(tail % n_pages) : 0;
     bool over = false;
     if (!flags) {
 #pragma unroll
@@ -279,6 +288,8 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
             tok_cum[r] = (int)x[0];
             pop_cum[r] = (int)x[1];
             push_cum[r] = (int)x[2];
+            old_len[r] = had[k];
+            kinds[r] = (unsigned char)c[k].w;
             x[0] += c[k].x;
             x[1] += c[k].y + (c[k].w == kReqCopies);
             x[2] += c[k].z;
@@ -290,18 +301,14 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
         push_cum[n] = n_push;
     }
     __syncthreads();
-    const int hm = ok ? (int)(head % n_pages) : 0, tm = ok ? (int)(tail % n_pages) : 0;
     auto ring = [&](int base, int j) {  // base, j < n_pages < 2^31: the sum may pass 2^31
         const long long p = (long long)base + j;
         return (int)(p < n_pages ? p : p - n_pages);
     };
-    const int first = blockIdx.x * NT + tid, step = gridDim.x * NT;
-    for (int r = first; r <= n; r += step) a.q_start[r] = ok ? tok_cum[r] : 0;
-    for (int r = first; r < n; r += step) {
-        const int kind = ok ? __ldcg(&a.w.req[r].w) : 0;
-        if (kind != kReqCopies) a.copy_src[r] = a.copy_dst[r] = -1;
-        if (kind == kReqKeeps) a.page_refs[a.block_table[(long long)r * a.max_blocks + (a.seq_len[r] - 1) / P]] = 1;  // nobody else's
-    }
+    // The jobs below are independent. Each begins at another block, so that short ones run side by side.
+    const int step = gridDim.x * NT;
+    int first = blockIdx.x * NT + tid;
+    auto turn = [&]() { first = (int)((blockIdx.x + (gridDim.x + 3) / 4 * ++turns) % gridDim.x) * NT + tid; };
     const bool wide = ((uintptr_t)a.slot_map & 15) == 0 && ((uintptr_t)a.positions & 15) == 0;
     for (long long i4 = (long long)first * kShrSlots; i4 < a.n_slots; i4 += (long long)step * kShrSlots) {
         const int i0 = (int)i4;
@@ -323,7 +330,7 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
                 if (k == 0 || i >= next) {
                     while (tok_cum[r + 1] <= i) ++r;
                     b = tok_cum[r], next = tok_cum[r + 1];
-                    const int o = a.seq_len[r], p = o + i - b;
+                    const int o = old_len[r], p = o + i - b;
                     // a page that is copied is the first of those taken
                     held = (o + P - 1) / P - copied(r);
                     pg = p / P;
@@ -352,10 +359,11 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
                 }
         }
     }
+    turn();
     for (int j = first; j < n_pop; j += step) {
+        const int p = a.free_pages[ring(hm, j)];
         const int r = find_row(pop_cum, n, j), k = j - pop_cum[r], copies = copied(r);
-        const int had = (a.seq_len[r] + P - 1) / P, p = a.free_pages[ring(hm, j)];
-        int* e = a.block_table + (long long)r * a.max_blocks + had - copies + k;
+        int* e = a.block_table + (long long)r * a.max_blocks + (old_len[r] + P - 1) / P - copies + k;
         if (copies && k == 0) {
             a.copy_src[r] = *e;
             a.copy_dst[r] = p;
@@ -364,7 +372,14 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
         if (p >= 0 && p < n_pages) a.page_refs[p] = 1;
         else set_status(a.status, ICE_ERR_BOUNDS);  // an id in the ring that is no page's
     }
-    const unsigned long long epoch = a.w.head->epoch;
+    turn();
+    for (int r = first; r <= n; r += step) a.q_start[r] = ok ? tok_cum[r] : 0;
+    for (int r = first; r < n; r += step) {
+        const int kind = ok ? kinds[r] : 0;
+        if (kind != kReqCopies) a.copy_src[r] = a.copy_dst[r] = -1;
+        if (kind == kReqKeeps) a.page_refs[a.block_table[(long long)r * a.max_blocks + (old_len[r] - 1) / P]] = 1;  // nobody else's
+    }
+    turn();
     const int pieces = share_pieces(a);
     if (!ok) {  // the claims taken back
         for (long long y = first >> 5; y < (long long)n * pieces; y += step >> 5) {
@@ -409,14 +424,19 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
             }
         }
     }
-    // the last block to come here: every block has read the lengths, the ring's state and the flags
-    __syncthreads();
-    if (tid == 0) {
-        __threadfence();
-        s_last = gridDim.x == 1 || atomicAdd(&a.w.head->ticket, 1u) == gridDim.x - 1;
+    // last, when every block has read the lengths, the ring's state and the flags: what may replace them
+    if (CLUSTER) {
+        cg::this_cluster().sync();
+        if (blockIdx.x != 0) return;
+    } else {
+        __syncthreads();
+        if (tid == 0) {
+            __threadfence();
+            s_last = gridDim.x == 1 || atomicAdd(&a.w.head->ticket, 1u) == gridDim.x - 1;
+        }
+        __syncthreads();
+        if (!s_last) return;
     }
-    __syncthreads();
-    if (!s_last) return;
     for (int r = tid; r < n; r += NT) a.seq_len_out[r] = ok ? a.seq_len[r] + a.n_new[r] : a.seq_len[r];
     if (tid == 0) {
         a.free_state_out[0] = head + n_pop;
@@ -440,7 +460,7 @@ __global__ void __launch_bounds__(kShrGridThreads) share_count_kernel(SharedTabl
 
 __global__ void __launch_bounds__(kShrThreads) share_fill_kernel(SharedTables a) {
     pdl_wait_then_release();
-    share_fill<kShrThreads>(a);
+    share_fill<kShrThreads, false>(a);
 }
 
 // The blocks of one cluster; its barrier orders their writes.
@@ -452,11 +472,11 @@ __global__ void __launch_bounds__(kShrThreads) share_step_kernel(SharedTables a)
     cl.sync();
     share_count(a, warp, warps);
     cl.sync();
-    share_fill<kShrThreads>(a);
+    share_fill<kShrThreads, true>(a);
 }
 
 cudaError_t launch_shared_tables(const SharedTables& a, cudaStream_t s) {
-    const size_t smem = (size_t)(a.n + 1) * 12;
+    const size_t smem = share_smem(a.n);
     // one cluster where its 256 warps have few requests each, few slots, and few pages to give back whatever the lengths
     if (a.n <= 1024 && a.n_slots <= 65536 && (long long)a.n * a.max_blocks <= 1 << 19)
         return launch_cluster(share_step_kernel, kShrCluster, kShrThreads, smem, s, a);
@@ -737,7 +757,8 @@ cudaError_t launch_page_copy(int n, const int* src, const int* dst, int n_layers
 }
 
 cudaError_t share_prepare() {
-    cudaError_t e = cudaFuncSetAttribute(share_fill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kPagedMaxRequests + 1) * 12);
+    cudaError_t e = cudaFuncSetAttribute(share_fill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)share_smem(kPagedMaxRequests));
     return e;
 }
 
