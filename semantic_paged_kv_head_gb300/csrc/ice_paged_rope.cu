@@ -19,11 +19,11 @@ namespace ice {
 // written once; six groups of four rows are under way together with bf16, two with fp32. Where tokens are few, `parts` warps share
 // the rows of a token.
 //
-// Bound by memory: 32768 tokens of 32 query and 8 KV heads in bf16 123 us, 6.5 TB/s of read and write (96 % of the measured copy
-// rate; three groups under way: 127); 30000 tokens of 8 + 4 heads in fp32 80.8 us (90 %); 64 tokens 3.3 us, the launch and two
-// dependent loads.
+// Bound by memory: 32768 tokens of 32 query and 8 KV heads in bf16 121.5 us, 6.6 TB/s of read and write (98 % of the measured copy
+// rate; three groups under way and blocks of 256 threads: 127); 30000 tokens of 8 + 4 heads in fp32 79.0 us (92 %); 64 tokens
+// 3.1 us, the launch and two dependent loads.
 // ---------------------------------------------------------------------------
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 64, kRopeWarps = kRopeThreads / 32;  // small blocks: an SM that has ended one takes another
 constexpr int kRopePairs = 64;
 
 template <typename T> constexpr int kRopeBatch = sizeof(T) == 2 ? 6 : 2;  // groups of four rows under way together
@@ -72,7 +72,7 @@ template <typename T, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeAppend a) {
     constexpr int W = sizeof(T) == 2 ? 1 : 2;   // 16-byte words of a piece
     constexpr int U = kRopeBatch<T>;
-    __shared__ float2 s_cs[kRopeThreads / 32][kRopePairs];
+    __shared__ float2 s_cs[kRopeWarps][kRopePairs];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = lane >> 3, l = lane & 7;
     float2* cs = s_cs[warp];
@@ -96,8 +96,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeAppend a)
     }
     const int rows = a.Hq + 2 * a.H, groups = (rows + 3) >> 2;
     pdl_wait_then_release();
-    const int nw = gridDim.x * (kRopeThreads / 32) / a.parts;  // warps that a part of the tokens' rows has
-    const int w = blockIdx.x * (kRopeThreads / 32) + warp;
+    const int nw = gridDim.x * (kRopeWarps) / a.parts;  // warps that a part of the tokens' rows has
+    const int w = blockIdx.x * (kRopeWarps) + warp;
     const int part = w % a.parts;
     if (w / a.parts >= nw) return;  // a rest of warps that makes no whole token
     for (long long t = w / a.parts; t < a.n_tokens; t += nw) {
@@ -214,7 +214,8 @@ cudaError_t launch_rope_append(RopeAppend a, const ice_rope& r, int dtype, cudaS
     const int groups = (a.Hq + 2 * a.H + 3) / 4;
     a.parts = (int)std::max<long long>(1, std::min<long long>(groups, 152LL * 16 / a.n_tokens));
     const long long warps = (long long)a.n_tokens * a.parts;
-    const int blocks = (int)std::min<long long>((warps + 7) / 8, std::max(152 * 16, (a.parts + 7) / 8));
+    const long long most = std::max(152 * 64, (a.parts + kRopeWarps - 1) / kRopeWarps);
+    const int blocks = (int)std::min((warps + kRopeWarps - 1) / kRopeWarps, most);
     const dim3 grid(blocks), block(kRopeThreads);
     if (dtype == ICE_BF16)
         return launch_pdl(r.interleaved ? rope_append_kernel<__nv_bfloat16, true> : rope_append_kernel<__nv_bfloat16, false>, grid,
