@@ -96,8 +96,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeAppend a)
     }
     const int rows = a.Hq + 2 * a.H, groups = (rows + 3) >> 2;
     pdl_wait_then_release();
-    const int nw = gridDim.x * (kRopeWarps) / a.parts;  // warps that a part of the tokens' rows has
-    const int w = blockIdx.x * (kRopeWarps) + warp;
+    const int nw = gridDim.x * kRopeWarps / a.parts;  // warps that a part of the tokens' rows has
+    const int w = blockIdx.x * kRopeWarps + warp;
     const int part = w % a.parts;
     if (w / a.parts >= nw) return;  // a rest of warps that makes no whole token
     for (long long t = w / a.parts; t < a.n_tokens; t += nw) {

@@ -28,7 +28,7 @@ struct Verify {
     int *out, *accepted, *n_new, *status;
     VerifyScratch* scratch;  // [n_req]
     int n_req, K, V;
-    int groups;  // of a row
+    int groups, blocks;  // of a row; sampling: blocks of a request
 };
 
 cudaError_t launch_verify(const Verify& a, int dtype, cudaStream_t s);
