@@ -454,56 +454,66 @@ template <> __device__ __forceinline__ float largest<__nv_bfloat16>(const uint4&
     return fmaxf(__low2float(m), __high2float(m));
 }
 
-// A lane's best entry of the tiles that it has seen: of a row's inner tiles the first 16 bytes that hold it, of its ends the index.
+// 16 bytes of entries from element `at` on, where some of them may lie outside the row: those are `fill`.
+template <typename T>
+__device__ __forceinline__ uint4 load_end(const T* p, int at, int V, unsigned fill) {
+    if (at >= 0 && at + kVec<T> <= V) return load16<true>(reinterpret_cast<const char*>(p + at));
+    unsigned w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = fill;
+#pragma unroll
+        for (int j = 0; j < kVec<T> / 4; ++j) {
+            const int k = at + i * (kVec<T> / 4) + j;
+            if (k < 0 || k >= V) continue;
+            if (sizeof(T) == 4) {
+                w[i] = reinterpret_cast<const unsigned*>(p)[k];
+            } else {
+                const unsigned x = reinterpret_cast<const unsigned short*>(p)[k];
+                w[i] = j ? (w[i] & 0xffffu) | x << 16 : (w[i] & 0xffff0000u) | x;
+            }
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A lane's best entry of the tiles that it has seen, and the first 16 bytes that hold it.
 struct Best {
-    float x = -INFINITY, y = -INFINITY;
-    int word = -1, j = -1;  // none yet
+    float x = -INFINITY;
+    int word = INT_MIN;  // none yet
 };
 
-template <typename T>
+constexpr unsigned kNothing = 0x7fff7fffu;  // NaN, of either type
+
+template <typename T, bool INSIDE>
 __device__ __forceinline__ void best_of_tile(const T* p, int V, int e0, Best& best) {
-    const int lane = threadIdx.x & 31;
-    if (e0 >= 0 && e0 + kTile<T> <= V) {
-        const int at = e0 + lane * kVec<T>;
-        uint4 w[kVerVecs];
+    const int at = e0 + (threadIdx.x & 31) * kVec<T>;
+    uint4 w[kVerVecs];
 #pragma unroll
-        for (int i = 0; i < kVerVecs; ++i) w[i] = load16<true>(reinterpret_cast<const char*>(p + at + i * 32 * kVec<T>));
-#pragma unroll
-        for (int i = 0; i < kVerVecs; ++i) {
-            const float m = largest<T>(w[i]);
-            if (m > best.x || (best.word < 0 && m == best.x)) best.x = m, best.word = at + i * 32 * kVec<T>;
-        }
-        return;
+    for (int i = 0; i < kVerVecs; ++i) {
+        const int k = at + i * 32 * kVec<T>;
+        w[i] = INSIDE ? load16<true>(reinterpret_cast<const char*>(p + k)) : load_end(p, k, V, kNothing);
     }
-    // a row's ends, as in add_tile
-#pragma unroll 1
-    for (int h = 0; h < kTile<T> / 32; h += 8) {
-        T v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = p[min(max(e0 + lane + 32 * (h + i), 0), V - 1)];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int j = e0 + lane + 32 * (h + i);
-            const float x = to_f<T>(v[i]);
-            if (j >= 0 && j < V && (x > best.y || (best.j < 0 && x == best.y))) best.y = x, best.j = j;
-        }
+    for (int i = 0; i < kVerVecs; ++i) {
+        const float m = largest<T>(w[i]);
+        if (m > best.x || (best.word == INT_MIN && m == best.x)) best.x = m, best.word = at + i * 32 * kVec<T>;
     }
 }
 
 // The warp's best entry, order and index (the lower is the larger), 0: none. The words that hold it are looked at again for the
 // index: most words are not, and a comparison for each entry would cost more than the loads.
 template <typename T>
-__device__ __forceinline__ unsigned long long warp_best(const T* p, const Best& best) {
-    const unsigned x = best.word < 0 ? 0u : greedy_order(best.x), y = best.j < 0 ? 0u : greedy_order(best.y);
-    const unsigned top = __reduce_max_sync(0xffffffffu, max(x, y));
+__device__ __forceinline__ unsigned long long warp_best(const T* p, int V, const Best& best) {
+    const unsigned x = best.word == INT_MIN ? 0u : greedy_order(best.x), top = __reduce_max_sync(0xffffffffu, x);
     if (top == 0) return 0;
-    unsigned j = y == top ? (unsigned)best.j : 0xffffffffu;
+    unsigned j = 0xffffffffu;
     if (x == top) {
         float v[kVec<T>];
-        unpack<T>(load16<true>(reinterpret_cast<const char*>(p + best.word)), v);
+        unpack<T>(load_end(p, best.word, V, kNothing), v);
 #pragma unroll
         for (int i = kVec<T> - 1; i >= 0; --i)
-            if (v[i] == best.x && (unsigned)(best.word + i) < j) j = (unsigned)(best.word + i);
+            if (v[i] == best.x) j = (unsigned)(best.word + i);
     }
     j = __reduce_min_sync(0xffffffffu, j);
     return (unsigned long long)top << 32 | (0xffffffffu - j);
@@ -527,8 +537,12 @@ __global__ void __launch_bounds__(kGrdThreads, sizeof(T) == 2 ? 12 : 8) verify_g
             int t0, t1;
             const int shift = row_shift(p);
             part_of((V + shift + kTile<T> - 1) / kTile<T>, g, G, t0, t1);
-            for (int t = t0; t < t1; ++t) best_of_tile(p, V, t * kTile<T> - shift, best);
-            const unsigned long long k = warp_best(p, best);
+            for (int t = t0; t < t1; ++t) {
+                const int e0 = t * kTile<T> - shift;
+                if (e0 >= 0 && e0 + kTile<T> <= V) best_of_tile<T, true>(p, V, e0, best);
+                else best_of_tile<T, false>(p, V, e0, best);
+            }
+            const unsigned long long k = warp_best(p, V, best);
             if (lane == 0 && k) atomicMax(&w->best[i], k);
         }
         int last = 0;
