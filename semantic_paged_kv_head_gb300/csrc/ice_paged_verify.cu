@@ -20,10 +20,17 @@ namespace ice {
 // the sum in the handle's scratch, and the last block of a request to have done so draws the token: the part by the
 // sums, then that part again, its tiles and at last the elements of a tile.
 //
-// Greedy: a row is cut into groups of tiles, a warp each; it leaves its group's best entry
-// in the scratch and counts it; the warp that counts the last group of a request's last row ends the request. Groups are
-// handed out row by row, all requests' first rows first; a warp skips its group when a draft before that row is
-// known not to stay, which changes what is read but not the result.
+// Greedy: a row is cut into groups of tiles, a warp each; it leaves its group's best entry in the scratch and counts it; the
+// warp that counts the last group of a request's last row ends the request. Groups are handed out row by row, all requests' first
+// rows first; a warp skips its group when a draft before that row is known not to stay, which changes what is read but
+// not the result.
+//
+// Measured: one request of four drafts on 128000 fp32 entries 7.3 us, three loads that depend on each other, the
+// count, and the search. 64 requests of up to seven 18 us (57 MB: 3.1 TB/s; the same fixed parts around one wave of loads);
+// 200 of two 38 us. Greedy, 128 requests of up to four drafts on 150001 bf16 entries 29.7 us, of which 136 MB are read where 94 are
+// needed (rows of the next draft are under way before the verdict on this one); 512 of one draft 45 us, 5.8 TB/s.
+// A thread-block cluster a request took 16 us for the 64 and 22 for 256 looked-up requests (18 here), and 61 for the
+// greedy ones, whose rows it read one after the other.
 // ---------------------------------------------------------------------------
 constexpr int kSmpThreads = 256, kSmpWarps = kSmpThreads / 32;
 constexpr int kGrdThreads = 128, kGrdWarps = kGrdThreads / 32;
