@@ -196,11 +196,18 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeAppend a)
     }
 }
 
-// f 2^64 / 2 pi modulo 2^64
+// f 2^64 / 2 pi modulo 2^64. A quotient in 53 bits would be off by up to 2^-23 turns at a position of 2^31, so what the division
+// cuts off is added.
 static unsigned long long turns(double f) {
-    double t = f / 6.283185307179586476925;
-    t -= std::floor(t);  // [0, 1]
-    return t >= 1.0 ? 0ull : (unsigned long long)std::ldexp(t, 64);
+    const double c = 6.283185307179586, c_lo = 2.4492935982947064e-16;  // 2 pi to 106 bits
+    const double t = f / c, rest = (std::fma(-t, c, f) - t * c_lo) / c;
+    // whole turns dropped, exactly; a magnitude below 1 fits 64 bits
+    auto bits = [](double x) {
+        const double y = std::fmod(x, 1.0);
+        const unsigned long long b = (unsigned long long)std::ldexp(std::fabs(y), 64);
+        return y < 0.0 ? 0ull - b : b;
+    };
+    return bits(t) + bits(rest);
 }
 
 cudaError_t launch_rope_append(RopeAppend a, const ice_rope& r, int dtype, cudaStream_t s) {

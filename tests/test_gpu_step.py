@@ -4,6 +4,7 @@ of all of them as a loop of speculative decoding uses them."""
 import ctypes
 import math
 import random
+from fractions import Fraction
 
 import pytest
 import torch
@@ -133,6 +134,35 @@ def test_rope_far_positions(ice, pos, offset):
     _rope_check(c, False, offset, *got)
     if pos + offset == 0:  # no turn: as it was
         assert torch.equal(got[0], c["q"])
+
+
+TURN = Fraction("6.2831853071795864769252867665590057683943387987502116419498891846156")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("pos,offset", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (-2 ** 31, -2 ** 31), (1234567891, 7), (120001, 40000)])
+def test_rope_far_angles_to_the_last_bits(ice, dtype, pos, offset):
+    """Angles in exact fractions: no part of the tolerance grows with the position."""
+    c = _rope_case(9, dtype, 3, 2, 2, 16, 64, 1)
+    c["pos"].fill_(pos)
+    c["freq"] = [1.0, 0.5, -0.25, 3.0, 6.5, 0.0, 1e-9, math.pi, 1e-3, -1e-5, 0.1, 1e6, -1e15, 1e300, 2.0 ** -60, 5e-324] + c["freq"][16:]
+    pc, *got = _rope_run(ice, c, offset=offset)
+    assert pc.get_error() == 0
+    # more than two turns a position have no use: those pairs only have to stay turns
+    known = torch.tensor([abs(f) < 10 for f in c["freq"]])
+    near = torch.tensor([float(Fraction(f) * (pos + offset) % TURN) for f in c["freq"]], dtype=torch.float64)
+    keys = got[1].transpose(1, 2).reshape(-1, 2, D)[c["slots"]]
+    for have, x in ((got[0], c["q"]), (keys, c["k"])):
+        a, b = x.double()[..., :64], x.double()[..., 64:]
+        want = torch.cat([a * near.cos() - b * near.sin(), b * near.cos() + a * near.sin()], 2)
+        u = 2.0 ** -8 if dtype == BF16 else 2.0 ** -24
+        # the fraction of a turn in 32 bits and in fp32, the functions, two products and their sum, the output; the
+        # frequency in 2^-64 turns, 2^-63 of a turn over 2^32 positions at most: 2 pi 2^-31
+        err = 2 * math.pi * (2.0 ** -33 + 2.0 ** -31) + math.pi * 2.0 ** -25 + 2.0 ** -22 + 2 * 2.0 ** -24
+        tol = err * (a.abs() + b.abs()).repeat(1, 1, 2) + u * want.abs()
+        assert bool((((have.double() - want).abs() <= tol) | ~known.repeat(2)).all())
+        size, size0 = torch.hypot(have.double()[..., :64], have.double()[..., 64:]), torch.hypot(a, b)
+        assert bool(((size - size0).abs() <= 4 * (err + u) * size0).all())
 
 
 def test_rope_keys_alone(ice):
