@@ -582,8 +582,8 @@ int ice_paged_rope_append(ice_paged* pg, int32_t n_tokens, const ice_rope* rope,
  * on by ice_paged_tables_shared; ice_paged_tables knows nothing of counts and is not to be
  * used with such a pool.
  *
- * The first of these calls on a handle allocates their scratch (8 bytes a page, 16 a request;
- * ICE_ERR_CAPACITY if that fails). A call that would have to allocate while its stream is
+ * The first of these calls on a handle allocates their scratch (8 bytes a page, 16 a request
+ * and a bit an entry of the block tables; ICE_ERR_CAPACITY if that fails). A call that would have to allocate while its stream is
  * captured returns ICE_ERR_INVALID_ARG: make one eager call before.
  */
 

@@ -126,24 +126,29 @@ cudaError_t launch_fork(const Fork& a, cudaStream_t s) {
 // Names make the result independent of the order in which the blocks run; the counts are whole numbers. If the step cannot be
 // carried out the claims are taken back by adding them again.
 //
-// Bound by latency. One thread-block cluster runs the phases of most steps, with its barrier between them: 256 requests
-// of a token and some drafts 13 us. As three launches that is 1 us less on the GPU and 5 more on the host; large steps are
-// launched so: 4096 requests 25 us. The end of 15 requests that share 2304 pages takes 28 us, five words a page and holder looked
-// up at random by the cluster's 8 SMs (21 us as three launches).
+// A warp takes eight requests and 32 columns at once: requests forked from one hold the same page in the same column, so where they
+// are neighbours one claim and one look-up serve all of them (16 requests that share 2304 pages, their end: 28 us with a claim
+// a request, 14 so). Which pages a request gives back is noted, a bit an entry, by the second phase for the third.
+//
+// Bound by latency: loads that depend on each other, three phases and the barriers between them. One thread-block cluster runs the
+// phases of most steps: 256 requests of a token, 128 columns, 12.2 us, their end 12.4. See the launch for the other form.
 // ---------------------------------------------------------------------------
 constexpr int kShrThreads = 1024, kShrGridThreads = 256;
 constexpr int kShrCluster = 8;
+constexpr int kShrFew = kShrThreads;  // requests of a call that a cluster may serve
 constexpr int kShrSlots = 4;    // consecutive slots of a thread
-constexpr int kShrPiece = 256;  // columns that a warp takes at once
+constexpr int kShrRows = 8;     // requests that a warp takes at once, with 32 columns
+constexpr int kShrLong = 256;   // columns above which a block instead of a warp gives a request's pages back
 
 __device__ __forceinline__ unsigned long long claim_name(unsigned long long epoch, bool writes, int r) {
     // above every word that a compaction leaves in the claims (below 2^31)
     return (epoch + (1ull << 20)) << 16 | (writes ? 1u << 15 : 0u) | (unsigned)(r + 1);
 }
 
-// A request's lengths in tokens and pages. grows: it writes into a page that is there.
+// A request's lengths in tokens and pages, and the columns whose pages it lets go of. grows: it writes into a page that is
+// there, and lets go of that one alone.
 struct ShareReq {
-    int old_len, new_len, had, has;
+    int old_len, new_len, had, has, lo, hi;
     int bad;
     bool grows;
 };
@@ -152,82 +157,132 @@ __device__ __forceinline__ ShareReq share_req(const SharedTables& a, int r) {
     const long long cap = (long long)a.max_blocks * a.P, o = a.seq_len[r], w = o + a.n_new[r];
     q.bad = o < 0 || o > cap || w < 0 ? kBadBounds : w > cap ? kBadCapacity : 0;
     q.old_len = (int)o, q.new_len = (int)w;
-    q.had = q.has = 0;
+    q.had = q.has = q.lo = q.hi = 0;
     q.grows = false;
     if (q.bad) return q;
-    q.had = (int)((o + a.P - 1) / a.P), q.has = (int)((w + a.P - 1) / a.P);
-    q.grows = w > o && (int)o % a.P != 0;
+    q.had = (q.old_len + a.P - 1) / a.P, q.has = (q.new_len + a.P - 1) / a.P;  // lengths up to 2^30
+    q.grows = w > o && q.old_len != q.had * a.P;
+    q.lo = q.grows ? q.had - 1 : q.has, q.hi = q.had;
     return q;
 }
 
-// Calls f(page) for the pages among a piece's columns that the request lets go of, a lane each; returns whether an id was out of
-// range.
-template <typename F>
-__device__ __forceinline__ bool for_claims(const SharedTables& a, int r, const ShareReq& q, int piece, F f) {
+// The work of the first two phases: kShrRows requests and 32 columns an item, a column a lane.
+struct ShareItems {
+    int groups, words;  // of requests, of 32 columns
+    long long n;
+};
+__device__ __forceinline__ ShareItems share_items(const SharedTables& a) {
+    ShareItems x;
+    x.groups = (a.n + kShrRows - 1) / kShrRows, x.words = (a.max_blocks + 31) / 32;
+    x.n = (long long)x.groups * x.words;
+    return x;
+}
+
+// An item's requests (request r0 + k with lane k < kShrRows; none has hi = 0) and, if any lets go of pages among its columns, the
+// pages (-1: none). Returns whether an id was out of range.
+struct ShareItem {
+    int r0, word;
+    ShareReq q;  // of this lane's request
+    bool any;
+    int p[kShrRows];
+};
+__device__ __forceinline__ bool share_item(const SharedTables& a, const ShareItems& items, long long x, ShareItem& it) {
     const int lane = threadIdx.x & 31;
-    const int* row = a.block_table + (long long)r * a.max_blocks;
+    const int g = (int)(x / items.words), word = (int)(x - (long long)g * items.words);
+    it.r0 = g * kShrRows, it.word = word;
+    it.q = {};
+    if (lane < kShrRows && it.r0 + lane < a.n) it.q = share_req(a, it.r0 + lane);
+    it.any = __any_sync(0xffffffffu, max(it.q.lo, 32 * word) < min(it.q.hi, 32 * word + 32));
     bool bad = false;
-    if (q.grows) {
-        if (piece == 0 && lane == 0) {
-            const int p = row[q.had - 1];
-            if (p >= 0 && p < a.n_pages) f(p);
-            else bad = true;
-        }
-        return bad;
+    if (!it.any) return bad;
+    const int c = 32 * word + lane;
+    const int* row = a.block_table + (long long)it.r0 * a.max_blocks + c;
+    bool in[kShrRows];
+#pragma unroll
+    for (int k = 0; k < kShrRows; ++k) {
+        const int lo = __shfl_sync(0xffffffffu, it.q.lo, k), hi = __shfl_sync(0xffffffffu, it.q.hi, k);
+        in[k] = c >= lo && c < hi;
+        it.p[k] = in[k] ? row[(long long)k * a.max_blocks] : -1;
     }
-    const int c0 = max(q.has, piece * kShrPiece), c1 = min(q.had, (piece + 1) * kShrPiece);
-#pragma unroll 4
-    for (int c = c0 + lane; c < c1; c += 32) {
-        const int p = row[c];
-        if (p >= 0 && p < a.n_pages) f(p);
-        else bad = true;
-    }
+#pragma unroll
+    for (int k = 0; k < kShrRows; ++k)
+        if (in[k] && (it.p[k] < 0 || it.p[k] >= a.n_pages)) it.p[k] = -1, bad = true;
     return bad;
 }
 
-__device__ __forceinline__ int share_pieces(const SharedTables& a) { return (a.max_blocks + kShrPiece - 1) / kShrPiece; }
-
 __device__ __forceinline__ void share_claim(const SharedTables& a, int warp, int warps) {
     const unsigned long long epoch = a.w.head->epoch;
-    const int pieces = share_pieces(a);
-    for (long long x = warp; x < (long long)a.n * pieces; x += warps) {
-        const int r = (int)(x / pieces), piece = (int)(x - (long long)r * pieces);
-        const ShareReq q = share_req(a, r);
-        const unsigned long long name = claim_name(epoch, q.grows, r);
-        int bad = q.bad;
-        if (for_claims(a, r, q, piece, [&](int p) {
-                atomicSub(a.page_refs + p, 1);
-                atomicMax(a.w.claim + p, name);
-            }))
-            bad |= kBadBounds;
+    const int lane = threadIdx.x & 31;
+    const ShareItems items = share_items(a);
+    ShareItem it;
+    for (long long x = warp; x < items.n; x += warps) {
+        int bad = share_item(a, items, x, it) ? kBadBounds : 0;
+        bad |= it.q.bad;
+        const unsigned writes = __ballot_sync(0xffffffffu, it.q.grows);
+        if (it.any) {
+            // neighbouring requests that hold the same page, as forks of one do: one claim for all of them
+            int held = 0;
+            bool write = false;
+            unsigned long long name = 0;
+#pragma unroll
+            for (int k = 0; k < kShrRows; ++k) {
+                if (it.p[k] < 0) continue;
+                const bool w = writes >> k & 1;
+                ++held;
+                if (w || !write) name = claim_name(epoch, w, it.r0 + k);  // the later, those that write first
+                write |= w;
+                if (k + 1 < kShrRows && it.p[k + 1] == it.p[k]) continue;
+                atomicSub(a.page_refs + it.p[k], held);
+                atomicMax(a.w.claim + it.p[k], name);
+                held = 0;
+                write = false;
+            }
+        }
         if (bad) atomicOr(&a.w.head->flags, bad);
-        if (piece == 0 && (threadIdx.x & 31) == 0) a.w.req[r] = make_int4(max(q.new_len - q.old_len, 0), max(q.has - q.had, 0), 0, q.grows ? kReqKeeps : 0);
+        if (it.word == 0 && lane < kShrRows && it.r0 + lane < a.n)
+            a.w.req[it.r0 + lane] = make_int4(max(it.q.new_len - it.q.old_len, 0), max(it.q.has - it.q.had, 0), 0, it.q.grows ? kReqKeeps : 0);
     }
-}
-
-// Whether the request is the one that decides on a page that it has let go of, and that nobody holds.
-__device__ __forceinline__ bool share_mine(const SharedTables& a, int p, unsigned long long name) {
-    return __ldcg(a.page_refs + p) == 0 && __ldcg(a.w.claim + p) == name;
 }
 
 __device__ __forceinline__ void share_count(const SharedTables& a, int warp, int warps) {
     const unsigned long long epoch = a.w.head->epoch;
-    const int pieces = share_pieces(a);
-    for (long long x = warp; x < (long long)a.n * pieces; x += warps) {
-        const int r = (int)(x / pieces), piece = (int)(x - (long long)r * pieces);
-        const ShareReq q = share_req(a, r);
-        const unsigned long long name = claim_name(epoch, q.grows, r);
-        int mine = 0;
+    const int lane = threadIdx.x & 31;
+    const ShareItems items = share_items(a);
+    ShareItem it;
+    for (long long x = warp; x < items.n; x += warps) {
+        share_item(a, items, x, it);
+        if (!it.any) continue;
+        const unsigned writes = __ballot_sync(0xffffffffu, it.q.grows);
+        unsigned long long claim[kShrRows];
+        int refs[kShrRows];
         bool bad = false;
-        for_claims(a, r, q, piece, [&](int p) {
-            mine += share_mine(a, p, name);
-            bad |= __ldcg(a.page_refs + p) < 0;  // more holders than the page's count
-        });
+#pragma unroll
+        for (int k = 0; k < kShrRows; ++k) {
+            claim[k] = 0, refs[k] = 1;
+            if (it.p[k] < 0 || (k > 0 && it.p[k] == it.p[k - 1])) continue;
+            claim[k] = __ldcg(a.w.claim + it.p[k]);
+            refs[k] = __ldcg(a.page_refs + it.p[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kShrRows; ++k) {
+            if (k > 0 && it.p[k] >= 0 && it.p[k] == it.p[k - 1]) claim[k] = claim[k - 1], refs[k] = refs[k - 1];
+            bad |= refs[k] < 0;  // more holders than the page's count
+        }
+        unsigned bits = 0;  // with lane k: the columns whose pages are request r0 + k's to decide on
+#pragma unroll
+        for (int k = 0; k < kShrRows; ++k) {
+            const unsigned m = __ballot_sync(0xffffffffu, refs[k] == 0 && claim[k] == claim_name(epoch, writes >> k & 1, it.r0 + k));
+            if (lane == k) bits = m;
+        }
         if (bad) atomicOr(&a.w.head->flags, kBadBounds);
-        mine = __reduce_add_sync(0xffffffffu, mine);
-        if ((threadIdx.x & 31) == 0) {
-            if (q.grows && piece == 0 && !mine) a.w.req[r].w = kReqCopies;
-            if (!q.grows && mine) atomicAdd(&a.w.req[r].z, mine);
+        if (max(it.q.lo, 32 * it.word) < min(it.q.hi, 32 * it.word + 32)) {
+            const int r = it.r0 + lane;
+            if (it.q.grows) {
+                if (!bits) a.w.req[r].w = kReqCopies;
+            } else {
+                a.w.freed[(long long)r * items.words + it.word] = bits;
+                if (bits) atomicAdd(&a.w.req[r].z, __popc(bits));
+            }
         }
     }
 }
@@ -253,7 +308,7 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
     unsigned x[3] = {0, 0, 0}, tot[3];
     int turns = 0;
     auto copied = [&](int r) { return (int)(kinds[r] == kReqCopies); };
-    constexpr int kPer = kPagedMaxRequests / NT;
+    constexpr int kPer = CLUSTER ? kShrFew / NT : kPagedMaxRequests / NT;
     int4 c[kPer];  // this thread's requests, all asked for at once
     int had[kPer];
 #pragma unroll
@@ -262,7 +317,11 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
         c[k] = make_int4(0, 0, 0, 0);
         if (r < r1) c[k] = __ldcg(a.w.req + r), had[k] = a.seq_len[r];
     }
-    const int hm = head >= 0 ? (int)(head % n_pages) : 0, tm = tail >= 0 ? (int)(tail % n_pages) : 0;
+    __shared__ int s_at[2];  // the ring's head and tail; the division is long, so one warp's
+    if (tid < 2) {
+        const long long at = tid == 0 ? head : tail;
+        s_at[tid] = at >= 0 ? (int)(at % n_pages) : 0;
+    }
     bool over = false;
     if (!flags) {
 #pragma unroll
@@ -276,6 +335,7 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
     bool wrapped;
     scan3<NT>(x, tot, wrapped, sums);
     over = __syncthreads_or(over);
+    const int hm = s_at[0], tm = s_at[1];
     // every block comes to the same verdict
     int code = ICE_OK;
     if ((flags & kBadBounds) || head < 0 || tail < head || tail - head > n_pages) code = ICE_ERR_BOUNDS;
@@ -363,8 +423,8 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
         }
     }
     turn();
-    for (int j = first; j < n_pop; j += step) {
-        const int p = a.free_pages[ring(hm, j)];
+    for (long long jj = first; jj < n_pop; jj += step) {
+        const int j = (int)jj, p = a.free_pages[ring(hm, j)];
         const int r = find_row(pop_cum, n, j), k = j - pop_cum[r], copies = copied(r);
         int* e = a.block_table + (long long)r * a.max_blocks + (old_len[r] + P - 1) / P - copies + k;
         if (copies && k == 0) {
@@ -383,47 +443,65 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
         if (kind == kReqKeeps) a.page_refs[a.block_table[(long long)r * a.max_blocks + (old_len[r] - 1) / P]] = 1;  // nobody else's
     }
     turn();
-    const int pieces = share_pieces(a);
+    const ShareItems items = share_items(a);
     if (!ok) {  // the claims taken back
-        for (long long y = first >> 5; y < (long long)n * pieces; y += step >> 5) {
-            const int r = (int)(y / pieces);
-            for_claims(a, r, share_req(a, r), (int)(y - (long long)r * pieces), [&](int p) { atomicAdd(a.page_refs + p, 1); });
+        ShareItem it;
+        for (long long y = first >> 5; y < items.n; y += step >> 5) {
+            share_item(a, items, y, it);
+            if (!it.any) continue;
+#pragma unroll
+            for (int k = 0; k < kShrRows; ++k)
+                if (it.p[k] >= 0) atomicAdd(a.page_refs + it.p[k], 1);
         }
-    } else if (pieces == 1) {  // pages given back, in order: a warp a request, or where rows are long a block
+    } else if (a.max_blocks <= kShrLong) {  // pages given back, in order: a warp a request, or where rows are long a block
+        constexpr int U = kShrLong / 32;
         for (int r = first >> 5; r < n; r += step >> 5) {
             if (push_cum[r + 1] == push_cum[r]) continue;
             const ShareReq q = share_req(a, r);
-            const unsigned long long name = claim_name(epoch, false, r);
-            const int* row = a.block_table + (long long)r * a.max_blocks;
+            int p[U];
+            unsigned m[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int c = 32 * k + lane;
+                p[k] = c >= q.lo && c < q.hi ? a.block_table[(long long)r * a.max_blocks + c] : -1;
+                m[k] = 32 * k < q.hi && 32 * k + 32 > q.lo ? __ldcg(a.w.freed + (long long)r * items.words + k) : 0;
+            }
             int at = push_cum[r];
-            for (int c0 = q.has; c0 < q.had; c0 += 32) {
-                const int p = c0 + lane < q.had ? row[c0 + lane] : -1;
-                const bool mine = p >= 0 && share_mine(a, p, name);
-                const unsigned m = __ballot_sync(0xffffffffu, mine);
-                if (mine) a.free_pages[ring(tm, at + __popc(m & ((1u << lane) - 1)))] = p;
-                at += __popc(m);
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                if (m[k] >> lane & 1) a.free_pages[ring(tm, at + __popc(m[k] & ((1u << lane) - 1)))] = p[k];
+                at += __popc(m[k]);
             }
         }
     } else {
-        __shared__ int s_warp[NT / 32];
+        constexpr int U = 4;  // columns of a thread, whose loads are under way together
+        __shared__ int s_warp[U][NT / 32];
         const int warp = tid >> 5;
         for (int r = blockIdx.x; r < n; r += gridDim.x) {
             if (push_cum[r + 1] == push_cum[r]) continue;
             const ShareReq q = share_req(a, r);
-            const unsigned long long name = claim_name(epoch, false, r);
-            const int* row = a.block_table + (long long)r * a.max_blocks;
             int at = push_cum[r];
-            for (int c0 = q.has; c0 < q.had; c0 += NT) {
-                const int p = c0 + tid < q.had ? row[c0 + tid] : -1;
-                const bool mine = p >= 0 && share_mine(a, p, name);
-                const unsigned m = __ballot_sync(0xffffffffu, mine);
+            for (int c0 = q.lo / 32 * 32; c0 < q.hi; c0 += U * NT) {
+                int p[U];
+                unsigned m[U];
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    const int c = c0 + k * NT + tid;
+                    p[k] = c >= q.lo && c < q.hi ? a.block_table[(long long)r * a.max_blocks + c] : -1;
+                    m[k] = c - lane < q.hi ? __ldcg(a.w.freed + (long long)r * items.words + (c >> 5)) : 0;
+                }
                 __syncthreads();
-                if (lane == 0) s_warp[warp] = __popc(m);
+#pragma unroll
+                for (int k = 0; k < U; ++k)
+                    if (lane == 0) s_warp[k][warp] = __popc(m[k]);
                 __syncthreads();
-                const int c = lane < NT / 32 ? s_warp[lane] : 0;
-                const int before = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
-                if (mine) a.free_pages[ring(tm, at + before + __popc(m & ((1u << lane) - 1)))] = p;
-                at += __reduce_add_sync(0xffffffffu, c);
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    const int c = lane < NT / 32 ? s_warp[k][lane] : 0;
+                    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
+                    if (m[k] >> lane & 1) a.free_pages[ring(tm, at + before + __popc(m[k] & ((1u << lane) - 1)))] = p[k];
+                    at += __reduce_add_sync(0xffffffffu, c);
+                }
             }
         }
     }
@@ -470,7 +548,7 @@ __global__ void __launch_bounds__(kShrThreads) share_fill_kernel(SharedTables a)
 __global__ void __launch_bounds__(kShrThreads) share_step_kernel(SharedTables a) {
     pdl_wait_then_release();
     const cg::cluster_group cl = cg::this_cluster();
-    const int warp = (blockIdx.x * kShrThreads + threadIdx.x) >> 5, warps = gridDim.x * kShrThreads >> 5;
+    const int warp = (threadIdx.x >> 5) * gridDim.x + blockIdx.x, warps = gridDim.x * kShrThreads >> 5;  // few items: on all SMs
     share_claim(a, warp, warps);
     cl.sync();
     share_count(a, warp, warps);
@@ -480,15 +558,18 @@ __global__ void __launch_bounds__(kShrThreads) share_step_kernel(SharedTables a)
 
 cudaError_t launch_shared_tables(const SharedTables& a, cudaStream_t s) {
     const size_t smem = share_smem(a.n);
-    // one cluster where its 256 warps have few requests each, few slots, and few pages to give back whatever the lengths
-    if (a.n <= 1024 && a.n_slots <= 65536 && (long long)a.n * a.max_blocks <= 1 << 19)
+    // One cluster of 8 SMs, or three launches on all: the first has 1 us less on the GPU where the tables are small, and 5 us less on
+    // the host. A step / the end of all requests: 16 with 128 columns 11.1 / 10.5 us (three launches 12.4 / 12.4), 16 with
+    // 2310 11.5 / 14.0 (12.5 / 12.6), 1024 with 64 14.4 / 19.7 (12.8 / 15.1), 64 with 2048 17.4 / 31.3 (13.1 / 13.7), 256 with
+    // 2048 42.2 / 102 (13.9 / 19.3).
+    if (a.n <= kShrFew && a.n_slots <= 65536 && (long long)a.n * a.max_blocks <= 1 << 16)
         return launch_cluster(share_step_kernel, kShrCluster, kShrThreads, smem, s, a);
     const int per = kShrGridThreads / 32;
-    const long long items = (long long)a.n * ((a.max_blocks + kShrPiece - 1) / kShrPiece);
+    const long long items = (long long)((a.n + kShrRows - 1) / kShrRows) * ((a.max_blocks + 31) / 32);
     const dim3 grid((unsigned)std::min<long long>(152 * 8, (items + per - 1) / per));
     cudaError_t e = launch_pdl(share_claim_kernel, grid, dim3(kShrGridThreads), 0, s, a);
     if (e == cudaSuccess) e = launch_pdl(share_count_kernel, grid, dim3(kShrGridThreads), 0, s, a);
-    const int blocks = std::max(1, std::min(152, std::max(a.n_slots / 1024, a.max_blocks > kShrPiece ? a.n : a.n / 32)));
+    const int blocks = std::max(1, std::min(152, std::max(a.n_slots / 1024, a.max_blocks > kShrLong ? a.n : a.n / 32)));
     if (e == cudaSuccess) e = launch_pdl(share_fill_kernel, dim3(blocks), dim3(kShrThreads), smem, s, a);
     return e;
 }
@@ -546,7 +627,7 @@ __device__ __forceinline__ void compact_count(const Compact& a) {
 #pragma unroll 4
         for (int c = lane; c < pages; c += 32) bad |= !named(a.block_table[(long long)r * a.max_blocks + c]);
     }
-    for (int i = blockIdx.x * NT + tid; i < a.n_extra; i += gridDim.x * NT) bad |= !named(a.extra[i]);
+    for (long long i = blockIdx.x * NT + tid; i < a.n_extra; i += gridDim.x * NT) bad |= !named(a.extra[i]);
     if (bad) atomicOr(&a.w.head->flags, kBadBounds);
 }
 
@@ -569,7 +650,7 @@ __device__ __forceinline__ void compact_move(const Compact& a) {
     // those in use before page L
     int low = 0;
     for (int c = tid; c < L / kChunk; c += NT) low += __ldcg(a.w.count + c);
-    for (int p = L / kChunk * kChunk + tid; p < L; p += NT) low += a.page_refs[p] > 0;
+    for (long long p = L / kChunk * kChunk + tid; p < L; p += NT) low += a.page_refs[p] > 0;
     low = block_sum<NT>(low, s_sum);
     const int moves = L - low;
     const int code = __ldcg(&a.w.head->flags) ? ICE_ERR_BOUNDS : moves > a.n_moves ? ICE_ERR_CAPACITY : ICE_OK;
@@ -611,7 +692,7 @@ __device__ __forceinline__ void compact_move(const Compact& a) {
             rank += f[k];
         }
     }
-    for (int k = (ok ? moves : 0) + blockIdx.x * NT + tid; k < a.n_moves; k += gridDim.x * NT)
+    for (long long k = (ok ? moves : 0) + blockIdx.x * NT + tid; k < a.n_moves; k += gridDim.x * NT)
         a.move_src[k] = a.move_dst[k] = -1;
     if (blockIdx.x == 0 && tid == 0) {
         a.w.head->plan[0] = ok;
@@ -642,10 +723,10 @@ __device__ __forceinline__ void compact_apply(const Compact& a) {
 #pragma unroll 4
         for (int c = lane; c < pages; c += 32) a.block_table_out[row + c] = goes(a.block_table[row + c]);
     }
-    for (int i = first; i < a.n_extra; i += step) a.extra_out[i] = goes(a.extra[i]);
+    for (long long i = first; i < a.n_extra; i += step) a.extra_out[i] = goes(a.extra[i]);
     // counts: a page that moves takes its own along
     if (ok) {
-        for (int k = first; k < moves; k += step) {
+        for (long long k = first; k < moves; k += step) {
             const int s = __ldcg(a.move_src + k), f = a.page_refs[s];
             a.page_refs_out[__ldcg(a.move_dst + k)] = f;
             a.page_refs_out[s] = 0;
@@ -742,7 +823,7 @@ __global__ void __launch_bounds__(kCpyThreads) page_copy_kernel(int n, const int
             uint4 v[kCpyBatch];
 #pragma unroll
             for (int k = 0; k < kCpyBatch; ++k)
-                if (at + 32 * k < page_vecs) v[k] = __ldg(from + at + 32 * k);
+                if (at + 32 * k < page_vecs) v[k] = from[at + 32 * k];
 #pragma unroll
             for (int k = 0; k < kCpyBatch; ++k)
                 if (at + 32 * k < page_vecs) to[at + 32 * k] = v[k];

@@ -5,7 +5,7 @@
 
 namespace ice {
 
-// Scratch of a handle, made by the first call that needs it: this head, then [n_pages] claims and [max_requests] counts.
+// Scratch of a handle, made by the first call that needs it: this head, then the arrays of ShareScratch.
 struct ShareHead {
     unsigned long long epoch;  // calls so far
     unsigned ticket;
@@ -24,6 +24,7 @@ struct ShareScratch {
     ShareHead* head;
     unsigned long long* claim;  // [n_pages]
     int4* req;                  // [max_requests] of a step: new tokens, pages more, pages given back, kReq*
+    unsigned* freed;            // [max_requests][ceil(max_blocks / 32)] of a step: which entries' pages are given back, a bit each
     int* count;                 // [ceil(n_pages / kCmpChunk)] of a compaction: pages in use
 };
 

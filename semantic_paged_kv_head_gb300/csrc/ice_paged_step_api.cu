@@ -24,7 +24,8 @@ int share_scratch(ice_paged* pg, const Buffers& b, void* stream, ShareScratch* w
     const size_t chunks = (size_t)((pg->p.n_pages + kCmpChunk - 1) / kCmpChunk);
     const size_t req = sizeof(ShareHead), claims = req + sizeof(int4) * (size_t)pg->p.max_requests;
     const size_t count = claims + 8 * (size_t)pg->p.n_pages;
-    const size_t bytes = count + 4 * chunks;
+    const size_t freed = count + 4 * chunks;
+    const size_t bytes = freed + 4 * (size_t)pg->p.max_requests * ((pg->p.max_blocks + 31) / 32);
     if (!pg->share) {
         if (b.capturing) return ICE_ERR_INVALID_ARG;
         char* p = nullptr;
@@ -32,7 +33,7 @@ int share_scratch(ice_paged* pg, const Buffers& b, void* stream, ShareScratch* w
             cudaGetLastError();
             return ICE_ERR_CAPACITY;
         }
-        if (cudaMemsetAsync(p, 0, bytes, (cudaStream_t)stream) != cudaSuccess) {
+        if (cudaMemsetAsync(p, 0, freed, (cudaStream_t)stream) != cudaSuccess) {
             cudaGetLastError();
             cudaFree(p);
             return ICE_ERR_CUDA;
@@ -43,6 +44,7 @@ int share_scratch(ice_paged* pg, const Buffers& b, void* stream, ShareScratch* w
     w->claim = (unsigned long long*)(pg->share + claims);
     w->req = (int4*)(pg->share + req);
     w->count = (int*)(pg->share + count);
+    w->freed = (unsigned*)(pg->share + freed);
     return ICE_OK;
 }
 

@@ -52,7 +52,7 @@ __device__ __forceinline__ uint4 load16(const char* p) {
     if (ALIGNED) return __ldcs(reinterpret_cast<const uint4*>(p));
     const unsigned sh = (unsigned)(uintptr_t)p & 15;
     const uint4* b = reinterpret_cast<const uint4*>(p - sh);
-    const uint4 x = __ldg(b), y = sh ? __ldg(b + 1) : x;
+    const uint4 x = b[0], y = sh ? b[1] : x;
     unsigned w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
     if (sh & 8) {
 #pragma unroll

@@ -310,7 +310,7 @@ def _pool_lists(p):
 
 @pytest.mark.parametrize("n,P,cols,n_pages,rounds", [
     (3, 4, 6, 20, 30), (9, 1, 12, 60, 25), (40, 16, 10, 160, 20), (128, 5, 12, 700, 10), (129, 16, 10, 500, 10), (300, 3, 40, 5000, 6),
-    (20, 2, 4000, 30000, 5), (140, 2, 4000, 60000, 4), (1100, 4, 20, 9000, 4)])
+    (20, 2, 4000, 30000, 5), (140, 2, 4000, 60000, 4), (1100, 4, 20, 9000, 4), (10, 2, 4000, 20000, 5), (70, 4, 300, 5000, 6)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_shared_tables_and_forks(ice, n, P, cols, n_pages, rounds, in_place):
     """A loop of forks and steps, moved on by the kernels and by the definition."""
