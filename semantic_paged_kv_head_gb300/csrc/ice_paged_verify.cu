@@ -41,7 +41,8 @@ template <typename T> constexpr int kTile = 32 * kVerVecs * kVec<T>;     // elem
 
 // What an entry counts for: NaN, negative and huge ones nothing (2^22 of 2^100 have a sum in fp32). As an unsigned number each
 // of those is above the bits of 2^100.
-__device__ __forceinline__ float clean(float x) { return __float_as_uint(x) <= 0x71800000u ? x : 0.0f; }
+constexpr unsigned kMostBits = 0x71800000u;
+__device__ __forceinline__ float clean(float x) { return __float_as_uint(x) <= kMostBits ? x : 0.0f; }
 
 __device__ __forceinline__ float clamp_uniform(float u) { return fminf(fmaxf(u, 0.0f), 0.99999994f); }
 
@@ -146,9 +147,30 @@ __device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make
 // Two sums of terms >= 0 with the parts that their additions cut off.
 struct Sum2 {
     float2 hi = {0.0f, 0.0f}, lo = {0.0f, 0.0f};
-    __device__ __forceinline__ float2 cut(float2 d) {
+    __device__ __forceinline__ void add(float2 d, float2 more) {
         const float2 s = add2(hi, d), t = sub2(s, hi);
         const float2 e = add2(sub2(hi, sub2(s, t)), sub2(d, t));
+        hi = s;
+        lo = add2(lo, add2(e, more));
+    }
+    __device__ __forceinline__ Wide value() const {
+        Wide a, b, c, d;
+        a.hi = hi.x, b.hi = lo.x, c.hi = hi.y, d.hi = lo.y;
+        return wide_add(wide_add(a, b), wide_add(c, d));
+    }
+};
+
+// The two sums of a tile. They begin at `base`, a power of two above every term: what an addition cuts off is then (d - (s - hi)),
+// two operations instead of five (Dekker 1971), and base comes off exactly at the end.
+struct TileSum {
+    float2 hi, lo = {0.0f, 0.0f};
+    float base;
+    __device__ __forceinline__ explicit TileSum(unsigned most) {  // the largest term's bits, of 2^100 at most
+        base = __uint_as_float((most & 0x7f800000u) + 0x00800000u);
+        hi = make_float2(base, base);
+    }
+    __device__ __forceinline__ float2 cut(float2 d) {
+        const float2 s = add2(hi, d), e = sub2(d, sub2(s, hi));
         hi = s;
         return e;
     }
@@ -159,12 +181,7 @@ struct Sum2 {
         const float2 d = sub2(p, q), e = sub2(sub2(p, d), q);
         lo = add2(lo, add2(cut(d), e));
     }
-    __device__ __forceinline__ Wide value() const {
-        Wide a, b;
-        a.hi = hi.x + lo.x, a.lo = lo.x - (a.hi - hi.x);
-        b.hi = hi.y + lo.y, b.lo = lo.y - (b.hi - hi.y);
-        return wide_add(a, b);
-    }
+    __device__ __forceinline__ void end(Sum2& s) const { s.add(sub2(hi, make_float2(base, base)), lo); }
 };
 
 __device__ __forceinline__ Wide above(float p, float q) {
@@ -187,15 +204,82 @@ __device__ __forceinline__ int row_shift(const T* p) { return (int)(((uintptr_t)
 // What is taken off the target's entries: nothing, a draft's row, or 1 at the token that the draft was certain of.
 enum { kOffNone = 0, kOffRow = 1, kOffSure = 2 };
 
-template <typename T, int OFF, bool ALIGNED>
-__device__ __forceinline__ void add_whole_tile(const T* p, const T* q, int sure, int e0, Sum2& s) {
+// 16 bytes of entries from element `at` on, where some of them may lie outside the row: those are `fill`.
+template <typename T>
+__device__ __forceinline__ uint4 load_end(const T* p, int at, int V, unsigned fill) {
+    if (at >= 0 && at + kVec<T> <= V && ((uintptr_t)(p + at) & 15) == 0) return load16<true>(reinterpret_cast<const char*>(p + at));
+    unsigned w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = fill;
+#pragma unroll
+        for (int j = 0; j < kVec<T> / 4; ++j) {
+            const int k = at + i * (kVec<T> / 4) + j;
+            if (k < 0 || k >= V) continue;
+            if (sizeof(T) == 4) {
+                w[i] = reinterpret_cast<const unsigned*>(p)[k];
+            } else {
+                const unsigned x = reinterpret_cast<const unsigned short*>(p)[k];
+                w[i] = j ? (w[i] & 0xffffu) | x << 16 : (w[i] & 0xffff0000u) | x;
+            }
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// What `clean` keeps of 16 bytes of entries.
+template <typename T> __device__ __forceinline__ uint4 clean_words(uint4 w);
+template <> __device__ __forceinline__ uint4 clean_words<float>(uint4 w) {
+    auto f = [](unsigned x) { return x <= kMostBits ? x : 0u; };
+    return make_uint4(f(w.x), f(w.y), f(w.z), f(w.w));
+}
+template <> __device__ __forceinline__ uint4 clean_words<__nv_bfloat16>(uint4 w) {
+    auto f = [](unsigned x) { return ((x & 0xffffu) <= kMostBits >> 16 ? x & 0xffffu : 0u) | ((x >> 16) <= kMostBits >> 16 ? x & 0xffff0000u : 0u); };
+    return make_uint4(f(w.x), f(w.y), f(w.z), f(w.w));
+}
+
+// The entries of a lane's part of a tile, cleaned. Returns the bits of the largest: most tiles hold nothing to be cleaned,
+// which that tells.
+template <typename T>
+__device__ __forceinline__ unsigned most_bits(const uint4 (&x)[kVerVecs]) {
+    unsigned m = 0;
+#pragma unroll
+    for (int i = 0; i < kVerVecs; ++i)
+        m = sizeof(T) == 4 ? __vimax3_u32(__vimax3_u32(m, x[i].x, x[i].y), x[i].z, x[i].w)
+                           : __vimax3_u16x2(__vimax3_u16x2(m, x[i].x, x[i].y), x[i].z, x[i].w);
+    return sizeof(T) == 4 ? m : max(m << 16, m & 0xffff0000u);
+}
+template <typename T>
+__device__ __forceinline__ unsigned clean_tile(uint4 (&x)[kVerVecs]) {
+    unsigned m = most_bits<T>(x);
+    if (m > kMostBits) {
+#pragma unroll
+        for (int i = 0; i < kVerVecs; ++i) x[i] = clean_words<T>(x[i]);
+        m = most_bits<T>(x);
+    }
+    return m;
+}
+
+// How a tile's entries are loaded: whole tiles, of which the draft's row may begin at another offset of 16 bytes, and a row's ends.
+enum { kTileAligned = 0, kTileShifted = 1, kTileEnd = 2 };
+
+template <typename T, int OFF, int HOW>
+__device__ __forceinline__ void add_tile_as(const T* p, const T* q, int sure, int V, int e0, Sum2& sum) {
     const int at = e0 + (threadIdx.x & 31) * kVec<T>;
     uint4 x[kVerVecs], y[OFF == kOffRow ? kVerVecs : 1];
 #pragma unroll
     for (int i = 0; i < kVerVecs; ++i) {
-        x[i] = load16<true>(reinterpret_cast<const char*>(p + at + i * 32 * kVec<T>));
-        if (OFF == kOffRow) y[i] = load16<ALIGNED>(reinterpret_cast<const char*>(q + at + i * 32 * kVec<T>));
+        const int k = at + i * 32 * kVec<T>;
+        if (HOW == kTileEnd) {
+            x[i] = load_end<T>(p, k, V, 0u);
+            if (OFF == kOffRow) y[i] = load_end<T>(q, k, V, 0u);
+        } else {
+            x[i] = load16<true>(reinterpret_cast<const char*>(p + k));
+            if (OFF == kOffRow) y[i] = load16<HOW == kTileAligned>(reinterpret_cast<const char*>(q + k));
+        }
     }
+    TileSum s(clean_tile<T>(x));
+    if constexpr (OFF == kOffRow) clean_tile<T>(y);
 #pragma unroll
     for (int i = 0; i < kVerVecs; ++i) {
         float a[kVec<T>], b[kVec<T>];
@@ -203,13 +287,14 @@ __device__ __forceinline__ void add_whole_tile(const T* p, const T* q, int sure,
         if (OFF == kOffRow) unpack<T>(y[i], b);
 #pragma unroll
         for (int j = 0; j < kVec<T>; j += 2) {
-            const float2 v = make_float2(clean(a[j]), clean(a[j + 1]));
+            const float2 v = make_float2(a[j], a[j + 1]);
             const int k = at + i * 32 * kVec<T> + j;
-            if (OFF == kOffRow) s.add_above(v, make_float2(clean(b[j]), clean(b[j + 1])));
+            if (OFF == kOffRow) s.add_above(v, make_float2(b[j], b[j + 1]));
             else if (OFF == kOffSure) s.add_above(v, make_float2(k == sure ? 1.0f : 0.0f, k + 1 == sure ? 1.0f : 0.0f));
             else s.add(v);
         }
     }
+    s.end(sum);
 }
 
 // Adds the lane's weights of a tile.
@@ -217,33 +302,12 @@ template <typename T>
 __device__ __forceinline__ void add_tile(const T* p, const T* q, int sure, int V, int e0, Sum2& s) {
     const bool inside = e0 >= 0 && e0 + kTile<T> <= V;
     if (q != nullptr) {
-        if (inside && ((uintptr_t)(q + e0) & 15) == 0) return add_whole_tile<T, kOffRow, true>(p, q, sure, e0, s);
-        if (e0 >= kVec<T> && e0 + kTile<T> + kVec<T> <= V) return add_whole_tile<T, kOffRow, false>(p, q, sure, e0, s);
-    } else if (inside) {
-        if (sure >= e0 && sure < e0 + kTile<T>) return add_whole_tile<T, kOffSure, true>(p, q, sure, e0, s);
-        return add_whole_tile<T, kOffNone, true>(p, q, sure, e0, s);
+        if (inside && ((uintptr_t)(q + e0) & 15) == 0) return add_tile_as<T, kOffRow, kTileAligned>(p, q, sure, V, e0, s);
+        if (e0 >= kVec<T> && e0 + kTile<T> + kVec<T> <= V) return add_tile_as<T, kOffRow, kTileShifted>(p, q, sure, V, e0, s);
+        return add_tile_as<T, kOffRow, kTileEnd>(p, q, sure, V, e0, s);
     }
-    // a row's ends: element by element, 16 loads of a row under way (at a place that is there, wherever the element is)
-    const int j0 = e0 + (threadIdx.x & 31);
-#pragma unroll 1
-    for (int h = 0; h < kTile<T> / 32; h += 16) {
-        T x[16], y[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = p[min(max(j0 + 32 * (h + i), 0), V - 1)];
-        if (q != nullptr) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = q[min(max(j0 + 32 * (h + i), 0), V - 1)];
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = from_f<T>(j0 + 32 * (h + i) == sure ? 1.0f : 0.0f);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            const int j = j0 + 32 * (h + i);
-            s.add_above(make_float2(j >= 0 && j < V ? clean(to_f<T>(x[i])) : 0.0f, j + 32 >= 0 && j + 32 < V ? clean(to_f<T>(x[i + 1])) : 0.0f),
-                        make_float2(clean(to_f<T>(y[i])), clean(to_f<T>(y[i + 1]))));
-        }
-    }
+    if (inside && !(sure >= e0 && sure < e0 + kTile<T>)) return add_tile_as<T, kOffNone, kTileAligned>(p, q, sure, V, e0, s);
+    add_tile_as<T, kOffSure, kTileEnd>(p, q, sure, V, e0, s);
 }
 
 // Tiles of part g of a row.
@@ -459,29 +523,6 @@ template <> __device__ __forceinline__ float largest<__nv_bfloat16>(const uint4&
     const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
     const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
     return fmaxf(__low2float(m), __high2float(m));
-}
-
-// 16 bytes of entries from element `at` on, where some of them may lie outside the row: those are `fill`.
-template <typename T>
-__device__ __forceinline__ uint4 load_end(const T* p, int at, int V, unsigned fill) {
-    if (at >= 0 && at + kVec<T> <= V) return load16<true>(reinterpret_cast<const char*>(p + at));
-    unsigned w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        w[i] = fill;
-#pragma unroll
-        for (int j = 0; j < kVec<T> / 4; ++j) {
-            const int k = at + i * (kVec<T> / 4) + j;
-            if (k < 0 || k >= V) continue;
-            if (sizeof(T) == 4) {
-                w[i] = reinterpret_cast<const unsigned*>(p)[k];
-            } else {
-                const unsigned x = reinterpret_cast<const unsigned short*>(p)[k];
-                w[i] = j ? (w[i] & 0xffffu) | x << 16 : (w[i] & 0xffff0000u) | x;
-            }
-        }
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // A lane's best entry of the tiles that it has seen, and the first 16 bytes that hold it.
