@@ -682,7 +682,7 @@ int ice_paged_compact(ice_paged* pg, int32_t n_req, const int32_t* seq_len, cons
  *   With them target and draft are probabilities p and q, not necessarily of sum 1. Draft x stays if u q(x) < p(x)
  *   and all before it stay. After the first that does not, the token is drawn from max(p - q, 0) of that place (from p if
  *   that is 0 everywhere); if all stay, from p of the last row: it is the first j with
- *   w_0 + .. + w_j > u (w_0 + .. + w_{vocab - 1}). The sums are held in more than 40 bits. NaN, negative entries and
+ *   w_0 + .. + w_j > u (w_0 + .. + w_{vocab - 1}). The sums are held in about 40 bits. NaN, negative entries and
  *   those above 2^100 count as 0.
  * uniform NULL: greedy. target may be logits; draft is not used. Draft x stays if it is the index of
  *   its row's largest entry (of equal ones the lowest index; NaN is passed over), and the token is that of the first

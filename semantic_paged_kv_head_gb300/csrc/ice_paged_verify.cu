@@ -13,7 +13,9 @@ namespace ice {
 //
 // A border between two tokens may lie anywhere, so sums have to be near those of exact arithmetic: with 2^17 tokens of
 // like weight fp32 sums would move one draw in ten. Sums therefore carry what each addition and each p - q cuts off (two-sum,
-// Knuth 1969): pairs of fp32, 46 bits or more.
+// Knuth 1969; within a tile the cheaper form of Dekker 1971): pairs of fp32, off by 2^-38 if every rounding went
+// the same way, by 2^-42 as they come. The fp32 pipe and the
+// entries' checks, not memory, would else bound short rows in bf16.
 //
 // No block waits for another in either case. Sampling: several blocks a request. Each finds the first rejected draft by
 // itself (K gathers), so that only the one or two rows that decide are read; each warp sums a part of the vocabulary and leaves
@@ -25,11 +27,12 @@ namespace ice {
 // rows first; a warp skips its group when a draft before that row is known not to stay, which changes what is read but
 // not the result.
 //
-// Measured: one request of four drafts on 128000 fp32 entries 7.3 us, three loads that depend on each other, the
-// count, and the search. 64 requests of up to seven 18 us (57 MB: 3.1 TB/s; the same fixed parts around one wave of loads);
-// 200 of two 38 us. Greedy, 128 requests of up to four drafts on 150001 bf16 entries 29.7 us, of which 136 MB are read where 94 are
+// Measured: one request of four drafts on 128000 fp32 entries 7.4 us, three loads that depend on each other, the
+// count, and the search. 64 requests of up to seven 16.8 us (57 MB: 3.4 TB/s; the same fixed parts around one wave of loads);
+// 256 looked-up requests on 50001 bf16 entries 16.9 us. Greedy, 128 requests of up to four drafts on 150001 bf16 entries
+// 29.6 us, of which 136 MB are read where 94 are
 // needed (rows of the next draft are under way before the verdict on this one); 512 of one draft 45 us, 5.8 TB/s.
-// A thread-block cluster a request took 16 us for the 64 and 22 for 256 looked-up requests (18 here), and 61 for the
+// A thread-block cluster a request took 16 us for the 64 and 22 for 256 looked-up requests (17 here), and 61 for the
 // greedy ones, whose rows it read one after the other.
 // ---------------------------------------------------------------------------
 constexpr int kSmpThreads = 256, kSmpWarps = kSmpThreads / 32;
