@@ -560,7 +560,8 @@ cudaError_t launch_shared_tables(const SharedTables& a, cudaStream_t s) {
     const size_t smem = share_smem(a.n);
     // One cluster of 8 SMs, or three launches on all: the first has 1 us less on the GPU where the tables are small, and 5 us less on
     // the host. A step / the end of all requests: 16 with 128 columns 11.1 / 10.5 us (three launches 12.4 / 12.4), 16 with
-    // 2310 11.5 / 14.0 (12.5 / 12.6), 1024 with 64 14.4 / 19.7 (12.8 / 15.1), 64 with 2048 17.4 / 31.3 (13.1 / 13.7), 256 with
+    // 2310 11.5 / 14.0 (12.5 / 12.6), 1024 with 64 14.4 / 19.7 (12.8 / 15.1; no page shared 15.8 / 32 and
+    // 15.3 / 15.5), 64 with 2048 17.4 / 31.3 (13.1 / 13.7), 256 with
     // 2048 42.2 / 102 (13.9 / 19.3).
     if (a.n <= kShrFew && a.n_slots <= 65536 && (long long)a.n * a.max_blocks <= 1 << 16)
         return launch_cluster(share_step_kernel, kShrCluster, kShrThreads, smem, s, a);
