@@ -114,6 +114,15 @@ def test_rope(ice, dtype, interleaved, n, H, G, P, pairs, axes):
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("in_place", [False, True])
+def test_rope_most_heads(ice, dtype, in_place):
+    c = _rope_case(4, dtype, 2, 512, 8, 1, 64, 2)
+    pc, *got = _rope_run(ice, c, in_place=in_place)
+    assert pc.get_error() == 0
+    _rope_check(c, False, 0, *got)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("in_place", [False, True])
 def test_rope_strided(ice, dtype, in_place):
     c = _rope_case(3, dtype, 130, 2, 4, 16, 64, 3, strided=True)
     c["pos"] = torch.cat([c["pos"], c["pos"]], 1)[:, :130]  # rows further apart than the tokens
@@ -774,6 +783,44 @@ def test_verify_one_entry_alone(ice, dtype, at):
         pc, got = _verify_run(ice, c)
         _verify_check(ice, c, got, pc.get_error())
         assert got[0].tolist() == [[at, -1]] * 3 and got[1].tolist() == [0, 0, 0]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("mode", ["alone", "draft", "lookup"])
+@pytest.mark.parametrize("V", [700, 9001])
+def test_verify_entries_of_every_size(ice, dtype, mode, V):
+    """Entries below the normal numbers, of 2^100, of both in one row, and tiles whose largest entry is far below the row's."""
+    g = torch.Generator().manual_seed(V)
+    j, some = torch.arange(V), lambda: torch.rand((V,), generator=g, dtype=torch.float64) + 0.01
+    least = 2.0 ** (-149 if dtype == F32 else -133)
+    rows = [torch.ceil(100 * some()) * least, torch.exp2(torch.floor(some() * 225 - 128)) * (1 + some()), torch.full((V,), 2.0 ** 100, dtype=torch.float64),
+            torch.exp2(-j / 50.0), torch.where(j < V // 2, some() * 2.0 ** -120, some()), torch.where(j % 512 < 3, 1.0 + some(), some() * 2.0 ** -30),
+            3.0 * some()]
+    target = torch.stack(rows).to(dtype).repeat(6, 1)[:, None].repeat(1, 2, 1)
+    n = len(target)
+    draft = None
+    if mode == "draft":
+        draft = (target[:, :1].double() * (0.25 + 1.5 * torch.rand((n, 1, V), generator=g, dtype=torch.float64))).to(dtype)
+    u = torch.rand((n, 2), generator=g)
+    u[:, 0] = 1.0
+    tokens = torch.randint(0, V, (n, 1), generator=g, dtype=torch.int32)
+    c = [tokens, torch.full((n,), 0 if mode == "alone" else 1, dtype=torch.int32), target, draft, u]
+    pc, got = _verify_run(ice, c)
+    _verify_check(ice, c, got, pc.get_error())
+
+
+def test_verify_same_rows_for_all(ice):
+    """Rows that are one row of memory (strides of 0)."""
+    V = 3001
+    g = torch.Generator().manual_seed(3)
+    row = torch.softmax(2 * torch.randn((V,), generator=g), 0)
+    c = [torch.randint(0, V, (7, 3), generator=g, dtype=torch.int32), torch.full((7,), 3, dtype=torch.int32), row.expand(7, 4, V),
+         row.expand(7, 3, V), torch.rand((7, 4), generator=g)]
+    for d in (c[3], None):
+        pc = _cache(ice, n_kv_heads=1, n_q_heads=1, n_pages=1, max_requests=7, max_blocks=1, max_tokens=1)
+        one = row.cuda()
+        got = pc.verify(c[0].cuda(), c[1].cuda(), one.expand(7, 4, V), None if d is None else one.expand(7, 3, V), c[4].cuda())
+        _verify_check(ice, [c[0], c[1], c[2], d, c[4]], [x.cpu() for x in got], pc.get_error())
 
 
 def test_verify_nothing_above_the_draft(ice):
