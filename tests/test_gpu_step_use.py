@@ -299,6 +299,39 @@ def test_rope_and_verify_in_graphs(ice, dtype):
                 assert int(accepted[r]) == kept and check(int(tokens[r, kept])), (m, r)
 
 
+def test_two_handles_at_once(ice):
+    """Steps of two pools on two streams, none waiting for the other; one by one cluster, one by three launches."""
+    from tests.step_helpers import plain_tables_shared
+    sizes = ((60, 4, 9, 400), (1100, 4, 9, 7000))
+    pools = [Pool(7 + i, *x) for i, x in enumerate(sizes)]
+    pcs = [_cache(ice, n_kv_heads=1, n_q_heads=1, page_size=P, n_pages=n_pages, max_requests=n, max_blocks=cols, max_tokens=1)
+           for n, P, cols, n_pages in sizes]
+    gpus = [Shared(pool, pc=pc) for pool, pc in zip(pools, pcs)]
+    streams = [torch.cuda.Stream() for _ in pools]
+    refs = [[], []]
+    changes = [[], []]
+    for i, pool in enumerate(pools):
+        for _ in range(8):
+            new = pool.change()
+            ref = plain_tables_shared(pool.lens, new, pool.table, pool.ring, pool.state, pool.refs, 9000, pool.P)
+            assert ref[0] == 0
+            _, pool.lens, pool.state, *rest, pool.table, pool.ring, pool.refs = ref
+            refs[i].append(rest)
+            changes[i].append(_i32(new))
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for t in range(8):
+        for i, (pc, gpu, st) in enumerate(zip(pcs, gpus, streams)):
+            outs[i].append(pc.tables_shared(gpu.lens, changes[i][t], gpu.table, gpu.ring, gpu.state, gpu.refs, 9000, gpu.lens, gpu.state,
+                                            stream=st)[2:])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert pcs[i].get_error() == 0
+        for t in range(8):
+            assert [x.tolist() for x in outs[i][t]] == list(refs[i][t]), (i, t)
+        assert gpus[i].lists() == _pool_lists(pools[i])
+
+
 def test_shared_pages_in_a_graph(ice):
     """Forks, steps and a compaction, captured once and replayed as lengths change, in place."""
     n, P, cols, n_pages = 40, 4, 9, 260
