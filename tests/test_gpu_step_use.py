@@ -39,7 +39,7 @@ class Calls:
             "rope_append": dict(n=3, rope=self.rope._ref, pos=i, pos_stride=3, offset=0, q=q, qs=1024, qo=self.qo.data_ptr(), qos=1024, k=kv,
                                 ks=256, v=kv, vs=256, slots=self.slots.data_ptr(), kp=kp, vp=vp),
             "fork": dict(n=0, src=i, dst=i, len=None, n_req=2, lens=i, table=i + 512, refs=i + 1024, out=i + 2048),
-            "tables_shared": dict(n_req=2, lens=i, new=i, table=i + 512, ring=i + 1024, state=i + 2048, refs=i + 2560, out=i + 3072,
+            "tables_shared": dict(n_req=2, lens=i, new=i, table=i + 512, ring=i + 1024, state=i + 2048, refs=i + 2560, out=i + 3328,
                                   state_out=i + 3584, q0=i + 4096, slots=i + 4608, pos=i + 5120, n_slots=2, src=i + 5632, dst=i + 6144),
             "copy": dict(n=2, src=i + 8192, dst=i + 8192, layers=1, stride=0, kp=kp, vp=vp),
             "compact": dict(n_req=2, lens=i, table=i + 512, n_extra=0, extra=None, refs=i + 1024, ring=i + 8192, state=i + 10240, n_moves=2,
