@@ -29,13 +29,12 @@ namespace ice {
 //
 // Measured: one request of four drafts on 128000 fp32 entries 7.4 us, three loads that depend on each other, the
 // count, and the search. 64 requests of up to seven 16.8 us (57 MB: 3.4 TB/s; the same fixed parts around one wave of loads);
-// 256 looked-up requests on 50001 bf16 entries 16.9 us. Greedy, 128 requests of up to four drafts on 150001 bf16 entries
-// 29.6 us, of which 136 MB are read where 94 are
-// needed (rows of the next draft are under way before the verdict on this one); 512 of one draft 45 us, 5.8 TB/s.
+// 256 looked-up requests on 50001 bf16 entries 16.3 us, 1000 of them 38. Greedy, 128 requests of up to four drafts on 150001 bf16
+// entries 29.6 us, of which 136 MB are read where 94 are needed (rows of the next draft are under way before the verdict on this one); 512 of one draft 45 us, 5.8 TB/s.
 // A thread-block cluster a request took 16 us for the 64 and 22 for 256 looked-up requests (17 here), and 61 for the
 // greedy ones, whose rows it read one after the other.
 // ---------------------------------------------------------------------------
-constexpr int kSmpThreads = 256, kSmpWarps = kSmpThreads / 32;
+constexpr int kSmpMost = 256;  // threads of a block: these, or half of them
 constexpr int kGrdThreads = 128, kGrdWarps = kGrdThreads / 32;
 constexpr int kVerVecs = 4;  // 16-byte words of a lane in a tile
 
@@ -333,8 +332,8 @@ __device__ __forceinline__ void write_request(const Verify& a, int r, int nd, in
 }
 
 struct SampleShared {
-    float2 warp[kSmpWarps];  // sums, as two numbers
-    unsigned some[kSmpWarps], over[kSmpWarps];
+    float2 warp[kSmpMost / 32];  // sums, as two numbers
+    unsigned some[kSmpMost / 32], over[kSmpMost / 32];
     unsigned keep[2];
     int last;
 };
@@ -345,7 +344,7 @@ struct BlockFind {
     int at;
     Wide before, all;
 };
-template <typename X>
+template <int kSmpWarps, typename X>
 __device__ __forceinline__ BlockFind block_find(Wide w, X want, SampleShared& sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     Wide before, base;
@@ -376,8 +375,9 @@ __device__ __forceinline__ BlockFind block_find(Wide w, X want, SampleShared& sh
     return f;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kSmpThreads, 4) verify_sample_kernel(Verify a) {
+template <typename T, int kSmpThreads>
+__global__ void __launch_bounds__(kSmpThreads, 1024 / kSmpThreads) verify_sample_kernel(Verify a) {
+    constexpr int kSmpWarps = kSmpThreads / 32;
     __shared__ SampleShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int blocks = a.blocks, r = blockIdx.x / blocks, chunk = blockIdx.x - r * blocks;
@@ -441,14 +441,13 @@ __global__ void __launch_bounds__(kSmpThreads, 4) verify_sample_kernel(Verify a)
     // the last block of the request. At most twice: where the target is nowhere above the draft, a token of the target's own
     int token = -1;
     for (;;) {
-        static_assert(kVerGroups == kSmpThreads, "a part a thread");
-        Wide mine;
+        Wide mine;  // a part a thread
         if (tid < a.groups) {
             const float2 x = __ldcg(&w->sum[tid]);
             mine.hi = x.x, mine.lo = x.y;
         }
         Wide x;
-        BlockFind f = block_find(mine, [&](Wide all) { return x = wide_mul(u, all); }, sh);
+        BlockFind f = block_find<kSmpWarps>(mine, [&](Wide all) { return x = wide_mul(u, all); }, sh);
         if (f.at >= 0) {
             x = wide_sub(x, f.before);
             int t0, t1;
@@ -463,7 +462,7 @@ __global__ void __launch_bounds__(kSmpThreads, 4) verify_sample_kernel(Verify a)
                     s = warp_sum(c.value());
                     if (lane != 0) s = Wide();
                 }
-                f = block_find(s, [&](Wide) { return x; }, sh);
+                f = block_find<kSmpWarps>(s, [&](Wide) { return x; }, sh);
                 if (t1 - t0 == n || wide_less(x, f.all)) {
                     if (f.at >= 0) {
                         x = wide_sub(x, f.before);
@@ -484,7 +483,7 @@ __global__ void __launch_bounds__(kSmpThreads, 4) verify_sample_kernel(Verify a)
                 if (j + k >= 0 && j + k < V) e[k] = weight(p, q, sure, j + k);
                 c = wide_add(c, e[k]);
             }
-            f = block_find(c, [&](Wide) { return x; }, sh);
+            f = block_find<kSmpWarps>(c, [&](Wide) { return x; }, sh);
             if (tid == f.at) {
                 Wide low = f.before;
 #pragma unroll
@@ -623,18 +622,34 @@ __global__ void __launch_bounds__(kGrdThreads, sizeof(T) == 2 ? 12 : 8) verify_g
     }
 }
 
+// Blocks of a request, and whether those of all run at once (1024 threads an SM). With a tile a warp at least the blocks that run
+// at once share the requests, where that leaves a warp no more than six tiles (100 requests of 128000 fp32 entries 21.2 us, in waves
+// 25.2); else a warp has four, and in several waves one's ends lie beside another's loads (256 of 128000 bf16 entries 29.6 us, in one wave
+// 33.3).
+template <typename T, int kSmpThreads>
+static bool sample_in_one_wave(Verify& a) {
+    constexpr int kSmpWarps = kSmpThreads / 32;
+    const int tiles = (a.V + kTile<T> - 1) / kTile<T>;
+    const int once = 152 * (1024 / kSmpThreads) / a.n_req, want = (tiles + 4 * kSmpWarps - 1) / (4 * kSmpWarps);
+    const bool one = 3 * once >= 2 * want;
+    a.blocks = std::min(32, one ? std::max(1, std::min(once, (tiles + kSmpWarps - 1) / kSmpWarps)) : want);
+    // In one wave each tile is a part of its own (a part a thread of the last block), so that the drawn part needs no search by tiles:
+    // 64 requests of 128000 entries 18.7 -> 18.2 us. In more waves the time is that of the sums, and a warp's tiles are one part: 200
+    // requests 40.2 -> 37.8.
+    const bool parts = a.n_req * a.blocks <= 152 * (1024 / kSmpThreads);
+    a.groups = parts ? std::min(kSmpThreads, tiles) : a.blocks * kSmpWarps;
+    return one;
+}
+
+// Blocks of 256 threads where they run at once and a smaller block's threads would be fewer than the tiles: one request of 128000
+// fp32 entries 7.3 us (8.4 with 128). Else of 128: the requests' ends are chains of loads, and more of them are under way (1000
+// requests of 50001 bf16 entries 38.3 us, 44.2 with 256; 4000 of 5000 fp32 entries 42.8 and 65.8; 256 looked-up 16.2 and 16.8).
 template <typename T>
 static cudaError_t launch_sample(Verify a, cudaStream_t s) {
-    const int tiles = (a.V + kTile<T> - 1) / kTile<T>;
-    // As many blocks as run at once (4 an SM) share the requests, with a tile a warp at least and four at most
-    const int room = 152 * 4;
-    a.blocks = std::max(std::min(room / a.n_req, (tiles + kSmpWarps - 1) / kSmpWarps), (tiles + 4 * kSmpWarps - 1) / (4 * kSmpWarps));
-    a.blocks = std::min(a.blocks, kVerGroups / kSmpWarps);
-    // Where that is one wave, each tile is a part of its own (of up to 256), so that the drawn part needs no search by tiles: 64
-    // requests of 128000 entries 18.7 -> 18.2 us. In more waves the time is that of the sums, and a warp's tiles are one
-    // part: 200 requests 40.2 -> 37.8.
-    a.groups = a.n_req * a.blocks <= room ? std::min(kVerGroups, tiles) : a.blocks * kSmpWarps;
-    return launch_pdl(verify_sample_kernel<T>, dim3(a.n_req * a.blocks), dim3(kSmpThreads), 0, s, a);
+    if (a.V > 128 * kTile<T> && sample_in_one_wave<T, 256>(a))
+        return launch_pdl(verify_sample_kernel<T, 256>, dim3(a.n_req * a.blocks), dim3(256), 0, s, a);
+    sample_in_one_wave<T, 128>(a);
+    return launch_pdl(verify_sample_kernel<T, 128>, dim3(a.n_req * a.blocks), dim3(128), 0, s, a);
 }
 
 template <typename T>
