@@ -704,7 +704,7 @@ int ice_paged_verify(ice_paged* pg, int32_t n_req, int32_t n_draft_max, int32_t 
 
 /*
  * ice_paged_debug_set_flags - test hooks (0 = normal operation).
- * ICE_DEBUG_STALL_ATTN: in ice_paged_attn with bf16 one copy of keys expects 16 bytes
+ * ICE_DEBUG_STALL_ATTN: in ice_paged_attn with bf16 one copy of keys a block expects 16 bytes
  * more than it delivers, so the bounded waits for it run out and the call reports
  * ICE_ERR_TIMEOUT. Nothing is left in flight, and later calls on the handle (with the
  * flag off) are exact. Used to test the timeout path.

@@ -544,9 +544,10 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                     if (!ok) break;
                     const unsigned bar = smem_u32(&full[st]), dst = dst0 + st * kFaTileB;
                     if (lane == 0) {
-                        // ICE_DEBUG_STALL_ATTN: the last key tile of the first block's first item with any expects 16 bytes that no
-                        // copy delivers, so that the waits for it run out
-                        const bool stall = a.debug && is_k && blockIdx.x == 0 && x == n - 1 && cnt == (unsigned)x;
+                        // ICE_DEBUG_STALL_ATTN: the last key tile of a block's first item with any expects 16 bytes that no
+                        // copy delivers, so that the waits for it run out (in every block: a block's own first item may have no
+                        // tiles, and the others may leave it none)
+                        const bool stall = a.debug && is_k && x == n - 1 && cnt == (unsigned)x;
                         fa_expect(&full[st], (unsigned)(cur.n * a.P * kD * 2) + (stall ? 16u : 0u));
                         if (is_k) watch->tiles = cnt + 1;
                     }
