@@ -695,7 +695,7 @@ def _verify_check(ice, c, got, code):
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("n,K,V", [
     (1, 0, 1), (3, 2, 1), (5, 4, 2), (40, 3, 30), (9, 1, 1023), (9, 5, 1024), (9, 2, 1025), (17, 4, 5001), (300, 2, 2049), (2, 63, 3001),
-    (6, 4, 50001), (3, 7, 128000), (2, 1, 150001), (1, 4, 150002)])
+    (6, 4, 50001), (3, 7, 128000), (2, 1, 150001), (1, 4, 150002), (100, 1, 66001), (200, 1, 66001), (1300, 1, 1025)])
 def test_verify(ice, mode, dtype, n, K, V):
     c = _verify_case(n + K + V, mode, dtype, n, K, V)
     pc, got = _verify_run(ice, c)
