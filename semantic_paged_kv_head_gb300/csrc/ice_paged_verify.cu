@@ -579,9 +579,12 @@ __global__ void __launch_bounds__(kGrdThreads, sizeof(T) == 2 ? 12 : 8) verify_g
         const long long rest = item - i * level;
         const int r = (int)(rest / G), g = (int)(rest - (long long)r * G);
         VerifyScratch* const w = a.scratch + r;
-        const int nd = a.n_draft[r], wrong = *(volatile int*)&w->wrong;
+        const int nd = a.n_draft[r];
+        // Other warps raise `wrong` meanwhile, so its loads may differ by lane: a vote, since the way taken has reductions over the whole
+        // warp in it.
+        const bool open = __any_sync(0xffffffffu, i <= kVerMaxDrafts + 1 - *(volatile int*)&w->wrong);
         const bool part = nd >= 0 && nd <= K && i <= nd;
-        if (part && i <= kVerMaxDrafts + 1 - wrong) {
+        if (part && open) {
             const T* p = (const T*)a.target + r * a.t_req + i * a.t_row;
             Best best;
             int t0, t1;

@@ -74,6 +74,21 @@ def test_kernels_wait_before_they_read():
                             "share_step_kernel", "verify_greedy_kernel", "verify_sample_kernel"]
 
 
+def test_words_that_others_change_decide_by_a_vote():
+    """A word that other blocks change meanwhile may read differently in each lane. What it decides is a vote of the warp, so that
+    all lanes go the same way and meet in the shuffles and reductions behind it."""
+    seen = 0
+    for name in ("ice_paged_rope.cu", "ice_paged_share.cu", "ice_paged_verify.cu"):
+        text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
+        for m in re.finditer(r"(?<!asm )volatile", text):
+            start = max(text.rfind(c, 0, m.start()) for c in ";{}")
+            statement = text[start + 1:text.index(";", m.end())]
+            # one declaration, nothing but the vote on the load
+            assert re.fullmatch(r"\s*const bool \w+ = __any_sync\(0xffffffffu, [\w +]+ <= [\w +]+ - \*\(volatile int\*\)&[\w>-]+\)", statement), statement
+            seen += 1
+    assert seen == 1
+
+
 @pytest.mark.parametrize("freq,axis", [
     ([], None), ([1.0] * 7, None), ([1.0] * 72, None), ([1.0] * 12, None), ([math.nan] + [1.0] * 7, None), ([math.inf] + [1.0] * 7, None),
     ([1.0] * 8, [0] * 7), ([1.0] * 8, [0] * 7 + [4]), ([1.0] * 8, [0] * 7 + [-1]), ([1.0] * 8, [0] * 7 + [1 << 32])])
