@@ -474,16 +474,25 @@ __global__ void __launch_bounds__(kSmpThreads, 1024 / kSmpThreads) verify_sample
                     t0 += n;
                 }
             }
-            // the tile's elements, neighbouring ones a thread
+            // The tile's elements, neighbouring ones a thread. The tiles' sums, added up in another order than the part's, may end just
+            // below it, and so lead on to tiles without any weight: the last weight before those is then meant.
             constexpr int E = kTile<T> / kSmpThreads;
-            const int j = t0 * kTile<T> - shift + E * tid;
-            Wide e[E], c;
+            Wide e[E];
+            int j;
+            for (;;) {
+                j = t0 * kTile<T> - shift + E * tid;
+                Wide c;
 #pragma unroll
-            for (int k = 0; k < E; ++k) {
-                if (j + k >= 0 && j + k < V) e[k] = weight(p, q, sure, j + k);
-                c = wide_add(c, e[k]);
+                for (int k = 0; k < E; ++k) {
+                    e[k] = Wide();
+                    if (j + k >= 0 && j + k < V) e[k] = weight(p, q, sure, j + k);
+                    c = wide_add(c, e[k]);
+                }
+                f = block_find<kSmpWarps>(c, [&](Wide) { return x; }, sh);
+                if (f.at >= 0 || t0 == 0) break;
+                --t0;
+                x.hi = INFINITY;
             }
-            f = block_find<kSmpWarps>(c, [&](Wide) { return x; }, sh);
             if (tid == f.at) {
                 Wide low = f.before;
 #pragma unroll

@@ -766,6 +766,23 @@ def test_verify_borders(ice, dtype, V):
     assert got[0][5, 0] == V // 2 and got[0][7, 0] == V - 1 and got[0][9, 0] == V - 1
 
 
+@pytest.mark.parametrize("dtype,V", [(F32, 1 << 19), (F32, 300001), (BF16, 1 << 20)])
+@pytest.mark.parametrize("spread", [3.0, 8.0])
+def test_verify_weight_before_empty_tiles(ice, dtype, V, spread):
+    """Half of the weight near the row's beginning and as much far behind, a long row of nothing after each: half the sum is the border
+    between the two, up to the sums' last bits, and what the first half's tiles hold in one order of addition may lie on either side of what
+    they hold in another. A token is drawn all the same, one with weight next to the border."""
+    n, tile = 64, 512 if dtype == F32 else 1024
+    g = torch.Generator().manual_seed(V)
+    target = torch.zeros((n, 1, V))
+    for r in range(n):
+        x = torch.exp(spread * torch.randn(4 * tile, generator=g))
+        target[r, 0, :4 * tile], target[r, 0, V // 2:V // 2 + 4 * tile] = x, x[torch.randperm(4 * tile, generator=g)]
+    c = [torch.zeros((n, 0), dtype=torch.int32), torch.zeros(n, dtype=torch.int32), target.to(dtype), None, torch.full((n, 1), 0.5)]
+    pc, got = _verify_run(ice, c)
+    _verify_check(ice, c, got, pc.get_error())
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("at", [0, 1023, 1024, 2500, 4999])
 def test_verify_one_entry_alone(ice, dtype, at):
