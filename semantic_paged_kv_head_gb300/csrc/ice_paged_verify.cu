@@ -98,7 +98,14 @@ __device__ __forceinline__ Wide wide_sub(Wide a, Wide b) {
     return wide_add(a, b);
 }
 __device__ __forceinline__ Wide wide_mul(float u, Wide a) {
-    const float p = u * a.hi, e = fmaf(u, a.hi, -p) + u * a.lo;
+    float p = u * a.hi, e = fmaf(u, a.hi, -p) + u * a.lo;
+    if (a.hi < 0x1p-90f) {
+        // What the products cut off may lie below the least number, 2^-149. Sums are multiples of that, so the product down to the
+        // next multiple has the same sums above it.
+        const double x = (double)u * ((double)a.hi + (double)a.lo);
+        p = (float)x;
+        e = __double2float_rd(x - (double)p);
+    }
     Wide r;
     r.hi = p + e;
     r.lo = e - (r.hi - p);

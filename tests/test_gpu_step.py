@@ -826,6 +826,27 @@ def test_verify_entries_of_every_size(ice, dtype, mode, V):
     _verify_check(ice, c, got, pc.get_error())
 
 
+@pytest.mark.parametrize("mode", ["alone", "draft", "lookup"])
+@pytest.mark.parametrize("V", [8, 601, 5000])
+def test_verify_sums_of_the_least_numbers(ice, mode, V):
+    """Weights of a few times 2^-149, as they are left where two models nearly agree: the border u W lies between two numbers."""
+    us = [i / 40 for i in range(40)] + [2.0 ** -30, 1 - 2.0 ** -24]
+    n = len(us)
+    least = 2.0 ** -149
+    w = (1 + torch.arange(V) % 3).double() * least
+    target, draft = w.float().expand(n, 2, V).contiguous(), None
+    u = torch.tensor([[1.0, x] for x in us])
+    if mode == "draft":  # every weight is what the target has above the draft
+        draft = (torch.arange(V) % 5).double() * least
+        target = (w + draft).float().expand(n, 2, V).contiguous()
+        draft = draft.float().expand(n, 1, V).contiguous()
+        target[:, 0, 5], u[:, 0] = 0.0, 1.0  # the draft itself is rejected
+    tokens = torch.full((n, 1), 5, dtype=torch.int32)
+    c = [tokens, torch.full((n,), 0 if mode == "alone" else 1, dtype=torch.int32), target, draft, u]
+    pc, got = _verify_run(ice, c)
+    _verify_check(ice, c, got, pc.get_error())
+
+
 def test_verify_same_rows_for_all(ice):
     """Rows that are one row of memory (strides of 0)."""
     V = 3001
