@@ -619,8 +619,8 @@ int ice_paged_fork(ice_paged* pg, int32_t n_fork, const int32_t* src, const int3
  *    that write into it keeps it.
  * copy_src, copy_dst: device int32 [n_req]; -1 where nothing is to be copied.
  * page_refs: in and out. A count below the number of a page's holders that let go of it is reported as
- *   ICE_ERR_BOUNDS, as is a page id out of range; as with any other failure nothing changes then, and
- *   copy_src and copy_dst are all -1.
+ *   ICE_ERR_BOUNDS, as is an id out of range of a page that a request lets go of or that the ring holds for one; as
+ *   with any other failure nothing changes then, and copy_src and copy_dst are all -1.
  */
 int ice_paged_tables_shared(ice_paged* pg, int32_t n_req, const int32_t* seq_len, const int32_t* n_new,
                             int32_t* block_table, int32_t* free_pages, const int64_t* free_state,

@@ -210,7 +210,22 @@ __device__ __forceinline__ bool share_item(const SharedTables& a, const ShareIte
     return bad;
 }
 
+// Ids that the ring holds for the step are looked at before anything is written for good, by the last warps: they have the fewest items.
+__device__ __forceinline__ void share_ring(const SharedTables& a, int warp, int warps) {
+    const int lane = threadIdx.x & 31;
+    int i = 32 * (warps - 1 - warp) + lane;
+    if (i >= a.most_taken) return;
+    const long long head = a.free_state[0], tail = a.free_state[1];
+    if (head < 0 || tail < head || tail - head > a.n_pages) return;  // another fault
+    const long long at = head % a.n_pages, n = min(tail - head, (long long)a.most_taken);
+    for (; i < n; i += 32 * warps) {
+        const int p = a.free_pages[at + i < a.n_pages ? at + i : at + i - a.n_pages];
+        if (p < 0 || p >= a.n_pages) atomicMax(&a.w.head->ring_bad, kRingNone - (unsigned)i);
+    }
+}
+
 __device__ __forceinline__ void share_claim(const SharedTables& a, int warp, int warps) {
+    share_ring(a, warp, warps);
     const unsigned long long epoch = a.w.head->epoch;
     const int lane = threadIdx.x & 31;
     const ShareItems items = share_items(a);
@@ -322,6 +337,8 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
         const long long at = tid == 0 ? head : tail;
         s_at[tid] = at >= 0 ? (int)(at % n_pages) : 0;
     }
+    __shared__ unsigned s_ring_bad;
+    if (tid == 32) s_ring_bad = __ldcg(&a.w.head->ring_bad);
     bool over = false;
     if (!flags) {
 #pragma unroll
@@ -340,7 +357,7 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
     int code = ICE_OK;
     if ((flags & kBadBounds) || head < 0 || tail < head || tail - head > n_pages) code = ICE_ERR_BOUNDS;
     else if ((flags & kBadCapacity) || over || wrapped || tot[1] > tail - head || tot[0] > (unsigned)a.n_slots) code = ICE_ERR_CAPACITY;
-    else if (tail - head + tot[2] > n_pages) code = ICE_ERR_BOUNDS;
+    else if (tail - head + tot[2] > n_pages || (s_ring_bad && kRingNone - s_ring_bad < tot[1])) code = ICE_ERR_BOUNDS;
     const bool ok = code == ICE_OK;
     const int n_tok = ok ? (int)tot[0] : 0, n_pop = ok ? (int)tot[1] : 0, n_push = ok ? (int)tot[2] : 0;
     if (ok) {
@@ -432,8 +449,7 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
             a.copy_dst[r] = p;
         }
         *e = p;
-        if (p >= 0 && p < n_pages) a.page_refs[p] = 1;
-        else set_status(a.status, ICE_ERR_BOUNDS);  // an id in the ring that is no page's
+        a.page_refs[p] = 1;
     }
     turn();
     for (int r = first; r <= n; r += step) a.q_start[r] = ok ? tok_cum[r] : 0;
@@ -525,6 +541,7 @@ __device__ __forceinline__ void share_fill(const SharedTables& a) {
         if (!ok) set_status(a.status, code);
         a.w.head->ticket = 0;
         a.w.head->flags = 0;
+        a.w.head->ring_bad = 0;
         a.w.head->epoch = epoch + 1;
     }
 }
@@ -556,8 +573,10 @@ __global__ void __launch_bounds__(kShrThreads) share_step_kernel(SharedTables a)
     share_fill<kShrThreads, true>(a);
 }
 
-cudaError_t launch_shared_tables(const SharedTables& a, cudaStream_t s) {
+cudaError_t launch_shared_tables(SharedTables a, cudaStream_t s) {
     const size_t smem = share_smem(a.n);
+    // a request of g new tokens takes at most ceil(g / P) pages, and one that it copies to
+    a.most_taken = a.n_slots / a.P + 2 * a.n;
     // One cluster of 8 SMs, or three launches on all: the first has 1 us less on the GPU where the tables are small, and 5 us less on
     // the host. A step / the end of all requests: 16 with 128 columns 11.1 / 10.5 us (three launches 12.4 / 12.4), 16 with
     // 2310 11.5 / 14.0 (12.5 / 12.6), 1024 with 64 14.4 / 19.7 (12.8 / 15.1; no page shared 15.8 / 32 and
@@ -568,7 +587,9 @@ cudaError_t launch_shared_tables(const SharedTables& a, cudaStream_t s) {
     const int per = kShrGridThreads / 32;
     const long long items = (long long)((a.n + kShrRows - 1) / kShrRows) * ((a.max_blocks + 31) / 32);
     const dim3 grid((unsigned)std::min<long long>(152 * 8, (items + per - 1) / per));
-    cudaError_t e = launch_pdl(share_claim_kernel, grid, dim3(kShrGridThreads), 0, s, a);
+    // with blocks of their own for the ring's ids
+    const dim3 claim(grid.x + std::min(152, (a.most_taken + kShrGridThreads - 1) / kShrGridThreads));
+    cudaError_t e = launch_pdl(share_claim_kernel, claim, dim3(kShrGridThreads), 0, s, a);
     if (e == cudaSuccess) e = launch_pdl(share_count_kernel, grid, dim3(kShrGridThreads), 0, s, a);
     const int blocks = std::max(1, std::min(152, std::max(a.n_slots / 1024, a.max_blocks > kShrLong ? a.n : a.n / 32)));
     if (e == cudaSuccess) e = launch_pdl(share_fill_kernel, dim3(blocks), dim3(kShrThreads), smem, s, a);

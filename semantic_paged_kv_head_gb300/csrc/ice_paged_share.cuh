@@ -11,10 +11,12 @@ struct ShareHead {
     unsigned ticket;
     int flags;                 // kBad*, zero between calls
     int plan[4];               // of a compaction: 1 if it is carried out, pages in use, pages moved
-    int pad[8];
+    unsigned ring_bad;         // of a step: kRingNone - the first place behind the ring's head whose id is no page's; zero between calls
+    int pad[7];
 };
 static_assert(sizeof(ShareHead) == 64, "claims begin at a multiple of 8 bytes");
 enum { kBadBounds = 1, kBadCapacity = 2 };
+constexpr unsigned kRingNone = 1u << 31;  // above every place in a ring
 constexpr int kCmpChunk = 1024;  // pages that a block of a compaction counts at once
 
 // what becomes of the page that a request writes into: kept, or copied
@@ -40,6 +42,7 @@ struct SharedTables {
     ShareScratch w;
     long long n_pages;
     int n, max_blocks, P, n_slots;
+    int most_taken;  // made by the launch: no step that is carried out takes more pages
 };
 
 struct Fork {
@@ -60,7 +63,7 @@ struct Compact {
     int n, max_blocks, P, n_extra, n_moves;
 };
 
-cudaError_t launch_shared_tables(const SharedTables& a, cudaStream_t s);
+cudaError_t launch_shared_tables(SharedTables a, cudaStream_t s);
 cudaError_t launch_fork(const Fork& a, cudaStream_t s);
 cudaError_t launch_compact(const Compact& a, cudaStream_t s);
 // page_bytes, layer_bytes: multiples of 16

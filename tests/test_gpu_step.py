@@ -493,6 +493,41 @@ def test_shared_tables_all_or_nothing(ice, fault, many):
     assert pc.get_error() == 0 and [x.tolist() for x in outs] == list(ref[1:8]) and rf.tolist() == ref[10]
 
 
+@pytest.mark.parametrize("bad", [-1, 8, 2 ** 31 - 1, -2 ** 31])
+@pytest.mark.parametrize("place", [0, 1, 2, 3, 4])
+@pytest.mark.parametrize("many", [False, True])
+def test_shared_tables_bad_ring(ice, bad, place, many):
+    """An id in the ring that is no page's: a step that would take it changes nothing, one that takes only those before it is carried
+    out. Of the requests here 0 copies, 1 keeps its page and takes another, 4 takes one: three pages."""
+    P = 4
+    lens, table, ring, state, refs = _three_holders(P)
+    new = [1, 3, -5, 0, 2]
+    head = 8 * 5 + 6  # the ring's free part runs over its end
+    ring = [ring[(i - head) % 8] for i in range(8)]
+    state = [head, head + 5]
+    if many:
+        lens, new, table = lens + [0] * 1100, new + [0] * 1100, table + [[-1] * 3 for _ in range(1100)]
+    pc = _cache(ice, n_kv_heads=1, n_q_heads=1, page_size=P, n_pages=8, max_requests=len(lens), max_blocks=3, max_tokens=1)
+    ref = plain_tables_shared(lens, new, table, ring, state, refs, 20, P)
+    assert ref[0] == 0 and ref[2][0] - head == 3
+    ring[(head + place) % 8] = bad
+    for in_place in (False, True):
+        t = [_i32(x) for x in (lens, new, table, ring)]
+        st, rf = torch.tensor(state, dtype=torch.int64, device="cuda"), _i32(refs)
+        outs = pc.tables_shared(*t, st, rf, 20, t[0] if in_place else None, st if in_place else None)
+        if place < 3:
+            n = len(lens)
+            assert pc.get_error() == ice.ICE_ERR_BOUNDS and pc.get_error() == 0
+            assert [x.tolist() for x in outs] == [lens, state, [0] * (n + 1), [-1] * 20, [0] * 20, [-1] * n, [-1] * n]
+            assert [t[2].tolist(), t[3].tolist(), rf.tolist()] == [table, ring, refs]
+        else:
+            assert pc.get_error() == 0
+            assert [x.tolist() for x in outs] == list(ref[1:8])
+            want = list(ref[9])
+            want[(head + place) % 8] = bad
+            assert [t[2].tolist(), t[3].tolist(), rf.tolist()] == [ref[8], want, ref[10]]
+
+
 @pytest.mark.parametrize("src,dst,lens", [
     ([0], [5], None), ([-1], [4], None), ([5], [4], None), ([0], [-1], None), ([0], [3], None), ([0, 1], [4, 4], None), ([0], [4], [7]),
     ([0], [4], [-1]), ([4], [4], None), ([0, 4], [4, 3], None)])
