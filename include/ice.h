@@ -565,7 +565,9 @@ typedef struct ice_rope {
  *   position of 32 bits.
  * q, q_out: device, n_tokens x [n_q_heads][d]; token i starts q_stride (q_out_stride)
  *   elements after token i - 1. q_out receives the rotated queries. It is q itself (same
- *   address and stride) or does not overlap it. Both NULL: keys and values alone.
+ *   address and stride) or does not overlap it: with one stride, as columns of a buffer that
+ *   holds both, row by row; with two, from the first row to the last. Both NULL: keys and
+ *   values alone.
  * The rest as in ice_paged_append. A token whose slot is -1, or out of range, is skipped
  * altogether: its row of q_out stays as it was.
  */

@@ -1,6 +1,7 @@
 // C ABI of the calls around the paged cache's attention: rotating append, shared pages, verification of drafts. See
 // include/ice.h for the contract of each call.
 #include <cmath>
+#include <utility>
 
 #include "ice_paged_handle.cuh"
 #include "ice_paged_rope.cuh"
@@ -48,6 +49,17 @@ int share_scratch(ice_paged* pg, const Buffers& b, void* stream, ShareScratch* w
     return ICE_OK;
 }
 
+// Whether n rows of `row` bytes each share memory: those at a + i sa and at b + j sb. With equal strides (>= row) exact: columns of one
+// buffer share none. Else by the spans from the first row to the end of the last.
+bool rows_overlap(uintptr_t a, int64_t sa, uintptr_t b, int64_t sb, int64_t row, int64_t n) {
+    if (a > b) std::swap(a, b), std::swap(sa, sb);
+    const uint64_t apart = b - a;  // b's first row begins so far behind a's
+    if (apart >= (uint64_t)(n - 1) * (uint64_t)sa + (uint64_t)row) return false;
+    if (sa != sb) return true;
+    const uint64_t off = apart % (uint64_t)sa, k = apart / (uint64_t)sa;  // it begins in or behind row k of a, k < n
+    return off < (uint64_t)row || (k + 1 < (uint64_t)n && off + (uint64_t)row > (uint64_t)sa);
+}
+
 bool req_ok(const ice_paged* pg, int32_t n_req) { return pg && n_req >= 1 && n_req <= pg->p.max_requests; }
 
 }  // namespace
@@ -67,10 +79,8 @@ int ice_paged_rope_append(ice_paged* pg, int32_t n_tokens, const ice_rope* rope,
     if (Hq && (!stride_ok(pg, q_stride, Hq) || !stride_ok(pg, q_out_stride, Hq))) return ICE_ERR_INVALID_ARG;
     if (n_tokens == 0) return ICE_OK;
     if (Hq && !(q == q_out && q_stride == q_out_stride)) {
-        const uintptr_t es = es_of(pg), row = (uintptr_t)Hq * kD * es, n1 = n_tokens - 1;
-        const uintptr_t q0 = (uintptr_t)q, o0 = (uintptr_t)q_out;
-        if (q0 < o0 + n1 * (uintptr_t)q_out_stride * es + row && o0 < q0 + n1 * (uintptr_t)q_stride * es + row)
-            return ICE_ERR_INVALID_ARG;
+        const int64_t es = es_of(pg), row = (int64_t)Hq * kD * es;
+        if (rows_overlap((uintptr_t)q, q_stride * es, (uintptr_t)q_out, q_out_stride * es, row, n_tokens)) return ICE_ERR_INVALID_ARG;
     }
     Buffers b(pg, stream);
     if (Hq) b.need(q, 16).need(q_out, 16);

@@ -132,6 +132,43 @@ def test_rope_strided(ice, dtype, in_place):
     _rope_check(c, False, 0, *got)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("first", [False, True])
+@pytest.mark.parametrize("n", [1, 2, 65])
+def test_rope_columns_of_one_buffer(ice, dtype, first, n):
+    """Queries and rotated queries as columns of one buffer, in either order: rows of one stride that share no memory."""
+    c = _rope_case(12, dtype, n, 2, 4, 16, 64, 1)
+    width, gap = 8 * D, 16
+    buf = torch.full((n, 2 * width + gap), 7.0, dtype=dtype, device="cuda")
+    a, b = (x.unflatten(1, (8, D)) for x in (buf[:, :width], buf[:, width:2 * width]))
+    q, out = (b, a) if first else (a, b)
+    q.copy_(c["q"])
+    pc = _cache(ice, n_pages=c["n_pages"], dtype=dtype)
+    kp, vp = pc.new_pages()
+    kp.fill_(7.0)
+    vp.fill_(7.0)
+    rest = (c["k"].cuda(), c["v"].cuda(), c["pos"].cuda(), ice.Rope(c["freq"]), c["slots"].cuda(), kp, vp)
+    assert pc.rope_append(q, *rest, q_out=out) is out
+    assert pc.get_error() == 0
+    _rope_check(c, False, 0, out.cpu(), kp.cpu(), vp.cpu())
+    assert torch.equal(q.cpu(), c["q"]) and bool((buf[:, 2 * width:] == 7.0).all())
+    # a part of a row, or of the row before or behind, in common: refused
+    step = 2 * width + gap
+    base = torch.zeros((2 * n + 2) * step, dtype=dtype, device="cuda")
+    at = lambda x: torch.as_strided(base, (n, 8, D), (step, D, 1), x)  # noqa: E731
+    for x, y, fine in ((width - 8, 0, False), (0, width - 8, False), (width + gap + 8, 0, n == 1), (0, width + gap + 8, n == 1),
+                       (step, 0, n == 1), (0, (n - 1) * step + width - 8, False), (0, (n - 1) * step + width, True),
+                       ((n - 1) * step + width, 0, True), (width, 0, True), (width + gap, 0, True), (0, width + gap, True)):
+        if fine:
+            pc.rope_append(at(x), *rest, q_out=at(y))
+            continue
+        with pytest.raises(ice.IceError) as e:
+            pc.rope_append(at(x), *rest, q_out=at(y))
+        assert e.value.code == ice.ICE_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert pc.get_error() == 0
+
+
 @pytest.mark.parametrize("pos,offset", [(0, 0), (2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (-2 ** 31, 0), (-2 ** 31, -2 ** 31), (-3, 3),
                                         (2 ** 24 + 1, 0)])
 def test_rope_far_positions(ice, pos, offset):
