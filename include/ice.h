@@ -562,7 +562,8 @@ typedef struct ice_rope {
  * positions: device int32, n_axes rows of n_tokens, row x at positions + x * pos_stride
  *   (pos_stride >= n_tokens where n_axes > 1). pos_offset is added to each (for the positions
  *   that ice_paged_tables writes, the length of the shared prefix). Angles are right at every
- *   position of 32 bits.
+ *   position of 32 bits: frequencies are held to 2^-65 of a turn (those above 2^32 to
+ *   |freq| 2^-109 more).
  * q, q_out: device, n_tokens x [n_q_heads][d]; token i starts q_stride (q_out_stride)
  *   elements after token i - 1. q_out receives the rotated queries. It is q itself (same
  *   address and stride) or does not overlap it: with one stride, as columns of a buffer that

@@ -1,8 +1,8 @@
 // New tokens' queries and keys rotated by their positions, keys and values written into the pages.
 #include <algorithm>
-#include <cmath>
 
 #include "ice_paged_rope.cuh"
+#include "ice_paged_turns.h"
 
 namespace ice {
 
@@ -194,20 +194,6 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeAppend a)
             }
         }
     }
-}
-
-// f 2^64 / 2 pi modulo 2^64. A quotient in 53 bits would be off by up to 2^-23 turns at a position of 2^31, so what the division
-// cuts off is added.
-static unsigned long long turns(double f) {
-    const double c = 6.283185307179586, c_lo = 2.4492935982947064e-16;  // 2 pi to 106 bits
-    const double t = f / c, rest = (std::fma(-t, c, f) - t * c_lo) / c;
-    // whole turns dropped, exactly; a magnitude below 1 fits 64 bits
-    auto bits = [](double x) {
-        const double y = std::fmod(x, 1.0);
-        const unsigned long long b = (unsigned long long)std::ldexp(std::fabs(y), 64);
-        return y < 0.0 ? 0ull - b : b;
-    };
-    return bits(t) + bits(rest);
 }
 
 cudaError_t launch_rope_append(RopeAppend a, const ice_rope& r, int dtype, cudaStream_t s) {

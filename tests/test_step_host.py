@@ -7,6 +7,7 @@ import random
 import re
 import shutil
 import subprocess
+from fractions import Fraction
 
 import pytest
 import torch
@@ -87,6 +88,40 @@ def test_words_that_others_change_decide_by_a_vote():
             assert re.fullmatch(r"\s*const bool \w+ = __any_sync\(0xffffffffu, [\w +]+ <= [\w +]+ - \*\(volatile int\*\)&[\w>-]+\)", statement), statement
             seen += 1
     assert seen == 1
+
+
+TURNS = r"""
+#include <cstdio>
+#include <cstdlib>
+#include "ice_paged_turns.h"
+
+int main() {
+    char line[64];
+    while (std::fgets(line, sizeof line, stdin)) std::printf("%llu\n", ice::turns(std::strtod(line, nullptr)));
+}
+"""
+
+
+def test_frequencies_to_the_nearest_part_of_a_turn(tmp_path):
+    """The 64-bit fraction of a turn that a frequency is held as, against exact fractions: to the nearest, 2^-65 turns. 2 pi is taken in
+    106 bits: a quotient t moves by t 2^-106 at most, 2^-42 t units of 2^-64."""
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no host C++ compiler")
+    src, exe = tmp_path / "turns.cpp", tmp_path / "turns"
+    src.write_text(TURNS)
+    subprocess.run([cxx, "-std=c++17", "-O2", "-I", CSRC, str(src), "-o", str(exe)], check=True)
+    turn = Fraction("6.2831853071795864769252867665590057683943387987502116419498891846156")
+    rng = random.Random(1)
+    freq = [base ** (-i / 64) for base in (10000.0, 500000.0, 5e6) for i in range(64)]
+    freq += [math.ldexp(1 + rng.random(), rng.randint(-70, 31)) for _ in range(3000)] + [0.0, 5e-324, 2.0 ** -1022, 2.0 ** -65, 2.0 ** -60, 1.0, 6.5, 2.0 ** 32]
+    freq += [k * float(turn) for k in (0.25, 0.5, 1, 2, 1000)] + [float(turn) * 2.0 ** -k for k in (11, 12, 13, 40, 64, 65)]
+    freq += [-f for f in freq]
+    r = subprocess.run([str(exe)], input="\n".join(f.hex() for f in freq) + "\n", capture_output=True, text=True, check=True)
+    for f, got in zip(freq, r.stdout.split(), strict=True):
+        units = Fraction(f) / turn * 2 ** 64
+        off = (int(got) - units + 2 ** 63) % 2 ** 64 - 2 ** 63
+        assert abs(off) <= Fraction(1, 2) + Fraction(1, 2 ** 16) + abs(Fraction(f) / turn) / 2 ** 42, (f, float(off))
 
 
 @pytest.mark.parametrize("freq,axis", [
