@@ -10,8 +10,9 @@ namespace ice {
 // Pair i of a head, (a, b), turns by the angle w_i p, with p the token's position on the pair's axis:
 // (a cos - b sin, b cos + a sin). An angle counts modulo whole turns, so w_i / 2 pi is held as a 64-bit
 // fraction of a turn and multiplied by p in whole numbers modulo 2^64: the product is right to 2^-65 |p| turns at
-// every position of 32 bits (in fp32 an angle of 2^20 radians would be off by 1/16). Its first 32 bits, signed, go to
-// sincospi.
+// every position of 32 bits (in fp32 an angle of 2^20 radians would be off by 1/16). Of its first 32 bits two, rounded, are the
+// quadrant, and the rest, at most an eighth of a turn either way, goes to sincospi in fp32: off by 2^-28 turns at most, less
+// near a quadrant's axes, where the sine or the cosine is small (the whole angle in fp32 would be off by 2^-26 there too).
 //
 // A warp works on one token: its lanes make the 64 pairs' sines and cosines, once for all heads, and pass
 // them through shared memory. Then eight lanes take a row (a head's 128 elements of q, k or v), each the two
@@ -67,6 +68,15 @@ template <> struct RopePiece<float> {
                               __float_as_uint(v[4 * i + 3]));
     }
 };
+
+// Cosine and sine of f / 2^64 turns.
+__device__ __forceinline__ float2 cos_sin(unsigned long long f) {
+    const unsigned u = (unsigned)((f + 0x80000000ull) >> 32), quadrant = (u + 0x20000000u) >> 30;
+    float s, c;
+    sincospif((float)(int)(u - (quadrant << 30)) * 0x1p-31f, &s, &c);  // 2^-31: half turns
+    const float x = quadrant & 1 ? s : c, y = quadrant & 1 ? c : s;
+    return make_float2(quadrant == 1 || quadrant == 2 ? -x : x, quadrant & 2 ? -y : y);
+}
 
 template <typename T, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeAppend a) {
@@ -142,9 +152,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeAppend a)
         // the token's sines and cosines
         const unsigned long long f0 = (unsigned long long)((long long)p0 + a.pos_offset) * turn0;
         const unsigned long long f1 = (unsigned long long)((long long)p1 + a.pos_offset) * turn1;
-        float2 c0, c1;
-        sincospif((float)(int)((f0 + 0x80000000ull) >> 32) * 4.656612873077393e-10f, &c0.y, &c0.x);  // 2^-31: half turns
-        sincospif((float)(int)((f1 + 0x80000000ull) >> 32) * 4.656612873077393e-10f, &c1.y, &c1.x);
+        const float2 c0 = cos_sin(f0), c1 = cos_sin(f1);
         __syncwarp();
         cs[lane] = c0;
         cs[lane + 32] = c1;

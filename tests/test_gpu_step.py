@@ -211,6 +211,32 @@ def test_rope_far_angles_to_the_last_bits(ice, dtype, pos, offset):
         assert bool(((size - size0).abs() <= 4 * (err + u) * size0).all())
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("pos,offset", [(1, 0), (1000003, 0), (-77, 50), (2 ** 31 - 1, 2 ** 31 - 1)])
+def test_rope_near_the_axes(ice, pos, offset, interleaved):
+    """Angles near quarters of a turn, where the sine or the cosine is small, in exact fractions. Rows (0, 1) come out as (-sin, cos)
+    with no rounding of their own.
+
+    The angle: its fraction of a turn in 32 bits, 2 pi 2^-33, and the frequency's 2^-65 turns a position; what is left of it in fp32 is exact below
+    2^24 / 2^32 of a turn from an axis. The functions: two steps of the result, 2^-22 of it."""
+    c = _rope_case(13, F32, 5, 2, 2, 16, 64, 1)
+    c["pos"].fill_(pos)
+    p, rng = pos + offset, random.Random(pos)
+    c["freq"] = [(math.pi / 2 * rng.randint(-9, 9) + rng.choice([1, -1]) * 10.0 ** -rng.uniform(1.7, 9)) / p for _ in range(64)]
+    first, second = (slice(0, D, 2), slice(1, D, 2)) if interleaved else (slice(0, 64), slice(64, D))
+    for name in ("q", "k"):
+        c[name][..., first], c[name][..., second] = 0.0, 1.0
+    pc, out, kp, _ = _rope_run(ice, c, interleaved, offset)
+    assert pc.get_error() == 0
+    near = torch.tensor([float((Fraction(f) * p + TURN / 2) % TURN - TURN / 2) for f in c["freq"]], dtype=torch.float64)
+    axis = torch.tensor([float((Fraction(f) * p + TURN / 8) % (TURN / 4) - TURN / 8) for f in c["freq"]], dtype=torch.float64)
+    assert bool((axis.abs() < 2 * math.pi * 2.0 ** -8).all())
+    angle = 2 * math.pi * (2.0 ** -33 + abs(p) * 2.0 ** -65)
+    for have in (out, kp.transpose(1, 2).reshape(-1, 2, D)[c["slots"]]):
+        for got, want in ((have[..., first], -near.sin()), (have[..., second], near.cos())):
+            assert bool(((got.double() - want).abs() <= 1.01 * angle + 2.0 ** -22 * want.abs()).all())
+
+
 def test_rope_keys_alone(ice):
     c = _rope_case(6, BF16, 77, 4, 2, 16, 64, 2)
     pc, _, kp, vp = _rope_run(ice, c, with_q=False)
