@@ -693,7 +693,8 @@ int ice_paged_compact(ice_paged* pg, int32_t n_req, const int32_t* seq_len, cons
  * tokens: device int32 [n_req][n_draft_max + 1]; receives the drafts that stay, the token, then -1.
  * n_accepted: device int32 [n_req]; receives the drafts that stay.
  * n_new: device int32 [n_req]; receives n_accepted - n_draft, by how many tokens the request changes in the next
- *   ice_paged_tables or ice_paged_tables_shared call: the rejected ones.
+ *   ice_paged_tables or ice_paged_tables_shared call: the rejected ones. That is a call of its own, before the one with the next
+ *   step's new tokens: a sum of the two would place those behind the rejected ones.
  *
  * A draft outside the vocabulary does not stay, and is reported (ICE_ERR_BOUNDS), as is an n_draft out of
  * range (the request takes no part) and a deciding row that leaves nothing (all entries 0 or NaN; the token is then

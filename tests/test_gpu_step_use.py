@@ -1,7 +1,9 @@
 """The calls around the paged cache's attention as a program uses them: refusals on a live handle, streams, graphs, and a loop of
 speculative decoding over requests that share pages."""
 import ctypes
+import os
 import random
+import re
 
 import pytest
 import torch
@@ -377,6 +379,37 @@ def test_shared_pages_in_a_graph(ice):
         assert [ms.tolist(), md.tolist()] == [msrc, mdst]
         assert gpu.lists() == _pool_lists(pool), t
         pool.check()
+
+
+@pytest.mark.parametrize("axes", [1, 3])
+def test_readme_examples(ice, axes):
+    """The examples of the paged cache, as they are written, one after the other."""
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    blocks = [b for b in re.findall(r"```python\n(.*?)```", text, re.S) if "pc." in b]
+    assert len(blocks) == 2 and "PagedCache" in blocks[0] and "compact" in blocks[1]
+    g = torch.Generator().manual_seed(1)
+    n_req, drafts, V, L = 8, 3, 500, 37
+    new = [1 + min(r, drafts) for r in range(n_req)]
+    n_slots = sum(new) + 5
+    rows = [torch.randn((n_slots, h, D), generator=g).to(BF16).cuda() for h in (32, 8, 8)]
+    probs = torch.softmax(torch.randn((n_req, drafts + 1, V), generator=g), -1).cuda()
+    here = dict(ice=ice, torch=torch, n_req=n_req, n_slots=n_slots, n_new=_i32(new), prefix_len=L, n_prefix_pages=pages_of(L, 16),
+                prefix_table=_i32([4095, 4094, 4093]), freq=[10000.0 ** (-i / 64) for i in range(64)], axis=[i % 3 for i in range(64)],
+                draft_tokens=torch.zeros((n_req, drafts), dtype=torch.int32, device="cuda"), n_draft=_i32(new) - 1, target_probs=probs,
+                draft_probs=probs[:, :drafts].flip(2).contiguous(), uniform=torch.rand((n_req, drafts + 1), generator=g).cuda())
+    for i, b in enumerate(blocks):
+        if axes > 1:  # as the comments beside the two lines say
+            b = b.replace("ice.Rope(freq)", "ice.Rope(freq, axis)").replace(", pos, rope", f", torch.stack([pos] * {axes}), rope")
+        here.update(q=rows[0], k=rows[1], v=rows[2], src=_i32([0, 0]), dst=_i32([6, 7]))
+        if i:
+            here["k_pages"].zero_(), here["v_pages"].zero_()
+        exec(b, here)
+        assert here["pc"].get_error() == 0
+    assert bool(torch.isfinite(here["out"][:sum(new)]).all())
+    lens, kept = here["seq_len"].tolist(), here["n_accepted"].tolist()
+    assert lens == [1 + a for a in kept]
+    pages = here["n_prefix_pages"] + n_req  # a page a request
+    assert here["state"].tolist() == [0, 4096 - pages] and int(here["refs"][:pages].sum()) == pages
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
