@@ -651,7 +651,8 @@ int ice_paged_copy(ice_paged* pg, int32_t n, const int32_t* src, const int32_t* 
  * move_src, move_dst: device int32 [n_moves]; receive the moves in order, for ice_paged_copy, and -1
  *   behind the last. n_moves = n_pages / 2 always suffices.
  * seq_len: device int32 [n_req]. block_table, block_table_out: device int32 [n_req][max_blocks]; the
- *   entries of each request's pages are rewritten, others in block_table_out stay as they were.
+ *   entries of each request's pages are rewritten (all of a request whose length is out of range, see
+ *   below), others in block_table_out stay as they were.
  * extra, extra_out: device int32 [n_extra], further page ids of the caller's (prefixes); NULL when
  *   n_extra is 0.
  * page_refs, page_refs_out: device int32 [n_pages].

@@ -740,7 +740,8 @@ __device__ __forceinline__ void compact_apply(const Compact& a) {
     const long long cap = (long long)a.max_blocks * a.P;
     for (int r = first >> 5; r < a.n; r += step >> 5) {
         const int len = a.seq_len[r];
-        const int pages = len < 0 || len > cap ? 0 : (len + a.P - 1) / a.P;
+        // a length that is out of range, with which nothing moves: the whole row
+        const int pages = len < 0 || len > cap ? a.max_blocks : (len + a.P - 1) / a.P;
         const long long row = (long long)r * a.max_blocks;
 #pragma unroll 4
         for (int c = lane; c < pages; c += 32) a.block_table_out[row + c] = goes(a.block_table[row + c]);

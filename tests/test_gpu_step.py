@@ -662,6 +662,24 @@ def test_compact_all_or_nothing(ice, fault):
         assert rg.tolist() == ring and st.tolist() == state
 
 
+@pytest.mark.parametrize("length", [-1, 13, 2 ** 31 - 1, -2 ** 31])
+@pytest.mark.parametrize("wide", [False, True])
+def test_compact_tables_of_a_refused_call(ice, length, wide):
+    """A call that changes nothing gives the tables that it was given: each request's entries, and the whole row of one whose length is
+    impossible. One cluster, and three launches."""
+    P, cols, n_pages = 4, 3, 20000 if wide else 8
+    table = [[5, 2, -1], [7, -9, 3], [0, 1, 4]]
+    refs = [1] * 8 + [0] * (n_pages - 8)
+    pc = _cache(ice, n_kv_heads=1, n_q_heads=1, page_size=P, n_pages=n_pages, max_requests=3, max_blocks=cols, max_tokens=1)
+    t, rf, ring = _i32(table), _i32(refs), _i32([-3] * n_pages)
+    st = torch.tensor([4, 5], dtype=torch.int64, device="cuda")
+    out = torch.full_like(t, 99)
+    src, dst, to, ro, _ = pc.compact(_i32([6, length, 12]), t, rf, ring, st, block_table_out=out, page_refs_out=torch.zeros_like(rf))
+    assert pc.get_error() == ice.ICE_ERR_BOUNDS and pc.get_error() == 0
+    assert to.tolist() == [[5, 2, 99], table[1], table[2]] and ro.tolist() == refs and t.tolist() == table
+    assert set(src.tolist() + dst.tolist()) == {-1} and st.tolist() == [4, 5] and set(ring.tolist()) == {-3}
+
+
 @pytest.mark.parametrize("n_pages,fill,n,cols", [
     (1, 0, 37, 50), (1, 1, 37, 50), (1023, 0.5, 37, 50), (4096, 0.3, 37, 50), (4097, 1.0, 37, 50), (5000, 0.02, 37, 50), (200000, 0.4, 37, 50),
     (1, 1, 300, 3600), (1025, 0.9, 300, 3600), (30000, 0.5, 300, 3600), (1100000, 0.3, 37, 50)])
