@@ -262,6 +262,29 @@ def test_outputs_belong_to_the_given_stream(ice):
     assert [t.tolist() for t in got] == plain and [t.tolist() for t in out] == ref and fk.tolist() == forked
 
 
+def test_outputs_without_the_short_allocation(ice, monkeypatch):
+    """Outputs are allocated by a short way where PyTorch has it, else by torch.empty: the same tensors, and calls give the same."""
+    shapes = [((5,), torch.int32), ((0,), torch.int32), ((2,), torch.int64), ((3, 4), torch.int32), ((1, 1), torch.float32), ((3, 1), torch.int32)]
+
+    def outputs():
+        pc = _cache(ice)
+        made = [ice._empty(shape, t, pc.device) for shape, t in shapes]
+        lens, table, ring, state = pc.new_tables(3)
+        refs = pc.new_refs()
+        step = pc.tables_shared(lens, _i32([3, 17, 0]), table, ring, state, refs, 24)
+        forked = pc.fork(_i32([1]), _i32([2]), step[0], table, refs)
+        moves = pc.compact(forked, table, refs, ring, state)
+        ver = pc.verify(*[None if x is None else x.cuda() for x in _verify_case(1, "sample", F32, 3, 2, 500)])
+        assert pc.get_error() == 0
+        return [(x.shape, x.stride(), x.dtype, x.device) for x in made], [x.tolist() for x in (*step, forked, *moves[:4], refs, *ver)]
+
+    first = outputs()
+    monkeypatch.setattr(ice, "_empty_strided", None)
+    second = outputs()
+    assert first == second
+    assert first[0] == [(x.shape, x.stride(), x.dtype, x.device) for x in (torch.empty(s, dtype=t, device="cuda") for s, t in shapes)]
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_rope_and_verify_in_graphs(ice, dtype):
     """Captured once, replayed on other inputs; two captured calls share a handle."""
