@@ -577,11 +577,12 @@ cudaError_t launch_shared_tables(SharedTables a, cudaStream_t s) {
     const size_t smem = share_smem(a.n);
     // a request of g new tokens takes at most ceil(g / P) pages, and one that it copies to
     a.most_taken = a.n_slots / a.P + 2 * a.n;
-    // One cluster of 8 SMs, or three launches on all: the first has 1 us less on the GPU where the tables are small, and 5 us less on
-    // the host. A step / the end of all requests: 16 with 128 columns 11.1 / 10.5 us (three launches 12.4 / 12.4), 16 with
-    // 2310 11.5 / 14.0 (12.5 / 12.6), 1024 with 64 14.4 / 19.7 (12.8 / 15.1; no page shared 15.8 / 32 and
-    // 15.3 / 15.5), 64 with 2048 17.4 / 31.3 (13.1 / 13.7), 256 with
-    // 2048 42.2 / 102 (13.9 / 19.3).
+    // One cluster of 8 SMs, or three launches on all. The first has 5 us less on the host, and up to 2 less on the GPU where the tables are
+    // small. Towards the bound of 2^16 entries the GPU loses 1 to 5 us (17 where 1024 requests that share no page end in one call),
+    // which only an eager caller has back from the host; beyond it more than that. A step / the end of all requests, one cluster
+    // (three launches): 16 with 128 columns 11.1 / 10.5 us (12.4 / 12.4), 16 with 2310 11.5 / 14.0 (12.5 / 12.6), 1024 with 64 14.4 / 19.7
+    // (12.8 / 15.1), with no page shared 15.8 / 32 (15.3 / 15.5), 64 with 2048 17.4 / 31.3 (13.1 / 13.7), 256 with 2048 42.2 / 102
+    // (13.9 / 19.3).
     if (a.n <= kShrFew && a.n_slots <= 65536 && (long long)a.n * a.max_blocks <= 1 << 16)
         return launch_cluster(share_step_kernel, kShrCluster, kShrThreads, smem, s, a);
     const int per = kShrGridThreads / 32;

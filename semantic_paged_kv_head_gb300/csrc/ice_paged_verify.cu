@@ -27,11 +27,12 @@ namespace ice {
 // rows first; a warp skips its group when a draft before that row is known not to stay, which changes what is read but
 // not the result.
 //
-// Measured: one request of four drafts on 128000 fp32 entries 7.4 us, three loads that depend on each other, the
-// count, and the search. 64 requests of up to seven 16.8 us (57 MB: 3.4 TB/s; the same fixed parts around one wave of loads);
-// 256 looked-up requests on 50001 bf16 entries 16.3 us, 1000 of them 38. Greedy, 128 requests of up to four drafts on 150001 bf16
-// entries 29.6 us, of which 136 MB are read where 94 are needed (rows of the next draft are under way before the verdict on this one); 512 of one draft 45 us, 5.8 TB/s.
-// A thread-block cluster a request took 16 us for the 64 and 22 for 256 looked-up requests (17 here), and 61 for the
+// Measured: one request of four drafts on 128000 fp32 entries 7.6 us, three loads that depend on each other, the
+// count, and the search. 64 requests of up to seven 16.7 us (57 MB: 3.4 TB/s): the same fixed parts around a warp's three or four
+// tiles, each of which is loaded, added up and reduced before the next one's loads; 256 looked-up requests on 50001 bf16 entries
+// (about three tiles a warp) 16.3 us, 1000 of them 38. At 64 registers, 1024 threads an SM, the bf16 forms spill 12 bytes. Greedy, 128 requests of up to four drafts on 150001 bf16
+// entries 29.8 us, of which 136 MB are read where 94 are needed (rows of the next draft are under way before the verdict on this one); 512 of one draft 45 us, 5.8 TB/s.
+// A thread-block cluster a request took as long for the 64 (16 us), but 22 us for the 256 looked-up ones and 61 for the
 // greedy ones, whose rows it read one after the other.
 // ---------------------------------------------------------------------------
 constexpr int kSmpMost = 256;  // threads of a block: these, or half of them
