@@ -211,6 +211,7 @@ __device__ __forceinline__ bool share_item(const SharedTables& a, const ShareIte
 }
 
 // Ids that the ring holds for the step are looked at before anything is written for good, by the last warps: they have the fewest items.
+// Beside the claims, so at no cost in a step of few tokens a request (up to 0.2 us); 1.2 us of 18 where 64000 pages of one token are taken.
 __device__ __forceinline__ void share_ring(const SharedTables& a, int warp, int warps) {
     const int lane = threadIdx.x & 31;
     int i = 32 * (warps - 1 - warp) + lane;
